@@ -8,7 +8,10 @@ if the library is missing or fails to load, `lib()` raises.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
+import struct
+from typing import NamedTuple
 
 import numpy as np
 
@@ -42,6 +45,7 @@ SYMBOLS = (
     "qi_dit_profile_read", "qi_last_error", "qi_gemm_bf16", "qi_attention_f16", "qi_gemm_bf16_noalloc", "qi_gemv_bf16",
     "qi_dit_step_cfg", "qi_dpmpp2m_coeffs", "qi_dpmpp2m_update", "qi_dit_step_fbcache", "qi_dit_fbcache_reset",
     "qi_dit_set_mxfp8", "qi_quant_mxfp8", "qi_gemm_mxfp8", "qi_debug_inject", "qi_dit_euler_step", "qi_dit_set_range_probe",
+    "qi_prefix_attention", "qi_prefix_attention_workspace", "qi_kv8_write", "qi_kv8_read", "qi_add_rmsnorm_mxfp8",
 )
 
 
@@ -121,6 +125,10 @@ def lib() -> ctypes.CDLL:
         "qi_quant_mxfp8": [P, I, I, I, P, P, P],
         "qi_gemm_mxfp8": [P, P, P, P, P, P, I, I, I, P],
         "qi_dpmpp2m_update": [P, P, P, I, P, I, I, P],
+        "qi_prefix_attention": [P, P],
+        "qi_kv8_write": [I, I, I, I, I, P, P, P, P, P, P, P, P, P],
+        "qi_kv8_read": [I, I, I, I, I, P, P, P, P, P, P, P, P, P],
+        "qi_add_rmsnorm_mxfp8": [P, P],
     }
     for name, args in sig.items():
         fn = getattr(L, name)
@@ -128,6 +136,8 @@ def lib() -> ctypes.CDLL:
         fn.restype = ctypes.c_int
     L.qi_kv_cache_bytes.argtypes = [I, I]
     L.qi_kv_cache_bytes.restype = S
+    L.qi_prefix_attention_workspace.argtypes = [P]
+    L.qi_prefix_attention_workspace.restype = S
     L.qi_last_error.argtypes = []
     L.qi_last_error.restype = ctypes.c_char_p
     _lib = L
@@ -279,6 +289,255 @@ def gemv(x, W, b, silu_in: bool = False):
     y = torch.empty(2, out_dim, dtype=torch.float32, device=x.device)
     _check(lib().qi_gemv_bf16(_ptr(x), in_dim, _ptr(W), _ptr(b), out_dim, _ptr(y), int(silu_in), _stream()))
     return y
+
+
+# ---------------------------------------------------------------- batches from one prompt
+
+DT_F16, DT_BF16, DT_F32 = 0, 1, 2
+_TENSOR4 = struct.Struct("@Pqqq")                          # qi_tensor4
+_PREFIX_ATTN = struct.Struct("@8if" + "Pqqq" * 6 + "6PNP")  # qi_prefix_attn
+_ADD_RMSNORM = struct.Struct("@6ifPqPqPqPPP")              # qi_add_rmsnorm
+_NO_TENSOR = (0, 0, 0, 0)
+_ws_bytes: dict = {}                                       # workspace bytes by sizes
+
+
+class KV8Cache(NamedTuple):
+    """8-bit K/V: E4M3 codes k, v [B, S, H, 128] and UE8M0 scales k_sf, v_sf [B, S, H, 4], all uint8
+    and contiguous. `kv8_cache` makes an empty one."""
+    k: "object"
+    v: "object"
+    k_sf: "object"
+    v_sf: "object"
+
+    def prefix(self, b: int, rows: int) -> "KV8Cache":
+        """The first `rows` rows of sequence b, as prefix_attention's prefix8 takes them (a view)."""
+        if not 0 <= b < self.k.shape[0] or not 1 <= rows <= self.k.shape[1]:
+            raise ValueError(f"prefix: sequence {b}, rows {rows} of a cache {tuple(self.k.shape)}")
+        return KV8Cache(*(t[b, :rows] for t in self))
+
+
+def kv8_cache(batch: int, rows: int, heads: int, device="cuda") -> KV8Cache:
+    """An 8-bit cache of zeros for `batch` sequences of up to `rows` rows."""
+    import torch
+    return KV8Cache(*(torch.zeros(batch, rows, heads, n, dtype=torch.uint8, device=device)
+                      for n in (HEAD_DIM, HEAD_DIM, HEAD_DIM // 32, HEAD_DIM // 32)))
+
+
+def _dt16(t, name):
+    import torch
+    if t.dtype == torch.float16:
+        return DT_F16
+    if t.dtype == torch.bfloat16:
+        return DT_BF16
+    raise ValueError(f"{name}: want float16 or bfloat16, got {t.dtype}")
+
+
+def _view4(t, like, shape, name):
+    """(pointer, batch, row, head strides) of a 16-bit tensor `shape` = [batch, row, head, 128] (batch may be left out)."""
+    if t.dtype != like.dtype or t.device != like.device or tuple(t.shape) != shape:
+        raise ValueError(f"{name}: want {like.dtype} {like.device} {shape}, got {t.dtype} {t.device} {tuple(t.shape)}")
+    st = t.stride()
+    if st[-1] != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    return (t.data_ptr(), *st[:3]) if len(st) == 4 else (t.data_ptr(), 0, *st[:2])
+
+
+def _int32_ptr(t, n, device, name):
+    import torch
+    if t is None:
+        return 0
+    if t.dtype != torch.int32 or t.device != device or tuple(t.shape) != (n,) or not t.is_contiguous():
+        raise ValueError(f"{name}: want contiguous int32 {device} ({n},), got {t.dtype} {t.device} {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _kv8_ptrs(cache, shape, device, name):
+    """Pointers of an 8-bit cache's four tensors of leading shape `shape`."""
+    import torch
+    out = []
+    for t, n in zip(cache, (HEAD_DIM, HEAD_DIM, HEAD_DIM // 32, HEAD_DIM // 32)):
+        if t.dtype != torch.uint8 or t.device != device or tuple(t.shape) != (*shape, n) or not t.is_contiguous():
+            raise ValueError(f"{name}: want contiguous uint8 {device} {(*shape, n)}, got {t.dtype} {t.device} "
+                             f"{tuple(t.shape)}")
+        out.append(t.data_ptr())
+    return out
+
+
+def _on_device(fn):
+    """Runs `fn` (first argument a tensor or a KV8Cache) with that tensor's device current, and with
+    `stream`, if given, as the current stream, so that what the call allocates belongs to it."""
+    import functools
+    name = fn.__code__.co_varnames[0]
+
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kw):
+        import torch
+        t = args[0] if args else kw[name]
+        t = t[0] if isinstance(t, tuple) else t
+        if not t.is_cuda:
+            raise ValueError(f"{fn.__name__}: CUDA tensors wanted, got {t.device}")
+        if stream is None and t.device.index == torch.cuda.current_device():
+            return fn(*args, **kw)
+        with torch.cuda.device(t.device):
+            if stream is None:
+                return fn(*args, **kw)
+            if stream.device != t.device:
+                raise ValueError(f"{fn.__name__}: a stream of {stream.device} for tensors of {t.device}")
+            with torch.cuda.stream(stream):
+                return fn(*args, **kw)
+    return call
+
+
+@_on_device
+def prefix_attention(q, k, v, prefix_k=None, prefix_v=None, prefix8: KV8Cache | None = None, own_len=None,
+                     causal: bool = False, scale: float | None = None, out=None, status=None):
+    """Attention of a batch whose sequences share a prefix of keys and have keys of their own.
+
+    q [B, T, Hq, 128]; k, v [B, S, Hkv, 128] (S may be 0, or k = v = None); prefix_k, prefix_v
+    [P, Hkv, 128], or prefix8, an 8-bit cache's rows ([P, Hkv, ...], KV8Cache.prefix). float16 or
+    bfloat16, any strides with a contiguous last dimension. own_len: int32 [B] on the device, the own
+    rows in use (None: S). causal: query row t of T sees own rows up to own_len - T + t. scale: default
+    1 / sqrt(128). status: int32 [1] on the device that receives a non-zero code if a wait in the
+    kernel expires. Returns o [B, T, Hq, 128] (`out`, if given)."""
+    import torch
+    if q.dim() != 4 or q.shape[3] != HEAD_DIM:
+        raise ValueError(f"q: want [B, T, Hq, {HEAD_DIM}], got {tuple(q.shape)}")
+    dt = _dt16(q, "q")
+    dev = q.device
+    B, T, Hq, _ = q.shape
+    if (k is None) != (v is None) or (prefix_k is None) != (prefix_v is None):
+        raise ValueError("k and v, and prefix_k and prefix_v, come in pairs")
+    if prefix8 is not None and prefix_k is not None:
+        raise ValueError("prefix8 and prefix_k / prefix_v exclude each other")
+    P = prefix8.k.shape[0] if prefix8 is not None else prefix_k.shape[0] if prefix_k is not None else 0
+    heads = [t.shape[-2] for t in (k, prefix_k, prefix8 and prefix8.k) if t is not None]
+    if not heads:
+        raise ValueError("neither own keys nor a prefix")
+    Hkv = heads[0]
+    S = k.shape[1] if k is not None else 0
+    kt = _view4(k, q, (B, S, Hkv, HEAD_DIM), "k") if S else _NO_TENSOR
+    vt = _view4(v, q, (B, S, Hkv, HEAD_DIM), "v") if S else _NO_TENSOR
+    pkt = pvt = _NO_TENSOR
+    p8 = (0, 0, 0, 0)
+    if P and prefix8 is not None:
+        p8 = _kv8_ptrs(prefix8, (P, Hkv), dev, "prefix8")
+    elif P:
+        pkt = _view4(prefix_k, q, (P, Hkv, HEAD_DIM), "prefix_k")
+        pvt = _view4(prefix_v, q, (P, Hkv, HEAD_DIM), "prefix_v")
+    if out is None:
+        out = torch.empty(B, T, Hq, HEAD_DIM, dtype=q.dtype, device=dev)
+    qt, ot = _view4(q, q, (B, T, Hq, HEAD_DIM), "q"), _view4(out, q, (B, T, Hq, HEAD_DIM), "out")
+    lens = _int32_ptr(own_len, B, dev, "own_len")
+    st = _int32_ptr(status, 1, dev, "status")
+    if scale is None:
+        scale = 1.0 / math.sqrt(HEAD_DIM)
+    sizes = (dt, B, T, Hq, Hkv, P, S, int(causal), scale)
+    ptrs = (*qt, *kt, *vt, *ot, *pkt, *pvt, *p8, lens)
+    L = _lib or lib()
+    key = (dev.index, B, T, Hq, Hkv, P, S, p8[0] != 0)
+    need = _ws_bytes.get(key)
+    if need is None:
+        need = L.qi_prefix_attention_workspace(_PREFIX_ATTN.pack(*sizes, *ptrs, 0, 0, st))
+        if len(_ws_bytes) > 4096:
+            _ws_bytes.clear()
+        _ws_bytes[key] = need
+    ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    _check(L.qi_prefix_attention(_PREFIX_ATTN.pack(*sizes, *ptrs, ws.data_ptr() if need else 0, need, st), _stream()))
+    return out
+
+
+def _kv8_call(name, cache, k, v, pos, lens):
+    if k.dim() != 4 or k.shape[3] != HEAD_DIM:
+        raise ValueError(f"k: want [B, T, H, {HEAD_DIM}], got {tuple(k.shape)}")
+    B, T, H, _ = k.shape
+    S = cache.k.shape[1]
+    dev = cache.k.device
+    if k.device != dev:
+        raise ValueError(f"k on {k.device}, the cache on {dev}")
+    dt = _dt16(k, "k")
+    c = _kv8_ptrs(cache, (B, S, H), dev, "cache")
+    kt = _TENSOR4.pack(*_view4(k, k, (B, T, H, HEAD_DIM), "k"))
+    vt = _TENSOR4.pack(*_view4(v, k, (B, T, H, HEAD_DIM), "v"))
+    at = (_int32_ptr(pos, B, dev, "pos"), _int32_ptr(lens, B, dev, "lens"))
+    if name == "write":
+        _check(lib().qi_kv8_write(dt, B, T, S, H, kt, vt, *c, *at, _stream()))
+    else:
+        _check(lib().qi_kv8_read(dt, B, T, S, H, *c, *at, kt, vt, _stream()))
+
+
+@_on_device
+def kv8_write(cache: KV8Cache, k, v, pos=None, lens=None):
+    """Quantises k, v [B, T, H, 128] (float16 or bfloat16, any strides with a contiguous last dimension)
+    into the cache: row t < lens[b] of sequence b becomes cache row pos[b] + t (int32 [B] on the device;
+    None: 0 and T). Rows that fall outside the cache are passed over."""
+    _kv8_call("write", cache, k, v, pos, lens)
+    return cache
+
+
+@_on_device
+def kv8_read(cache: KV8Cache, T: int, dtype, pos=None, lens=None, out=None):
+    """(k, v) [B, T, H, 128] in `dtype` from cache rows pos[b] + t, t < lens[b]. Rows at or past lens[b] or
+    outside the cache stay as they are in `out` = (k, v), and are zero without `out`."""
+    import torch
+    B, S, H, _ = cache.k.shape
+    if out is None:
+        make = torch.empty if pos is None and lens is None and T <= S else torch.zeros
+        out = tuple(make(B, T, H, HEAD_DIM, dtype=dtype, device=cache.k.device) for _ in range(2))
+    k, v = out
+    if k.dtype != dtype or tuple(k.shape) != (B, T, H, HEAD_DIM):
+        raise ValueError(f"out: want {dtype} {(B, T, H, HEAD_DIM)}, got {k.dtype} {tuple(k.shape)}")
+    _kv8_call("read", cache, k, v, pos, lens)
+    return k, v
+
+
+@_on_device
+def add_rmsnorm_mxfp8(x, delta=None, w=None, plus_one: bool = False, eps: float = 1e-6, x_out=None, q=None, sf=None):
+    """x_out = x + delta in x's type, then MXFP8 of RMSNorm(x_out) * gain along the last axis.
+
+    x [rows, K] float32, float16 or bfloat16, delta [rows, K] of any of them (None: no addition), rows
+    any multiple of 16 bytes apart; w [K] bfloat16 or float32: gain w, or 1 + w with plus_one. Returns
+    (x_out, codes [rows, K] uint8, scale chunks uint8) as quant_mxfp8 lays them out; x_out may be x, and
+    a new tensor is made for each of the three that is not given."""
+    import torch
+    kinds = {torch.float16: DT_F16, torch.bfloat16: DT_BF16, torch.float32: DT_F32}
+    if x.dim() != 2 or x.dtype not in kinds:
+        raise ValueError(f"x: want [rows, K] of a floating type, got {x.dtype} {tuple(x.shape)}")
+    rows, K = x.shape
+    dev = x.device
+    chunks = ((rows + 127) // 128) * (K // 128) * 512
+
+    def rows_of(t, name):
+        if t.dtype not in kinds or t.device != dev or tuple(t.shape) != (rows, K) or (K > 1 and t.stride(1) != 1):
+            raise ValueError(f"{name}: want {dev} {(rows, K)} with contiguous rows, got {t.dtype} {t.device} "
+                             f"{tuple(t.shape)}")
+        return t.data_ptr(), t.stride(0)
+
+    def bytes_of(t, shape, name):
+        if t.dtype != torch.uint8 or t.device != dev or tuple(t.shape) != shape or not t.is_contiguous():
+            raise ValueError(f"{name}: want contiguous uint8 {dev} {shape}, got {t.dtype} {t.device} {tuple(t.shape)}")
+        return t.data_ptr()
+
+    if x_out is None:
+        x_out = torch.empty(rows, K, dtype=x.dtype, device=dev)
+    elif x_out.dtype != x.dtype:
+        raise ValueError(f"x_out: want {x.dtype}, got {x_out.dtype}")
+    if q is None:
+        q = torch.empty(rows, K, dtype=torch.uint8, device=dev)
+    if sf is None:
+        sf = torch.zeros(chunks, dtype=torch.uint8, device=dev)
+    wp = 0
+    if w is not None:
+        if w.dtype not in (torch.bfloat16, torch.float32) or w.device != dev or tuple(w.shape) != (K,) or \
+                not w.is_contiguous():
+            raise ValueError(f"w: want contiguous bfloat16 or float32 {dev} ({K},), got {w.dtype} {w.device} "
+                             f"{tuple(w.shape)}")
+        wp = w.data_ptr()
+    d = rows_of(delta, "delta") if delta is not None else (0, 0)
+    args = _ADD_RMSNORM.pack(kinds[x.dtype], kinds[delta.dtype] if delta is not None else 0, rows, K,
+                             int(w is not None and w.dtype == torch.float32), int(plus_one), eps, *rows_of(x, "x"), *d,
+                             *rows_of(x_out, "x_out"), wp, bytes_of(q, (rows, K), "q"), bytes_of(sf, (chunks,), "sf"))
+    _check(lib().qi_add_rmsnorm_mxfp8(args, _stream()))
+    return x_out, q, sf
 
 
 # ---------------------------------------------------------------- the DiT

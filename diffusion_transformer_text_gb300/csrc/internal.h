@@ -7,6 +7,8 @@
 #include <atomic>
 #include <cstdint>
 
+#include "../../include/qidit.h"
+
 namespace qi {
 
 constexpr int kHidden = 4096;
@@ -185,6 +187,27 @@ cudaError_t launch_attention(const AttnParams& p, cudaStream_t stream);
 // 2-D 16-bit TMA map over a row-major [rows, cols] matrix, box = box_rows x 64
 // columns with 128-byte swizzle; rows past `rows` read as zero (qidit.cu).
 bool encode_map16(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint32_t box_rows, bool bf16);
+
+// 16-bit TMA map of `rank` dimensions (first innermost, contiguous), byte strides of the
+// others, 128-byte swizzle; what lies outside the dimensions reads as zero (qidit.cu).
+bool encode_map16_nd(CUtensorMap* m, const void* base, int rank, const unsigned long long* dims,
+                     const unsigned long long* strides, const unsigned* box);
+
+// 8-bit K/V cache (batch_ops.cu): rows t < lens[b] of k and v [B, T, H, 128] (16 bits, element
+// strides) against rows pos[b] + t of the cache [B, S, H, 128] codes and [B, S, H, 4] scales;
+// rows outside 0 .. S-1 are passed over. pos NULL: 0; lens NULL: T.
+struct Kv8Args {
+  int B, T, S, H;
+  qi_tensor4 k, v;
+  uint8_t* k8;
+  uint8_t* v8;
+  uint8_t* k_sf;
+  uint8_t* v_sf;
+  const int* pos;
+  const int* lens;
+};
+cudaError_t launch_kv8_write(const Kv8Args& a, bool bf16, cudaStream_t s);
+cudaError_t launch_kv8_read(const Kv8Args& a, bool bf16, cudaStream_t s);
 
 // Small kernels (kernels_small.cu)
 cudaError_t launch_timestep_embed(float t, float* e, cudaStream_t s);

@@ -1,0 +1,977 @@
+// Attention of a batch whose sequences share a prefix of keys (one prompt's K/V)
+// and have keys of their own, on the 5th-generation tensor cores.
+//
+// Row (b, t, hq) of a batch of B sequences with T query rows and Hq heads sees the
+// P prefix keys and the first lim(b, t) of sequence b's own keys of head hq / G
+// (G = Hq / Hkv), lim = own_len[b], or with `causal` own_len[b] - T + t + 1 (the
+// sequence's last query row sees all of its keys), clamped to 0 .. own_len[b]:
+//   s_j = scale q.k_j,  o = sum_j 2^(s_j log2 e - m) v_j / sum_j 2^(s_j log2 e - m).
+// A row without a key is zero. Keys are visited in 128-key tiles with a running
+// maximum and sum, so scores never reach memory.
+//
+// Work unit: a block of up to 128 query rows of one key head against a run of key
+// tiles. The G heads of a group and the tokens of a block share the key tiles, so
+// they are the rows of one MMA. Two decompositions (make_plan):
+//   joint   block = tb tokens of one sequence; its tiles are the prefix's, then the
+//           sequence's own. For blocks that fill the 128 MMA rows.
+//   packed  the prefix is visited once for rb sequences together (T G rows each),
+//           and each sequence's own keys by units of their own. For few query rows
+//           per sequence, where a joint unit would read the whole prefix for T G of
+//           the MMA's 128 rows.
+// Where the units would not fill the SMs, or leave a ragged last wave, a unit's
+// tiles are cut into chunks; each writes its unnormalised O with its maximum and
+// sum, and merge_partials joins a row's parts in a fixed order (no atomics).
+//
+// The inside of a unit is that of the block-causal kernel (attention.cu): one CTA
+// per SM, K and V rings filled by TMA, S and the two key halves' O in tensor
+// memory, P written back there as the A operand of P V, separate Q K^T and P V
+// issuing threads, two softmax warpgroups of one key half each, an epilogue
+// warpgroup. What differs: Q comes by a five-dimensional tensor map whose box
+// gathers the block's (sequence, token, head of the group) rows; K and V by maps
+// over the prefix and over the own keys with the caller's strides; and rows of an
+// own V tile at or past own_len are set to zero in shared memory before the
+// product, so that whatever the cache holds there (0 x NaN is NaN) cannot reach O.
+// P is rounded to the operands' 16-bit type, as the tensor cores need it: an error
+// of half a step of that type per term, as large as the rounding of the output.
+#include <climits>
+#include <cstdarg>
+#include <cstdio>
+#include <mutex>
+
+#include "../../include/qidit.h"
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace qi {
+namespace {
+
+constexpr int kRows = 128;                    // MMA rows: query rows per block at most
+constexpr int kKeys = 128;                    // keys per tile
+constexpr int kBox = 128 * 64 * 2;            // 128 rows x 64 dims, 128-byte swizzle (16 KB)
+constexpr int kTile = 2 * kBox;               // Q, K or V tile (32 KB)
+constexpr int kKStages = 3;
+constexpr int kVStages = 2;
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kColO = 0;                 // O_h at kColO + 128 h
+constexpr uint32_t kColS = 256;
+constexpr uint32_t kColP = 384;               // buffer b at kColP + 64 b, half h at + 32 h
+constexpr float kRescaleLog2 = 8.0f;          // rescale O_h only when its max grows by > 2^8
+constexpr int kThreads = 512;
+constexpr uint32_t kRegsLow = 104, kRegsHigh = 152, kRegsEpi = 104;
+static_assert(kRegsLow + 2 * kRegsHigh + kRegsEpi == 4 * 128, "register split must equal the launch allotment");
+
+// mbarriers, as in attention.cu
+enum : int {
+  kKFull = 0,
+  kKEmpty = kKFull + kKStages,
+  kVFull = kKEmpty + kKStages,
+  kVEmpty = kVFull + kVStages,
+  kQFull = kVEmpty + kVStages,
+  kQEmpty = kQFull + 1,
+  kSFull = kQEmpty + 1,
+  kSFree = kSFull + 1,
+  kPFull = kSFree + 1,
+  kPvDone = kPFull + 4,
+  kOFull = kPvDone + 4,
+  kOEmpty = kOFull + 1,
+  kLFull = kOEmpty + 1,
+  kDrainQK = kLFull + 1,
+  kDrainPV = kDrainQK + 1,
+  kNumBars = kDrainPV + 1
+};
+__device__ __forceinline__ uint32_t bar_count(int i) {
+  if (i == kSFree || i == kLFull) return 8;
+  if ((i >= kPFull && i < kPFull + 4) || i == kOEmpty) return 4;
+  return 1;
+}
+constexpr int kSmem = (1 + kKStages + kVStages) * kTile + 1024 + kNumBars * 8 + 16 + 2 * 2 * kRows * 4;
+static_assert(kSmem <= 227 * 1024, "shared memory over the per-block limit");
+
+// The decomposition, decided on the host from sizes alone.
+struct Plan {
+  int G;          // query heads per key head
+  int tb;         // tokens per row block
+  int nqb;        // row blocks per sequence
+  int rb;         // sequences per prefix block (packed), else 1
+  int npb;        // prefix blocks per key head (packed)
+  int pt, ot;     // prefix tiles; own tiles at the largest own length
+  int ct;         // tiles per chunk
+  int nch;        // joint: chunks per unit; packed: chunks of the own keys
+  int nchp;       // packed: chunks of the prefix
+  int packed;
+  int split;      // 1: partials and merge_partials
+  int units_p;    // packed: units over the prefix (they come first)
+  int units;
+  int rows_p;     // rows of a prefix block's partial
+  int rows_o;     // rows of a joint / own block's partial
+};
+
+struct Params {
+  Plan pl;
+  int B, T, Hq, Hkv, P, S, causal;
+  const int* own_len;
+  uint16_t* o;
+  long long ob, orow, oh;  // element strides of o
+  float* part;             // partial O rows, 128 floats each
+  float2* ml;              // (maximum in base-2 units, sum) of each partial row
+  int* err;
+};
+
+struct Unit {
+  int h, b0, t0;
+  int p0, pn;      // prefix tiles [p0, p0 + pn)
+  int o0, on;      // own tiles of sequence b0
+  int n;           // pn + on
+  int len;         // own keys of sequence b0
+  int rows;        // rows of the block (the MMA's other rows are ignored)
+  long long slot;  // first partial row
+};
+
+__device__ __forceinline__ int own_len_of(const Params& p, int b) {
+  return p.own_len ? min(max(p.own_len[b], 0), p.S) : p.S;
+}
+// own keys that token t of a sequence with `len` own keys sees
+__device__ __forceinline__ int own_lim(const Params& p, int len, int t) {
+  return p.causal ? min(max(len - p.T + t + 1, 0), len) : len;
+}
+__device__ __forceinline__ int own_tiles(const Params& p, int len, int t0, int tb) {
+  return (own_lim(p, len, min(t0 + tb, p.T) - 1) + kKeys - 1) / kKeys;
+}
+
+__device__ __forceinline__ Unit unit_of(const Params& p, int u) {
+  const Plan& pl = p.pl;
+  Unit x;
+  x.p0 = x.pn = x.o0 = x.on = x.len = 0;
+  if (u < pl.units_p) {  // packed: prefix
+    const int c = u % pl.nchp, r = u / pl.nchp;
+    x.h = r / pl.npb;
+    x.b0 = (r - x.h * pl.npb) * pl.rb;
+    x.t0 = 0;
+    x.p0 = c * pl.ct;
+    x.pn = min(pl.ct, pl.pt - x.p0);
+    x.rows = pl.rows_p;
+    x.slot = static_cast<long long>(u) * pl.rows_p;
+  } else {
+    const int v = u - pl.units_p;
+    const int c = v % pl.nch;
+    int r = v / pl.nch;
+    int qb = r % pl.nqb;
+    r /= pl.nqb;
+    x.h = r / p.B;
+    x.b0 = r - x.h * p.B;
+    if (p.causal) qb = pl.nqb - 1 - qb;  // longest first
+    x.t0 = qb * pl.tb;
+    x.len = own_len_of(p, x.b0);
+    const int pt = pl.packed ? 0 : pl.pt;
+    const int tiles = pt + own_tiles(p, x.len, x.t0, pl.tb);
+    const int lo = c * pl.ct;
+    const int hi = min(lo + pl.ct, tiles);
+    if (lo < hi) {
+      x.p0 = min(lo, pt);
+      x.pn = min(hi, pt) - x.p0;
+      x.o0 = max(lo, pt) - pt;
+      x.on = max(hi, pt) - pt - x.o0;
+    }
+    x.rows = pl.rows_o;
+    x.slot = static_cast<long long>(pl.units_p) * pl.rows_p + static_cast<long long>(v) * pl.rows_o;
+  }
+  x.n = x.pn + x.on;
+  return x;
+}
+
+// 4-D tiled load: (dim, head, row, sequence); 5-D: (dim, head of the group, key head, token, sequence)
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int h, int row,
+                                            int b) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(h), "r"(row), "r"(b)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_5d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int g, int h,
+                                            int t, int b) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(g), "r"(h), "r"(t), "r"(b)
+      : "memory");
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
+  return BF16 ? pack_bf16x2(lo, hi) : pack_f16x2(lo, hi);
+}
+
+// Maps: Q over (dim, G, Hkv, T, B), once with the prefix block's box and once with
+// the own / joint block's; K and V over (dim, Hkv, rows, sequences), prefix and own.
+struct Maps {
+  CUtensorMap qp, qo, pk, pv, k, v;
+};
+
+template <bool BF16>
+__global__ void __launch_bounds__(kThreads, 1)
+    prefix_attn_tc(const __grid_constant__ Maps tm, const __grid_constant__ Params p, float scale_log2) {
+  constexpr uint32_t kIdescQK = BF16 ? idesc_bf16_f32(128, kKeys) : idesc_f16_f32(128, kKeys);
+  constexpr uint32_t kIdescPV = BF16 ? idesc_bf16_f32_bmn(128, 128) : idesc_f16_f32_bmn(128, 128);
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sQ = smem;
+  uint8_t* sK = sQ + kTile;
+  uint8_t* sV = sK + kKStages * kTile;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sV + kVStages * kTile);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kNumBars);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  float* lsum = reinterpret_cast<float*>(tmem_slot + 4);  // [2][kRows]
+  float* msum = lsum + 2 * kRows;                         // [2][kRows]
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int total = p.pl.units;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kNumBars; ++i) mbar_init(&bars[i], bar_count(i));
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 0 && lane == 0) {
+    prefetch_tmap(&tm.qp);
+    prefetch_tmap(&tm.qo);
+    prefetch_tmap(&tm.pk);
+    prefetch_tmap(&tm.k);
+  }
+  if (warp == 2 && lane == 0) {
+    prefetch_tmap(&tm.pv);
+    prefetch_tmap(&tm.v);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  grid_dep_wait();
+  grid_dep_launch_dependents();
+
+  if (warp < 4) {
+    regs_release<kRegsLow>();
+    if (warp == 3) {
+      // ---------------- P V issuer (lane 0); the whole warp clears V rows past own_len.
+      // Every lane walks the same units and tiles; lane 0's failure only stops its
+      // waits and MMAs, so the warp meets at every cleared tile whatever happens.
+      const uint64_t vdesc0 = sw128_mnmajor_desc(smem_u32(sV), kBox, 1024);
+      uint32_t t = 0;
+      int ku = 0;
+      bool ok = true;
+      for (int u = blockIdx.x; u < total; u += gridDim.x) {
+        const Unit un = unit_of(p, u);
+        if (un.n == 0) continue;
+        for (int j = 0; j < un.n; ++j, ++t) {
+          const uint32_t b = t & 1u;
+          const uint32_t st = t % kVStages;
+          const int row0 = j >= un.pn ? (un.o0 + j - un.pn) * kKeys : 0;
+          const bool clear = j >= un.pn && un.len - row0 < kKeys && un.len < p.S;
+          if (lane == 0 && ok)
+            ok = !*abort_flag &&
+                 (j > 0 || ku == 0 || mbar_wait(&bars[kOEmpty], static_cast<uint32_t>(ku - 1) & 1u)) &&
+                 mbar_wait(&bars[kVFull + st], (t / kVStages) & 1u);
+          if (clear) {
+            // rows len - row0 .. 127 of both 64-dim boxes (a row's 128 bytes stay
+            // within the row under the swizzle)
+            const bool go = __shfl_sync(0xffffffffu, static_cast<int>(ok), 0) != 0;
+            if (go) {
+              const int r0 = un.len - row0;
+              const int n16 = (kKeys - r0) * 8;
+              for (int i = lane; i < 2 * n16; i += 32) {
+                const int box = i >= n16 ? 1 : 0;
+                *reinterpret_cast<uint4*>(sV + st * kTile + box * kBox + r0 * 128 + (i - box * n16) * 16) =
+                    make_uint4(0u, 0u, 0u, 0u);
+              }
+              fence_proxy_async_smem();
+            }
+            __syncwarp();
+          }
+          if (lane == 0 && ok) {
+            const uint64_t vd = vdesc0 + ((st * kTile) >> 4);
+            for (int h = 0; h < 2; ++h) {
+              ok = mbar_wait(&bars[kPFull + b * 2 + h], (t >> 1) & 1u);
+              if (!ok) break;
+              tc_fence_after();
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                mma_ts(tmem + kColO + 128u * h, tmem + kColP + b * 64 + h * 32 + k * 8,
+                       vd + ((static_cast<uint32_t>(4 * h + k) * 2048) >> 4), kIdescPV, (j > 0 || k > 0) ? 1u : 0u);
+              mma_commit(&bars[kPvDone + b * 2 + h]);
+            }
+            if (ok) {
+              mma_commit(&bars[kVEmpty + st]);
+              if (j + 1 == un.n) mma_commit(&bars[kOFull]);
+            }
+          }
+        }
+        ++ku;
+      }
+      if (lane == 0) {
+        if (!ok && !*abort_flag) report_error(p.err, kErrTimeoutMma);
+        if (!ok) *abort_flag = 1;
+        mma_commit(&bars[kDrainPV]);
+        if (!mbar_wait(&bars[kDrainPV], 0)) report_error(p.err, kErrTimeoutDrain);
+      }
+    } else if (lane != 0) {
+      // one thread per warp works in these
+    } else if (warp == 0) {
+      // ---------------- TMA producer of the K tiles
+      uint32_t t = 0;
+      bool ok = true;
+      for (int u = blockIdx.x; ok && u < total; u += gridDim.x) {
+        const Unit un = unit_of(p, u);
+        for (int j = 0; j < un.n; ++j, ++t) {
+          const uint32_t st = t % kKStages;
+          if (*abort_flag || !mbar_wait(&bars[kKEmpty + st], ((t / kKStages) & 1u) ^ 1u)) {
+            if (!*abort_flag) report_error(p.err, kErrTimeoutProducer);
+            *abort_flag = 1;
+            ok = false;
+            break;
+          }
+          const bool pre = j < un.pn;
+          const CUtensorMap* m = pre ? &tm.pk : &tm.k;
+          const int row = (pre ? un.p0 + j : un.o0 + j - un.pn) * kKeys;
+          const int bs = pre ? 0 : un.b0;
+          mbar_arrive_expect_tx(&bars[kKFull + st], kTile);
+          tma_load_4d(sK + st * kTile, m, &bars[kKFull + st], 0, un.h, row, bs);
+          tma_load_4d(sK + st * kTile + kBox, m, &bars[kKFull + st], 64, un.h, row, bs);
+        }
+      }
+      for (uint32_t i = t > kKStages ? t - kKStages : 0; i < t; ++i)
+        if (!mbar_wait(&bars[kKFull + i % kKStages], (i / kKStages) & 1u)) report_error(p.err, kErrTimeoutDrain);
+    } else if (warp == 2) {
+      // ---------------- TMA producer of the V tiles and of each unit's Q rows
+      uint32_t t = 0;
+      int nq = 0;
+      bool ok = true;
+      for (int u = blockIdx.x; ok && u < total; u += gridDim.x) {
+        const Unit un = unit_of(p, u);
+        if (un.n == 0) continue;
+        if (*abort_flag || (nq > 0 && !mbar_wait(&bars[kQEmpty], static_cast<uint32_t>(nq - 1) & 1u))) {
+          ok = false;
+          break;
+        }
+        const CUtensorMap* mq = u < p.pl.units_p ? &tm.qp : &tm.qo;
+        mbar_arrive_expect_tx(&bars[kQFull], static_cast<uint32_t>(un.rows) * 256u);  // the whole boxes, also past the ends
+        tma_load_5d(sQ, mq, &bars[kQFull], 0, 0, un.h, un.t0, un.b0);
+        tma_load_5d(sQ + kBox, mq, &bars[kQFull], 64, 0, un.h, un.t0, un.b0);
+        ++nq;
+        for (int j = 0; j < un.n; ++j, ++t) {
+          const uint32_t st = t % kVStages;
+          if (*abort_flag || !mbar_wait(&bars[kVEmpty + st], ((t / kVStages) & 1u) ^ 1u)) {
+            ok = false;
+            break;
+          }
+          const bool pre = j < un.pn;
+          const CUtensorMap* m = pre ? &tm.pv : &tm.v;
+          const int row = (pre ? un.p0 + j : un.o0 + j - un.pn) * kKeys;
+          const int bs = pre ? 0 : un.b0;
+          mbar_arrive_expect_tx(&bars[kVFull + st], kTile);
+          tma_load_4d(sV + st * kTile, m, &bars[kVFull + st], 0, un.h, row, bs);
+          tma_load_4d(sV + st * kTile + kBox, m, &bars[kVFull + st], 64, un.h, row, bs);
+        }
+      }
+      if (!ok) {
+        if (!*abort_flag) report_error(p.err, kErrTimeoutProducer);
+        *abort_flag = 1;
+      }
+      for (uint32_t i = t > kVStages ? t - kVStages : 0; i < t; ++i)
+        if (!mbar_wait(&bars[kVFull + i % kVStages], (i / kVStages) & 1u)) report_error(p.err, kErrTimeoutDrain);
+      if (nq > 0 && !mbar_wait(&bars[kQFull], static_cast<uint32_t>(nq - 1) & 1u))
+        report_error(p.err, kErrTimeoutDrain);
+    } else {
+      // ---------------- Q K^T issuer
+      const uint64_t qdesc = sw128_kmajor_desc(smem_u32(sQ));
+      const uint64_t kdesc0 = sw128_kmajor_desc(smem_u32(sK));
+      uint32_t t = 0;
+      int ku = 0;
+      bool ok = true;
+      for (int u = blockIdx.x; ok && u < total; u += gridDim.x) {
+        const Unit un = unit_of(p, u);
+        if (un.n == 0) continue;
+        ok = !*abort_flag && mbar_wait(&bars[kQFull], static_cast<uint32_t>(ku) & 1u);
+        if (!ok) break;
+        tc_fence_after();
+        for (int j = 0; j < un.n; ++j, ++t) {
+          const uint32_t st = t % kKStages;
+          ok = (t < 1 || mbar_wait(&bars[kSFree], (t - 1) & 1u)) &&
+               mbar_wait(&bars[kKFull + st], (t / kKStages) & 1u);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t kd = kdesc0 + ((st * kTile) >> 4);
+#pragma unroll
+          for (int k = 0; k < kHeadDim / 16; ++k) {
+            const uint32_t off = static_cast<uint32_t>(((k >> 2) * kBox + (k & 3) * 32) >> 4);
+            mma_ss(tmem + kColS, qdesc + off, kd + off, kIdescQK, k > 0 ? 1u : 0u);
+          }
+          mma_commit(&bars[kSFull]);
+          mma_commit(&bars[kKEmpty + st]);
+        }
+        if (!ok) break;
+        mma_commit(&bars[kQEmpty]);
+        ++ku;
+      }
+      if (!ok) {
+        report_error(p.err, kErrTimeoutMma);
+        *abort_flag = 1;
+      }
+      mma_commit(&bars[kDrainQK]);
+      if (!mbar_wait(&bars[kDrainQK], 0)) report_error(p.err, kErrTimeoutDrain);
+    }
+  } else if (warp < 12) {
+    regs_acquire<kRegsHigh>();
+    // ---------------- softmax: warps 4..7 keys 0-63, warps 8..11 keys 64-127 of every
+    // tile; thread = one query row's half
+    const int h = warp >= 8 ? 1 : 0;
+    const int quarter = warp & 3;
+    const int rit = quarter * 32 + lane;
+    const int tok = rit / p.pl.G;  // the row's token within a joint / own block
+    const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t tO = tmem + lane_off + kColO + 128u * h;
+    const uint64_t sc2 = f2_pack(scale_log2, scale_log2);
+    uint32_t t = 0;
+    int ku = 0;
+    bool ok = true;
+    for (int u = blockIdx.x; u < total; u += gridDim.x) {
+      if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
+      const Unit un = unit_of(p, u);
+      if (un.n == 0) continue;
+      const int lim_own = own_lim(p, un.len, un.t0 + tok);
+      float m_used = -INFINITY;
+      float l = 0.f;
+      for (int j = 0; j < un.n; ++j) {
+        const uint32_t tt = t + j;
+        const uint32_t b = tt & 1u;
+        ok = __all_sync(0xffffffffu, mbar_wait(&bars[kSFull], tt & 1u));
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t r[2][32];
+        tmem_ld32(tmem + lane_off + kColS + h * 64, r[0]);
+        tmem_ld32(tmem + lane_off + kColS + h * 64 + 32, r[1]);
+        tmem_ld_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[kSFree]);
+        // keys at or past the row's limit become -inf, whatever their scores are
+        const bool pre = j < un.pn;
+        const int left =
+            (pre ? p.P - (un.p0 + j) * kKeys : lim_own - (un.o0 + j - un.pn) * kKeys) - h * 64;
+        if (__any_sync(0xffffffffu, left < 64)) {
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (c * 32 + i >= left) r[c][i] = 0xff800000u;
+        }
+        float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int i = 0; i < 32; i += 2)
+            mx4[(i >> 1) & 3] = fmax3(mx4[(i >> 1) & 3], __uint_as_float(r[c][i]), __uint_as_float(r[c][i + 1]));
+        const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * scale_log2;
+        const float m_new = fmaxf(m_used, mx);
+        if (j == 0) {
+          m_used = m_new;
+        } else {
+          const bool mine = m_new > m_used + kRescaleLog2;
+          if (__any_sync(0xffffffffu, mine)) {
+            const uint32_t tp = tt - 1;
+            if (!__all_sync(0xffffffffu, mbar_wait(&bars[kPvDone + (tp & 1u) * 2 + h], (tp >> 1) & 1u))) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const float alpha = mine ? fast_exp2(m_used - m_new) : 1.0f;
+#pragma unroll 1
+            for (int c = 0; c < 8; ++c) {
+              uint32_t o[16];
+              tmem_ld16(tO + c * 16, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+              tmem_st16(tO + c * 16, o);
+            }
+            if (mine) {
+              l *= alpha;
+              m_used = m_new;
+            }
+          }
+        }
+        const float base = m_used == -INFINITY ? 0.f : m_used;
+        const uint64_t nm2 = f2_pack(-base, -base);
+        uint64_t rs2[4] = {0ull, 0ull, 0ull, 0ull};
+        uint32_t pk[2][16];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const uint64_t x2 =
+                fma_f32x2(f2_pack(__uint_as_float(r[c][2 * i]), __uint_as_float(r[c][2 * i + 1])), sc2, nm2);
+            float x0, x1;
+            f2_unpack(x2, x0, x1);
+            const float e0 = fast_exp2(x0);
+            const float e1 = fast_exp2(x1);
+            rs2[i & 3] = add_f32x2(rs2[i & 3], f2_pack(e0, e1));
+            pk[c][i] = pack16<BF16>(e0, e1);
+          }
+        }
+        if (tt >= 2) {
+          ok = __all_sync(0xffffffffu, mbar_wait(&bars[kPvDone + b * 2 + h], ((tt - 2) >> 1) & 1u));
+          if (!ok) break;
+          tc_fence_after();
+        }
+        const uint32_t tP = tmem + lane_off + kColP + b * 64 + h * 32;
+        tmem_st16(tP, pk[0]);
+        tmem_st16(tP + 16, pk[1]);
+        float s[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f2_unpack(rs2[i], s[2 * i], s[2 * i + 1]);
+        l += ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]));
+        tmem_st_wait();
+        tc_fence_before();
+        const bool last = j + 1 == un.n;
+        if (last) {
+          if (ku > 0) {
+            ok = __all_sync(0xffffffffu, mbar_wait(&bars[kOEmpty], static_cast<uint32_t>(ku - 1) & 1u));
+            if (!ok) break;
+          }
+          lsum[h * kRows + rit] = l;
+          msum[h * kRows + rit] = m_used;
+        }
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&bars[kPFull + b * 2 + h]);
+          if (last) mbar_arrive(&bars[kLFull]);
+        }
+      }
+      if (!ok) break;
+      t += un.n;
+      ++ku;
+    }
+    if (!ok) {
+      if (lane == 0) report_error(p.err, kErrTimeoutEpilogue);
+      *abort_flag = 1;
+    }
+  } else {
+    regs_release<kRegsEpi>();
+    // ---------------- epilogue (warps 12..15), thread = one row of the block
+    const int quarter = warp & 3;
+    const int rit = quarter * 32 + lane;
+    const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+    const int tok = rit / p.pl.G;
+    const int g = rit - tok * p.pl.G;
+    bool ok = true;
+    int ku = 0;
+    for (int u = blockIdx.x; ok && u < total; u += gridDim.x) {
+      if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
+      const Unit un = unit_of(p, u);
+      // where the row goes: token and sequence (a prefix block runs over sequences)
+      int b = un.b0, tk = un.t0 + tok;
+      if (u < p.pl.units_p) {
+        const int q = tok / p.T;
+        b += q;
+        tk = tok - q * p.T;
+      }
+      const bool mine = rit < un.rows && tk < p.T && b < p.B;
+      uint16_t* orow = p.o + b * p.ob + tk * p.orow + static_cast<long long>(un.h * p.pl.G + g) * p.oh;
+      if (un.n == 0) {
+        // no key at all: a joint unit that is its row's only one writes zeros
+        if (!p.pl.split && mine) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) reinterpret_cast<uint4*>(orow)[i] = make_uint4(0u, 0u, 0u, 0u);
+        }
+        continue;
+      }
+      ok = __all_sync(0xffffffffu, mbar_wait(&bars[kOFull], static_cast<uint32_t>(ku) & 1u)) &&
+           __all_sync(0xffffffffu, mbar_wait(&bars[kLFull], static_cast<uint32_t>(ku) & 1u));
+      if (!ok) break;
+      tc_fence_after();
+      const float m0 = msum[rit], m1 = msum[kRows + rit];
+      const float mm = fmaxf(m0, m1);
+      // a half without a visible key has m = -inf and weight 0; in a row without one both
+      // sums and O are 0 already (or NaN, if its scores are)
+      const float a0 = mm == -INFINITY ? 1.f : fast_exp2(m0 - mm);
+      const float a1 = mm == -INFINITY ? 1.f : fast_exp2(m1 - mm);
+      const float den = lsum[rit] * a0 + lsum[kRows + rit] * a1;
+      const float inv = p.pl.split ? 1.f : (den == 0.f ? 0.f : 1.f / den);
+      const float w0 = a0 * inv, w1 = a1 * inv;
+      if (p.pl.split && mine) p.ml[un.slot + rit] = make_float2(mm, den);
+#pragma unroll 1
+      for (int c = 0; c < 4; ++c) {
+        uint32_t o0[32], o1[32];
+        tmem_ld32(tmem + lane_off + kColO + c * 32, o0);
+        tmem_ld32(tmem + lane_off + kColO + 128 + c * 32, o1);
+        tmem_ld_wait();
+        if (c == 3) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars[kOEmpty]);
+        }
+        if (mine) {
+          float ov[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) ov[i] = __uint_as_float(o0[i]) * w0 + __uint_as_float(o1[i]) * w1;
+          if (p.pl.split) {
+            float4* d = reinterpret_cast<float4*>(p.part + (un.slot + rit) * kHeadDim + c * 32);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) d[i] = make_float4(ov[4 * i], ov[4 * i + 1], ov[4 * i + 2], ov[4 * i + 3]);
+          } else {
+            uint4* d = reinterpret_cast<uint4*>(orow + c * 32);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              d[i] = make_uint4(pack16<BF16>(ov[8 * i], ov[8 * i + 1]), pack16<BF16>(ov[8 * i + 2], ov[8 * i + 3]),
+                                pack16<BF16>(ov[8 * i + 4], ov[8 * i + 5]), pack16<BF16>(ov[8 * i + 6], ov[8 * i + 7]));
+          }
+        }
+      }
+      ++ku;
+    }
+    if (!ok) {
+      if (lane == 0) report_error(p.err, kErrTimeoutEpilogue);
+      *abort_flag = 1;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// One warp per output row: joins the row's partials (prefix chunks in order, then own
+// chunks) by their maxima and sums. Chunks without a tile were not written; they are
+// told from the lengths, as the units told them.
+constexpr int kMergeWarps = 4;
+template <bool BF16>
+__global__ void __launch_bounds__(kMergeWarps * 32) merge_partials(const __grid_constant__ Params p) {
+  grid_dep_wait();
+  grid_dep_launch_dependents();
+  const Plan& pl = p.pl;
+  const int lane = threadIdx.x & 31;
+  const long long row = static_cast<long long>(blockIdx.x) * kMergeWarps + (threadIdx.x >> 5);
+  if (row >= static_cast<long long>(p.B) * p.T * p.Hq) return;
+  const int hq = static_cast<int>(row % p.Hq);
+  const long long bt = row / p.Hq;
+  const int b = static_cast<int>(bt / p.T), t = static_cast<int>(bt - static_cast<long long>(b) * p.T);
+  const int h = hq / pl.G, g = hq - h * pl.G;
+  const int qb = t / pl.tb;
+  const int len = own_len_of(p, b);
+  const int ot = own_tiles(p, len, qb * pl.tb, pl.tb);
+  const int qpos = p.causal ? pl.nqb - 1 - qb : qb;
+  const long long unit_o = ((static_cast<long long>(h) * p.B + b) * pl.nqb + qpos) * pl.nch;
+  const long long slot_o = static_cast<long long>(pl.units_p) * pl.rows_p + unit_o * pl.rows_o + (t - qb * pl.tb) * pl.G + g;
+  const int parts_o = (ot + (pl.packed ? 0 : pl.pt) + pl.ct - 1) / pl.ct;
+  long long slot_p = 0;
+  int parts_p = 0;
+  if (pl.packed) {
+    const int pb = b / pl.rb;
+    slot_p = (static_cast<long long>(h) * pl.npb + pb) * pl.nchp * pl.rows_p + ((b - pb * pl.rb) * p.T + t) * pl.G + g;
+    parts_p = pl.nchp;
+  }
+  const int n = parts_p + parts_o;
+  float m = -INFINITY;
+  for (int i = lane; i < n; i += 32) {
+    const long long s = i < parts_p ? slot_p + static_cast<long long>(i) * pl.rows_p
+                                    : slot_o + static_cast<long long>(i - parts_p) * pl.rows_o;
+    m = fmaxf(m, p.ml[s].x);
+  }
+#pragma unroll
+  for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+  float den = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int i = 0; i < n; ++i) {
+    const long long s = i < parts_p ? slot_p + static_cast<long long>(i) * pl.rows_p
+                                    : slot_o + static_cast<long long>(i - parts_p) * pl.rows_o;
+    const float2 ml = p.ml[s];
+    const float4 v = reinterpret_cast<const float4*>(p.part + s * kHeadDim)[lane];
+    // a chunk in which the row sees no key has m = -inf, sum 0 and O = 0: weight 0, or 1
+    // if no chunk has a key
+    const float w = m == -INFINITY ? 1.f : fast_exp2(ml.x - m);
+    den += ml.y * w;
+    acc.x += v.x * w;
+    acc.y += v.y * w;
+    acc.z += v.z * w;
+    acc.w += v.w * w;
+  }
+  const float inv = den == 0.f ? 0.f : 1.f / den;
+  uint16_t* orow = p.o + b * p.ob + t * p.orow + static_cast<long long>(hq) * p.oh;
+  reinterpret_cast<uint2*>(orow)[lane] =
+      make_uint2(pack16<BF16>(acc.x * inv, acc.y * inv), pack16<BF16>(acc.z * inv, acc.w * inv));
+}
+
+// ---------------------------------------------------------------- host
+
+qi_status op_fail(qi_status st, const char* fmt, ...) {
+  char buf[256];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof(buf), fmt, ap);
+  va_end(ap);
+  set_last_error(buf);
+  return st;
+}
+
+int ceil_div(int a, int b) { return (a + b - 1) / b; }
+
+// Chooses the decomposition from sizes alone (own lengths, which only the device
+// knows, count as S). Time is counted in key tiles: a unit costs its tiles plus
+// kUnitTiles for its Q load, pipeline fill and epilogue, and splitting costs
+// kMergeTiles for the partials and the second launch.
+constexpr int kUnitTiles = 3;
+constexpr int kMergeTiles = 6;
+Plan make_plan(int B, int T, int Hq, int Hkv, int P, int S, int sms) {
+  Plan a{};
+  a.G = Hq / Hkv;
+  a.tb = kRows / a.G < T ? kRows / a.G : T;
+  a.nqb = ceil_div(T, a.tb);
+  a.pt = ceil_div(P, kKeys);
+  a.ot = ceil_div(S, kKeys);
+  a.rb = 1;
+  a.rows_o = a.tb * a.G;
+  a.rows_p = 0;
+  Plan best = a;
+  long long best_cost = LLONG_MAX;
+  const int n = a.pt + a.ot;
+  const long long blocks = static_cast<long long>(Hkv) * B * a.nqb;
+  // joint: every number of chunks that keeps the grid within a few waves
+  for (int nch = 1; nch <= n; ++nch) {
+    if (nch > 1 && blocks * nch > 4ll * sms) break;  // (at most 4 x SMs rounds of this loop)
+    Plan c = a;
+    c.ct = ceil_div(n, nch);
+    if (ceil_div(n, c.ct) != nch) continue;
+    c.nch = nch;
+    const long long waves = (blocks * nch + sms - 1) / sms;
+    const long long cost = waves * (c.ct + kUnitTiles) + (nch > 1 ? kMergeTiles : 0);
+    if (cost < best_cost && blocks * nch <= INT_MAX) {
+      best_cost = cost;
+      c.split = nch > 1;
+      c.units = static_cast<int>(blocks * nch);
+      best = c;
+    }
+  }
+  // packed: only if two or more sequences' rows fit one block and there are both kinds of keys
+  const int rows_seq = T * a.G;
+  if (a.nqb == 1 && B > 1 && P > 0 && S > 0 && 2 * rows_seq <= kRows) {
+    Plan c = a;
+    c.packed = 1;
+    c.split = 1;
+    c.rb = kRows / rows_seq < B ? kRows / rows_seq : B;
+    c.npb = ceil_div(B, c.rb);
+    c.rows_p = c.rb * rows_seq;
+    const int most = a.pt > a.ot ? a.pt : a.ot;
+    for (int ct = 1; ct <= most; ct += 1 + ct / 32) {
+      c.ct = ct;
+      c.nchp = ceil_div(a.pt, ct);
+      c.nch = ceil_div(a.ot, ct);
+      const long long up = static_cast<long long>(Hkv) * c.npb * c.nchp, uo = blocks * c.nch;
+      if (up + uo > INT_MAX / 2) continue;
+      const long long tiles = static_cast<long long>(Hkv) * c.npb * a.pt + blocks * a.ot + (up + uo) * kUnitTiles;
+      const long long cost = (tiles + sms - 1) / sms + ct / 2 + kMergeTiles;
+      if (cost < best_cost) {
+        best_cost = cost;
+        c.units_p = static_cast<int>(up);
+        c.units = static_cast<int>(up + uo);
+        best = c;
+      }
+    }
+  }
+  return best;
+}
+
+size_t align256(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
+size_t partial_rows(const Plan& pl) {
+  return pl.split ? static_cast<size_t>(pl.units_p) * pl.rows_p +
+                        static_cast<size_t>(pl.units - pl.units_p) * pl.rows_o
+                  : 0;
+}
+// workspace: the prefix in 16 bits (8-bit prefix only), partial O rows, their (max, sum)
+struct WsLayout {
+  size_t pk, pv, part, ml, total;
+};
+WsLayout ws_layout(const Plan& pl, int P, int Hkv, bool from8) {
+  WsLayout w{};
+  const size_t pre = from8 ? align256(static_cast<size_t>(P) * Hkv * kHeadDim * 2) : 0;
+  const size_t rows = partial_rows(pl);
+  w.pk = 0;
+  w.pv = pre;
+  w.part = 2 * pre;
+  w.ml = w.part + align256(rows * kHeadDim * 4);
+  w.total = w.ml + align256(rows * 8);
+  return w;
+}
+
+// A stride of a dimension of size 1 is never followed: any legal value will do.
+bool fix_stride(long long* s, int size) {
+  if (size == 1) *s = 8;
+  return *s > 0 && *s % 8 == 0 && *s < (1ll << 38);
+}
+
+bool map_kv(CUtensorMap* m, const qi_tensor4& t, int heads, int rows, int batch) {
+  const unsigned long long dims[4] = {kHeadDim, static_cast<unsigned long long>(heads),
+                                      static_cast<unsigned long long>(rows), static_cast<unsigned long long>(batch)};
+  const unsigned long long str[3] = {static_cast<unsigned long long>(t.head) * 2,
+                                     static_cast<unsigned long long>(t.row) * 2,
+                                     static_cast<unsigned long long>(t.batch) * 2};
+  const unsigned box[4] = {64, 1, kKeys, 1};
+  return encode_map16_nd(m, t.data, 4, dims, str, box);
+}
+
+bool map_q(CUtensorMap* m, const qi_tensor4& t, int G, int Hkv, int T, int B, int tb, int rb) {
+  const unsigned long long dims[5] = {kHeadDim, static_cast<unsigned long long>(G),
+                                      static_cast<unsigned long long>(Hkv), static_cast<unsigned long long>(T),
+                                      static_cast<unsigned long long>(B)};
+  const unsigned long long str[4] = {
+      static_cast<unsigned long long>(t.head) * 2, static_cast<unsigned long long>(t.head) * G * 2,
+      static_cast<unsigned long long>(t.row) * 2, static_cast<unsigned long long>(t.batch) * 2};
+  const unsigned box[5] = {64, static_cast<unsigned>(G), 1, static_cast<unsigned>(tb), static_cast<unsigned>(rb)};
+  return encode_map16_nd(m, t.data, 5, dims, str, box);
+}
+
+qi_status check_sizes(const qi_prefix_attn* a) {
+  if (!a) return op_fail(QI_ERR_INVALID_ARG, "qi_prefix_attention: NULL argument");
+  if (a->dtype != QI_DT_F16 && a->dtype != QI_DT_BF16)
+    return op_fail(QI_ERR_INVALID_ARG, "qi_prefix_attention: dtype %d", a->dtype);
+  constexpr int kMost = 1 << 24;
+  if (a->B < 1 || a->B > 65535 || a->T < 1 || a->T > kMost || a->Hkv < 1 || a->Hkv > 65535 || a->Hq < a->Hkv ||
+      a->Hq % a->Hkv != 0 || a->Hq / a->Hkv > kRows || a->P < 0 || a->P > kMost || a->S < 0 || a->S > kMost ||
+      (a->P == 0 && a->S == 0) || static_cast<long long>(a->B) * a->T * a->Hq > (1ll << 31))
+    return op_fail(QI_ERR_SHAPE, "qi_prefix_attention: B %d T %d Hq %d Hkv %d P %d S %d", a->B, a->T, a->Hq, a->Hkv,
+                   a->P, a->S);
+  return QI_OK;
+}
+
+int sm_count() {
+  static std::atomic<int> cached[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  if (dev >= 0 && dev < 64) {
+    const int c = cached[dev].load(std::memory_order_relaxed);
+    if (c > 0) return c;
+  }
+  int n = 0;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+  if (dev >= 0 && dev < 64) cached[dev].store(n, std::memory_order_relaxed);
+  return n;
+}
+
+template <bool BF16>
+cudaError_t launch(const Maps& tm, const Params& p, float scale_log2, int sms, cudaStream_t stream) {
+  static std::atomic<unsigned long long> attr_done{0};
+  cudaError_t e = ensure_smem_limit(prefix_attn_tc<BF16>, kSmem, attr_done);
+  if (e != cudaSuccess) return e;
+  const int grid = p.pl.units < sms ? p.pl.units : sms;
+  e = launch_dependent(prefix_attn_tc<BF16>, dim3(grid), dim3(kThreads), kSmem, stream, tm, p, scale_log2);
+  if (e != cudaSuccess || !p.pl.split) return e;
+  const long long rows = static_cast<long long>(p.B) * p.T * p.Hq;
+  return launch_dependent(merge_partials<BF16>, dim3(static_cast<unsigned>((rows + kMergeWarps - 1) / kMergeWarps)),
+                          dim3(kMergeWarps * 32), 0, stream, p);
+}
+
+}  // namespace
+}  // namespace qi
+
+extern "C" size_t qi_prefix_attention_workspace(const qi_prefix_attn* a) {
+  using namespace qi;
+  if (check_sizes(a) != QI_OK) return 0;
+  const int sms = sm_count();
+  if (sms <= 0) return 0;
+  const Plan pl = make_plan(a->B, a->T, a->Hq, a->Hkv, a->P, a->S, sms);
+  return ws_layout(pl, a->P, a->Hkv, a->P > 0 && a->pk8 != nullptr).total;
+}
+
+extern "C" qi_status qi_prefix_attention(const qi_prefix_attn* a, qi_stream_t stream) {
+  using namespace qi;
+  qi_status st = check_sizes(a);
+  if (st != QI_OK) return st;
+  const bool from8 = a->pk8 || a->pv8 || a->pk_sf || a->pv_sf;
+  if (!a->q.data || !a->o.data || (a->S > 0 && (!a->k.data || !a->v.data)))
+    return op_fail(QI_ERR_INVALID_ARG, "qi_prefix_attention: NULL q, o, k or v");
+  if (a->P > 0 && from8 && (!a->pk8 || !a->pv8 || !a->pk_sf || !a->pv_sf || a->pk.data || a->pv.data))
+    return op_fail(QI_ERR_INVALID_ARG, "qi_prefix_attention: give the prefix either as pk, pv or as all of pk8, pv8, pk_sf, pv_sf");
+  if (a->P > 0 && !from8 && (!a->pk.data || !a->pv.data))
+    return op_fail(QI_ERR_INVALID_ARG, "qi_prefix_attention: NULL prefix");
+  if (!(a->scale > 0.f) || !(a->scale < 3e38f))
+    return op_fail(QI_ERR_INVALID_ARG, "qi_prefix_attention: scale must be positive and finite");
+  qi_tensor4 q = a->q, o = a->o, k = a->k, v = a->v, pk = a->pk, pv = a->pv;
+  auto good = [](qi_tensor4* t, int batch, int rows, int heads) {
+    return (reinterpret_cast<uintptr_t>(t->data) & 15) == 0 && fix_stride(&t->batch, batch) &&
+           fix_stride(&t->row, rows) && fix_stride(&t->head, heads);
+  };
+  const char* kAlign = "qi_prefix_attention: %s needs 16-byte alignment and strides that are positive multiples of 8";
+  if (!good(&q, a->B, a->T, a->Hq)) return op_fail(QI_ERR_INVALID_ARG, kAlign, "q");
+  if (!good(&o, a->B, a->T, a->Hq)) return op_fail(QI_ERR_INVALID_ARG, kAlign, "o");
+  if (a->S > 0 && (!good(&k, a->B, a->S, a->Hkv) || !good(&v, a->B, a->S, a->Hkv)))
+    return op_fail(QI_ERR_INVALID_ARG, kAlign, "k / v");
+  if (a->P > 0 && !from8 && (!good(&pk, 1, a->P, a->Hkv) || !good(&pv, 1, a->P, a->Hkv)))
+    return op_fail(QI_ERR_INVALID_ARG, kAlign, "pk / pv");
+  if (a->P > 0 && from8 &&
+      (((reinterpret_cast<uintptr_t>(a->pk8) | reinterpret_cast<uintptr_t>(a->pv8)) & 15) ||
+       ((reinterpret_cast<uintptr_t>(a->pk_sf) | reinterpret_cast<uintptr_t>(a->pv_sf)) & 3)))
+    return op_fail(QI_ERR_INVALID_ARG, "qi_prefix_attention: the 8-bit prefix needs 16-byte aligned codes and 4-byte aligned scales");
+  const int sms = sm_count();
+  if (sms <= 0) return op_fail(QI_ERR_CUDA, "qi_prefix_attention: no CUDA device");
+  const Plan pl = make_plan(a->B, a->T, a->Hq, a->Hkv, a->P, a->S, sms);
+  if (pl.units <= 0) return op_fail(QI_ERR_SHAPE, "qi_prefix_attention: too many rows and heads");
+  const bool pre8 = a->P > 0 && from8;
+  const WsLayout w = ws_layout(pl, a->P, a->Hkv, pre8);
+  if (w.total > 0 && (!a->ws || a->ws_bytes < w.total || (reinterpret_cast<uintptr_t>(a->ws) & 255)))
+    return op_fail(QI_ERR_INVALID_ARG, "qi_prefix_attention: needs a 256-byte aligned workspace of %zu bytes", w.total);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const bool bf16 = a->dtype == QI_DT_BF16;
+  uint8_t* ws = static_cast<uint8_t*>(a->ws);
+  if (pre8) {
+    // the prefix in 16 bits, once for all row blocks
+    Kv8Args r{};
+    r.B = 1;
+    r.T = r.S = a->P;
+    r.H = a->Hkv;
+    r.k8 = const_cast<uint8_t*>(a->pk8);
+    r.v8 = const_cast<uint8_t*>(a->pv8);
+    r.k_sf = const_cast<uint8_t*>(a->pk_sf);
+    r.v_sf = const_cast<uint8_t*>(a->pv_sf);
+    const long long head = kHeadDim, row = static_cast<long long>(a->Hkv) * kHeadDim;
+    r.k = pk = qi_tensor4{ws + w.pk, row, row, head};
+    r.v = pv = qi_tensor4{ws + w.pv, row, row, head};
+    const cudaError_t e = launch_kv8_read(r, bf16, s);
+    if (e != cudaSuccess) return op_fail(QI_ERR_CUDA, "qi_prefix_attention: %s", cudaGetErrorString(e));
+  }
+  Maps tm;
+  bool ok = map_q(&tm.qo, q, pl.G, a->Hkv, a->T, a->B, pl.tb, 1) &&
+            (pl.packed ? map_q(&tm.qp, q, pl.G, a->Hkv, a->T, a->B, pl.tb, pl.rb) : (tm.qp = tm.qo, true));
+  if (a->P > 0) ok = ok && map_kv(&tm.pk, pk, a->Hkv, a->P, 1) && map_kv(&tm.pv, pv, a->Hkv, a->P, 1);
+  if (a->S > 0) ok = ok && map_kv(&tm.k, k, a->Hkv, a->S, a->B) && map_kv(&tm.v, v, a->Hkv, a->S, a->B);
+  if (!ok) return op_fail(QI_ERR_INVALID_ARG, "qi_prefix_attention: tensor map encoding failed (strides?)");
+  if (a->P == 0) tm.pk = tm.k, tm.pv = tm.v;  // never loaded from
+  if (a->S == 0) tm.k = tm.pk, tm.v = tm.pv;
+  Params p{};
+  p.pl = pl;
+  p.B = a->B;
+  p.T = a->T;
+  p.Hq = a->Hq;
+  p.Hkv = a->Hkv;
+  p.P = a->P;
+  p.S = a->S;
+  p.causal = a->causal != 0;
+  p.own_len = a->S > 0 ? a->own_len : nullptr;
+  p.o = static_cast<uint16_t*>(const_cast<void*>(o.data));
+  p.ob = o.batch;
+  p.orow = o.row;
+  p.oh = o.head;
+  p.part = reinterpret_cast<float*>(ws + w.part);
+  p.ml = reinterpret_cast<float2*>(ws + w.ml);
+  p.err = a->status;
+  const float scale_log2 = a->scale * 1.4426950408889634f;
+  const cudaError_t e = bf16 ? launch<true>(tm, p, scale_log2, sms, s) : launch<false>(tm, p, scale_log2, sms, s);
+  if (e != cudaSuccess) return op_fail(QI_ERR_CUDA, "qi_prefix_attention: %s", cudaGetErrorString(e));
+  return QI_OK;
+}

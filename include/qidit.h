@@ -483,6 +483,119 @@ qi_status qi_dit_profile_classes(qi_dit* dit, unsigned mask, int block_stride);
  * the last reset, then resets. ms/launches: host arrays [QI_PROF_CLASSES]. */
 qi_status qi_dit_profile_read(qi_dit* dit, double* ms, long long* launches);
 
+/* ------------------------------------------------------------------ batches from one prompt
+ *
+ * Operators for a server that makes several images, or continues several sequences,
+ * from one prompt: attention over a prefix of K/V that the whole batch shares, an 8-bit
+ * cache to hold prompts in, and the residual norm that ends in an MXFP8 operand. They
+ * need no handle, run on the current device and allocate nothing; every pointer is memory
+ * of that device. Any number of calls may be in flight, on any streams, as long as no two
+ * that overlap share a workspace or an output. All can be captured into a graph. */
+
+/* Element types of the 16-bit (and, for the norm, 32-bit) tensors below. */
+#define QI_DT_F16 0
+#define QI_DT_BF16 1
+#define QI_DT_F32 2
+
+/* A tensor [batch, row, head, 128] of 16-bit values: element strides of the first three
+ * dimensions, the last one contiguous. data is 16-byte aligned; a stride is a positive
+ * multiple of 8 (that of a dimension of size 1 is ignored). */
+typedef struct qi_tensor4 {
+  const void* data;
+  long long batch, row, head;
+} qi_tensor4;
+
+/* Attention of a batch that shares a prefix. For sequence b < B, query row t < T and
+ * query head hq < Hq, with key head h = hq / (Hq / Hkv):
+ *   o[b,t,hq] = softmax over j of scale q[b,t,hq].key_j, times value_j,
+ * over the P prefix rows (pk, pv [P, Hkv, 128]) and the first lim rows of the sequence's
+ * own k, v [S, Hkv, 128]: lim = own_len[b], or with `causal` own_len[b] - T + t + 1 (the
+ * last query row sees all own_len[b] keys), each clamped to 0 .. own_len[b]. own_len is a
+ * device array of B, read when the kernels run and clamped to 0 .. S; NULL means S. A row
+ * that sees no key is zero. Rows of k and v at or past own_len[b] may hold anything; K and
+ * V rows that some query row of the sequence sees must be finite.
+ * With P = 0 this is attention of each sequence over its own states of any lengths (cross
+ * attention to an encoder's states); with S = 0 over the prefix alone.
+ *
+ * dtype QI_DT_F16 or QI_DT_BF16 for q, o and every 16-bit K/V; scores, maxima, sums and O
+ * are fp32, the probabilities are rounded to dtype as tensor-core operands. q and o are
+ * [B, T, Hq, 128], o written with 16-byte stores and not overlapping any input.
+ * The prefix is given either as pk, pv (batch stride ignored), or with pk.data = pv.data =
+ * NULL as rows of an 8-bit cache (qi_kv8_write): codes pk8, pv8 [P, Hkv, 128] and scales
+ * pk_sf, pv_sf [P, Hkv, 4], contiguous, codes 16-byte and scales 4-byte aligned; its values
+ * are the codes times their scales, rounded to dtype.
+ * ws: 256-byte aligned scratch of at least qi_prefix_attention_workspace(args) bytes (which
+ * depends on the sizes, on whether pk8 is NULL and on the current device only; NULL if 0).
+ * status: device int, or NULL: receives a non-zero code if a bounded wait in the kernel
+ * expires (the result is then undefined); never cleared by the library.
+ * Results do not depend on the other sequences' contents, and repeat bit for bit.
+ * Errors: INVALID_ARG (NULL, dtype, alignment, strides, scale not positive, workspace),
+ * SHAPE (B, T, Hkv < 1, Hq % Hkv != 0, Hq / Hkv > 128, P + S = 0, B or Hkv > 65535, T, P or
+ * S > 2^24, B T Hq > 2^31), CUDA. */
+typedef struct qi_prefix_attn {
+  int dtype, B, T, Hq, Hkv, P, S, causal;
+  float scale;
+  qi_tensor4 q, k, v, o, pk, pv;
+  const uint8_t* pk8;
+  const uint8_t* pv8;
+  const uint8_t* pk_sf;
+  const uint8_t* pv_sf;
+  const int* own_len;
+  void* ws;
+  size_t ws_bytes;
+  int* status;
+} qi_prefix_attn;
+size_t qi_prefix_attention_workspace(const qi_prefix_attn* args); /* 0 also for bad sizes */
+qi_status qi_prefix_attention(const qi_prefix_attn* args, qi_stream_t stream);
+
+/* The 8-bit K/V cache: MXFP8 (as qi_quant_mxfp8) along the head dimension. k8, v8: E4M3
+ * codes [B, S, H, 128]; k_sf, v_sf: UE8M0 scale bytes [B, S, H, 4], one per 32 values; all
+ * contiguous, codes 16-byte and scales 4-byte aligned: 2 x 132 bytes a row and head, against
+ * 2 x 256 in 16 bits. A value is code * 2^(scale - 127).
+ *
+ * qi_kv8_write quantises k and v [B, T, H, 128] (dtype QI_DT_F16 or QI_DT_BF16) into the
+ * cache as they arrive: row t of sequence b, for t < lens[b], goes to cache row pos[b] + t.
+ * qi_kv8_read is its inverse: cache row pos[b] + t to row t of k and v, rounded to dtype.
+ * pos, lens: device int32 [B], read when the kernel runs; pos NULL means 0, lens NULL means
+ * T. Rows at or past lens[b] and rows whose cache row is outside 0 .. S - 1 are passed over:
+ * nothing of them is read, and what is there stays as it was.
+ * Errors: INVALID_ARG (NULL, dtype, alignment, strides), SHAPE (B, T, H, S < 1, B or H >
+ * 65535, T or S > 2^24), CUDA. */
+qi_status qi_kv8_write(int dtype, int B, int T, int S, int H, const qi_tensor4* k, const qi_tensor4* v, uint8_t* k8,
+                       uint8_t* v8, uint8_t* k_sf, uint8_t* v_sf, const int* pos, const int* lens,
+                       qi_stream_t stream);
+qi_status qi_kv8_read(int dtype, int B, int T, int S, int H, const uint8_t* k8, const uint8_t* v8,
+                      const uint8_t* k_sf, const uint8_t* v_sf, const int* pos, const int* lens, const qi_tensor4* k,
+                      const qi_tensor4* v, qi_stream_t stream);
+
+/* Residual addition, RMSNorm and the MXFP8 operand of the next block-scaled GEMM:
+ *   x_out = round(x + delta), y = x_out / sqrt(mean(x_out^2) + eps) * gain,
+ *   (q, sf) = MXFP8(y) as qi_quant_mxfp8 lays it out for qi_gemm_mxfp8.
+ * x, x_out: [rows, K] of x_dtype; delta: [rows, K] of delta_dtype, or NULL (x_out, if given,
+ * is then a copy of x); row strides in elements. x_out may be x itself, or NULL if the sum
+ * is not wanted. The norm is that of the stored sum, rounded to x_dtype. gain: w [K] (fp32
+ * if w_f32, else bf16 bits), 1 + w if plus_one (the ZeroCenterRMSNorm form), 1 if w is NULL.
+ * The statistics and the products carry an error term beside each fp32 value, so that y is
+ * the fp32 rounding of its exact value but for the last bits of rsqrt's correction.
+ * K a multiple of 128 up to 16384, pointers and row strides in bytes multiples of 16, w
+ * 16-byte aligned; sf holds ceil(rows / 128) * (K / 128) * 512 bytes, 4-byte aligned, of which
+ * those of rows past `rows` are left as they were.
+ * Errors: INVALID_ARG (NULL, dtype, alignment, eps negative or not finite), SHAPE, CUDA. */
+typedef struct qi_add_rmsnorm {
+  int x_dtype, delta_dtype, rows, K, w_f32, plus_one;
+  float eps;
+  const void* x;
+  long long x_stride;
+  const void* delta;
+  long long delta_stride;
+  void* x_out;
+  long long x_out_stride;
+  const void* w;
+  uint8_t* q;
+  uint8_t* sf;
+} qi_add_rmsnorm;
+qi_status qi_add_rmsnorm_mxfp8(const qi_add_rmsnorm* args, qi_stream_t stream);
+
 /* Message for the calling thread's last failed call ("" if none). */
 const char* qi_last_error(void);
 
