@@ -297,8 +297,22 @@ DT_F16, DT_BF16, DT_F32 = 0, 1, 2
 _TENSOR4 = struct.Struct("@Pqqq")                          # qi_tensor4
 _PREFIX_ATTN = struct.Struct("@8if" + "Pqqq" * 6 + "6PNP")  # qi_prefix_attn
 _ADD_RMSNORM = struct.Struct("@6ifPqPqPqPPP")              # qi_add_rmsnorm
-_NO_TENSOR = (0, 0, 0, 0)
-_ws_bytes: dict = {}                                       # workspace bytes by sizes
+_SCALE = 1.0 / math.sqrt(HEAD_DIM)
+# Layouts (types, devices, shapes and strides of all tensor arguments) that a call has checked, with
+# what it packs for them; the checks and the workspace size depend on nothing else, and take longer
+# than the launch. Pointers are read anew on every call.
+_layouts: dict = {}
+
+
+def _layout(t):
+    return None if t is None else (t.dtype, t.device, t.shape, t.stride())
+
+
+def _remember(key, value):
+    if len(_layouts) >= 4096:
+        _layouts.clear()
+    _layouts[key] = value
+    return value
 
 
 class KV8Cache(NamedTuple):
@@ -332,65 +346,101 @@ def _dt16(t, name):
     raise ValueError(f"{name}: want float16 or bfloat16, got {t.dtype}")
 
 
-def _view4(t, like, shape, name):
-    """(pointer, batch, row, head strides) of a 16-bit tensor `shape` = [batch, row, head, 128] (batch may be left out)."""
+def _strides4(t, like, shape, name):
+    """Batch, row and head strides of a 16-bit tensor `shape` = [batch, row, head, 128] (batch may be left out)."""
     if t.dtype != like.dtype or t.device != like.device or tuple(t.shape) != shape:
         raise ValueError(f"{name}: want {like.dtype} {like.device} {shape}, got {t.dtype} {t.device} {tuple(t.shape)}")
     st = t.stride()
     if st[-1] != 1:
         raise ValueError(f"{name}: the last dimension must be contiguous")
-    return (t.data_ptr(), *st[:3]) if len(st) == 4 else (t.data_ptr(), 0, *st[:2])
+    return st[:3] if len(st) == 4 else (0, *st[:2])
 
 
-def _int32_ptr(t, n, device, name):
+def _want(t, dtype, shape, device, name):
+    if t is not None and (t.dtype != dtype or t.device != device or tuple(t.shape) != shape or not t.is_contiguous()):
+        raise ValueError(f"{name}: want contiguous {dtype} {device} {shape}, got {t.dtype} {t.device} {tuple(t.shape)}")
+
+
+def _want_kv8(cache, shape, device, name):
+    """An 8-bit cache's four tensors, of leading shape `shape`."""
     import torch
-    if t is None:
-        return 0
-    if t.dtype != torch.int32 or t.device != device or tuple(t.shape) != (n,) or not t.is_contiguous():
-        raise ValueError(f"{name}: want contiguous int32 {device} ({n},), got {t.dtype} {t.device} {tuple(t.shape)}")
-    return t.data_ptr()
-
-
-def _kv8_ptrs(cache, shape, device, name):
-    """Pointers of an 8-bit cache's four tensors of leading shape `shape`."""
-    import torch
-    out = []
     for t, n in zip(cache, (HEAD_DIM, HEAD_DIM, HEAD_DIM // 32, HEAD_DIM // 32)):
-        if t.dtype != torch.uint8 or t.device != device or tuple(t.shape) != (*shape, n) or not t.is_contiguous():
-            raise ValueError(f"{name}: want contiguous uint8 {device} {(*shape, n)}, got {t.dtype} {t.device} "
-                             f"{tuple(t.shape)}")
-        out.append(t.data_ptr())
-    return out
+        _want(t, torch.uint8, (*shape, n), device, name)
+
+
+def _addr(t):
+    return 0 if t is None else t.data_ptr()
 
 
 def _on_device(fn):
-    """Runs `fn` (first argument a tensor or a KV8Cache) with that tensor's device current, and with
-    `stream`, if given, as the current stream, so that what the call allocates belongs to it."""
+    """Calls fn(*args, raw stream, **kw) with its first argument's device (that of a tensor, or of a
+    KV8Cache) current, on `stream` or else on that device's current stream; with `stream`, it is the
+    current stream, too, so that what the call allocates belongs to it."""
     import functools
-    name = fn.__code__.co_varnames[0]
+    import inspect
+    name = next(iter(inspect.signature(fn).parameters))
 
     @functools.wraps(fn)
     def call(*args, stream=None, **kw):
         import torch
         t = args[0] if args else kw[name]
-        t = t[0] if isinstance(t, tuple) else t
-        if not t.is_cuda:
-            raise ValueError(f"{fn.__name__}: CUDA tensors wanted, got {t.device}")
-        if stream is None and t.device.index == torch.cuda.current_device():
-            return fn(*args, **kw)
-        with torch.cuda.device(t.device):
+        dev = (t[0] if isinstance(t, tuple) else t).device
+        if dev.type != "cuda":
+            raise ValueError(f"{fn.__name__}: CUDA tensors wanted, got {dev}")
+        if stream is None and dev.index == torch.cuda.current_device():
+            return fn(*args, **kw, _raw=torch._C._cuda_getCurrentRawStream(dev.index))
+        with torch.cuda.device(dev):
             if stream is None:
-                return fn(*args, **kw)
-            if stream.device != t.device:
-                raise ValueError(f"{fn.__name__}: a stream of {stream.device} for tensors of {t.device}")
+                return fn(*args, **kw, _raw=torch._C._cuda_getCurrentRawStream(dev.index))
+            if stream.device != dev:
+                raise ValueError(f"{fn.__name__}: a stream of {stream.device} for tensors of {dev}")
             with torch.cuda.stream(stream):
-                return fn(*args, **kw)
+                return fn(*args, **kw, _raw=stream.cuda_stream)
     return call
+
+
+def _check_prefix_attention(key, q, k, v, prefix_k, prefix_v, prefix8, own_len, out, status):
+    """(leading sizes, strides by tensor, workspace bytes, output shape) of arguments in this layout."""
+    import torch
+    if q.dim() != 4 or q.shape[3] != HEAD_DIM:
+        raise ValueError(f"q: want [B, T, Hq, {HEAD_DIM}], got {tuple(q.shape)}")
+    dt, dev = _dt16(q, "q"), q.device
+    B, T, Hq, _ = q.shape
+    if (k is None) != (v is None) or (prefix_k is None) != (prefix_v is None):
+        raise ValueError("k and v, and prefix_k and prefix_v, come in pairs")
+    if prefix8 is not None and prefix_k is not None:
+        raise ValueError("prefix8 and prefix_k / prefix_v exclude each other")
+    pre = prefix8.k if prefix8 is not None else prefix_k
+    for t, n, name in ((k, 4, "k"), (pre, 3, "prefix")):
+        if t is not None and t.dim() != n:
+            raise ValueError(f"{name}: want {n} dimensions, got {tuple(t.shape)}")
+    heads = [t.shape[-2] for t in (k, pre) if t is not None]
+    if not heads:
+        raise ValueError("neither own keys nor a prefix")
+    S, P, Hkv = (0 if k is None else k.shape[1]), (0 if pre is None else pre.shape[0]), heads[0]
+    none = (0, 0, 0)
+    ks = vs = pks = pvs = none
+    if k is not None:
+        ks, vs = (_strides4(t, q, (B, S, Hkv, HEAD_DIM), n) for t, n in ((k, "k"), (v, "v")))
+    if prefix8 is not None:
+        _want_kv8(prefix8, (P, Hkv), dev, "prefix8")
+    elif prefix_k is not None:
+        pks, pvs = (_strides4(t, q, (P, Hkv, HEAD_DIM), n) for t, n in ((prefix_k, "prefix_k"), (prefix_v, "prefix_v")))
+    shape = (B, T, Hq, HEAD_DIM)
+    qs = _strides4(q, q, shape, "q")
+    os_ = (T * Hq * HEAD_DIM, Hq * HEAD_DIM, HEAD_DIM) if out is None else _strides4(out, q, shape, "out")
+    _want(own_len, torch.int32, (B,), dev, "own_len")
+    _want(status, torch.int32, (1,), dev, "status")
+    sizes = (dt, B, T, Hq, Hkv, P, S)
+    p8 = int(prefix8 is not None and P > 0)
+    need = lib().qi_prefix_attention_workspace(
+        _PREFIX_ATTN.pack(*sizes, 0, 1.0, *(0, 0, 0, 0) * 6, p8, 0, 0, 0, 0, 0, 0, 0))
+    return _remember(key, (sizes, qs, ks, vs, os_, pks, pvs, need, shape))
 
 
 @_on_device
 def prefix_attention(q, k, v, prefix_k=None, prefix_v=None, prefix8: KV8Cache | None = None, own_len=None,
-                     causal: bool = False, scale: float | None = None, out=None, status=None):
+                     causal: bool = False, scale: float | None = None, out=None, status=None, *, _raw=None):
     """Attention of a batch whose sequences share a prefix of keys and have keys of their own.
 
     q [B, T, Hq, 128]; k, v [B, S, Hkv, 128] (S may be 0, or k = v = None); prefix_k, prefix_v
@@ -398,106 +448,92 @@ def prefix_attention(q, k, v, prefix_k=None, prefix_v=None, prefix8: KV8Cache | 
     bfloat16, any strides with a contiguous last dimension. own_len: int32 [B] on the device, the own
     rows in use (None: S). causal: query row t of T sees own rows up to own_len - T + t. scale: default
     1 / sqrt(128). status: int32 [1] on the device that receives a non-zero code if a wait in the
-    kernel expires. Returns o [B, T, Hq, 128] (`out`, if given)."""
+    kernel expires. stream: default the current one. Returns o [B, T, Hq, 128] (`out`, if given)."""
     import torch
-    if q.dim() != 4 or q.shape[3] != HEAD_DIM:
-        raise ValueError(f"q: want [B, T, Hq, {HEAD_DIM}], got {tuple(q.shape)}")
-    dt = _dt16(q, "q")
-    dev = q.device
-    B, T, Hq, _ = q.shape
-    if (k is None) != (v is None) or (prefix_k is None) != (prefix_v is None):
-        raise ValueError("k and v, and prefix_k and prefix_v, come in pairs")
-    if prefix8 is not None and prefix_k is not None:
-        raise ValueError("prefix8 and prefix_k / prefix_v exclude each other")
-    P = prefix8.k.shape[0] if prefix8 is not None else prefix_k.shape[0] if prefix_k is not None else 0
-    heads = [t.shape[-2] for t in (k, prefix_k, prefix8 and prefix8.k) if t is not None]
-    if not heads:
-        raise ValueError("neither own keys nor a prefix")
-    Hkv = heads[0]
-    S = k.shape[1] if k is not None else 0
-    kt = _view4(k, q, (B, S, Hkv, HEAD_DIM), "k") if S else _NO_TENSOR
-    vt = _view4(v, q, (B, S, Hkv, HEAD_DIM), "v") if S else _NO_TENSOR
-    pkt = pvt = _NO_TENSOR
-    p8 = (0, 0, 0, 0)
-    if P and prefix8 is not None:
-        p8 = _kv8_ptrs(prefix8, (P, Hkv), dev, "prefix8")
-    elif P:
-        pkt = _view4(prefix_k, q, (P, Hkv, HEAD_DIM), "prefix_k")
-        pvt = _view4(prefix_v, q, (P, Hkv, HEAD_DIM), "prefix_v")
+    p8 = prefix8 if prefix8 is not None else (None, None, None, None)
+    key = (_layout(q), _layout(k), _layout(v), _layout(prefix_k), _layout(prefix_v), *map(_layout, p8),
+           _layout(own_len), _layout(out), _layout(status))
+    plan = _layouts.get(key)
+    if plan is None:
+        plan = _check_prefix_attention(key, q, k, v, prefix_k, prefix_v, prefix8, own_len, out, status)
+    sizes, qs, ks, vs, os_, pks, pvs, need, shape = plan
     if out is None:
-        out = torch.empty(B, T, Hq, HEAD_DIM, dtype=q.dtype, device=dev)
-    qt, ot = _view4(q, q, (B, T, Hq, HEAD_DIM), "q"), _view4(out, q, (B, T, Hq, HEAD_DIM), "out")
-    lens = _int32_ptr(own_len, B, dev, "own_len")
-    st = _int32_ptr(status, 1, dev, "status")
-    if scale is None:
-        scale = 1.0 / math.sqrt(HEAD_DIM)
-    sizes = (dt, B, T, Hq, Hkv, P, S, int(causal), scale)
-    ptrs = (*qt, *kt, *vt, *ot, *pkt, *pvt, *p8, lens)
-    L = _lib or lib()
-    key = (dev.index, B, T, Hq, Hkv, P, S, p8[0] != 0)
-    need = _ws_bytes.get(key)
-    if need is None:
-        need = L.qi_prefix_attention_workspace(_PREFIX_ATTN.pack(*sizes, *ptrs, 0, 0, st))
-        if len(_ws_bytes) > 4096:
-            _ws_bytes.clear()
-        _ws_bytes[key] = need
-    ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-    _check(L.qi_prefix_attention(_PREFIX_ATTN.pack(*sizes, *ptrs, ws.data_ptr() if need else 0, need, st), _stream()))
+        out = torch.empty(shape, dtype=q.dtype, device=q.device)
+    ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
+    args = _PREFIX_ATTN.pack(
+        *sizes, 1 if causal else 0, _SCALE if scale is None else scale, q.data_ptr(), *qs, _addr(k), *ks, _addr(v),
+        *vs, out.data_ptr(), *os_, _addr(prefix_k), *pks, _addr(prefix_v), *pvs, *map(_addr, p8), _addr(own_len),
+        _addr(ws), need, _addr(status))
+    st = _lib.qi_prefix_attention(args, _raw)
+    if st:
+        _check(st)
     return out
 
 
-def _kv8_call(name, cache, k, v, pos, lens):
+def _check_kv8(key, cache, k, v, pos, lens):
+    import torch
     if k.dim() != 4 or k.shape[3] != HEAD_DIM:
         raise ValueError(f"k: want [B, T, H, {HEAD_DIM}], got {tuple(k.shape)}")
     B, T, H, _ = k.shape
-    S = cache.k.shape[1]
     dev = cache.k.device
     if k.device != dev:
         raise ValueError(f"k on {k.device}, the cache on {dev}")
+    if cache.k.dim() != 4:
+        raise ValueError(f"cache: want [B, S, H, {HEAD_DIM}] codes, got {tuple(cache.k.shape)}")
+    S = cache.k.shape[1]
     dt = _dt16(k, "k")
-    c = _kv8_ptrs(cache, (B, S, H), dev, "cache")
-    kt = _TENSOR4.pack(*_view4(k, k, (B, T, H, HEAD_DIM), "k"))
-    vt = _TENSOR4.pack(*_view4(v, k, (B, T, H, HEAD_DIM), "v"))
-    at = (_int32_ptr(pos, B, dev, "pos"), _int32_ptr(lens, B, dev, "lens"))
-    if name == "write":
-        _check(lib().qi_kv8_write(dt, B, T, S, H, kt, vt, *c, *at, _stream()))
-    else:
-        _check(lib().qi_kv8_read(dt, B, T, S, H, *c, *at, kt, vt, _stream()))
+    _want_kv8(cache, (B, S, H), dev, "cache")
+    strides = tuple(_strides4(t, k, (B, T, H, HEAD_DIM), n) for t, n in ((k, "k"), (v, "v")))
+    _want(pos, torch.int32, (B,), dev, "pos")
+    _want(lens, torch.int32, (B,), dev, "lens")
+    lib()
+    return _remember(key, ((dt, B, T, S, H), *strides))
+
+
+def _kv8_args(cache, k, v, pos, lens):
+    key = (*map(_layout, cache), _layout(k), _layout(v), _layout(pos), _layout(lens))
+    plan = _layouts.get(key)
+    if plan is None:
+        plan = _check_kv8(key, cache, k, v, pos, lens)
+    sizes, ks, vs = plan
+    c = (cache.k.data_ptr(), cache.v.data_ptr(), cache.k_sf.data_ptr(), cache.v_sf.data_ptr())
+    return (sizes, _TENSOR4.pack(k.data_ptr(), *ks), _TENSOR4.pack(v.data_ptr(), *vs), c, _addr(pos), _addr(lens))
 
 
 @_on_device
-def kv8_write(cache: KV8Cache, k, v, pos=None, lens=None):
+def kv8_write(cache: KV8Cache, k, v, pos=None, lens=None, *, _raw=None):
     """Quantises k, v [B, T, H, 128] (float16 or bfloat16, any strides with a contiguous last dimension)
     into the cache: row t < lens[b] of sequence b becomes cache row pos[b] + t (int32 [B] on the device;
-    None: 0 and T). Rows that fall outside the cache are passed over."""
-    _kv8_call("write", cache, k, v, pos, lens)
+    None: 0 and T). Rows that fall outside the cache are passed over. stream: default the current one."""
+    sizes, kt, vt, c, pp, lp = _kv8_args(cache, k, v, pos, lens)
+    st = _lib.qi_kv8_write(*sizes, kt, vt, *c, pp, lp, _raw)
+    if st:
+        _check(st)
     return cache
 
 
 @_on_device
-def kv8_read(cache: KV8Cache, T: int, dtype, pos=None, lens=None, out=None):
+def kv8_read(cache: KV8Cache, T: int, dtype, pos=None, lens=None, out=None, *, _raw=None):
     """(k, v) [B, T, H, 128] in `dtype` from cache rows pos[b] + t, t < lens[b]. Rows at or past lens[b] or
-    outside the cache stay as they are in `out` = (k, v), and are zero without `out`."""
+    outside the cache stay as they are in `out` = (k, v), and are zero without `out`. stream: default the
+    current one."""
     import torch
-    B, S, H, _ = cache.k.shape
     if out is None:
+        B, S, H, _ = cache.k.shape
         make = torch.empty if pos is None and lens is None and T <= S else torch.zeros
         out = tuple(make(B, T, H, HEAD_DIM, dtype=dtype, device=cache.k.device) for _ in range(2))
     k, v = out
-    if k.dtype != dtype or tuple(k.shape) != (B, T, H, HEAD_DIM):
-        raise ValueError(f"out: want {dtype} {(B, T, H, HEAD_DIM)}, got {k.dtype} {tuple(k.shape)}")
-    _kv8_call("read", cache, k, v, pos, lens)
+    if k.dtype != dtype or k.dim() != 4 or k.shape[1] != T:
+        raise ValueError(f"out: want {dtype} [B, {T}, H, {HEAD_DIM}], got {k.dtype} {tuple(k.shape)}")
+    sizes, kt, vt, c, pp, lp = _kv8_args(cache, k, v, pos, lens)
+    st = _lib.qi_kv8_read(*sizes, *c, pp, lp, kt, vt, _raw)
+    if st:
+        _check(st)
     return k, v
 
 
-@_on_device
-def add_rmsnorm_mxfp8(x, delta=None, w=None, plus_one: bool = False, eps: float = 1e-6, x_out=None, q=None, sf=None):
-    """x_out = x + delta in x's type, then MXFP8 of RMSNorm(x_out) * gain along the last axis.
-
-    x [rows, K] float32, float16 or bfloat16, delta [rows, K] of any of them (None: no addition), rows
-    any multiple of 16 bytes apart; w [K] bfloat16 or float32: gain w, or 1 + w with plus_one. Returns
-    (x_out, codes [rows, K] uint8, scale chunks uint8) as quant_mxfp8 lays them out; x_out may be x, and
-    a new tensor is made for each of the three that is not given."""
+def _check_norm(key, x, delta, w, x_out, q, sf):
+    """(leading arguments, row strides, bytes of the scale chunks) of arguments in this layout."""
     import torch
     kinds = {torch.float16: DT_F16, torch.bfloat16: DT_BF16, torch.float32: DT_F32}
     if x.dim() != 2 or x.dtype not in kinds:
@@ -505,38 +541,48 @@ def add_rmsnorm_mxfp8(x, delta=None, w=None, plus_one: bool = False, eps: float 
     rows, K = x.shape
     dev = x.device
     chunks = ((rows + 127) // 128) * (K // 128) * 512
-
-    def rows_of(t, name):
-        if t.dtype not in kinds or t.device != dev or tuple(t.shape) != (rows, K) or (K > 1 and t.stride(1) != 1):
+    for t, types, name in ((x, kinds, "x"), (delta, kinds, "delta"), (x_out, (x.dtype,), "x_out")):
+        if t is not None and (t.dtype not in types or t.device != dev or tuple(t.shape) != (rows, K)
+                              or (K > 1 and t.stride(1) != 1)):
             raise ValueError(f"{name}: want {dev} {(rows, K)} with contiguous rows, got {t.dtype} {t.device} "
                              f"{tuple(t.shape)}")
-        return t.data_ptr(), t.stride(0)
-
-    def bytes_of(t, shape, name):
-        if t.dtype != torch.uint8 or t.device != dev or tuple(t.shape) != shape or not t.is_contiguous():
-            raise ValueError(f"{name}: want contiguous uint8 {dev} {shape}, got {t.dtype} {t.device} {tuple(t.shape)}")
-        return t.data_ptr()
-
-    if x_out is None:
-        x_out = torch.empty(rows, K, dtype=x.dtype, device=dev)
-    elif x_out.dtype != x.dtype:
-        raise ValueError(f"x_out: want {x.dtype}, got {x_out.dtype}")
-    if q is None:
-        q = torch.empty(rows, K, dtype=torch.uint8, device=dev)
-    if sf is None:
-        sf = torch.zeros(chunks, dtype=torch.uint8, device=dev)
-    wp = 0
+    _want(q, torch.uint8, (rows, K), dev, "q")
+    _want(sf, torch.uint8, (chunks,), dev, "sf")
     if w is not None:
-        if w.dtype not in (torch.bfloat16, torch.float32) or w.device != dev or tuple(w.shape) != (K,) or \
-                not w.is_contiguous():
-            raise ValueError(f"w: want contiguous bfloat16 or float32 {dev} ({K},), got {w.dtype} {w.device} "
-                             f"{tuple(w.shape)}")
-        wp = w.data_ptr()
-    d = rows_of(delta, "delta") if delta is not None else (0, 0)
-    args = _ADD_RMSNORM.pack(kinds[x.dtype], kinds[delta.dtype] if delta is not None else 0, rows, K,
-                             int(w is not None and w.dtype == torch.float32), int(plus_one), eps, *rows_of(x, "x"), *d,
-                             *rows_of(x_out, "x_out"), wp, bytes_of(q, (rows, K), "q"), bytes_of(sf, (chunks,), "sf"))
-    _check(lib().qi_add_rmsnorm_mxfp8(args, _stream()))
+        _want(w, w.dtype if w.dtype in (torch.bfloat16, torch.float32) else torch.bfloat16, (K,), dev, "w")
+    lib()
+    stride = lambda t: K if t is None else t.stride(0)
+    return _remember(key, ((kinds[x.dtype], 0 if delta is None else kinds[delta.dtype], rows, K,
+                            int(w is not None and w.dtype == torch.float32)), stride(x), stride(delta), stride(x_out),
+                           chunks))
+
+
+@_on_device
+def add_rmsnorm_mxfp8(x, delta=None, w=None, plus_one: bool = False, eps: float = 1e-6, x_out=None, q=None, sf=None,
+                      *, _raw=None):
+    """x_out = x + delta in x's type, then MXFP8 of RMSNorm(x_out) * gain along the last axis.
+
+    x [rows, K] float32, float16 or bfloat16, delta [rows, K] of any of them (None: no addition), rows
+    any multiple of 16 bytes apart; w [K] bfloat16 or float32: gain w, or 1 + w with plus_one. Returns
+    (x_out, codes [rows, K] uint8, scale chunks uint8) as quant_mxfp8 lays them out; x_out may be x, and
+    a new tensor is made for each of the three that is not given. stream: default the current one."""
+    import torch
+    key = (_layout(x), _layout(delta), _layout(w), _layout(x_out), _layout(q), _layout(sf))
+    plan = _layouts.get(key)
+    if plan is None:
+        plan = _check_norm(key, x, delta, w, x_out, q, sf)
+    head, xs, ds, os_, chunks = plan
+    if x_out is None:
+        x_out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    if q is None:
+        q = torch.empty(x.shape, dtype=torch.uint8, device=x.device)
+    if sf is None:
+        sf = torch.zeros(chunks, dtype=torch.uint8, device=x.device)
+    st = _lib.qi_add_rmsnorm_mxfp8(
+        _ADD_RMSNORM.pack(*head, 1 if plus_one else 0, eps, x.data_ptr(), xs, _addr(delta), ds, x_out.data_ptr(), os_,
+                          _addr(w), q.data_ptr(), sf.data_ptr()), _raw)
+    if st:
+        _check(st)
     return x_out, q, sf
 
 

@@ -49,8 +49,9 @@ constexpr int kRows = 128;                    // MMA rows: query rows per block 
 constexpr int kKeys = 128;                    // keys per tile
 constexpr int kBox = 128 * 64 * 2;            // 128 rows x 64 dims, 128-byte swizzle (16 KB)
 constexpr int kTile = 2 * kBox;               // Q, K or V tile (32 KB)
-constexpr int kKStages = 3;
+constexpr int kKStages = 2;  // (a third measured 1 % slower at 1024^2)
 constexpr int kVStages = 2;
+constexpr int kQBufs = 2;                     // the next unit's Q loads while this one's tiles run
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 0;                 // O_h at kColO + 128 h
 constexpr uint32_t kColS = 256;
@@ -66,26 +67,39 @@ enum : int {
   kKEmpty = kKFull + kKStages,
   kVFull = kKEmpty + kKStages,
   kVEmpty = kVFull + kVStages,
-  kQFull = kVEmpty + kVStages,
-  kQEmpty = kQFull + 1,
-  kSFull = kQEmpty + 1,
+  kVClean = kVEmpty + kVStages,  // rows past own_len of a unit's last V tile cleared
+  kQFull = kVClean + 1,
+  kQEmpty = kQFull + kQBufs,
+  kSFull = kQEmpty + kQBufs,
   kSFree = kSFull + 1,
   kPFull = kSFree + 1,
   kPvDone = kPFull + 4,
   kOFull = kPvDone + 4,
   kOEmpty = kOFull + 1,
-  kLFull = kOEmpty + 1,
-  kDrainQK = kLFull + 1,
+  kLFull = kOEmpty + 1,  // the unit's row sums and maxima in shared memory (8 softmax warps)
+  kLFree = kLFull + 1,   // ... read by the epilogue (4 warps)
+  kDrainQK = kLFree + 1,
   kDrainPV = kDrainQK + 1,
   kNumBars = kDrainPV + 1
 };
 __device__ __forceinline__ uint32_t bar_count(int i) {
   if (i == kSFree || i == kLFull) return 8;
-  if ((i >= kPFull && i < kPFull + 4) || i == kOEmpty) return 4;
+  if ((i >= kPFull && i < kPFull + 4) || i == kOEmpty || i == kLFree) return 4;
   return 1;
 }
-constexpr int kSmem = (1 + kKStages + kVStages) * kTile + 1024 + kNumBars * 8 + 16 + 2 * 2 * kRows * 4;
+constexpr int kSmem = (kQBufs + kKStages + kVStages) * kTile + 1024 + kNumBars * 8 + 16 + 2 * 2 * kRows * 4;
 static_assert(kSmem <= 227 * 1024, "shared memory over the per-block limit");
+
+// n / d for 0 <= n < 2^31 as one widening product: m = ceil(2^s / d) with s = 31 +
+// ceil(log2 d) errs by less than 2^(s - 31) d / d, too little to reach the next quotient.
+// (Every role works out every unit it meets; with the compiler's division that took each
+// of them about 1200 cycles a unit, more than a key tile's products.)
+struct Div {
+  uint32_t m, s, d;
+};
+__device__ __forceinline__ int quot(const Div& v, int n) {
+  return static_cast<int>((static_cast<unsigned long long>(static_cast<uint32_t>(n)) * v.m) >> v.s);
+}
 
 // The decomposition, decided on the host from sizes alone.
 struct Plan {
@@ -100,6 +114,7 @@ struct Plan {
   int nchp;       // packed: chunks of the prefix
   int packed;
   int split;      // 1: partials and merge_partials
+  int by_block;   // joint units ordered by row block, last first, before head and sequence
   int units_p;    // packed: units over the prefix (they come first)
   int units;
   int rows_p;     // rows of a prefix block's partial
@@ -108,6 +123,7 @@ struct Plan {
 
 struct Params {
   Plan pl;
+  Div d_nch, d_nchp, d_nqb, d_npb, d_B, d_hb, d_G, d_T;  // divisors: the plan's, B, Hkv B, G, T
   int B, T, Hq, Hkv, P, S, causal;
   const int* own_len;
   uint16_t* o;
@@ -124,6 +140,7 @@ struct Unit {
   int n;           // pn + on
   int len;         // own keys of sequence b0
   int rows;        // rows of the block (the MMA's other rows are ignored)
+  bool clear;      // the last tile holds own rows at or past len
   long long slot;  // first partial row
 };
 
@@ -142,9 +159,10 @@ __device__ __forceinline__ Unit unit_of(const Params& p, int u) {
   const Plan& pl = p.pl;
   Unit x;
   x.p0 = x.pn = x.o0 = x.on = x.len = 0;
+  x.clear = false;
   if (u < pl.units_p) {  // packed: prefix
-    const int c = u % pl.nchp, r = u / pl.nchp;
-    x.h = r / pl.npb;
+    const int r = quot(p.d_nchp, u), c = u - r * pl.nchp;
+    x.h = quot(p.d_npb, r);
     x.b0 = (r - x.h * pl.npb) * pl.rb;
     x.t0 = 0;
     x.p0 = c * pl.ct;
@@ -153,13 +171,20 @@ __device__ __forceinline__ Unit unit_of(const Params& p, int u) {
     x.slot = static_cast<long long>(u) * pl.rows_p;
   } else {
     const int v = u - pl.units_p;
-    const int c = v % pl.nch;
-    int r = v / pl.nch;
-    int qb = r % pl.nqb;
-    r /= pl.nqb;
-    x.h = r / p.B;
+    int r = quot(p.d_nch, v);
+    const int c = v - r * pl.nch;
+    int qb;
+    if (pl.by_block) {  // causal: longest first over all heads and sequences
+      const int k = quot(p.d_hb, r);
+      qb = pl.nqb - 1 - k;
+      r -= k * static_cast<int>(p.d_hb.d);
+    } else {
+      const int k = quot(p.d_nqb, r);
+      qb = r - k * pl.nqb;
+      r = k;
+    }
+    x.h = quot(p.d_B, r);
     x.b0 = r - x.h * p.B;
-    if (p.causal) qb = pl.nqb - 1 - qb;  // longest first
     x.t0 = qb * pl.tb;
     x.len = own_len_of(p, x.b0);
     const int pt = pl.packed ? 0 : pl.pt;
@@ -171,6 +196,7 @@ __device__ __forceinline__ Unit unit_of(const Params& p, int u) {
       x.pn = min(hi, pt) - x.p0;
       x.o0 = max(lo, pt) - pt;
       x.on = max(hi, pt) - pt - x.o0;
+      x.clear = x.on > 0 && x.len < (x.o0 + x.on) * kKeys && x.len < p.S;
     }
     x.rows = pl.rows_o;
     x.slot = static_cast<long long>(pl.units_p) * pl.rows_p + static_cast<long long>(v) * pl.rows_o;
@@ -197,6 +223,12 @@ __device__ __forceinline__ void tma_load_5d(void* dst, const CUtensorMap* map, u
       : "memory");
 }
 
+__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
 template <bool BF16>
 __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
   return BF16 ? pack_bf16x2(lo, hi) : pack_f16x2(lo, hi);
@@ -216,13 +248,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = smem;
-  uint8_t* sK = sQ + kTile;
+  uint8_t* sK = sQ + kQBufs * kTile;
   uint8_t* sV = sK + kKStages * kTile;
   uint64_t* bars = reinterpret_cast<uint64_t*>(sV + kVStages * kTile);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kNumBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  float* lsum = reinterpret_cast<float*>(tmem_slot + 4);  // [2][kRows]
-  float* msum = lsum + 2 * kRows;                         // [2][kRows]
+  float* lsum = reinterpret_cast<float*>(tmem_slot + 4);  // [half][kRows]
+  float* msum = lsum + 2 * kRows;
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -256,76 +288,126 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp < 4) {
     regs_release<kRegsLow>();
-    if (warp == 3) {
-      // ---------------- P V issuer (lane 0); the whole warp clears V rows past own_len.
-      // Every lane walks the same units and tiles; lane 0's failure only stops its
-      // waits and MMAs, so the warp meets at every cleared tile whatever happens.
-      const uint64_t vdesc0 = sw128_mnmajor_desc(smem_u32(sV), kBox, 1024);
+    if (warp == 2) {
+      // ---------------- V tiles: lane 0 loads them; the whole warp clears the rows past
+      // own_len of a sequence's last tile. Every lane walks the same units; lane 0's failure
+      // only stops its waits and loads, so the warp meets at every cleared tile.
       uint32_t t = 0;
-      int ku = 0;
       bool ok = true;
       for (int u = blockIdx.x; u < total; u += gridDim.x) {
         const Unit un = unit_of(p, u);
-        if (un.n == 0) continue;
-        for (int j = 0; j < un.n; ++j, ++t) {
-          const uint32_t b = t & 1u;
-          const uint32_t st = t % kVStages;
-          const int row0 = j >= un.pn ? (un.o0 + j - un.pn) * kKeys : 0;
-          const bool clear = j >= un.pn && un.len - row0 < kKeys && un.len < p.S;
-          if (lane == 0 && ok)
-            ok = !*abort_flag &&
-                 (j > 0 || ku == 0 || mbar_wait(&bars[kOEmpty], static_cast<uint32_t>(ku - 1) & 1u)) &&
-                 mbar_wait(&bars[kVFull + st], (t / kVStages) & 1u);
-          if (clear) {
-            // rows len - row0 .. 127 of both 64-dim boxes (a row's 128 bytes stay
-            // within the row under the swizzle)
-            const bool go = __shfl_sync(0xffffffffu, static_cast<int>(ok), 0) != 0;
-            if (go) {
-              const int r0 = un.len - row0;
-              const int n16 = (kKeys - r0) * 8;
-              for (int i = lane; i < 2 * n16; i += 32) {
-                const int box = i >= n16 ? 1 : 0;
-                *reinterpret_cast<uint4*>(sV + st * kTile + box * kBox + r0 * 128 + (i - box * n16) * 16) =
-                    make_uint4(0u, 0u, 0u, 0u);
-              }
-              fence_proxy_async_smem();
+        if (lane == 0 && ok) {
+          for (int j = 0; j < un.n; ++j) {
+            const uint32_t tt = t + j, st = tt % kVStages;
+            if (*abort_flag || !mbar_wait(&bars[kVEmpty + st], ((tt / kVStages) & 1u) ^ 1u)) {
+              if (!*abort_flag) report_error(p.err, kErrTimeoutProducer);
+              *abort_flag = 1;
+              t = tt;  // tiles issued, for the drain below
+              ok = false;
+              break;
             }
-            __syncwarp();
-          }
-          if (lane == 0 && ok) {
-            const uint64_t vd = vdesc0 + ((st * kTile) >> 4);
-            for (int h = 0; h < 2; ++h) {
-              ok = mbar_wait(&bars[kPFull + b * 2 + h], (t >> 1) & 1u);
-              if (!ok) break;
-              tc_fence_after();
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                mma_ts(tmem + kColO + 128u * h, tmem + kColP + b * 64 + h * 32 + k * 8,
-                       vd + ((static_cast<uint32_t>(4 * h + k) * 2048) >> 4), kIdescPV, (j > 0 || k > 0) ? 1u : 0u);
-              mma_commit(&bars[kPvDone + b * 2 + h]);
-            }
-            if (ok) {
-              mma_commit(&bars[kVEmpty + st]);
-              if (j + 1 == un.n) mma_commit(&bars[kOFull]);
-            }
+            const bool pre = j < un.pn;
+            const CUtensorMap* m = pre ? &tm.pv : &tm.v;
+            const int row = (pre ? un.p0 + j : un.o0 + j - un.pn) * kKeys;
+            const int bs = pre ? 0 : un.b0;
+            mbar_arrive_expect_tx(&bars[kVFull + st], kTile);
+            tma_load_4d(sV + st * kTile, m, &bars[kVFull + st], 0, un.h, row, bs);
+            tma_load_4d(sV + st * kTile + kBox, m, &bars[kVFull + st], 64, un.h, row, bs);
           }
         }
-        ++ku;
+        if (ok) t += un.n;
+        if (un.clear) {
+          const uint32_t last = t - 1, st = last % kVStages;
+          if (lane == 0 && ok && !mbar_wait(&bars[kVFull + st], (last / kVStages) & 1u)) {
+            if (!*abort_flag) report_error(p.err, kErrTimeoutProducer);
+            *abort_flag = 1;
+            ok = false;
+          }
+          if (__shfl_sync(0xffffffffu, static_cast<int>(ok), 0)) {
+            // rows r0 .. 127 of both 64-dim boxes (a row's 128 bytes stay within the row
+            // under the swizzle)
+            const int r0 = un.len - (un.o0 + un.on - 1) * kKeys;
+            const int n16 = (kKeys - r0) * 8;
+            uint8_t* base = sV + st * kTile + r0 * 128;
+            for (int i = lane; i < n16; i += 32) {
+              *reinterpret_cast<uint4*>(base + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+              *reinterpret_cast<uint4*>(base + kBox + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+            }
+            fence_proxy_async_smem();
+          }
+          __syncwarp();
+          if (lane == 0 && ok) mbar_arrive(&bars[kVClean]);
+        }
       }
       if (lane == 0) {
-        if (!ok && !*abort_flag) report_error(p.err, kErrTimeoutMma);
-        if (!ok) *abort_flag = 1;
-        mma_commit(&bars[kDrainPV]);
-        if (!mbar_wait(&bars[kDrainPV], 0)) report_error(p.err, kErrTimeoutDrain);
+        for (uint32_t i = t > kVStages ? t - kVStages : 0; i < t; ++i)
+          if (!mbar_wait(&bars[kVFull + i % kVStages], (i / kVStages) & 1u)) report_error(p.err, kErrTimeoutDrain);
       }
     } else if (lane != 0) {
       // one thread per warp works in these
-    } else if (warp == 0) {
-      // ---------------- TMA producer of the K tiles
+    } else if (warp == 3) {
+      // ---------------- P V issuer: nothing between its waits but what it must decide; a
+      // flag read for every tile here cost 4 % of a 1024^2 image's time
+      const uint64_t vdesc0 = sw128_mnmajor_desc(smem_u32(sV), kBox, 1024);
       uint32_t t = 0;
+      uint32_t ku = 0, cleared = 0;
       bool ok = true;
       for (int u = blockIdx.x; ok && u < total; u += gridDim.x) {
         const Unit un = unit_of(p, u);
+        if (un.n == 0) continue;
+        ok = !*abort_flag;
+        if (!ok) break;
+        for (int j = 0; j < un.n; ++j, ++t) {
+          const uint32_t b = t & 1u;
+          const uint32_t st = t % kVStages;
+          ok = (j > 0 || ku == 0 || mbar_wait(&bars[kOEmpty], (ku - 1) & 1u)) &&
+               mbar_wait(&bars[kVFull + st], (t / kVStages) & 1u);
+          if (un.clear && j + 1 == un.n) {
+            ok = ok && mbar_wait(&bars[kVClean], cleared & 1u);
+            ++cleared;
+          }
+          if (!ok) break;
+          const uint64_t vd = vdesc0 + ((st * kTile) >> 4);
+          for (int h = 0; h < 2; ++h) {
+            ok = mbar_wait(&bars[kPFull + b * 2 + h], (t >> 1) & 1u);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mma_ts(tmem + kColO + 128u * h, tmem + kColP + b * 64 + h * 32 + k * 8,
+                     vd + ((static_cast<uint32_t>(4 * h + k) * 2048) >> 4), kIdescPV, (j > 0 || k > 0) ? 1u : 0u);
+            mma_commit(&bars[kPvDone + b * 2 + h]);
+          }
+          if (!ok) break;
+          mma_commit(&bars[kVEmpty + st]);
+        }
+        if (!ok) break;
+        mma_commit(&bars[kOFull]);
+        ++ku;
+      }
+      if (!ok && !*abort_flag) report_error(p.err, kErrTimeoutMma);
+      if (!ok) *abort_flag = 1;
+      mma_commit(&bars[kDrainPV]);
+      if (!mbar_wait(&bars[kDrainPV], 0)) report_error(p.err, kErrTimeoutDrain);
+    } else if (warp == 0) {
+      // ---------------- TMA producer of the K tiles and of each unit's Q rows
+      uint32_t t = 0;
+      uint32_t nq = 0;
+      bool ok = true;
+      for (int u = blockIdx.x; ok && u < total; u += gridDim.x) {
+        const Unit un = unit_of(p, u);
+        if (un.n == 0) continue;
+        const uint32_t qb = nq % kQBufs;
+        if (*abort_flag || !mbar_wait(&bars[kQEmpty + qb], ((nq / kQBufs) & 1u) ^ 1u)) {
+          if (!*abort_flag) report_error(p.err, kErrTimeoutProducer);
+          *abort_flag = 1;
+          break;
+        }
+        const CUtensorMap* mq = u < p.pl.units_p ? &tm.qp : &tm.qo;
+        mbar_arrive_expect_tx(&bars[kQFull + qb], static_cast<uint32_t>(un.rows) * 256u);  // whole boxes, also past the ends
+        tma_load_5d(sQ + qb * kTile, mq, &bars[kQFull + qb], 0, 0, un.h, un.t0, un.b0);
+        tma_load_5d(sQ + qb * kTile + kBox, mq, &bars[kQFull + qb], 64, 0, un.h, un.t0, un.b0);
+        ++nq;
         for (int j = 0; j < un.n; ++j, ++t) {
           const uint32_t st = t % kKStages;
           if (*abort_flag || !mbar_wait(&bars[kKEmpty + st], ((t / kKStages) & 1u) ^ 1u)) {
@@ -345,59 +427,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       for (uint32_t i = t > kKStages ? t - kKStages : 0; i < t; ++i)
         if (!mbar_wait(&bars[kKFull + i % kKStages], (i / kKStages) & 1u)) report_error(p.err, kErrTimeoutDrain);
-    } else if (warp == 2) {
-      // ---------------- TMA producer of the V tiles and of each unit's Q rows
-      uint32_t t = 0;
-      int nq = 0;
-      bool ok = true;
-      for (int u = blockIdx.x; ok && u < total; u += gridDim.x) {
-        const Unit un = unit_of(p, u);
-        if (un.n == 0) continue;
-        if (*abort_flag || (nq > 0 && !mbar_wait(&bars[kQEmpty], static_cast<uint32_t>(nq - 1) & 1u))) {
-          ok = false;
-          break;
-        }
-        const CUtensorMap* mq = u < p.pl.units_p ? &tm.qp : &tm.qo;
-        mbar_arrive_expect_tx(&bars[kQFull], static_cast<uint32_t>(un.rows) * 256u);  // the whole boxes, also past the ends
-        tma_load_5d(sQ, mq, &bars[kQFull], 0, 0, un.h, un.t0, un.b0);
-        tma_load_5d(sQ + kBox, mq, &bars[kQFull], 64, 0, un.h, un.t0, un.b0);
-        ++nq;
-        for (int j = 0; j < un.n; ++j, ++t) {
-          const uint32_t st = t % kVStages;
-          if (*abort_flag || !mbar_wait(&bars[kVEmpty + st], ((t / kVStages) & 1u) ^ 1u)) {
-            ok = false;
-            break;
-          }
-          const bool pre = j < un.pn;
-          const CUtensorMap* m = pre ? &tm.pv : &tm.v;
-          const int row = (pre ? un.p0 + j : un.o0 + j - un.pn) * kKeys;
-          const int bs = pre ? 0 : un.b0;
-          mbar_arrive_expect_tx(&bars[kVFull + st], kTile);
-          tma_load_4d(sV + st * kTile, m, &bars[kVFull + st], 0, un.h, row, bs);
-          tma_load_4d(sV + st * kTile + kBox, m, &bars[kVFull + st], 64, un.h, row, bs);
-        }
-      }
-      if (!ok) {
-        if (!*abort_flag) report_error(p.err, kErrTimeoutProducer);
-        *abort_flag = 1;
-      }
-      for (uint32_t i = t > kVStages ? t - kVStages : 0; i < t; ++i)
-        if (!mbar_wait(&bars[kVFull + i % kVStages], (i / kVStages) & 1u)) report_error(p.err, kErrTimeoutDrain);
-      if (nq > 0 && !mbar_wait(&bars[kQFull], static_cast<uint32_t>(nq - 1) & 1u))
-        report_error(p.err, kErrTimeoutDrain);
+      for (uint32_t i = nq > kQBufs ? nq - kQBufs : 0; i < nq; ++i)
+        if (!mbar_wait(&bars[kQFull + i % kQBufs], (i / kQBufs) & 1u)) report_error(p.err, kErrTimeoutDrain);
     } else {
       // ---------------- Q K^T issuer
-      const uint64_t qdesc = sw128_kmajor_desc(smem_u32(sQ));
+      const uint64_t qdesc0 = sw128_kmajor_desc(smem_u32(sQ));
       const uint64_t kdesc0 = sw128_kmajor_desc(smem_u32(sK));
       uint32_t t = 0;
-      int ku = 0;
+      uint32_t ku = 0;
       bool ok = true;
       for (int u = blockIdx.x; ok && u < total; u += gridDim.x) {
         const Unit un = unit_of(p, u);
         if (un.n == 0) continue;
-        ok = !*abort_flag && mbar_wait(&bars[kQFull], static_cast<uint32_t>(ku) & 1u);
+        const uint32_t qb = ku % kQBufs;
+        ok = !*abort_flag && mbar_wait(&bars[kQFull + qb], (ku / kQBufs) & 1u);
         if (!ok) break;
         tc_fence_after();
+        const uint64_t qdesc = qdesc0 + ((qb * kTile) >> 4);
         for (int j = 0; j < un.n; ++j, ++t) {
           const uint32_t st = t % kKStages;
           ok = (t < 1 || mbar_wait(&bars[kSFree], (t - 1) & 1u)) &&
@@ -414,7 +460,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           mma_commit(&bars[kKEmpty + st]);
         }
         if (!ok) break;
-        mma_commit(&bars[kQEmpty]);
+        mma_commit(&bars[kQEmpty + qb]);
         ++ku;
       }
       if (!ok) {
@@ -431,25 +477,43 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int h = warp >= 8 ? 1 : 0;
     const int quarter = warp & 3;
     const int rit = quarter * 32 + lane;
-    const int tok = rit / p.pl.G;  // the row's token within a joint / own block
+    const int tok = quot(p.d_G, rit);  // the row's token within a joint / own block
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t tO = tmem + lane_off + kColO + 128u * h;
     const uint64_t sc2 = f2_pack(scale_log2, scale_log2);
     uint32_t t = 0;
-    int ku = 0;
+    uint32_t ku = 0;
     bool ok = true;
     for (int u = blockIdx.x; u < total; u += gridDim.x) {
       if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
       const Unit un = unit_of(p, u);
       if (un.n == 0) continue;
       const int lim_own = own_lim(p, un.len, un.t0 + tok);
+      // A warp whose 32 rows lie past the block's has nothing to compute: it only keeps the
+      // barriers' counts (its lanes of S, P and O hold whatever they held). It still waits
+      // for every S, so it is never a phase ahead of the other warps on a P buffer.
+      const bool idle = quarter * 32 >= un.rows;
       float m_used = -INFINITY;
       float l = 0.f;
       for (int j = 0; j < un.n; ++j) {
         const uint32_t tt = t + j;
         const uint32_t b = tt & 1u;
+        const bool last = j + 1 == un.n;
         ok = __all_sync(0xffffffffu, mbar_wait(&bars[kSFull], tt & 1u));
         if (!ok) break;
+        if (idle) {
+          if (last) {
+            ok = __all_sync(0xffffffffu, mbar_wait(&bars[kLFree], (ku & 1u) ^ 1u));
+            if (!ok) break;
+          }
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&bars[kSFree]);
+            mbar_arrive(&bars[kPFull + b * 2 + h]);
+            if (last) mbar_arrive(&bars[kLFull]);
+          }
+          continue;
+        }
         tc_fence_after();
         uint32_t r[2][32];
         tmem_ld32(tmem + lane_off + kColS + h * 64, r[0]);
@@ -536,12 +600,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         l += ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]));
         tmem_st_wait();
         tc_fence_before();
-        const bool last = j + 1 == un.n;
         if (last) {
-          if (ku > 0) {
-            ok = __all_sync(0xffffffffu, mbar_wait(&bars[kOEmpty], static_cast<uint32_t>(ku - 1) & 1u));
-            if (!ok) break;
-          }
+          ok = __all_sync(0xffffffffu, mbar_wait(&bars[kLFree], (ku & 1u) ^ 1u));
+          if (!ok) break;
           lsum[h * kRows + rit] = l;
           msum[h * kRows + rit] = m_used;
         }
@@ -565,17 +626,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int quarter = warp & 3;
     const int rit = quarter * 32 + lane;
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
-    const int tok = rit / p.pl.G;
+    const int tok = quot(p.d_G, rit);
     const int g = rit - tok * p.pl.G;
     bool ok = true;
-    int ku = 0;
+    uint32_t ku = 0;
     for (int u = blockIdx.x; ok && u < total; u += gridDim.x) {
       if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
       const Unit un = unit_of(p, u);
       // where the row goes: token and sequence (a prefix block runs over sequences)
       int b = un.b0, tk = un.t0 + tok;
       if (u < p.pl.units_p) {
-        const int q = tok / p.T;
+        const int q = quot(p.d_T, tok);
         b += q;
         tk = tok - q * p.T;
       }
@@ -589,43 +650,65 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         continue;
       }
-      ok = __all_sync(0xffffffffu, mbar_wait(&bars[kOFull], static_cast<uint32_t>(ku) & 1u)) &&
-           __all_sync(0xffffffffu, mbar_wait(&bars[kLFull], static_cast<uint32_t>(ku) & 1u));
+      ok = __all_sync(0xffffffffu, mbar_wait(&bars[kLFull], ku & 1u));
       if (!ok) break;
-      tc_fence_after();
       const float m0 = msum[rit], m1 = msum[kRows + rit];
+      const float l0 = lsum[rit], l1 = lsum[kRows + rit];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[kLFree]);
       const float mm = fmaxf(m0, m1);
       // a half without a visible key has m = -inf and weight 0; in a row without one both
       // sums and O are 0 already (or NaN, if its scores are)
       const float a0 = mm == -INFINITY ? 1.f : fast_exp2(m0 - mm);
       const float a1 = mm == -INFINITY ? 1.f : fast_exp2(m1 - mm);
-      const float den = lsum[rit] * a0 + lsum[kRows + rit] * a1;
+      const float den = l0 * a0 + l1 * a1;
       const float inv = p.pl.split ? 1.f : (den == 0.f ? 0.f : 1.f / den);
       const float w0 = a0 * inv, w1 = a1 * inv;
       if (p.pl.split && mine) p.ml[un.slot + rit] = make_float2(mm, den);
-#pragma unroll 1
-      for (int c = 0; c < 4; ++c) {
-        uint32_t o0[32], o1[32];
-        tmem_ld32(tmem + lane_off + kColO + c * 32, o0);
-        tmem_ld32(tmem + lane_off + kColO + 128 + c * 32, o1);
+      ok = __all_sync(0xffffffffu, mbar_wait(&bars[kOFull], ku & 1u));
+      if (!ok) break;
+      if (quarter * 32 >= un.rows) {  // none of the warp's rows are the block's
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[kOEmpty]);
+        ++ku;
+        continue;
+      }
+      tc_fence_after();
+      // 16 columns of both halves at a time, the next ones loading while these are stored
+      const uint32_t tO = tmem + lane_off + kColO;
+      const uint64_t w00 = f2_pack(w0, w0), w11 = f2_pack(w1, w1);
+      uint32_t oa[2][16], ob[2][16];
+      tmem_ld16(tO, oa[0]);
+      tmem_ld16(tO + 128, ob[0]);
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
         tmem_ld_wait();
-        if (c == 3) {
+        if (c < 7) {
+          tmem_ld16(tO + (c + 1) * 16, oa[(c + 1) & 1]);
+          tmem_ld16(tO + 128 + (c + 1) * 16, ob[(c + 1) & 1]);
+        } else {
+          // O_0 and O_1 are in registers: the next unit's first P V may overwrite them
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&bars[kOEmpty]);
         }
+        const uint32_t* x = oa[c & 1];
+        const uint32_t* y = ob[c & 1];
         if (mine) {
-          float ov[32];
+          float ov[16];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) ov[i] = __uint_as_float(o0[i]) * w0 + __uint_as_float(o1[i]) * w1;
+          for (int i = 0; i < 8; ++i)
+            f2_unpack(fma_f32x2(f2_pack(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), w00,
+                                mul_f32x2(f2_pack(__uint_as_float(y[2 * i]), __uint_as_float(y[2 * i + 1])), w11)),
+                      ov[2 * i], ov[2 * i + 1]);
           if (p.pl.split) {
-            float4* d = reinterpret_cast<float4*>(p.part + (un.slot + rit) * kHeadDim + c * 32);
+            float4* d = reinterpret_cast<float4*>(p.part + (un.slot + rit) * kHeadDim + c * 16);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) d[i] = make_float4(ov[4 * i], ov[4 * i + 1], ov[4 * i + 2], ov[4 * i + 3]);
+            for (int i = 0; i < 4; ++i) d[i] = make_float4(ov[4 * i], ov[4 * i + 1], ov[4 * i + 2], ov[4 * i + 3]);
           } else {
-            uint4* d = reinterpret_cast<uint4*>(orow + c * 32);
+            uint4* d = reinterpret_cast<uint4*>(orow + c * 16);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 2; ++i)
               d[i] = make_uint4(pack16<BF16>(ov[8 * i], ov[8 * i + 1]), pack16<BF16>(ov[8 * i + 2], ov[8 * i + 3]),
                                 pack16<BF16>(ov[8 * i + 4], ov[8 * i + 5]), pack16<BF16>(ov[8 * i + 6], ov[8 * i + 7]));
           }
@@ -666,8 +749,9 @@ __global__ void __launch_bounds__(kMergeWarps * 32) merge_partials(const __grid_
   const int qb = t / pl.tb;
   const int len = own_len_of(p, b);
   const int ot = own_tiles(p, len, qb * pl.tb, pl.tb);
-  const int qpos = p.causal ? pl.nqb - 1 - qb : qb;
-  const long long unit_o = ((static_cast<long long>(h) * p.B + b) * pl.nqb + qpos) * pl.nch;
+  const long long hb = static_cast<long long>(h) * p.B + b;
+  const long long unit_o =
+      (pl.by_block ? (pl.nqb - 1 - qb) * static_cast<long long>(p.Hkv) * p.B + hb : hb * pl.nqb + qb) * pl.nch;
   const long long slot_o = static_cast<long long>(pl.units_p) * pl.rows_p + unit_o * pl.rows_o + (t - qb * pl.tb) * pl.G + g;
   const int parts_o = (ot + (pl.packed ? 0 : pl.pt) + pl.ct - 1) / pl.ct;
   long long slot_p = 0;
@@ -723,14 +807,28 @@ qi_status op_fail(qi_status st, const char* fmt, ...) {
 
 int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
+Div make_div(int d) {
+  uint32_t l = 0;
+  while ((1ull << l) < static_cast<unsigned long long>(d)) ++l;
+  const uint32_t s = 31 + l;
+  return {static_cast<uint32_t>(((1ull << s) + d - 1) / d), s, static_cast<uint32_t>(d)};
+}
+
 // Chooses the decomposition from sizes alone (own lengths, which only the device
 // knows, count as S). Time is counted in key tiles: a unit costs its tiles plus
 // kUnitTiles for its Q load, pipeline fill and epilogue, and splitting costs
 // kMergeTiles for the partials and the second launch.
 constexpr int kUnitTiles = 3;
 constexpr int kMergeTiles = 6;
-Plan make_plan(int B, int T, int Hq, int Hkv, int P, int S, int sms) {
+//
+// Order of the joint units: head-major, so that the CTAs running at one time share a few
+// heads' K/V in L2; with `causal`, whose units differ in length, last row blocks first
+// over all heads and sequences, so that the CTAs' sums of lengths agree (3 x 777 rows over
+// 2048 + 1201 keys, 4 key heads: %BYBLOCK%), as long as all K/V stay in half of the L2.
+constexpr long long kL2Half = 64ll << 20;
+Plan make_plan(int B, int T, int Hq, int Hkv, int P, int S, int causal, int sms) {
   Plan a{};
+  a.by_block = causal && (static_cast<long long>(B) * S + P) * Hkv * kHeadDim * 4 <= kL2Half;
   a.G = Hq / Hkv;
   a.tb = kRows / a.G < T ? kRows / a.G : T;
   a.nqb = ceil_div(T, a.tb);
@@ -759,9 +857,9 @@ Plan make_plan(int B, int T, int Hq, int Hkv, int P, int S, int sms) {
       best = c;
     }
   }
-  // packed: only if two or more sequences' rows fit one block and there are both kinds of keys
+  // packed: only if two or more sequences' rows fit one block
   const int rows_seq = T * a.G;
-  if (a.nqb == 1 && B > 1 && P > 0 && S > 0 && 2 * rows_seq <= kRows) {
+  if (a.nqb == 1 && B > 1 && P > 0 && 2 * rows_seq <= kRows) {
     Plan c = a;
     c.packed = 1;
     c.split = 1;
@@ -772,8 +870,8 @@ Plan make_plan(int B, int T, int Hq, int Hkv, int P, int S, int sms) {
     for (int ct = 1; ct <= most; ct += 1 + ct / 32) {
       c.ct = ct;
       c.nchp = ceil_div(a.pt, ct);
-      c.nch = ceil_div(a.ot, ct);
-      const long long up = static_cast<long long>(Hkv) * c.npb * c.nchp, uo = blocks * c.nch;
+      c.nch = a.ot ? ceil_div(a.ot, ct) : 1;
+      const long long up = static_cast<long long>(Hkv) * c.npb * c.nchp, uo = a.ot ? blocks * c.nch : 0;
       if (up + uo > INT_MAX / 2) continue;
       const long long tiles = static_cast<long long>(Hkv) * c.npb * a.pt + blocks * a.ot + (up + uo) * kUnitTiles;
       const long long cost = (tiles + sms - 1) / sms + ct / 2 + kMergeTiles;
@@ -885,7 +983,7 @@ extern "C" size_t qi_prefix_attention_workspace(const qi_prefix_attn* a) {
   if (check_sizes(a) != QI_OK) return 0;
   const int sms = sm_count();
   if (sms <= 0) return 0;
-  const Plan pl = make_plan(a->B, a->T, a->Hq, a->Hkv, a->P, a->S, sms);
+  const Plan pl = make_plan(a->B, a->T, a->Hq, a->Hkv, a->P, a->S, a->causal, sms);
   return ws_layout(pl, a->P, a->Hkv, a->P > 0 && a->pk8 != nullptr).total;
 }
 
@@ -920,7 +1018,7 @@ extern "C" qi_status qi_prefix_attention(const qi_prefix_attn* a, qi_stream_t st
     return op_fail(QI_ERR_INVALID_ARG, "qi_prefix_attention: the 8-bit prefix needs 16-byte aligned codes and 4-byte aligned scales");
   const int sms = sm_count();
   if (sms <= 0) return op_fail(QI_ERR_CUDA, "qi_prefix_attention: no CUDA device");
-  const Plan pl = make_plan(a->B, a->T, a->Hq, a->Hkv, a->P, a->S, sms);
+  const Plan pl = make_plan(a->B, a->T, a->Hq, a->Hkv, a->P, a->S, a->causal, sms);
   if (pl.units <= 0) return op_fail(QI_ERR_SHAPE, "qi_prefix_attention: too many rows and heads");
   const bool pre8 = a->P > 0 && from8;
   const WsLayout w = ws_layout(pl, a->P, a->Hkv, pre8);
@@ -955,6 +1053,14 @@ extern "C" qi_status qi_prefix_attention(const qi_prefix_attn* a, qi_stream_t st
   if (a->S == 0) tm.k = tm.pk, tm.v = tm.pv;
   Params p{};
   p.pl = pl;
+  p.d_nch = make_div(pl.nch);
+  p.d_nchp = make_div(pl.packed ? pl.nchp : 1);
+  p.d_nqb = make_div(pl.nqb);
+  p.d_npb = make_div(pl.packed ? pl.npb : 1);
+  p.d_B = make_div(a->B);
+  p.d_hb = make_div(a->Hkv * a->B);
+  p.d_G = make_div(pl.G);
+  p.d_T = make_div(a->T);
   p.B = a->B;
   p.T = a->T;
   p.Hq = a->Hq;
