@@ -16,17 +16,11 @@ namespace {
 
 // ---------------------------------------------------------------- values
 
+// 8 values of a 16-bit type from 16 bytes
 template <typename T>
-__device__ __forceinline__ void load8(const T* src, float (&v)[8]);
+__device__ __forceinline__ void unpack8(uint4 w, float (&v)[8]);
 template <>
-__device__ __forceinline__ void load8(const float* src, float (&v)[8]) {
-  const float4 a = reinterpret_cast<const float4*>(src)[0], b = reinterpret_cast<const float4*>(src)[1];
-  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-  v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-}
-template <>
-__device__ __forceinline__ void load8(const __half* src, float (&v)[8]) {
-  const uint4 w = *reinterpret_cast<const uint4*>(src);
+__device__ __forceinline__ void unpack8<__half>(uint4 w, float (&v)[8]) {
   const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -36,14 +30,23 @@ __device__ __forceinline__ void load8(const __half* src, float (&v)[8]) {
   }
 }
 template <>
-__device__ __forceinline__ void load8(const __nv_bfloat16* src, float (&v)[8]) {
-  const uint4 w = *reinterpret_cast<const uint4*>(src);
+__device__ __forceinline__ void unpack8<__nv_bfloat16>(uint4 w, float (&v)[8]) {
   const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     v[2 * i] = __uint_as_float(u[i] << 16);
     v[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
   }
+}
+template <typename T>
+__device__ __forceinline__ void load8(const T* src, float (&v)[8]) {
+  unpack8<T>(*reinterpret_cast<const uint4*>(src), v);
+}
+template <>
+__device__ __forceinline__ void load8(const float* src, float (&v)[8]) {
+  const float4 a = reinterpret_cast<const float4*>(src)[0], b = reinterpret_cast<const float4*>(src)[1];
+  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+  v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
 }
 
 // Stores 8 values in T and leaves in v what was stored.
@@ -72,58 +75,145 @@ __device__ __forceinline__ void round8(const __nv_bfloat16*, float (&v)[8]) {
   for (int i = 0; i < 8; ++i) v[i] = __bfloat162float(__float2bfloat16_rn(v[i]));
 }
 
-// MXFP8 of a block of 32 values held by four neighbouring lanes (8 each): this lane's 8
-// codes, and the block's scale byte. Same definition as mx_quant32; the scaling by a power
-// of two is exact, so the only rounding is the one to E4M3 (nearest, ties to even).
-__device__ __forceinline__ uint2 mx_quant8(const float (&v)[8], uint32_t& scale) {
-  float top = 0.f;
+// 2^n for -127 <= n <= 128 (2^128 = inf)
+__device__ __forceinline__ float pow2(int n) {
+  return __uint_as_float(n == -127 ? 0x00400000u : static_cast<uint32_t>(n + 127) << 23);
+}
+
+// The shared exponent of a block by its largest magnitude: floor(log2 top) - 8 from the exponent
+// field; below 2^-119 (zero and subnormals among it) it clamps to -127; an infinity takes 127,
+// as in mx_quant32.
+__device__ __forceinline__ int mx_exponent(float top) {
+  const int field = static_cast<int>(__float_as_uint(top) >> 23);
+  return field == 255 ? 127 : max(field - 135, -127);
+}
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+  return lo | (hi << 16);
+}
+
+// The largest magnitude of 16 packed values, in fp32 (NaNs are passed over)
+__device__ __forceinline__ float absmax16(const uint32_t (&u)[8], const __half*) {
+  __half2 m = __habs2(*reinterpret_cast<const __half2*>(&u[0]));
+#pragma unroll
+  for (int i = 1; i < 8; ++i) m = __hmax2(m, __habs2(*reinterpret_cast<const __half2*>(&u[i])));
+  return __half2float(__hmax(__low2half(m), __high2half(m)));
+}
+__device__ __forceinline__ float absmax16(const uint32_t (&u)[8], const __nv_bfloat16*) {
+  __nv_bfloat162 m = __habs2(*reinterpret_cast<const __nv_bfloat162*>(&u[0]));
+#pragma unroll
+  for (int i = 1; i < 8; ++i) m = __hmax2(m, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&u[i])));
+  return __bfloat162float(__hmax(__low2bfloat16(m), __high2bfloat16(m)));
+}
+
+// MXFP8 of a block of 32 values held by two neighbouring lanes (16 each): this lane's 16 codes
+// and the block's scale byte. Same definition as mx_quant32; the scaling by a power of two is
+// exact, so the only rounding is the one to E4M3 (nearest, ties to even).
+template <typename T>
+__device__ __forceinline__ uint4 mx_quant16(uint4 a, uint4 b, uint32_t& scale) {
+  const uint32_t u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  float top = absmax16(u, static_cast<const T*>(nullptr));
+  top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+  const int e = mx_exponent(top);
+  const float inv = pow2(-e);
+  float v[16];
+  unpack8<T>(a, *reinterpret_cast<float(*)[8]>(v));
+  unpack8<T>(b, *reinterpret_cast<float(*)[8]>(v + 8));
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] *= inv;
+  scale = static_cast<uint32_t>(e + 127);
+  return make_uint4(e4m3x4(v[0], v[1], v[2], v[3]), e4m3x4(v[4], v[5], v[6], v[7]), e4m3x4(v[8], v[9], v[10], v[11]),
+                    e4m3x4(v[12], v[13], v[14], v[15]));
+}
+
+// The exponent of a block of 32 values held by four neighbouring lanes (8 each)
+__device__ __forceinline__ int mx_exponent8(const float (&v)[8], float& top) {
+  top = 0.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(v[i]));
   top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
   top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-  int e = top > 0.f ? ilogbf(top) - 8 : -127;
-  e = max(-127, min(127, e));
-  const float inv = ldexpf(1.f, -e);
-  uint32_t c[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    c[i] = __nv_cvt_float2_to_fp8x2(make_float2(v[2 * i] * inv, v[2 * i + 1] * inv), __NV_SATFINITE, __NV_E4M3);
-  scale = static_cast<uint32_t>(e + 127);
-  return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+  return mx_exponent(top);
 }
 
 // ---------------------------------------------------------------- 8-bit K/V cache
 
 constexpr int kKv8Threads = 256;
+// Groups of K and of V per thread, a block's width apart: all their loads are issued before
+// the first is used, so that a warp's loads cover HBM's latency.
+constexpr int kKv8Groups = 2;       // write: 16 values each, 128 bytes in flight per thread
+constexpr int kKv8ReadGroups = 4;   // read: 8 codes each
 
-// Thread = 8 values of one (row, head) of K and the same of V; blockIdx.y strides over sequences.
+// Item i of a sequence, items being a head's 128 values in `1 << LOG` parts: row, head, part, and
+// the cache row of the row, or -1 if it is passed over.
+struct Kv8At {
+  int t, h, part, row;
+};
+template <int LOG>
+__device__ __forceinline__ Kv8At kv8_at(const Kv8Args& a, int i, int n, int pos) {
+  Kv8At x;
+  const int th = i >> LOG;
+  x.part = i & ((1 << LOG) - 1);
+  x.t = quot(a.d_H, th);
+  x.h = th - x.t * a.H;
+  // (pos + t wraps only where pos alone is past any cache, and then to a negative row)
+  const int row = static_cast<int>(static_cast<uint32_t>(pos) + static_cast<uint32_t>(x.t));
+  x.row = x.t < n && row >= 0 && row < a.S ? row : -1;
+  return x;
+}
+__device__ __forceinline__ long long kv8_offset(const qi_tensor4& t, const Kv8At& x) {
+  return x.t * t.row + x.h * t.head;
+}
+
+// Thread = kKv8Groups groups of 16 values of one (row, head) of K and the same of V; two lanes
+// share a scale. Bound by the ALU pipe and HBM together: 17.7 instructions a value with groups
+// of 8 and the position worked out for each, %KV8W% now (16 prompts of up to 2048 rows, 8 heads).
 template <typename T>
 __global__ void __launch_bounds__(kKv8Threads) kv8_write_kernel(const __grid_constant__ Kv8Args a) {
   grid_dep_wait();
   grid_dep_launch_dependents();
-  const uint32_t i = blockIdx.x * kKv8Threads + threadIdx.x;
-  const uint32_t part = i & 15u, th = i >> 4;
-  const int t = static_cast<int>(th / static_cast<uint32_t>(a.H));
-  const int h = static_cast<int>(th - static_cast<uint32_t>(t) * a.H);
-  for (int b = blockIdx.y; b < a.B; b += gridDim.y) {
-    const int n = a.lens ? min(a.lens[b], a.T) : a.T;
-    const long long row = static_cast<long long>(a.pos ? a.pos[b] : 0) + t;
-    const bool in = t < n && row >= 0 && row < a.S;
-    // (the four lanes of a scale block share a row, so they are in or out together)
-    float kv[8] = {}, vv[8] = {};
-    if (in) {
-      load8(static_cast<const T*>(a.k.data) + b * a.k.batch + t * a.k.row + h * a.k.head + part * 8, kv);
-      load8(static_cast<const T*>(a.v.data) + b * a.v.batch + t * a.v.row + h * a.v.head + part * 8, vv);
+  const int b = blockIdx.y;
+  const int n = a.lens ? min(a.lens[b], a.T) : a.T;
+  const int pos = a.pos ? a.pos[b] : 0;
+  const T* kb = static_cast<const T*>(a.k.data) + b * a.k.batch;
+  const T* vb = static_cast<const T*>(a.v.data) + b * a.v.batch;
+  const int i0 = static_cast<int>(blockIdx.x) * (kKv8Threads * kKv8Groups) + threadIdx.x;
+  uint4 w[kKv8Groups][4];
+  Kv8At at[kKv8Groups];
+#pragma unroll
+  for (int u = 0; u < kKv8Groups; ++u) {
+    const Kv8At x = at[u] = kv8_at<3>(a, i0 + u * kKv8Threads, n, pos);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[u][j] = make_uint4(0u, 0u, 0u, 0u);
+    if (x.row >= 0) {
+      const uint4* ks = reinterpret_cast<const uint4*>(kb + kv8_offset(a.k, x) + x.part * 16);
+      const uint4* vs = reinterpret_cast<const uint4*>(vb + kv8_offset(a.v, x) + x.part * 16);
+      w[u][0] = ks[0];
+      w[u][1] = ks[1];
+      w[u][2] = vs[0];
+      w[u][3] = vs[1];
     }
-    uint32_t ks, vs;
-    const uint2 kc = mx_quant8(kv, ks), vc = mx_quant8(vv, vs);
-    if (in) {
-      const long long at = (static_cast<long long>(b) * a.S + row) * a.H + h;
-      reinterpret_cast<uint2*>(a.k8 + at * kHeadDim)[part] = kc;
-      reinterpret_cast<uint2*>(a.v8 + at * kHeadDim)[part] = vc;
-      if ((part & 3u) == 0) {
-        a.k_sf[at * 4 + part / 4] = static_cast<uint8_t>(ks);
-        a.v_sf[at * 4 + part / 4] = static_cast<uint8_t>(vs);
+  }
+#pragma unroll
+  for (int u = 0; u < kKv8Groups; ++u) {
+    uint4 codes[2];
+    uint32_t sf[2];
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      codes[c] = mx_quant16<T>(w[u][2 * c], w[u][2 * c + 1], sf[c]);
+      // the head's four scale bytes come together in its first lane
+      sf[c] |= __shfl_down_sync(0xffffffffu, sf[c], 2) << 8;
+      sf[c] |= __shfl_down_sync(0xffffffffu, sf[c], 4) << 16;
+    }
+    // (a head's eight lanes are in or out together)
+    if (at[u].row >= 0) {
+      const long long o = (static_cast<long long>(b) * a.S + at[u].row) * a.H + at[u].h;
+      reinterpret_cast<uint4*>(a.k8 + o * kHeadDim)[at[u].part] = codes[0];
+      reinterpret_cast<uint4*>(a.v8 + o * kHeadDim)[at[u].part] = codes[1];
+      if (at[u].part == 0) {
+        reinterpret_cast<uint32_t*>(a.k_sf)[o] = sf[0];
+        reinterpret_cast<uint32_t*>(a.v_sf)[o] = sf[1];
       }
     }
   }
@@ -131,7 +221,7 @@ __global__ void __launch_bounds__(kKv8Threads) kv8_write_kernel(const __grid_con
 
 // 8 codes times their scale, in fp32 (exact: 4 significant bits times a power of two)
 __device__ __forceinline__ void mx_values8(uint2 c, uint32_t scale, float (&v)[8]) {
-  const float s = ldexpf(1.f, static_cast<int>(scale) - 127);
+  const float s = pow2(static_cast<int>(scale) - 127);
   const uint32_t w[4] = {c.x & 0xFFFFu, c.x >> 16, c.y & 0xFFFFu, c.y >> 16};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -142,40 +232,58 @@ __device__ __forceinline__ void mx_values8(uint2 c, uint32_t scale, float (&v)[8
   }
 }
 
+// Bound by HBM: 4 prompts of 1999 rows of 32 heads in %KV8R%.
 template <typename T>
 __global__ void __launch_bounds__(kKv8Threads) kv8_read_kernel(const __grid_constant__ Kv8Args a) {
   grid_dep_wait();
   grid_dep_launch_dependents();
-  const uint32_t i = blockIdx.x * kKv8Threads + threadIdx.x;
-  const uint32_t part = i & 15u, th = i >> 4;
-  const int t = static_cast<int>(th / static_cast<uint32_t>(a.H));
-  const int h = static_cast<int>(th - static_cast<uint32_t>(t) * a.H);
-  for (int b = blockIdx.y; b < a.B; b += gridDim.y) {
-    const int n = a.lens ? min(a.lens[b], a.T) : a.T;
-    const long long row = static_cast<long long>(a.pos ? a.pos[b] : 0) + t;
-    if (t >= n || row < 0 || row >= a.S) continue;
-    const long long at = (static_cast<long long>(b) * a.S + row) * a.H + h;
-    const uint2 kc = reinterpret_cast<const uint2*>(a.k8 + at * kHeadDim)[part];
-    const uint2 vc = reinterpret_cast<const uint2*>(a.v8 + at * kHeadDim)[part];
+  const int b = blockIdx.y;
+  const int n = a.lens ? min(a.lens[b], a.T) : a.T;
+  const int pos = a.pos ? a.pos[b] : 0;
+  T* kb = static_cast<T*>(const_cast<void*>(a.k.data)) + b * a.k.batch;
+  T* vb = static_cast<T*>(const_cast<void*>(a.v.data)) + b * a.v.batch;
+  const int i0 = static_cast<int>(blockIdx.x) * (kKv8Threads * kKv8ReadGroups) + threadIdx.x;
+  uint2 kc[kKv8ReadGroups], vc[kKv8ReadGroups];
+  uint32_t ks[kKv8ReadGroups], vs[kKv8ReadGroups];
+  Kv8At at[kKv8ReadGroups];
+#pragma unroll
+  for (int u = 0; u < kKv8ReadGroups; ++u) {
+    const Kv8At x = at[u] = kv8_at<4>(a, i0 + u * kKv8Threads, n, pos);
+    if (x.row >= 0) {
+      const long long o = (static_cast<long long>(b) * a.S + x.row) * a.H + x.h;
+      kc[u] = reinterpret_cast<const uint2*>(a.k8 + o * kHeadDim)[x.part];
+      vc[u] = reinterpret_cast<const uint2*>(a.v8 + o * kHeadDim)[x.part];
+      ks[u] = a.k_sf[o * 4 + x.part / 4];
+      vs[u] = a.v_sf[o * 4 + x.part / 4];
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < kKv8ReadGroups; ++u) {
+    if (at[u].row < 0) continue;
     float kv[8], vv[8];
-    mx_values8(kc, a.k_sf[at * 4 + part / 4], kv);
-    mx_values8(vc, a.v_sf[at * 4 + part / 4], vv);
-    store8(static_cast<T*>(const_cast<void*>(a.k.data)) + b * a.k.batch + t * a.k.row + h * a.k.head + part * 8, kv);
-    store8(static_cast<T*>(const_cast<void*>(a.v.data)) + b * a.v.batch + t * a.v.row + h * a.v.head + part * 8, vv);
+    mx_values8(kc[u], ks[u], kv);
+    mx_values8(vc[u], vs[u], vv);
+    store8(kb + kv8_offset(a.k, at[u]) + at[u].part * 8, kv);
+    store8(vb + kv8_offset(a.v, at[u]) + at[u].part * 8, vv);
   }
 }
 
-cudaError_t launch_kv8(void (*kernel)(Kv8Args), const Kv8Args& a, cudaStream_t s) {
-  const unsigned x = static_cast<unsigned>((static_cast<long long>(a.T) * a.H * 16 + kKv8Threads - 1) / kKv8Threads);
+cudaError_t launch_kv8(void (*kernel)(Kv8Args), Kv8Args a, int parts, int per_block, cudaStream_t s) {
+  a.d_H = make_div(a.H);
+  const unsigned x = static_cast<unsigned>((static_cast<long long>(a.T) * a.H * parts + per_block - 1) / per_block);
   return launch_dependent(kernel, dim3(x, static_cast<unsigned>(a.B)), dim3(kKv8Threads), 0, s, a);
 }
 
 // ---------------------------------------------------------------- residual RMSNorm to MXFP8
 
 // An fp32 value with an error term: hi + lo. Sums and products that keep the rounding
-// error of each fp32 operation (Knuth's two-sum, the FMA remainder of a product), so that
-// y is rounded to fp32 once and a code differs from the exact one only where the exact
-// value lies within an fp32 half step of a border between two codes.
+// error of each fp32 operation (Knuth's two-sum, the FMA remainder of a product).
+// Where it matters (a value next to a border between two codes, see below) y keeps its error
+// term up to the quantiser and is then rounded to odd (the last bit set if anything was lost),
+// which makes the rounding to E4M3, and the block's exponent, those of the unrounded value:
+// codes differ from the exact ones only by the error of the mean square. That is summed in
+// plain fp32 within a thread (its up to 64 roundings are unbiased and there are hundreds of
+// threads) and with error terms across threads, so it is off by about 2^-27.
 struct F2 {
   float hi, lo;
 };
@@ -199,6 +307,17 @@ __device__ __forceinline__ F2 inv_sqrt(F2 m) {
   return {r, isfinite(c) ? c : 0.f};
 }
 
+// hi + lo (hi its nearest fp32) as the fp32 value between which and the exact one no other lies,
+// with an odd last bit unless it is exact
+__device__ __forceinline__ float round_odd(F2 x) {
+  const uint32_t b = __float_as_uint(x.hi);
+  // toward lo: away from zero if the signs agree (hi is not zero where lo is not)
+  const uint32_t step = ((__float_as_uint(x.lo) ^ b) >> 31) ? 0xFFFFFFFFu : 1u;
+  return __uint_as_float(x.lo == 0.f || (b & 1u) ? b : b + step);
+}
+
+constexpr uint32_t kNear = 16;  // fp32 steps around a border
+
 struct NormParams {
   qi_add_rmsnorm a;
   int groups;  // ceil(rows / 128)
@@ -214,7 +333,7 @@ __global__ void add_rmsnorm_kernel(const __grid_constant__ NormParams p) {
   const int r = blockIdx.x;
   const int groups8 = a.K / 8;
   float v[NC][8];
-  F2 sum = {0.f, 0.f};
+  float sq[4] = {};
 #pragma unroll
   for (int i = 0; i < NC; ++i) {
     const int c = threadIdx.x + i * blockDim.x;
@@ -232,11 +351,9 @@ __global__ void add_rmsnorm_kernel(const __grid_constant__ NormParams p) {
       if (a.x_out) store8(static_cast<TX*>(a.x_out) + r * a.x_out_stride + c * 8, v[i]);
     }
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const float sq = __fmul_rn(v[i][k], v[i][k]);
-      sum = add(sum, F2{sq, __fmaf_rn(v[i][k], v[i][k], -sq)});
-    }
+    for (int k = 0; k < 8; ++k) sq[k & 3] = __fmaf_rn(v[i][k], v[i][k], sq[k & 3]);
   }
+  F2 sum = add(two_sum(sq[0], sq[1]), two_sum(sq[2], sq[3]));
 #pragma unroll
   for (int d = 16; d; d >>= 1)
     sum = add(sum, F2{__shfl_xor_sync(0xffffffffu, sum.hi, d), __shfl_xor_sync(0xffffffffu, sum.lo, d)});
@@ -250,40 +367,63 @@ __global__ void add_rmsnorm_kernel(const __grid_constant__ NormParams p) {
   const float mh = __fdiv_rn(sum.hi, n);
   const F2 m = add(F2{mh, __fdiv_rn(__fmaf_rn(-mh, n, sum.hi) + sum.lo, n)}, F2{a.eps, 0.f});
   const F2 rs = inv_sqrt(m);
+  const float r1 = rs.hi + rs.lo;
 #pragma unroll
   for (int i = 0; i < NC; ++i) {
     const int c = threadIdx.x + i * blockDim.x;
     const bool in = c < groups8;  // groups8 is a multiple of 16: the lanes of a scale block agree
-    float g[8], gl[8];
+    float g[8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) g[k] = 1.f, gl[k] = 0.f;
+    for (int k = 0; k < 8; ++k) g[k] = 1.f;
     if (in && a.w) {
       if (a.w_f32)
         load8(static_cast<const float*>(a.w) + c * 8, g);
       else
         load8(static_cast<const __nv_bfloat16*>(a.w) + c * 8, g);
-      if (a.plus_one) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const F2 s = two_sum(1.f, g[k]);
-          g[k] = s.hi;
-          gl[k] = s.lo;
-        }
-      }
     }
-    float y[8];
+    const bool one = a.w && a.plus_one;
+    // y in fp32: three roundings (r1, the two products; a fourth in 1 + w), at most 4 half
+    // steps and 2^-27 of the statistics off, that is within kNear steps with room to spare
+    float y[8], top;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) y[k] = v[i][k] * r1 * (one ? 1.f + g[k] : g[k]);
+    int e = mx_exponent8(y, top);
+    float inv = pow2(-e);
+    // Borders: a scaled value of 2^-6 and more lies between two codes where the 20 bits below
+    // its three leading fraction bits are 80000h; below 2^-6 the codes are evenly spaced and no
+    // bit pattern tells, so those (one in 10^4) count as near. The exponent's border is a power
+    // of two. If any lane is near one, the warp takes the sums with error terms.
+    uint32_t near = 0xFFFFFu;
+    float least = 1.f;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      const float q = __fmul_rn(v[i][k], rs.hi);
-      const float qe = __fmaf_rn(v[i][k], rs.hi, -q) + v[i][k] * rs.lo;
-      const float z = __fmul_rn(q, g[k]);
-      y[k] = z + (__fmaf_rn(q, g[k], -z) + (qe * g[k] + q * gl[k]));
+      const float s = y[k] * inv;
+      near = min(near, (__float_as_uint(s) - 0x80000u + kNear) & 0xFFFFFu);
+      least = fminf(least, fabsf(s));
     }
-    uint32_t scale;
-    const uint2 codes = mx_quant8(y, scale);
+    const bool edge = near <= 2 * kNear || least < 0x1p-6f ||
+                      ((__float_as_uint(top) + kNear) & 0x7FFFFFu) <= 2 * kNear;
+    if (__any_sync(0xffffffffu, edge && in)) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const F2 h = one ? two_sum(1.f, g[k]) : F2{g[k], 0.f};
+        const float q = __fmul_rn(v[i][k], rs.hi);
+        const float qe = __fmaf_rn(v[i][k], rs.hi, -q) + v[i][k] * rs.lo;
+        const float z = __fmul_rn(q, h.hi);
+        y[k] = round_odd(two_sum(z, __fmaf_rn(q, h.hi, -z) + (qe * h.hi + q * h.lo)));
+      }
+      e = mx_exponent8(y, top);
+      inv = pow2(-e);
+    }
+    // the four scale bytes of 128 columns are neighbours: they come together in the first lane
+    uint32_t scale = static_cast<uint32_t>(e + 127);
+    scale |= __shfl_down_sync(0xffffffffu, scale, 4) << 8;
+    scale |= __shfl_down_sync(0xffffffffu, scale, 8) << 16;
     if (in) {
-      reinterpret_cast<uint2*>(a.q + static_cast<size_t>(r) * a.K)[c] = codes;
-      if ((c & 3) == 0) a.sf[mx_sf_offset(r, c / 4, p.groups)] = static_cast<uint8_t>(scale);
+      reinterpret_cast<uint2*>(a.q + r * static_cast<size_t>(a.K))[c] =
+          make_uint2(e4m3x4(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv),
+                     e4m3x4(y[4] * inv, y[5] * inv, y[6] * inv, y[7] * inv));
+      if ((c & 15) == 0) *reinterpret_cast<uint32_t*>(a.sf + mx_sf_offset(r, c / 4, p.groups)) = scale;
     }
   }
 }
@@ -361,10 +501,12 @@ qi_status kv8_call(const char* name, int dtype, int B, int T, int S, int H, cons
 }  // namespace
 
 cudaError_t launch_kv8_write(const Kv8Args& a, bool bf16, cudaStream_t s) {
-  return launch_kv8(bf16 ? kv8_write_kernel<__nv_bfloat16> : kv8_write_kernel<__half>, a, s);
+  return launch_kv8(bf16 ? kv8_write_kernel<__nv_bfloat16> : kv8_write_kernel<__half>, a, 8, kKv8Threads * kKv8Groups,
+                    s);
 }
 cudaError_t launch_kv8_read(const Kv8Args& a, bool bf16, cudaStream_t s) {
-  return launch_kv8(bf16 ? kv8_read_kernel<__nv_bfloat16> : kv8_read_kernel<__half>, a, s);
+  return launch_kv8(bf16 ? kv8_read_kernel<__nv_bfloat16> : kv8_read_kernel<__half>, a, 16,
+                    kKv8Threads * kKv8ReadGroups, s);
 }
 
 }  // namespace qi

@@ -193,6 +193,23 @@ bool encode_map16(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols
 bool encode_map16_nd(CUtensorMap* m, const void* base, int rank, const unsigned long long* dims,
                      const unsigned long long* strides, const unsigned* box);
 
+// n / d for 0 <= n < 2^31 as one widening product: m = ceil(2^s / d) with s = 31 +
+// ceil(log2 d) is too large by less than 1, which moves the quotient by less than n / 2^s <=
+// 1 / d, too little to reach the next one. (In the attention kernel every role works out every
+// unit it meets; with the compiler's division that took each of them about 1200 cycles a unit.)
+struct Div {
+  uint32_t m, s, d;
+};
+inline Div make_div(int d) {
+  uint32_t l = 0;
+  while ((1ull << l) < static_cast<unsigned long long>(d)) ++l;
+  const uint32_t s = 31 + l;
+  return {static_cast<uint32_t>(((1ull << s) + d - 1) / d), s, static_cast<uint32_t>(d)};
+}
+__device__ __forceinline__ int quot(const Div& v, int n) {
+  return static_cast<int>((static_cast<unsigned long long>(static_cast<uint32_t>(n)) * v.m) >> v.s);
+}
+
 // 8-bit K/V cache (batch_ops.cu): rows t < lens[b] of k and v [B, T, H, 128] (16 bits, element
 // strides) against rows pos[b] + t of the cache [B, S, H, 128] codes and [B, S, H, 4] scales;
 // rows outside 0 .. S-1 are passed over. pos NULL: 0; lens NULL: T.
@@ -205,6 +222,7 @@ struct Kv8Args {
   uint8_t* v_sf;
   const int* pos;
   const int* lens;
+  Div d_H;  // set by the launcher
 };
 cudaError_t launch_kv8_write(const Kv8Args& a, bool bf16, cudaStream_t s);
 cudaError_t launch_kv8_read(const Kv8Args& a, bool bf16, cudaStream_t s);

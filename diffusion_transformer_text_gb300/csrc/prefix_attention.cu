@@ -90,17 +90,6 @@ __device__ __forceinline__ uint32_t bar_count(int i) {
 constexpr int kSmem = (kQBufs + kKStages + kVStages) * kTile + 1024 + kNumBars * 8 + 16 + 2 * 2 * kRows * 4;
 static_assert(kSmem <= 227 * 1024, "shared memory over the per-block limit");
 
-// n / d for 0 <= n < 2^31 as one widening product: m = ceil(2^s / d) with s = 31 +
-// ceil(log2 d) errs by less than 2^(s - 31) d / d, too little to reach the next quotient.
-// (Every role works out every unit it meets; with the compiler's division that took each
-// of them about 1200 cycles a unit, more than a key tile's products.)
-struct Div {
-  uint32_t m, s, d;
-};
-__device__ __forceinline__ int quot(const Div& v, int n) {
-  return static_cast<int>((static_cast<unsigned long long>(static_cast<uint32_t>(n)) * v.m) >> v.s);
-}
-
 // The decomposition, decided on the host from sizes alone.
 struct Plan {
   int G;          // query heads per key head
@@ -123,7 +112,8 @@ struct Plan {
 
 struct Params {
   Plan pl;
-  Div d_nch, d_nchp, d_nqb, d_npb, d_B, d_hb, d_G, d_T;  // divisors: the plan's, B, Hkv B, G, T
+  Div d_nch, d_nchp, d_nqb, d_npb, d_tb, d_rb, d_ct;  // divisors: the plan's,
+  Div d_B, d_hb, d_G, d_T, d_Hq;                      // B, Hkv B, G, T, Hq
   int B, T, Hq, Hkv, P, S, causal;
   const int* own_len;
   uint16_t* o;
@@ -730,63 +720,83 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// One warp per output row: joins the row's partials (prefix chunks in order, then own
-// chunks) by their maxima and sums. Chunks without a tile were not written; they are
-// told from the lengths, as the units told them.
-constexpr int kMergeWarps = 4;
-template <bool BF16>
+// Joins an output row's partials (prefix chunks in order, then own chunks) by their maxima
+// and sums: kMergeWarps / W rows per block, W warps per row. Warp w of a row takes parts w,
+// w + W, ...; the W sums are added in order. Chunks without a tile were not written; they are
+// told from the lengths, as the units told them. What comes before the wait reads only what
+// was complete before the attention kernel began.
+constexpr int kMergeWarps = 8;
+template <bool BF16, int W>
 __global__ void __launch_bounds__(kMergeWarps * 32) merge_partials(const __grid_constant__ Params p) {
-  grid_dep_wait();
-  grid_dep_launch_dependents();
+  __shared__ float4 sacc[kMergeWarps][32];
+  __shared__ float sden[kMergeWarps];
   const Plan& pl = p.pl;
-  const int lane = threadIdx.x & 31;
-  const long long row = static_cast<long long>(blockIdx.x) * kMergeWarps + (threadIdx.x >> 5);
-  if (row >= static_cast<long long>(p.B) * p.T * p.Hq) return;
-  const int hq = static_cast<int>(row % p.Hq);
-  const long long bt = row / p.Hq;
-  const int b = static_cast<int>(bt / p.T), t = static_cast<int>(bt - static_cast<long long>(b) * p.T);
-  const int h = hq / pl.G, g = hq - h * pl.G;
-  const int qb = t / pl.tb;
-  const int len = own_len_of(p, b);
-  const int ot = own_tiles(p, len, qb * pl.tb, pl.tb);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int w = warp % W;
+  const long long row = static_cast<long long>(blockIdx.x) * (kMergeWarps / W) + warp / W;
+  const bool in = row < static_cast<long long>(p.B) * p.T * p.Hq;  // below 2^31
+  const int r = in ? static_cast<int>(row) : 0;
+  const int bt = quot(p.d_Hq, r), hq = r - bt * p.Hq;
+  const int b = quot(p.d_T, bt), t = bt - b * p.T;
+  const int h = quot(p.d_G, hq), g = hq - h * pl.G;
+  const int qb = quot(p.d_tb, t);
+  const int ot = own_tiles(p, own_len_of(p, b), qb * pl.tb, pl.tb);
   const long long hb = static_cast<long long>(h) * p.B + b;
   const long long unit_o =
       (pl.by_block ? (pl.nqb - 1 - qb) * static_cast<long long>(p.Hkv) * p.B + hb : hb * pl.nqb + qb) * pl.nch;
-  const long long slot_o = static_cast<long long>(pl.units_p) * pl.rows_p + unit_o * pl.rows_o + (t - qb * pl.tb) * pl.G + g;
-  const int parts_o = (ot + (pl.packed ? 0 : pl.pt) + pl.ct - 1) / pl.ct;
+  const long long slot_o =
+      static_cast<long long>(pl.units_p) * pl.rows_p + unit_o * pl.rows_o + (t - qb * pl.tb) * pl.G + g;
+  const int parts_o = quot(p.d_ct, ot + (pl.packed ? 0 : pl.pt) + pl.ct - 1);
   long long slot_p = 0;
   int parts_p = 0;
   if (pl.packed) {
-    const int pb = b / pl.rb;
+    const int pb = quot(p.d_rb, b);
     slot_p = (static_cast<long long>(h) * pl.npb + pb) * pl.nchp * pl.rows_p + ((b - pb * pl.rb) * p.T + t) * pl.G + g;
     parts_p = pl.nchp;
   }
-  const int n = parts_p + parts_o;
+  const int n = in ? parts_p + parts_o : 0;
+  const auto slot = [&](int i) {
+    return i < parts_p ? slot_p + static_cast<long long>(i) * pl.rows_p
+                       : slot_o + static_cast<long long>(i - parts_p) * pl.rows_o;
+  };
+  grid_dep_wait();
+  grid_dep_launch_dependents();
   float m = -INFINITY;
-  for (int i = lane; i < n; i += 32) {
-    const long long s = i < parts_p ? slot_p + static_cast<long long>(i) * pl.rows_p
-                                    : slot_o + static_cast<long long>(i - parts_p) * pl.rows_o;
-    m = fmaxf(m, p.ml[s].x);
-  }
+  for (int i = lane; i < n; i += 32) m = fmaxf(m, p.ml[slot(i)].x);
 #pragma unroll
   for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
   float den = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-  for (int i = 0; i < n; ++i) {
-    const long long s = i < parts_p ? slot_p + static_cast<long long>(i) * pl.rows_p
-                                    : slot_o + static_cast<long long>(i - parts_p) * pl.rows_o;
+  for (int i = w; i < n; i += W) {
+    const long long s = slot(i);
     const float2 ml = p.ml[s];
     const float4 v = reinterpret_cast<const float4*>(p.part + s * kHeadDim)[lane];
     // a chunk in which the row sees no key has m = -inf, sum 0 and O = 0: weight 0, or 1
     // if no chunk has a key
-    const float w = m == -INFINITY ? 1.f : fast_exp2(ml.x - m);
-    den += ml.y * w;
-    acc.x += v.x * w;
-    acc.y += v.y * w;
-    acc.z += v.z * w;
-    acc.w += v.w * w;
+    const float a = m == -INFINITY ? 1.f : fast_exp2(ml.x - m);
+    den += ml.y * a;
+    acc.x += v.x * a;
+    acc.y += v.y * a;
+    acc.z += v.z * a;
+    acc.w += v.w * a;
   }
+  if (W > 1) {
+    sacc[warp][lane] = acc;
+    if (lane == 0) sden[warp] = den;
+    __syncthreads();
+    if (w != 0) return;
+#pragma unroll
+    for (int i = 1; i < W; ++i) {
+      const float4 v = sacc[warp + i][lane];
+      den += sden[warp + i];
+      acc.x += v.x;
+      acc.y += v.y;
+      acc.z += v.z;
+      acc.w += v.w;
+    }
+  }
+  if (!in) return;
   const float inv = den == 0.f ? 0.f : 1.f / den;
   uint16_t* orow = p.o + b * p.ob + t * p.orow + static_cast<long long>(hq) * p.oh;
   reinterpret_cast<uint2*>(orow)[lane] =
@@ -806,13 +816,6 @@ qi_status op_fail(qi_status st, const char* fmt, ...) {
 }
 
 int ceil_div(int a, int b) { return (a + b - 1) / b; }
-
-Div make_div(int d) {
-  uint32_t l = 0;
-  while ((1ull << l) < static_cast<unsigned long long>(d)) ++l;
-  const uint32_t s = 31 + l;
-  return {static_cast<uint32_t>(((1ull << s) + d - 1) / d), s, static_cast<uint32_t>(d)};
-}
 
 // Chooses the decomposition from sizes alone (own lengths, which only the device
 // knows, count as S). Time is counted in key tiles: a unit costs its tiles plus
@@ -942,7 +945,7 @@ qi_status check_sizes(const qi_prefix_attn* a) {
   constexpr int kMost = 1 << 24;
   if (a->B < 1 || a->B > 65535 || a->T < 1 || a->T > kMost || a->Hkv < 1 || a->Hkv > 65535 || a->Hq < a->Hkv ||
       a->Hq % a->Hkv != 0 || a->Hq / a->Hkv > kRows || a->P < 0 || a->P > kMost || a->S < 0 || a->S > kMost ||
-      (a->P == 0 && a->S == 0) || static_cast<long long>(a->B) * a->T * a->Hq > (1ll << 31))
+      (a->P == 0 && a->S == 0) || static_cast<long long>(a->B) * a->T * a->Hq >= (1ll << 31))
     return op_fail(QI_ERR_SHAPE, "qi_prefix_attention: B %d T %d Hq %d Hkv %d P %d S %d", a->B, a->T, a->Hq, a->Hkv,
                    a->P, a->S);
   return QI_OK;
@@ -970,9 +973,15 @@ cudaError_t launch(const Maps& tm, const Params& p, float scale_log2, int sms, c
   const int grid = p.pl.units < sms ? p.pl.units : sms;
   e = launch_dependent(prefix_attn_tc<BF16>, dim3(grid), dim3(kThreads), kSmem, stream, tm, p, scale_log2);
   if (e != cudaSuccess || !p.pl.split) return e;
+  // Warps per row: as many as its parts keep busy, unless the rows alone fill the GPU (1024
+  // rows of 16 parts: %MERGE%)
   const long long rows = static_cast<long long>(p.B) * p.T * p.Hq;
-  return launch_dependent(merge_partials<BF16>, dim3(static_cast<unsigned>((rows + kMergeWarps - 1) / kMergeWarps)),
-                          dim3(kMergeWarps * 32), 0, stream, p);
+  const int parts = p.pl.packed ? p.pl.nchp + p.pl.nch : p.pl.nch;
+  const int w = rows > 16384 || parts < 4 ? 1 : parts < 16 ? 4 : 8;
+  const auto kernel = w == 1 ? merge_partials<BF16, 1> : w == 4 ? merge_partials<BF16, 4> : merge_partials<BF16, 8>;
+  const long long per = kMergeWarps / w;
+  return launch_dependent(kernel, dim3(static_cast<unsigned>((rows + per - 1) / per)), dim3(kMergeWarps * 32), 0, stream,
+                          p);
 }
 
 }  // namespace
@@ -1057,6 +1066,10 @@ extern "C" qi_status qi_prefix_attention(const qi_prefix_attn* a, qi_stream_t st
   p.d_nchp = make_div(pl.packed ? pl.nchp : 1);
   p.d_nqb = make_div(pl.nqb);
   p.d_npb = make_div(pl.packed ? pl.npb : 1);
+  p.d_tb = make_div(pl.tb);
+  p.d_rb = make_div(pl.rb);
+  p.d_ct = make_div(pl.ct);
+  p.d_Hq = make_div(a->Hq);
   p.d_B = make_div(a->B);
   p.d_hb = make_div(a->Hkv * a->B);
   p.d_G = make_div(pl.G);

@@ -531,7 +531,7 @@ typedef struct qi_tensor4 {
  * Results do not depend on the other sequences' contents, and repeat bit for bit.
  * Errors: INVALID_ARG (NULL, dtype, alignment, strides, scale not positive, workspace),
  * SHAPE (B, T, Hkv < 1, Hq % Hkv != 0, Hq / Hkv > 128, P + S = 0, B or Hkv > 65535, T, P or
- * S > 2^24, B T Hq > 2^31), CUDA. */
+ * S > 2^24, B T Hq >= 2^31), CUDA. */
 typedef struct qi_prefix_attn {
   int dtype, B, T, Hq, Hkv, P, S, causal;
   float scale;
