@@ -49,11 +49,6 @@ __device__ __forceinline__ void load8(const float* src, float (&v)[8]) {
   v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
 }
 
-// Stores 8 values in T and leaves in v what was stored.
-__device__ __forceinline__ void store8(float* dst, float (&v)[8]) {
-  reinterpret_cast<float4*>(dst)[0] = make_float4(v[0], v[1], v[2], v[3]);
-  reinterpret_cast<float4*>(dst)[1] = make_float4(v[4], v[5], v[6], v[7]);
-}
 __device__ __forceinline__ uint4 pack8(const __half*, const float (&v)[8]) {
   return make_uint4(pack_f16x2(v[0], v[1]), pack_f16x2(v[2], v[3]), pack_f16x2(v[4], v[5]), pack_f16x2(v[6], v[7]));
 }
@@ -62,17 +57,30 @@ __device__ __forceinline__ uint4 pack8(const __nv_bfloat16*, const float (&v)[8]
                     pack_bf16x2(v[6], v[7]));
 }
 template <typename T>
-__device__ __forceinline__ void store8(T* dst, float (&v)[8]) {
+__device__ __forceinline__ void store8(T* dst, const float (&v)[8]) {
   *reinterpret_cast<uint4*>(dst) = pack8(dst, v);
 }
-__device__ __forceinline__ void round8(const float*, float (&)[8]) {}
-__device__ __forceinline__ void round8(const __half*, float (&v)[8]) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = __half2float(__float2half_rn(v[i]));
+
+// 8 values in 16-byte pieces: one of a 16-bit type, two of fp32
+template <typename T>
+__device__ __forceinline__ void from_pieces(const uint4 (&u)[1], float (&v)[8]) {
+  unpack8<T>(u[0], v);
 }
-__device__ __forceinline__ void round8(const __nv_bfloat16*, float (&v)[8]) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = __bfloat162float(__float2bfloat16_rn(v[i]));
+template <typename T>
+__device__ __forceinline__ void from_pieces(const uint4 (&u)[2], float (&v)[8]) {
+  v[0] = __uint_as_float(u[0].x), v[1] = __uint_as_float(u[0].y), v[2] = __uint_as_float(u[0].z);
+  v[3] = __uint_as_float(u[0].w), v[4] = __uint_as_float(u[1].x), v[5] = __uint_as_float(u[1].y);
+  v[6] = __uint_as_float(u[1].z), v[7] = __uint_as_float(u[1].w);
+}
+// ... and back; v becomes what was stored
+template <typename T>
+__device__ __forceinline__ void to_pieces(const T* type, float (&v)[8], uint4 (&u)[1]) {
+  u[0] = pack8(type, v);
+  unpack8<T>(u[0], v);
+}
+__device__ __forceinline__ void to_pieces(const float*, float (&v)[8], uint4 (&u)[2]) {
+  u[0] = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+  u[1] = make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7]));
 }
 
 // 2^n for -127 <= n <= 128 (2^128 = inf)
@@ -320,95 +328,126 @@ constexpr uint32_t kNear = 16;  // fp32 steps around a border
 
 struct NormParams {
   qi_add_rmsnorm a;
-  int groups;  // ceil(rows / 128)
+  int groups;          // ceil(rows / 128)
+  float n_hi, n_lo;    // 1 / K
 };
 
-// One CTA per row; a thread holds NC groups of 8 values (group threadIdx.x + i blockDim.x).
-template <typename TX, typename TD, int NC>
+// The sum of `lanes` (a power of two) neighbouring lanes' values, in each of them
+__device__ __forceinline__ F2 lanes_sum(F2 x, int lanes) {
+  for (int d = lanes / 2; d; d >>= 1)
+    x = add(x, F2{__shfl_xor_sync(0xffffffffu, x.hi, d), __shfl_xor_sync(0xffffffffu, x.lo, d)});
+  return x;
+}
+
+// One CTA per row. The sum goes to shared memory (as it is stored, in TX) between the two
+// passes over it: a thread reads back only what it wrote, so the one barrier is that of the
+// reduction, and there is none in a CTA of one warp. %NORM%
+constexpr int kNormUnroll = 2;  // groups of 8 whose loads are issued together
+template <typename TX, typename TD>
 __global__ void add_rmsnorm_kernel(const __grid_constant__ NormParams p) {
-  grid_dep_wait();
-  grid_dep_launch_dependents();
+  extern __shared__ __align__(16) uint8_t stash[];
   __shared__ F2 part[32];
   const qi_add_rmsnorm& a = p.a;
-  const int r = blockIdx.x;
   const int groups8 = a.K / 8;
-  float v[NC][8];
+  const int threads = blockDim.x, r = blockIdx.x;
+  constexpr int kX = sizeof(TX) / 2, kD = sizeof(TD) / 2;  // 16-byte pieces of a group
+  // piece-major, so that a warp's accesses are contiguous
+  const auto piece = [&](int c, int j) { return reinterpret_cast<uint4*>(stash) + j * groups8 + c; };
+  grid_dep_wait();
+  grid_dep_launch_dependents();
+  const uint4* x = reinterpret_cast<const uint4*>(static_cast<const TX*>(a.x) + r * a.x_stride);
+  const uint4* d = a.delta ? reinterpret_cast<const uint4*>(static_cast<const TD*>(a.delta) + r * a.delta_stride) : nullptr;
+  TX* xo = a.x_out ? static_cast<TX*>(a.x_out) + r * a.x_out_stride : nullptr;
   float sq[4] = {};
+  for (int c0 = threadIdx.x; c0 < groups8; c0 += kNormUnroll * threads) {
+    uint4 xr[kNormUnroll][kX], dr[kNormUnroll][kD];
 #pragma unroll
-  for (int i = 0; i < NC; ++i) {
-    const int c = threadIdx.x + i * blockDim.x;
+    for (int i = 0; i < kNormUnroll; ++i) {
+      const int c = c0 + i * threads;
+      if (c < groups8) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[i][k] = 0.f;
-    if (c < groups8) {
-      load8(static_cast<const TX*>(a.x) + r * a.x_stride + c * 8, v[i]);
-      if (a.delta) {
-        float d[8];
-        load8(static_cast<const TD*>(a.delta) + r * a.delta_stride + c * 8, d);
+        for (int j = 0; j < kX; ++j) xr[i][j] = x[c * kX + j];
+        if (d) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[i][k] = __fadd_rn(v[i][k], d[k]);
-        round8(static_cast<const TX*>(nullptr), v[i]);
+          for (int j = 0; j < kD; ++j) dr[i][j] = d[c * kD + j];
+        }
       }
-      if (a.x_out) store8(static_cast<TX*>(a.x_out) + r * a.x_out_stride + c * 8, v[i]);
     }
 #pragma unroll
-    for (int k = 0; k < 8; ++k) sq[k & 3] = __fmaf_rn(v[i][k], v[i][k], sq[k & 3]);
+    for (int i = 0; i < kNormUnroll; ++i) {
+      const int c = c0 + i * threads;
+      if (c < groups8) {
+        float v[8];
+        from_pieces<TX>(xr[i], v);
+        if (d) {
+          float f[8];
+          from_pieces<TD>(dr[i], f);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) v[k] = __fadd_rn(v[k], f[k]);
+          to_pieces(static_cast<const TX*>(nullptr), v, xr[i]);
+        }
+#pragma unroll
+        for (int j = 0; j < kX; ++j) {
+          *piece(c, j) = xr[i][j];
+          if (xo) reinterpret_cast<uint4*>(xo)[c * kX + j] = xr[i][j];
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) sq[k & 3] = __fmaf_rn(v[k], v[k], sq[k & 3]);
+      }
+    }
   }
-  F2 sum = add(two_sum(sq[0], sq[1]), two_sum(sq[2], sq[3]));
-#pragma unroll
-  for (int d = 16; d; d >>= 1)
-    sum = add(sum, F2{__shfl_xor_sync(0xffffffffu, sum.hi, d), __shfl_xor_sync(0xffffffffu, sum.lo, d)});
-  const int warps = (blockDim.x + 31) / 32;
-  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = sum;
-  __syncthreads();
-  sum = part[0];
-  for (int i = 1; i < warps; ++i) sum = add(sum, part[i]);
-  // mean + eps, with the division's remainder
-  const float n = static_cast<float>(a.K);
-  const float mh = __fdiv_rn(sum.hi, n);
-  const F2 m = add(F2{mh, __fdiv_rn(__fmaf_rn(-mh, n, sum.hi) + sum.lo, n)}, F2{a.eps, 0.f});
-  const F2 rs = inv_sqrt(m);
+  F2 sum = lanes_sum(add(two_sum(sq[0], sq[1]), two_sum(sq[2], sq[3])), 32);
+  if (threads > 32) {
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = sum;
+    __syncthreads();
+    const int lane = threadIdx.x & 31;
+    sum = lanes_sum(part[lane & (threads / 32 - 1)], threads / 32);
+  }
+  // mean + eps
+  const float mh = __fmul_rn(sum.hi, p.n_hi);
+  const float ml = __fmaf_rn(sum.hi, p.n_hi, -mh) + (sum.hi * p.n_lo + sum.lo * p.n_hi);
+  const F2 rs = inv_sqrt(add(F2{mh, ml}, F2{a.eps, 0.f}));
   const float r1 = rs.hi + rs.lo;
-#pragma unroll
-  for (int i = 0; i < NC; ++i) {
-    const int c = threadIdx.x + i * blockDim.x;
+  const float bias = a.w && a.plus_one ? 1.f : 0.f;
+  uint2* codes = reinterpret_cast<uint2*>(a.q + r * static_cast<size_t>(a.K));
+  uint32_t* scales = reinterpret_cast<uint32_t*>(a.sf + mx_sf_offset(r, 0, p.groups));
+  // (all lanes of a warp run the same rounds: the shuffles need them)
+  for (int c = threadIdx.x; (c & ~31) < groups8; c += threads) {
     const bool in = c < groups8;  // groups8 is a multiple of 16: the lanes of a scale block agree
-    float g[8];
+    float v[8] = {}, g[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) g[k] = 1.f;
-    if (in && a.w) {
-      if (a.w_f32)
-        load8(static_cast<const float*>(a.w) + c * 8, g);
-      else
-        load8(static_cast<const __nv_bfloat16*>(a.w) + c * 8, g);
+    if (in) {
+      uint4 u[kX];
+#pragma unroll
+      for (int j = 0; j < kX; ++j) u[j] = *piece(c, j);
+      from_pieces<TX>(u, v);
+      if (a.w) {
+        if (a.w_f32)
+          load8(static_cast<const float*>(a.w) + c * 8, g);
+        else
+          load8(static_cast<const __nv_bfloat16*>(a.w) + c * 8, g);
+      }
     }
-    const bool one = a.w && a.plus_one;
-    // y in fp32: three roundings (r1, the two products; a fourth in 1 + w), at most 4 half
-    // steps and 2^-27 of the statistics off, that is within kNear steps with room to spare
+    // y in fp32: roundings of r1, of 1 + w and of the two products, at most 2 fp32 steps and
+    // 2^-27 of the statistics off, that is within kNear steps with room to spare
     float y[8], top;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) y[k] = v[i][k] * r1 * (one ? 1.f + g[k] : g[k]);
+    for (int k = 0; k < 8; ++k) y[k] = v[k] * r1 * (g[k] + bias);
     int e = mx_exponent8(y, top);
     float inv = pow2(-e);
-    // Borders: a scaled value of 2^-6 and more lies between two codes where the 20 bits below
-    // its three leading fraction bits are 80000h; below 2^-6 the codes are evenly spaced and no
-    // bit pattern tells, so those (one in 10^4) count as near. The exponent's border is a power
-    // of two. If any lane is near one, the warp takes the sums with error terms.
-    uint32_t near = 0xFFFFFu;
-    float least = 1.f;
+    // Borders between codes, of the evenly spaced ones below 2^-6 too, and the powers of two at
+    // which the exponent changes all have 19 or more zero bits at the end; so has one value in
+    // 16000. If any lane's value is that near one, the warp takes the sums with error terms.
+    uint32_t near = 0xFFFFFFFFu;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const float s = y[k] * inv;
-      near = min(near, (__float_as_uint(s) - 0x80000u + kNear) & 0xFFFFFu);
-      least = fminf(least, fabsf(s));
-    }
-    const bool edge = near <= 2 * kNear || least < 0x1p-6f ||
-                      ((__float_as_uint(top) + kNear) & 0x7FFFFFu) <= 2 * kNear;
-    if (__any_sync(0xffffffffu, edge && in)) {
+    for (int k = 0; k < 8; ++k) near = min(near, __float_as_uint(y[k]) * 8192u + kNear * 8192u);
+    if (__any_sync(0xffffffffu, near <= 2 * kNear * 8192u && in)) {
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const F2 h = one ? two_sum(1.f, g[k]) : F2{g[k], 0.f};
-        const float q = __fmul_rn(v[i][k], rs.hi);
-        const float qe = __fmaf_rn(v[i][k], rs.hi, -q) + v[i][k] * rs.lo;
+        const F2 h = two_sum(g[k], bias);
+        const float q = __fmul_rn(v[k], rs.hi);
+        const float qe = __fmaf_rn(v[k], rs.hi, -q) + v[k] * rs.lo;
         const float z = __fmul_rn(q, h.hi);
         y[k] = round_odd(two_sum(z, __fmaf_rn(q, h.hi, -z) + (qe * h.hi + q * h.lo)));
       }
@@ -420,10 +459,9 @@ __global__ void add_rmsnorm_kernel(const __grid_constant__ NormParams p) {
     scale |= __shfl_down_sync(0xffffffffu, scale, 4) << 8;
     scale |= __shfl_down_sync(0xffffffffu, scale, 8) << 16;
     if (in) {
-      reinterpret_cast<uint2*>(a.q + r * static_cast<size_t>(a.K))[c] =
-          make_uint2(e4m3x4(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv),
-                     e4m3x4(y[4] * inv, y[5] * inv, y[6] * inv, y[7] * inv));
-      if ((c & 15) == 0) *reinterpret_cast<uint32_t*>(a.sf + mx_sf_offset(r, c / 4, p.groups)) = scale;
+      codes[c] = make_uint2(e4m3x4(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv),
+                            e4m3x4(y[4] * inv, y[5] * inv, y[6] * inv, y[7] * inv));
+      if ((c & 15) == 0) scales[(c >> 4) * static_cast<size_t>(p.groups) * 128] = scale;
     }
   }
 }
@@ -431,13 +469,18 @@ __global__ void add_rmsnorm_kernel(const __grid_constant__ NormParams p) {
 template <typename TX, typename TD>
 cudaError_t launch_norm(const NormParams& p, cudaStream_t s) {
   const int groups8 = p.a.K / 8;
-  const int threads = groups8 < 256 ? (groups8 + 31) / 32 * 32 : 256;
-  const int nc = (groups8 + threads - 1) / threads;
-  const dim3 grid(static_cast<unsigned>(p.a.rows)), block(static_cast<unsigned>(threads));
-  if (nc <= 1) return launch_dependent(add_rmsnorm_kernel<TX, TD, 1>, grid, block, 0, s, p);
-  if (nc <= 2) return launch_dependent(add_rmsnorm_kernel<TX, TD, 2>, grid, block, 0, s, p);
-  if (nc <= 4) return launch_dependent(add_rmsnorm_kernel<TX, TD, 4>, grid, block, 0, s, p);
-  return launch_dependent(add_rmsnorm_kernel<TX, TD, 8>, grid, block, 0, s, p);
+  const int bytes = p.a.K * static_cast<int>(sizeof(TX));
+  const auto kernel = add_rmsnorm_kernel<TX, TD>;
+  static std::atomic<unsigned long long> attr_done{0};
+  const cudaError_t e = ensure_smem_limit(kernel, 64 * 1024, attr_done);
+  if (e != cudaSuccess) return e;
+  // 128 threads a row where the rows alone fill the GPU; where they do not, as many as halve
+  // the row's passes, to 512 (3 rows of 4096: 4.2 us with 128 threads, 2.9 with 512)
+  const int most = p.a.rows >= 2 * device_sms() ? 128 : 512;
+  int threads = 32;
+  while (threads < most && threads < groups8) threads *= 2;
+  return launch_dependent(kernel, dim3(static_cast<unsigned>(p.a.rows)), dim3(static_cast<unsigned>(threads)),
+                          static_cast<size_t>(bytes), s, p);
 }
 template <typename TX>
 cudaError_t launch_norm_d(const NormParams& p, cudaStream_t s) {
@@ -536,7 +579,7 @@ extern "C" qi_status qi_add_rmsnorm_mxfp8(const qi_add_rmsnorm* args, qi_stream_
   using namespace qi;
   if (!args || !args->x || !args->q || !args->sf)
     return op_fail(QI_ERR_INVALID_ARG, "qi_add_rmsnorm_mxfp8: NULL argument");
-  NormParams p{*args, 0};
+  NormParams p{*args, 0, 0.f, 0.f};
   qi_add_rmsnorm& a = p.a;
   const auto known = [](int d) { return d == QI_DT_F16 || d == QI_DT_BF16 || d == QI_DT_F32; };
   if (!known(a.x_dtype) || (a.delta && !known(a.delta_dtype)))
@@ -556,6 +599,8 @@ extern "C" qi_status qi_add_rmsnorm_mxfp8(const qi_add_rmsnorm* args, qi_stream_
                    "qi_add_rmsnorm_mxfp8: x, delta, x_out, w and q need 16-byte alignment, rows at least K apart in "
                    "multiples of 16 bytes");
   p.groups = (a.rows + 127) / 128;
+  p.n_hi = static_cast<float>(1.0 / a.K);
+  p.n_lo = static_cast<float>(1.0 / a.K - static_cast<double>(p.n_hi));
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t e = a.x_dtype == QI_DT_F16    ? launch_norm_d<__half>(p, s)
                         : a.x_dtype == QI_DT_BF16 ? launch_norm_d<__nv_bfloat16>(p, s)

@@ -193,6 +193,9 @@ bool encode_map16(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols
 bool encode_map16_nd(CUtensorMap* m, const void* base, int rank, const unsigned long long* dims,
                      const unsigned long long* strides, const unsigned* box);
 
+// SMs of the current device, looked up once per device; 0 if there is none (prefix_attention.cu).
+int device_sms();
+
 // n / d for 0 <= n < 2^31 as one widening product: m = ceil(2^s / d) with s = 31 +
 // ceil(log2 d) is too large by less than 1, which moves the quotient by less than n / 2^s <=
 // 1 / d, too little to reach the next one. (In the attention kernel every role works out every

@@ -951,20 +951,6 @@ qi_status check_sizes(const qi_prefix_attn* a) {
   return QI_OK;
 }
 
-int sm_count() {
-  static std::atomic<int> cached[64];
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-  if (dev >= 0 && dev < 64) {
-    const int c = cached[dev].load(std::memory_order_relaxed);
-    if (c > 0) return c;
-  }
-  int n = 0;
-  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-  if (dev >= 0 && dev < 64) cached[dev].store(n, std::memory_order_relaxed);
-  return n;
-}
-
 template <bool BF16>
 cudaError_t launch(const Maps& tm, const Params& p, float scale_log2, int sms, cudaStream_t stream) {
   static std::atomic<unsigned long long> attr_done{0};
@@ -985,12 +971,27 @@ cudaError_t launch(const Maps& tm, const Params& p, float scale_log2, int sms, c
 }
 
 }  // namespace
+
+int device_sms() {
+  static std::atomic<int> cached[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  if (dev >= 0 && dev < 64) {
+    const int c = cached[dev].load(std::memory_order_relaxed);
+    if (c > 0) return c;
+  }
+  int n = 0;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+  if (dev >= 0 && dev < 64) cached[dev].store(n, std::memory_order_relaxed);
+  return n;
+}
+
 }  // namespace qi
 
 extern "C" size_t qi_prefix_attention_workspace(const qi_prefix_attn* a) {
   using namespace qi;
   if (check_sizes(a) != QI_OK) return 0;
-  const int sms = sm_count();
+  const int sms = device_sms();
   if (sms <= 0) return 0;
   const Plan pl = make_plan(a->B, a->T, a->Hq, a->Hkv, a->P, a->S, a->causal, sms);
   return ws_layout(pl, a->P, a->Hkv, a->P > 0 && a->pk8 != nullptr).total;
@@ -1025,7 +1026,7 @@ extern "C" qi_status qi_prefix_attention(const qi_prefix_attn* a, qi_stream_t st
       (((reinterpret_cast<uintptr_t>(a->pk8) | reinterpret_cast<uintptr_t>(a->pv8)) & 15) ||
        ((reinterpret_cast<uintptr_t>(a->pk_sf) | reinterpret_cast<uintptr_t>(a->pv_sf)) & 3)))
     return op_fail(QI_ERR_INVALID_ARG, "qi_prefix_attention: the 8-bit prefix needs 16-byte aligned codes and 4-byte aligned scales");
-  const int sms = sm_count();
+  const int sms = device_sms();
   if (sms <= 0) return op_fail(QI_ERR_CUDA, "qi_prefix_attention: no CUDA device");
   const Plan pl = make_plan(a->B, a->T, a->Hq, a->Hkv, a->P, a->S, a->causal, sms);
   if (pl.units <= 0) return op_fail(QI_ERR_SHAPE, "qi_prefix_attention: too many rows and heads");
