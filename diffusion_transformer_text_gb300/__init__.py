@@ -301,17 +301,19 @@ _SCALE = 1.0 / math.sqrt(HEAD_DIM)
 # Layouts (types, devices, shapes and strides of all tensor arguments) that a call has checked, with
 # what it packs for them; the checks and the workspace size depend on nothing else, and take longer
 # than the launch. Pointers are read anew on every call.
-_layouts: dict = {}
+_attn_layouts: dict = {}
+_kv8_layouts: dict = {}
+_norm_layouts: dict = {}
 
 
 def _layout(t):
     return None if t is None else (t.dtype, t.device, t.shape, t.stride())
 
 
-def _remember(key, value):
-    if len(_layouts) >= 4096:
-        _layouts.clear()
-    _layouts[key] = value
+def _remember(layouts, key, value):
+    if len(layouts) >= 4096:
+        layouts.clear()
+    layouts[key] = value
     return value
 
 
@@ -372,31 +374,20 @@ def _addr(t):
     return 0 if t is None else t.data_ptr()
 
 
-def _on_device(fn):
-    """Calls fn(*args, raw stream, **kw) with its first argument's device (that of a tensor, or of a
-    KV8Cache) current, on `stream` or else on that device's current stream; with `stream`, it is the
-    current stream, too, so that what the call allocates belongs to it."""
-    import functools
-    import inspect
-    name = next(iter(inspect.signature(fn).parameters))
-
-    @functools.wraps(fn)
-    def call(*args, stream=None, **kw):
-        import torch
-        t = args[0] if args else kw[name]
-        dev = (t[0] if isinstance(t, tuple) else t).device
-        if dev.type != "cuda":
-            raise ValueError(f"{fn.__name__}: CUDA tensors wanted, got {dev}")
-        if stream is None and dev.index == torch.cuda.current_device():
-            return fn(*args, **kw, _raw=torch._C._cuda_getCurrentRawStream(dev.index))
-        with torch.cuda.device(dev):
-            if stream is None:
-                return fn(*args, **kw, _raw=torch._C._cuda_getCurrentRawStream(dev.index))
-            if stream.device != dev:
-                raise ValueError(f"{fn.__name__}: a stream of {stream.device} for tensors of {dev}")
-            with torch.cuda.stream(stream):
-                return fn(*args, **kw, _raw=stream.cuda_stream)
-    return call
+def _elsewhere(t, stream):
+    """A context in which t's device is current and `stream` (None: that device's current one) the current
+    stream, so that what a call allocates belongs to it. Raises for tensors that are not on a GPU."""
+    import contextlib
+    import torch
+    if not t.is_cuda:
+        raise ValueError(f"CUDA tensors wanted, got {t.device}")
+    if stream is not None and stream.device != t.device:
+        raise ValueError(f"a stream of {stream.device} for tensors of {t.device}")
+    stack = contextlib.ExitStack()
+    stack.enter_context(torch.cuda.device(t.device))
+    if stream is not None:
+        stack.enter_context(torch.cuda.stream(stream))
+    return stack
 
 
 def _check_prefix_attention(key, q, k, v, prefix_k, prefix_v, prefix8, own_len, out, status):
@@ -435,12 +426,11 @@ def _check_prefix_attention(key, q, k, v, prefix_k, prefix_v, prefix8, own_len, 
     p8 = int(prefix8 is not None and P > 0)
     need = lib().qi_prefix_attention_workspace(
         _PREFIX_ATTN.pack(*sizes, 0, 1.0, *(0, 0, 0, 0) * 6, p8, 0, 0, 0, 0, 0, 0, 0))
-    return _remember(key, (sizes, qs, ks, vs, os_, pks, pvs, need, shape))
+    return _remember(_attn_layouts, key, (sizes, qs, ks, vs, os_, pks, pvs, need, shape))
 
 
-@_on_device
 def prefix_attention(q, k, v, prefix_k=None, prefix_v=None, prefix8: KV8Cache | None = None, own_len=None,
-                     causal: bool = False, scale: float | None = None, out=None, status=None, *, _raw=None):
+                     causal: bool = False, scale: float | None = None, out=None, status=None, stream=None):
     """Attention of a batch whose sequences share a prefix of keys and have keys of their own.
 
     q [B, T, Hq, 128]; k, v [B, S, Hkv, 128] (S may be 0, or k = v = None); prefix_k, prefix_v
@@ -448,23 +438,27 @@ def prefix_attention(q, k, v, prefix_k=None, prefix_v=None, prefix8: KV8Cache | 
     bfloat16, any strides with a contiguous last dimension. own_len: int32 [B] on the device, the own
     rows in use (None: S). causal: query row t of T sees own rows up to own_len - T + t. scale: default
     1 / sqrt(128). status: int32 [1] on the device that receives a non-zero code if a wait in the
-    kernel expires. stream: default the current one. Returns o [B, T, Hq, 128] (`out`, if given)."""
+    kernel expires. stream: default the current one of q's device. Returns o [B, T, Hq, 128] (`out`, if
+    given)."""
     import torch
-    p8 = prefix8 if prefix8 is not None else (None, None, None, None)
-    key = (_layout(q), _layout(k), _layout(v), _layout(prefix_k), _layout(prefix_v), *map(_layout, p8),
-           _layout(own_len), _layout(out), _layout(status))
-    plan = _layouts.get(key)
+    dev = q.get_device()
+    if stream is not None or dev < 0 or dev != torch._C._cuda_getDevice():
+        with _elsewhere(q, stream):
+            return prefix_attention(q, k, v, prefix_k, prefix_v, prefix8, own_len, causal, scale, out, status)
+    key = (q.dtype, q.device, q.shape, q.stride(), _layout(k), _layout(v), _layout(prefix_k), _layout(prefix_v),
+           None if prefix8 is None else (*map(_layout, prefix8),), _layout(own_len), _layout(out), _layout(status))
+    plan = _attn_layouts.get(key)
     if plan is None:
         plan = _check_prefix_attention(key, q, k, v, prefix_k, prefix_v, prefix8, own_len, out, status)
     sizes, qs, ks, vs, os_, pks, pvs, need, shape = plan
     if out is None:
-        out = torch.empty(shape, dtype=q.dtype, device=q.device)
-    ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
-    args = _PREFIX_ATTN.pack(
+        out = q.new_empty(shape)
+    ws = q.new_empty(need, dtype=torch.uint8) if need else None
+    p8 = (0, 0, 0, 0) if prefix8 is None else [t.data_ptr() for t in prefix8]
+    st = _lib.qi_prefix_attention(_PREFIX_ATTN.pack(
         *sizes, 1 if causal else 0, _SCALE if scale is None else scale, q.data_ptr(), *qs, _addr(k), *ks, _addr(v),
-        *vs, out.data_ptr(), *os_, _addr(prefix_k), *pks, _addr(prefix_v), *pvs, *map(_addr, p8), _addr(own_len),
-        _addr(ws), need, _addr(status))
-    st = _lib.qi_prefix_attention(args, _raw)
+        *vs, out.data_ptr(), *os_, _addr(prefix_k), *pks, _addr(prefix_v), *pvs, *p8, _addr(own_len), _addr(ws), need,
+        _addr(status)), torch._C._cuda_getCurrentRawStream(dev))
     if st:
         _check(st)
     return out
@@ -487,37 +481,49 @@ def _check_kv8(key, cache, k, v, pos, lens):
     _want(pos, torch.int32, (B,), dev, "pos")
     _want(lens, torch.int32, (B,), dev, "lens")
     lib()
-    return _remember(key, ((dt, B, T, S, H), *strides))
+    return _remember(_kv8_layouts, key, ((dt, B, T, S, H), *strides))
 
 
-def _kv8_args(cache, k, v, pos, lens):
-    key = (*map(_layout, cache), _layout(k), _layout(v), _layout(pos), _layout(lens))
-    plan = _layouts.get(key)
+def _kv8_call(write, cache, k, v, pos, lens, dev):
+    import torch
+    ck, cv, ck_sf, cv_sf = cache
+    key = (ck.dtype, ck.device, ck.shape, ck.stride(), _layout(cv), _layout(ck_sf), _layout(cv_sf), _layout(k),
+           _layout(v), _layout(pos), _layout(lens))
+    plan = _kv8_layouts.get(key)
     if plan is None:
         plan = _check_kv8(key, cache, k, v, pos, lens)
     sizes, ks, vs = plan
-    c = (cache.k.data_ptr(), cache.v.data_ptr(), cache.k_sf.data_ptr(), cache.v_sf.data_ptr())
-    return (sizes, _TENSOR4.pack(k.data_ptr(), *ks), _TENSOR4.pack(v.data_ptr(), *vs), c, _addr(pos), _addr(lens))
-
-
-@_on_device
-def kv8_write(cache: KV8Cache, k, v, pos=None, lens=None, *, _raw=None):
-    """Quantises k, v [B, T, H, 128] (float16 or bfloat16, any strides with a contiguous last dimension)
-    into the cache: row t < lens[b] of sequence b becomes cache row pos[b] + t (int32 [B] on the device;
-    None: 0 and T). Rows that fall outside the cache are passed over. stream: default the current one."""
-    sizes, kt, vt, c, pp, lp = _kv8_args(cache, k, v, pos, lens)
-    st = _lib.qi_kv8_write(*sizes, kt, vt, *c, pp, lp, _raw)
+    kt, vt = _TENSOR4.pack(k.data_ptr(), *ks), _TENSOR4.pack(v.data_ptr(), *vs)
+    c = (ck.data_ptr(), cv.data_ptr(), ck_sf.data_ptr(), cv_sf.data_ptr(), _addr(pos), _addr(lens))
+    raw = torch._C._cuda_getCurrentRawStream(dev)
+    st = _lib.qi_kv8_write(*sizes, kt, vt, *c, raw) if write else _lib.qi_kv8_read(*sizes, *c, kt, vt, raw)
     if st:
         _check(st)
+
+
+def kv8_write(cache: KV8Cache, k, v, pos=None, lens=None, stream=None):
+    """Quantises k, v [B, T, H, 128] (float16 or bfloat16, any strides with a contiguous last dimension)
+    into the cache: row t < lens[b] of sequence b becomes cache row pos[b] + t (int32 [B] on the device;
+    None: 0 and T). Rows that fall outside the cache are passed over. stream: default the current one of
+    the cache's device. Returns the cache."""
+    import torch
+    dev = cache.k.get_device()
+    if stream is not None or dev < 0 or dev != torch._C._cuda_getDevice():
+        with _elsewhere(cache.k, stream):
+            return kv8_write(cache, k, v, pos, lens)
+    _kv8_call(True, cache, k, v, pos, lens, dev)
     return cache
 
 
-@_on_device
-def kv8_read(cache: KV8Cache, T: int, dtype, pos=None, lens=None, out=None, *, _raw=None):
+def kv8_read(cache: KV8Cache, T: int, dtype, pos=None, lens=None, out=None, stream=None):
     """(k, v) [B, T, H, 128] in `dtype` from cache rows pos[b] + t, t < lens[b]. Rows at or past lens[b] or
     outside the cache stay as they are in `out` = (k, v), and are zero without `out`. stream: default the
-    current one."""
+    current one of the cache's device."""
     import torch
+    dev = cache.k.get_device()
+    if stream is not None or dev < 0 or dev != torch._C._cuda_getDevice():
+        with _elsewhere(cache.k, stream):
+            return kv8_read(cache, T, dtype, pos, lens, out)
     if out is None:
         B, S, H, _ = cache.k.shape
         make = torch.empty if pos is None and lens is None and T <= S else torch.zeros
@@ -525,10 +531,7 @@ def kv8_read(cache: KV8Cache, T: int, dtype, pos=None, lens=None, out=None, *, _
     k, v = out
     if k.dtype != dtype or k.dim() != 4 or k.shape[1] != T:
         raise ValueError(f"out: want {dtype} [B, {T}, H, {HEAD_DIM}], got {k.dtype} {tuple(k.shape)}")
-    sizes, kt, vt, c, pp, lp = _kv8_args(cache, k, v, pos, lens)
-    st = _lib.qi_kv8_read(*sizes, *c, pp, lp, kt, vt, _raw)
-    if st:
-        _check(st)
+    _kv8_call(False, cache, k, v, pos, lens, dev)
     return k, v
 
 
@@ -552,35 +555,39 @@ def _check_norm(key, x, delta, w, x_out, q, sf):
         _want(w, w.dtype if w.dtype in (torch.bfloat16, torch.float32) else torch.bfloat16, (K,), dev, "w")
     lib()
     stride = lambda t: K if t is None else t.stride(0)
-    return _remember(key, ((kinds[x.dtype], 0 if delta is None else kinds[delta.dtype], rows, K,
+    return _remember(_norm_layouts, key, ((kinds[x.dtype], 0 if delta is None else kinds[delta.dtype], rows, K,
                             int(w is not None and w.dtype == torch.float32)), stride(x), stride(delta), stride(x_out),
                            chunks))
 
 
-@_on_device
 def add_rmsnorm_mxfp8(x, delta=None, w=None, plus_one: bool = False, eps: float = 1e-6, x_out=None, q=None, sf=None,
-                      *, _raw=None):
+                      stream=None):
     """x_out = x + delta in x's type, then MXFP8 of RMSNorm(x_out) * gain along the last axis.
 
     x [rows, K] float32, float16 or bfloat16, delta [rows, K] of any of them (None: no addition), rows
     any multiple of 16 bytes apart; w [K] bfloat16 or float32: gain w, or 1 + w with plus_one. Returns
     (x_out, codes [rows, K] uint8, scale chunks uint8) as quant_mxfp8 lays them out; x_out may be x, and
-    a new tensor is made for each of the three that is not given. stream: default the current one."""
+    a new tensor is made for each of the three that is not given. stream: default the current one of x's
+    device."""
     import torch
-    key = (_layout(x), _layout(delta), _layout(w), _layout(x_out), _layout(q), _layout(sf))
-    plan = _layouts.get(key)
+    dev = x.get_device()
+    if stream is not None or dev < 0 or dev != torch._C._cuda_getDevice():
+        with _elsewhere(x, stream):
+            return add_rmsnorm_mxfp8(x, delta, w, plus_one, eps, x_out, q, sf)
+    key = (x.dtype, x.device, x.shape, x.stride(), _layout(delta), _layout(w), _layout(x_out), _layout(q), _layout(sf))
+    plan = _norm_layouts.get(key)
     if plan is None:
         plan = _check_norm(key, x, delta, w, x_out, q, sf)
     head, xs, ds, os_, chunks = plan
     if x_out is None:
-        x_out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        x_out = x.new_empty(x.shape)
     if q is None:
-        q = torch.empty(x.shape, dtype=torch.uint8, device=x.device)
+        q = x.new_empty(x.shape, dtype=torch.uint8)
     if sf is None:
-        sf = torch.zeros(chunks, dtype=torch.uint8, device=x.device)
+        sf = x.new_zeros(chunks, dtype=torch.uint8)
     st = _lib.qi_add_rmsnorm_mxfp8(
         _ADD_RMSNORM.pack(*head, 1 if plus_one else 0, eps, x.data_ptr(), xs, _addr(delta), ds, x_out.data_ptr(), os_,
-                          _addr(w), q.data_ptr(), sf.data_ptr()), _raw)
+                          _addr(w), q.data_ptr(), sf.data_ptr()), torch._C._cuda_getCurrentRawStream(dev))
     if st:
         _check(st)
     return x_out, q, sf
