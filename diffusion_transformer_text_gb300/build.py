@@ -20,8 +20,8 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libqidit.so")
 SOURCES = ["qidit.cu", "gemm.cu", "attention.cu", "kernels_small.cu", "gemm_noalloc.cu", "prefix_attention.cu",
-           "batch_ops.cu"]
-HEADERS = ["ptx.cuh", "internal.h"]
+           "prefix_attention_few.cu", "batch_ops.cu"]
+HEADERS = ["ptx.cuh", "internal.h", "prefix_attention.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xptxas", "-v",
          "-I" + os.path.join(ROOT, "include")]

@@ -188,10 +188,11 @@ cudaError_t launch_attention(const AttnParams& p, cudaStream_t stream);
 // columns with 128-byte swizzle; rows past `rows` read as zero (qidit.cu).
 bool encode_map16(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint32_t box_rows, bool bf16);
 
-// 16-bit TMA map of `rank` dimensions (first innermost, contiguous), byte strides of the
-// others, 128-byte swizzle; what lies outside the dimensions reads as zero (qidit.cu).
-bool encode_map16_nd(CUtensorMap* m, const void* base, int rank, const unsigned long long* dims,
-                     const unsigned long long* strides, const unsigned* box);
+// TMA map of `rank` dimensions (first innermost, contiguous) of 16-bit values with 128-byte
+// swizzle, or of bytes without one; byte strides of the other dimensions; what lies outside
+// the dimensions reads as zero (qidit.cu).
+bool encode_map_nd(CUtensorMap* m, const void* base, bool bytes, int rank, const unsigned long long* dims,
+                   const unsigned long long* strides, const unsigned* box);
 
 // SMs of the current device, looked up once per device; 0 if there is none (prefix_attention.cu).
 int device_sms();

@@ -39,16 +39,13 @@
 #include <mutex>
 
 #include "../../include/qidit.h"
-#include "internal.h"
-#include "ptx.cuh"
+#include "prefix_attention.cuh"
 
 namespace qi {
+using namespace pa;
 namespace {
 
 constexpr int kRows = 128;                    // MMA rows: query rows per block at most
-constexpr int kKeys = 128;                    // keys per tile
-constexpr int kBox = 128 * 64 * 2;            // 128 rows x 64 dims, 128-byte swizzle (16 KB)
-constexpr int kTile = 2 * kBox;               // Q, K or V tile (32 KB)
 constexpr int kKStages = 2;  // (a third measured 1 % slower at 1024^2)
 constexpr int kVStages = 2;
 constexpr int kQBufs = 2;                     // the next unit's Q loads while this one's tiles run
@@ -56,7 +53,6 @@ constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 0;                 // O_h at kColO + 128 h
 constexpr uint32_t kColS = 256;
 constexpr uint32_t kColP = 384;               // buffer b at kColP + 64 b, half h at + 32 h
-constexpr float kRescaleLog2 = 8.0f;          // rescale O_h only when its max grows by > 2^8
 constexpr int kThreads = 512;
 constexpr uint32_t kRegsLow = 104, kRegsHigh = 152, kRegsEpi = 104;
 static_assert(kRegsLow + 2 * kRegsHigh + kRegsEpi == 4 * 128, "register split must equal the launch allotment");
@@ -67,8 +63,10 @@ enum : int {
   kKEmpty = kKFull + kKStages,
   kVFull = kKEmpty + kKStages,
   kVEmpty = kVFull + kVStages,
-  kVClean = kVEmpty + kVStages,  // rows past own_len of a unit's last V tile cleared
-  kQFull = kVClean + 1,
+  // rows past own_len of a unit's last V tile cleared; one per stage, so that the next one cannot
+  // complete before the issuer has seen this one (units may have one tile each)
+  kVClean = kVEmpty + kVStages,
+  kQFull = kVClean + kVStages,
   kQEmpty = kQFull + kQBufs,
   kSFull = kQEmpty + kQBufs,
   kSFree = kSFull + 1,
@@ -89,146 +87,6 @@ __device__ __forceinline__ uint32_t bar_count(int i) {
 }
 constexpr int kSmem = (kQBufs + kKStages + kVStages) * kTile + 1024 + kNumBars * 8 + 16 + 2 * 2 * kRows * 4;
 static_assert(kSmem <= 227 * 1024, "shared memory over the per-block limit");
-
-// The decomposition, decided on the host from sizes alone.
-struct Plan {
-  int G;          // query heads per key head
-  int tb;         // tokens per row block
-  int nqb;        // row blocks per sequence
-  int rb;         // sequences per prefix block (packed), else 1
-  int npb;        // prefix blocks per key head (packed)
-  int pt, ot;     // prefix tiles; own tiles at the largest own length
-  int ct;         // tiles per chunk
-  int nch;        // joint: chunks per unit; packed: chunks of the own keys
-  int nchp;       // packed: chunks of the prefix
-  int packed;
-  int split;      // 1: partials and merge_partials
-  int by_block;   // joint units ordered by row block, last first, before head and sequence
-  int units_p;    // packed: units over the prefix (they come first)
-  int units;
-  int rows_p;     // rows of a prefix block's partial
-  int rows_o;     // rows of a joint / own block's partial
-};
-
-struct Params {
-  Plan pl;
-  Div d_nch, d_nchp, d_nqb, d_npb, d_tb, d_rb, d_ct;  // divisors: the plan's,
-  Div d_B, d_hb, d_G, d_T, d_Hq;                      // B, Hkv B, G, T, Hq
-  int B, T, Hq, Hkv, P, S, causal;
-  const int* own_len;
-  uint16_t* o;
-  long long ob, orow, oh;  // element strides of o
-  float* part;             // partial O rows, 128 floats each
-  float2* ml;              // (maximum in base-2 units, sum) of each partial row
-  int* err;
-};
-
-struct Unit {
-  int h, b0, t0;
-  int p0, pn;      // prefix tiles [p0, p0 + pn)
-  int o0, on;      // own tiles of sequence b0
-  int n;           // pn + on
-  int len;         // own keys of sequence b0
-  int rows;        // rows of the block (the MMA's other rows are ignored)
-  bool clear;      // the last tile holds own rows at or past len
-  long long slot;  // first partial row
-};
-
-__device__ __forceinline__ int own_len_of(const Params& p, int b) {
-  return p.own_len ? min(max(p.own_len[b], 0), p.S) : p.S;
-}
-// own keys that token t of a sequence with `len` own keys sees
-__device__ __forceinline__ int own_lim(const Params& p, int len, int t) {
-  return p.causal ? min(max(len - p.T + t + 1, 0), len) : len;
-}
-__device__ __forceinline__ int own_tiles(const Params& p, int len, int t0, int tb) {
-  return (own_lim(p, len, min(t0 + tb, p.T) - 1) + kKeys - 1) / kKeys;
-}
-
-__device__ __forceinline__ Unit unit_of(const Params& p, int u) {
-  const Plan& pl = p.pl;
-  Unit x;
-  x.p0 = x.pn = x.o0 = x.on = x.len = 0;
-  x.clear = false;
-  if (u < pl.units_p) {  // packed: prefix
-    const int r = quot(p.d_nchp, u), c = u - r * pl.nchp;
-    x.h = quot(p.d_npb, r);
-    x.b0 = (r - x.h * pl.npb) * pl.rb;
-    x.t0 = 0;
-    x.p0 = c * pl.ct;
-    x.pn = min(pl.ct, pl.pt - x.p0);
-    x.rows = pl.rows_p;
-    x.slot = static_cast<long long>(u) * pl.rows_p;
-  } else {
-    const int v = u - pl.units_p;
-    int r = quot(p.d_nch, v);
-    const int c = v - r * pl.nch;
-    int qb;
-    if (pl.by_block) {  // causal: longest first over all heads and sequences
-      const int k = quot(p.d_hb, r);
-      qb = pl.nqb - 1 - k;
-      r -= k * static_cast<int>(p.d_hb.d);
-    } else {
-      const int k = quot(p.d_nqb, r);
-      qb = r - k * pl.nqb;
-      r = k;
-    }
-    x.h = quot(p.d_B, r);
-    x.b0 = r - x.h * p.B;
-    x.t0 = qb * pl.tb;
-    x.len = own_len_of(p, x.b0);
-    const int pt = pl.packed ? 0 : pl.pt;
-    const int tiles = pt + own_tiles(p, x.len, x.t0, pl.tb);
-    const int lo = c * pl.ct;
-    const int hi = min(lo + pl.ct, tiles);
-    if (lo < hi) {
-      x.p0 = min(lo, pt);
-      x.pn = min(hi, pt) - x.p0;
-      x.o0 = max(lo, pt) - pt;
-      x.on = max(hi, pt) - pt - x.o0;
-      x.clear = x.on > 0 && x.len < (x.o0 + x.on) * kKeys && x.len < p.S;
-    }
-    x.rows = pl.rows_o;
-    x.slot = static_cast<long long>(pl.units_p) * pl.rows_p + static_cast<long long>(v) * pl.rows_o;
-  }
-  x.n = x.pn + x.on;
-  return x;
-}
-
-// 4-D tiled load: (dim, head, row, sequence); 5-D: (dim, head of the group, key head, token, sequence)
-__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int h, int row,
-                                            int b) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(h), "r"(row), "r"(b)
-      : "memory");
-}
-__device__ __forceinline__ void tma_load_5d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int g, int h,
-                                            int t, int b) {
-  asm volatile(
-      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(g), "r"(h), "r"(t), "r"(b)
-      : "memory");
-}
-
-__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-
-template <bool BF16>
-__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
-  return BF16 ? pack_bf16x2(lo, hi) : pack_f16x2(lo, hi);
-}
-
-// Maps: Q over (dim, G, Hkv, T, B), once with the prefix block's box and once with
-// the own / joint block's; K and V over (dim, Hkv, rows, sequences), prefix and own.
-struct Maps {
-  CUtensorMap qp, qo, pk, pv, k, v;
-};
 
 template <bool BF16>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -326,7 +184,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             fence_proxy_async_smem();
           }
           __syncwarp();
-          if (lane == 0 && ok) mbar_arrive(&bars[kVClean]);
+          if (lane == 0 && ok) mbar_arrive(&bars[kVClean + st]);
         }
       }
       if (lane == 0) {
@@ -353,8 +211,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = (j > 0 || ku == 0 || mbar_wait(&bars[kOEmpty], (ku - 1) & 1u)) &&
                mbar_wait(&bars[kVFull + st], (t / kVStages) & 1u);
           if (un.clear && j + 1 == un.n) {
-            ok = ok && mbar_wait(&bars[kVClean], cleared & 1u);
-            ++cleared;
+            ok = ok && mbar_wait(&bars[kVClean + st], (cleared >> st) & 1u);
+            cleared ^= 1u << st;  // the stage's phase
           }
           if (!ok) break;
           const uint64_t vd = vdesc0 + ((st * kTile) >> 4);
@@ -745,14 +603,15 @@ __global__ void __launch_bounds__(kMergeWarps * 32) merge_partials(const __grid_
   const long long unit_o =
       (pl.by_block ? (pl.nqb - 1 - qb) * static_cast<long long>(p.Hkv) * p.B + hb : hb * pl.nqb + qb) * pl.nch;
   const long long slot_o =
-      static_cast<long long>(pl.units_p) * pl.rows_p + unit_o * pl.rows_o + (t - qb * pl.tb) * pl.G + g;
-  const int parts_o = quot(p.d_ct, ot + (pl.packed ? 0 : pl.pt) + pl.ct - 1);
+      (static_cast<long long>(pl.units_p) * pl.rows_p + unit_o * pl.rows_o) * pl.per + (t - qb * pl.tb) * pl.G + g;
+  const int parts_o = quot(p.d_ct, ot + (pl.packed ? 0 : pl.pt) + pl.ct - 1) * pl.per;
   long long slot_p = 0;
   int parts_p = 0;
   if (pl.packed) {
     const int pb = quot(p.d_rb, b);
-    slot_p = (static_cast<long long>(h) * pl.npb + pb) * pl.nchp * pl.rows_p + ((b - pb * pl.rb) * p.T + t) * pl.G + g;
-    parts_p = pl.nchp;
+    slot_p =
+        (static_cast<long long>(h) * pl.npb + pb) * pl.nchp * pl.per * pl.rows_p + ((b - pb * pl.rb) * p.T + t) * pl.G + g;
+    parts_p = pl.nchp * pl.per;
   }
   const int n = in ? parts_p + parts_o : 0;
   const auto slot = [&](int i) {
@@ -772,14 +631,15 @@ __global__ void __launch_bounds__(kMergeWarps * 32) merge_partials(const __grid_
     const long long s = slot(i);
     const float2 ml = p.ml[s];
     const float4 v = reinterpret_cast<const float4*>(p.part + s * kHeadDim)[lane];
-    // a chunk in which the row sees no key has m = -inf, sum 0 and O = 0: weight 0, or 1
-    // if no chunk has a key
+    // a part in which the row sees no key has m = -inf and sum 0 (and O may not have been
+    // written); m = -inf with another sum is a row of NaN scores, which stays one
+    const bool none = ml.x == -INFINITY && ml.y == 0.f;
     const float a = m == -INFINITY ? 1.f : fast_exp2(ml.x - m);
-    den += ml.y * a;
-    acc.x += v.x * a;
-    acc.y += v.y * a;
-    acc.z += v.z * a;
-    acc.w += v.w * a;
+    den += none ? 0.f : ml.y * a;
+    acc.x += none ? 0.f : v.x * a;
+    acc.y += none ? 0.f : v.y * a;
+    acc.z += none ? 0.f : v.z * a;
+    acc.w += none ? 0.f : v.w * a;
   }
   if (W > 1) {
     sacc[warp][lane] = acc;
@@ -818,66 +678,80 @@ qi_status op_fail(qi_status st, const char* fmt, ...) {
 int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
 // Chooses the decomposition from sizes alone (own lengths, which only the device
-// knows, count as S). Time is counted in key tiles: a unit costs its tiles plus
-// kUnitTiles for its Q load, pipeline fill and epilogue, and splitting costs
-// kMergeTiles for the partials and the second launch.
-constexpr int kUnitTiles = 3;
-constexpr int kMergeTiles = 6;
+// knows, count as S). Time is counted in key tiles of the 128-row kernel (about 0.9 us):
+// a unit costs its tiles plus kUnitTiles for its Q load, pipeline fill and epilogue, and
+// splitting costs kMergeTiles for the partials and the second launch. The few-row kernel's
+// tiles and units cost less (kFewTile, kFewUnit), and it reads an 8-bit prefix as it is; the
+// others first turn it into 16 bits (kConvert tiles a 2^20 values: written and read again).
 //
 // Order of the joint units: head-major, so that the CTAs running at one time share a few
 // heads' K/V in L2; with `causal`, whose units differ in length, last row blocks first
 // over all heads and sequences, so that the CTAs' sums of lengths agree (3 x 777 rows over
 // 2048 + 1201 keys, 4 key heads: %BYBLOCK%), as long as all K/V stay in half of the L2.
+constexpr float kUnitTiles = 3.f;
+constexpr float kMergeTiles = 5.f;
+constexpr float kFewTile = 0.6f, kFewUnit = 1.5f;
+constexpr float kConvert = 0.5f;
 constexpr long long kL2Half = 64ll << 20;
-Plan make_plan(int B, int T, int Hq, int Hkv, int P, int S, int causal, int sms) {
+struct Sizes {
+  int B, T, Hq, Hkv, P, S, causal;
+  bool from8;
+};
+Plan make_plan(const Sizes& z, int sms) {
   Plan a{};
-  a.by_block = causal && (static_cast<long long>(B) * S + P) * Hkv * kHeadDim * 4 <= kL2Half;
-  a.G = Hq / Hkv;
-  a.tb = kRows / a.G < T ? kRows / a.G : T;
-  a.nqb = ceil_div(T, a.tb);
-  a.pt = ceil_div(P, kKeys);
-  a.ot = ceil_div(S, kKeys);
-  a.rb = 1;
-  a.rows_o = a.tb * a.G;
-  a.rows_p = 0;
+  a.G = z.Hq / z.Hkv;
+  a.by_block = z.causal && (static_cast<long long>(z.B) * z.S + z.P) * z.Hkv * kHeadDim * 4 <= kL2Half;
+  a.pt = ceil_div(z.P, kKeys);
+  a.ot = ceil_div(z.S, kKeys);
+  a.per = 1;
   Plan best = a;
-  long long best_cost = LLONG_MAX;
-  const int n = a.pt + a.ot;
-  const long long blocks = static_cast<long long>(Hkv) * B * a.nqb;
-  // joint: every number of chunks that keeps the grid within a few waves
-  for (int nch = 1; nch <= n; ++nch) {
-    if (nch > 1 && blocks * nch > 4ll * sms) break;  // (at most 4 x SMs rounds of this loop)
-    Plan c = a;
-    c.ct = ceil_div(n, nch);
-    if (ceil_div(n, c.ct) != nch) continue;
-    c.nch = nch;
-    const long long waves = (blocks * nch + sms - 1) / sms;
-    const long long cost = waves * (c.ct + kUnitTiles) + (nch > 1 ? kMergeTiles : 0);
-    if (cost < best_cost && blocks * nch <= INT_MAX) {
-      best_cost = cost;
-      c.split = nch > 1;
-      c.units = static_cast<int>(blocks * nch);
-      best = c;
+  float best_cost = 3e38f;
+  const auto rows_of = [&](Plan& c, int most, bool pack) {
+    c.tb = most / c.G < z.T ? most / c.G : z.T;
+    c.nqb = ceil_div(z.T, c.tb);
+    c.rows_o = c.tb * c.G;
+    c.rb = 1;
+    c.packed = 0;
+    if (pack) {
+      c.packed = 1;
+      c.rb = most / c.rows_o < z.B ? most / c.rows_o : z.B;
+      c.npb = ceil_div(z.B, c.rb);
+      c.rows_p = c.rb * c.rows_o;
     }
-  }
-  // packed: only if two or more sequences' rows fit one block
-  const int rows_seq = T * a.G;
-  if (a.nqb == 1 && B > 1 && P > 0 && 2 * rows_seq <= kRows) {
-    Plan c = a;
-    c.packed = 1;
+  };
+  const float convert = z.from8 && z.P > 0 ? kConvert * static_cast<float>(z.P) * z.Hkv * kHeadDim / (1 << 20) : 0.f;
+  // joint units, every number of chunks that keeps the grid within a few waves
+  const auto joint = [&](Plan c, float tile, float unit, bool always_split, float more) {
+    const int n = c.pt + c.ot;
+    const long long blocks = static_cast<long long>(z.Hkv) * z.B * c.nqb;
+    for (int nch = 1; nch <= n; ++nch) {
+      if (nch > 1 && blocks * nch > 4ll * sms) break;  // (at most 4 x SMs rounds of this loop)
+      c.ct = ceil_div(n, nch);
+      if (ceil_div(n, c.ct) != nch) continue;
+      c.nch = nch;
+      c.split = always_split || nch > 1;
+      const float waves = static_cast<float>((blocks * nch + sms - 1) / sms);
+      const float cost = waves * (c.ct * tile + unit) + (c.split ? kMergeTiles : 0.f) + more;
+      if (cost < best_cost && blocks * nch <= INT_MAX / 2) {
+        best_cost = cost;
+        c.units = static_cast<int>(blocks * nch);
+        best = c;
+      }
+    }
+  };
+  // the prefix once per rb sequences, own keys by sequence
+  const auto packed = [&](Plan c, float tile, float unit, float more) {
     c.split = 1;
-    c.rb = kRows / rows_seq < B ? kRows / rows_seq : B;
-    c.npb = ceil_div(B, c.rb);
-    c.rows_p = c.rb * rows_seq;
-    const int most = a.pt > a.ot ? a.pt : a.ot;
+    const long long blocks = static_cast<long long>(z.Hkv) * z.B;
+    const int most = c.pt > c.ot ? c.pt : c.ot;
     for (int ct = 1; ct <= most; ct += 1 + ct / 32) {
       c.ct = ct;
-      c.nchp = ceil_div(a.pt, ct);
-      c.nch = a.ot ? ceil_div(a.ot, ct) : 1;
-      const long long up = static_cast<long long>(Hkv) * c.npb * c.nchp, uo = a.ot ? blocks * c.nch : 0;
+      c.nchp = ceil_div(c.pt, ct);
+      c.nch = c.ot ? ceil_div(c.ot, ct) : 1;
+      const long long up = static_cast<long long>(z.Hkv) * c.npb * c.nchp, uo = c.ot ? blocks * c.nch : 0;
       if (up + uo > INT_MAX / 2) continue;
-      const long long tiles = static_cast<long long>(Hkv) * c.npb * a.pt + blocks * a.ot + (up + uo) * kUnitTiles;
-      const long long cost = (tiles + sms - 1) / sms + ct / 2 + kMergeTiles;
+      const float tiles = static_cast<float>(static_cast<long long>(z.Hkv) * c.npb * c.pt + blocks * c.ot);
+      const float cost = (tiles * tile + static_cast<float>(up + uo) * unit) / sms + ct * tile / 2 + unit + kMergeTiles + more;
       if (cost < best_cost) {
         best_cost = cost;
         c.units_p = static_cast<int>(up);
@@ -885,14 +759,53 @@ Plan make_plan(int B, int T, int Hq, int Hkv, int P, int S, int causal, int sms)
         best = c;
       }
     }
+  };
+  Plan c = a;
+  rows_of(c, kRows, false);
+  joint(c, 1.f, kUnitTiles, false, convert);
+  const int rows_seq = z.T * a.G;
+  // packed: only if two or more sequences' rows fit one block
+  if (z.P > 0 && z.B > 1 && 2 * rows_seq <= kRows) {
+    rows_of(c, kRows, true);
+    packed(c, 1.f, kUnitTiles, convert);
+  }
+  if (rows_seq <= kFewRows) {
+    c = a;
+    c.few = 1;
+    c.per = 2;
+    rows_of(c, kFewRows, false);
+    joint(c, kFewTile, kFewUnit, true, 0.f);
+    if (z.P > 0 && z.B > 1) {
+      rows_of(c, kFewRows, true);
+      packed(c, kFewTile, kFewUnit, 0.f);
+    }
   }
   return best;
 }
 
+// make_plan weighs hundreds of candidates, which takes longer than a launch: each thread keeps
+// the plans of the sizes it met last.
+Plan plan_for(const Sizes& z, int sms) {
+  struct Entry {
+    Sizes z;
+    int sms;
+    Plan plan;
+  };
+  static thread_local Entry kept[16];
+  unsigned h = static_cast<unsigned>(z.B);
+  for (int v : {z.T, z.Hq, z.Hkv, z.P, z.S, z.causal * 2 + (z.from8 ? 1 : 0), sms})
+    h = h * 0x9E3779B1u + static_cast<unsigned>(v);
+  Entry& e = kept[(h ^ (h >> 16)) & 15u];
+  if (e.sms != sms || e.z.B != z.B || e.z.T != z.T || e.z.Hq != z.Hq || e.z.Hkv != z.Hkv || e.z.P != z.P ||
+      e.z.S != z.S || e.z.causal != z.causal || e.z.from8 != z.from8)
+    e = Entry{z, sms, make_plan(z, sms)};
+  return e.plan;
+}
+
 size_t align256(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
 size_t partial_rows(const Plan& pl) {
-  return pl.split ? static_cast<size_t>(pl.units_p) * pl.rows_p +
-                        static_cast<size_t>(pl.units - pl.units_p) * pl.rows_o
+  return pl.split ? (static_cast<size_t>(pl.units_p) * pl.rows_p +
+                     static_cast<size_t>(pl.units - pl.units_p) * pl.rows_o) * pl.per
                   : 0;
 }
 // workspace: the prefix in 16 bits (8-bit prefix only), partial O rows, their (max, sum)
@@ -901,7 +814,7 @@ struct WsLayout {
 };
 WsLayout ws_layout(const Plan& pl, int P, int Hkv, bool from8) {
   WsLayout w{};
-  const size_t pre = from8 ? align256(static_cast<size_t>(P) * Hkv * kHeadDim * 2) : 0;
+  const size_t pre = from8 && !pl.few ? align256(static_cast<size_t>(P) * Hkv * kHeadDim * 2) : 0;
   const size_t rows = partial_rows(pl);
   w.pk = 0;
   w.pv = pre;
@@ -924,7 +837,15 @@ bool map_kv(CUtensorMap* m, const qi_tensor4& t, int heads, int rows, int batch)
                                      static_cast<unsigned long long>(t.row) * 2,
                                      static_cast<unsigned long long>(t.batch) * 2};
   const unsigned box[4] = {64, 1, kKeys, 1};
-  return encode_map16_nd(m, t.data, 4, dims, str, box);
+  return encode_map_nd(m, t.data, false, 4, dims, str, box);
+}
+
+bool map_codes(CUtensorMap* m, const uint8_t* codes, int heads, int rows) {
+  const unsigned long long dims[3] = {kHeadDim, static_cast<unsigned long long>(heads),
+                                      static_cast<unsigned long long>(rows)};
+  const unsigned long long str[2] = {kHeadDim, static_cast<unsigned long long>(heads) * kHeadDim};
+  const unsigned box[3] = {kHeadDim, 1, kKeys};
+  return encode_map_nd(m, codes, true, 3, dims, str, box);
 }
 
 bool map_q(CUtensorMap* m, const qi_tensor4& t, int G, int Hkv, int T, int B, int tb, int rb) {
@@ -935,7 +856,7 @@ bool map_q(CUtensorMap* m, const qi_tensor4& t, int G, int Hkv, int T, int B, in
       static_cast<unsigned long long>(t.head) * 2, static_cast<unsigned long long>(t.head) * G * 2,
       static_cast<unsigned long long>(t.row) * 2, static_cast<unsigned long long>(t.batch) * 2};
   const unsigned box[5] = {64, static_cast<unsigned>(G), 1, static_cast<unsigned>(tb), static_cast<unsigned>(rb)};
-  return encode_map16_nd(m, t.data, 5, dims, str, box);
+  return encode_map_nd(m, t.data, false, 5, dims, str, box);
 }
 
 qi_status check_sizes(const qi_prefix_attn* a) {
@@ -952,17 +873,22 @@ qi_status check_sizes(const qi_prefix_attn* a) {
 }
 
 template <bool BF16>
-cudaError_t launch(const Maps& tm, const Params& p, float scale_log2, int sms, cudaStream_t stream) {
-  static std::atomic<unsigned long long> attr_done{0};
-  cudaError_t e = ensure_smem_limit(prefix_attn_tc<BF16>, kSmem, attr_done);
-  if (e != cudaSuccess) return e;
-  const int grid = p.pl.units < sms ? p.pl.units : sms;
-  e = launch_dependent(prefix_attn_tc<BF16>, dim3(grid), dim3(kThreads), kSmem, stream, tm, p, scale_log2);
+cudaError_t launch(const Maps& tm, const Maps8* t8, const Params& p, float scale_log2, int sms, cudaStream_t stream) {
+  cudaError_t e;
+  if (p.pl.few) {
+    e = launch_few(tm, t8, p, BF16, scale_log2, sms, stream);
+  } else {
+    static std::atomic<unsigned long long> attr_done{0};
+    e = ensure_smem_limit(prefix_attn_tc<BF16>, kSmem, attr_done);
+    if (e != cudaSuccess) return e;
+    const int grid = p.pl.units < sms ? p.pl.units : sms;
+    e = launch_dependent(prefix_attn_tc<BF16>, dim3(grid), dim3(kThreads), kSmem, stream, tm, p, scale_log2);
+  }
   if (e != cudaSuccess || !p.pl.split) return e;
   // Warps per row: as many as its parts keep busy, unless the rows alone fill the GPU (1024
   // rows of 16 parts: %MERGE%)
   const long long rows = static_cast<long long>(p.B) * p.T * p.Hq;
-  const int parts = p.pl.packed ? p.pl.nchp + p.pl.nch : p.pl.nch;
+  const int parts = (p.pl.packed ? p.pl.nchp + p.pl.nch : p.pl.nch) * p.pl.per;
   const int w = rows > 16384 || parts < 4 ? 1 : parts < 16 ? 4 : 8;
   const auto kernel = w == 1 ? merge_partials<BF16, 1> : w == 4 ? merge_partials<BF16, 4> : merge_partials<BF16, 8>;
   const long long per = kMergeWarps / w;
@@ -993,7 +919,7 @@ extern "C" size_t qi_prefix_attention_workspace(const qi_prefix_attn* a) {
   if (check_sizes(a) != QI_OK) return 0;
   const int sms = device_sms();
   if (sms <= 0) return 0;
-  const Plan pl = make_plan(a->B, a->T, a->Hq, a->Hkv, a->P, a->S, a->causal, sms);
+  const Plan pl = plan_for({a->B, a->T, a->Hq, a->Hkv, a->P, a->S, a->causal != 0, a->P > 0 && a->pk8 != nullptr}, sms);
   return ws_layout(pl, a->P, a->Hkv, a->P > 0 && a->pk8 != nullptr).total;
 }
 
@@ -1028,16 +954,17 @@ extern "C" qi_status qi_prefix_attention(const qi_prefix_attn* a, qi_stream_t st
     return op_fail(QI_ERR_INVALID_ARG, "qi_prefix_attention: the 8-bit prefix needs 16-byte aligned codes and 4-byte aligned scales");
   const int sms = device_sms();
   if (sms <= 0) return op_fail(QI_ERR_CUDA, "qi_prefix_attention: no CUDA device");
-  const Plan pl = make_plan(a->B, a->T, a->Hq, a->Hkv, a->P, a->S, a->causal, sms);
+  const Plan pl = plan_for({a->B, a->T, a->Hq, a->Hkv, a->P, a->S, a->causal != 0, a->P > 0 && a->pk8 != nullptr}, sms);
   if (pl.units <= 0) return op_fail(QI_ERR_SHAPE, "qi_prefix_attention: too many rows and heads");
   const bool pre8 = a->P > 0 && from8;
+  const bool convert = pre8 && !pl.few;  // the prefix goes through 16 bits in the workspace
   const WsLayout w = ws_layout(pl, a->P, a->Hkv, pre8);
   if (w.total > 0 && (!a->ws || a->ws_bytes < w.total || (reinterpret_cast<uintptr_t>(a->ws) & 255)))
     return op_fail(QI_ERR_INVALID_ARG, "qi_prefix_attention: needs a 256-byte aligned workspace of %zu bytes", w.total);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const bool bf16 = a->dtype == QI_DT_BF16;
   uint8_t* ws = static_cast<uint8_t*>(a->ws);
-  if (pre8) {
+  if (convert) {
     // the prefix in 16 bits, once for all row blocks
     Kv8Args r{};
     r.B = 1;
@@ -1056,7 +983,17 @@ extern "C" qi_status qi_prefix_attention(const qi_prefix_attn* a, qi_stream_t st
   Maps tm;
   bool ok = map_q(&tm.qo, q, pl.G, a->Hkv, a->T, a->B, pl.tb, 1) &&
             (pl.packed ? map_q(&tm.qp, q, pl.G, a->Hkv, a->T, a->B, pl.tb, pl.rb) : (tm.qp = tm.qo, true));
-  if (a->P > 0) ok = ok && map_kv(&tm.pk, pk, a->Hkv, a->P, 1) && map_kv(&tm.pv, pv, a->Hkv, a->P, 1);
+  Maps8 t8;
+  const Maps8* use8 = nullptr;
+  if (pre8 && !convert) {
+    ok = ok && map_codes(&t8.k, a->pk8, a->Hkv, a->P) && map_codes(&t8.v, a->pv8, a->Hkv, a->P);
+    t8.k_sf = a->pk_sf;
+    t8.v_sf = a->pv_sf;
+    use8 = &t8;
+    tm.pk = tm.pv = tm.qo;  // never loaded from
+  } else if (a->P > 0) {
+    ok = ok && map_kv(&tm.pk, pk, a->Hkv, a->P, 1) && map_kv(&tm.pv, pv, a->Hkv, a->P, 1);
+  }
   if (a->S > 0) ok = ok && map_kv(&tm.k, k, a->Hkv, a->S, a->B) && map_kv(&tm.v, v, a->Hkv, a->S, a->B);
   if (!ok) return op_fail(QI_ERR_INVALID_ARG, "qi_prefix_attention: tensor map encoding failed (strides?)");
   if (a->P == 0) tm.pk = tm.k, tm.pv = tm.v;  // never loaded from
@@ -1091,7 +1028,7 @@ extern "C" qi_status qi_prefix_attention(const qi_prefix_attn* a, qi_stream_t st
   p.ml = reinterpret_cast<float2*>(ws + w.ml);
   p.err = a->status;
   const float scale_log2 = a->scale * 1.4426950408889634f;
-  const cudaError_t e = bf16 ? launch<true>(tm, p, scale_log2, sms, s) : launch<false>(tm, p, scale_log2, sms, s);
+  const cudaError_t e = bf16 ? launch<true>(tm, use8, p, scale_log2, sms, s) : launch<false>(tm, use8, p, scale_log2, sms, s);
   if (e != cudaSuccess) return op_fail(QI_ERR_CUDA, "qi_prefix_attention: %s", cudaGetErrorString(e));
   return QI_OK;
 }

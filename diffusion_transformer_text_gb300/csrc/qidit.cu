@@ -670,8 +670,8 @@ bool qi::encode_map8(CUtensorMap* m, const void* base, uint64_t rows, uint64_t c
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-bool qi::encode_map16_nd(CUtensorMap* m, const void* base, int rank, const unsigned long long* dims,
-                         const unsigned long long* strides, const unsigned* box) {
+bool qi::encode_map_nd(CUtensorMap* m, const void* base, bool bytes, int rank, const unsigned long long* dims,
+                       const unsigned long long* strides, const unsigned* box) {
   EncodeTiledFn enc = encode_fn();
   if (!enc) return false;
   cuuint64_t d[5], st[4];
@@ -682,8 +682,9 @@ bool qi::encode_map16_nd(CUtensorMap* m, const void* base, int rank, const unsig
     estr[i] = 1;
     if (i + 1 < rank) st[i] = strides[i];
   }
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, static_cast<cuuint32_t>(rank), const_cast<void*>(base), d, st, b, estr,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+  return enc(m, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, static_cast<cuuint32_t>(rank),
+             const_cast<void*>(base), d, st, b, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             bytes ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

@@ -137,6 +137,12 @@ CASES = [
     dict(B=1, T=1, Hq=2, Hkv=1, P=5000, S=1300, lens=[1257], causal=True),        # split over the keys
     dict(B=20, T=1, Hq=4, Hkv=4, P=2000, S=30, causal=True, lens=list(range(1, 21))),
     dict(B=2, T=4, Hq=4, Hkv=2, P=9, S=12, lens=[2000000000, -7]),                # lengths are clamped
+    # several units per block: codes after own tiles and the other way round, runs of one-tile units
+    dict(B=16, T=1, Hq=32, Hkv=32, P=700, S=256, lens=[256 - 15 * i for i in range(16)], causal=True),
+    dict(B=1, T=1, Hq=200, Hkv=200, P=300, S=300, lens=[290]),
+    dict(B=40, T=1, Hq=8, Hkv=8, P=1, S=100, lens=[(37 * i) % 101 for i in range(40)]),
+    dict(B=3, T=64, Hq=60, Hkv=60, P=100, S=64, lens=[64, 1, 40], causal=True),
+    dict(B=30, T=20, Hq=12, Hkv=12, P=0, S=90, lens=[(31 * i) % 91 for i in range(30)]),
 ]
 
 
@@ -147,7 +153,7 @@ def test_attention(qi, case, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["fp16", "bf16"])
-@pytest.mark.parametrize("case", [c for c in CASES if c["P"] > 0][::2], ids=lambda c: f"P{c['P']}-T{c['T']}-B{c['B']}")
+@pytest.mark.parametrize("case", [c for c in CASES if c["P"] > 0][::2] + CASES[-5:-1], ids=lambda c: f"P{c['P']}-T{c['T']}-B{c['B']}")
 def test_attention_8bit_prefix(qi, case, dtype):
     _check_attention(qi, dtype=dtype, bits=8, seed=case["B"] * 100 + case["P"], **case)
 
