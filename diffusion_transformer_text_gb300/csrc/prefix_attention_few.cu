@@ -76,6 +76,9 @@ struct Exchange {
   float nm[8][kR], alpha[8][kR];
   int lim[8][kR];
   uint32_t issued[3][5];
+  uint32_t pad;
+  uint32_t scales[2][2][kKeys];  // [K, V][tile parity] a row's four scale bytes,
+  uint2 halves[2][2][kKeys];     // and their half_scale
 };
 template <bool Q8>
 constexpr int smem_bytes() {
@@ -114,38 +117,39 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, u
       : "memory");
 }
 
-// 16 codes times 2^(scale - 127), rounded to the 16-bit type: two 16-byte pieces. A code has 4
-// significant bits, so the product is exact in fp32, and in half precision wherever 2^e is a
-// half and the result not subnormal; other exponents take the fp32 way.
-template <bool BF16>
-__device__ __forceinline__ void codes_to_16bit(uint4 c, uint32_t scale, uint4 (&out)[2]) {
-  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-  const int e = static_cast<int>(scale) - 127;
-  uint32_t r[8];
-  if (!BF16 && e >= -24 && e <= 15) {
-    // 2^e in half precision, subnormal below 2^-14
-    const uint32_t bits = e >= -14 ? static_cast<uint32_t>(e + 15) << 10 : 1u << (e + 24);
-    const uint32_t pair = bits | (bits << 16);
+// 2^e as a half, for the exponents with which code * 2^e can be formed in half precision (codes
+// have 4 significant bits: the product is exact or, below 2^-14, rounded once); kNoHalf else.
+constexpr uint32_t kNoHalf = 0xFFFFu;
+__device__ __forceinline__ uint32_t half_scale(uint32_t byte) {
+  const int e = static_cast<int>(byte) - 127;
+  return e < -24 || e > 15 ? kNoHalf : e >= -14 ? static_cast<uint32_t>(e + 15) << 10 : 1u << (e + 24);
+}
+
+// 8 codes times their scale, rounded to the 16-bit type: in half precision by half_scale's value
+// if HALF, else in fp32 by the scale byte
+template <bool BF16, bool HALF>
+__device__ __forceinline__ uint4 codes_to_16bit(uint2 c, uint32_t scale) {
+  const uint32_t w[4] = {c.x & 0xFFFFu, c.x >> 16, c.y & 0xFFFFu, c.y >> 16};
+  uint32_t r[4];
+  if (HALF) {
+    const uint32_t pair = scale | (scale << 16);
     const __half2 s = *reinterpret_cast<const __half2*>(&pair);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
-          static_cast<__nv_fp8x2_storage_t>((i & 1) ? w[i / 2] >> 16 : w[i / 2] & 0xFFFFu), __NV_E4M3);
-      const __half2 v = __hmul2(__half2(h), s);
+    for (int i = 0; i < 4; ++i) {
+      const __half2 v =
+          __hmul2(__half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w[i]), __NV_E4M3)), s);
       r[i] = *reinterpret_cast<const uint32_t*>(&v);
     }
   } else {
-    const float s = scale == 0 ? __uint_as_float(0x00400000u) : __uint_as_float(scale << 23);
+    const float s = __uint_as_float(scale == 0 ? 0x00400000u : scale << 23);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
-          static_cast<__nv_fp8x2_storage_t>((i & 1) ? w[i / 2] >> 16 : w[i / 2] & 0xFFFFu), __NV_E4M3);
-      const float2 f = __half22float2(__half2(h));
+    for (int i = 0; i < 4; ++i) {
+      const float2 f =
+          __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w[i]), __NV_E4M3)));
       r[i] = pack16<BF16>(f.x * s, f.y * s);
     }
   }
-  out[0] = make_uint4(r[0], r[1], r[2], r[3]);
-  out[1] = make_uint4(r[4], r[5], r[6], r[7]);
+  return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
 template <bool BF16, bool Q8>
@@ -493,46 +497,71 @@ __global__ void __launch_bounds__(Cfg<Q8>::kThreads, 1)
     }
     if (!ok && lane == 0) give_up(kErrTimeoutEpilogue);
   } else if constexpr (Q8) {
-    // ---------------- codes to 16 bits: warps 12..15 K, 16..19 V; eight lanes per row
+    // ---------------- codes to 16 bits: warps 12..15 K, 16..19 V. Sixteen lanes per row, 8 codes
+    // each: a 16-byte piece of the swizzled tile per lane, eight lanes to a 128-byte line (with 16
+    // codes a lane, two pieces, the stores met in the banks: shared memory is what bounds this
+    // kernel, %FEW8%)
     const int kv = warp >= 16 ? 1 : 0;
     const int tid = (warp & 3) * 32 + lane;
-    const int chunk = tid & 7, r0 = tid >> 3;
-    const uint8_t* sf = kv ? t8.v_sf : t8.k_sf;
+    const int chunk = tid & 15, r0 = tid >> 4;  // rows r0 + 8 i
+    const uint8_t* sf = kv ? t8.v_sf : t8.k_sf;  // 4-byte aligned
     uint8_t* tiles = sT + kv * kSt * kTile;
     const uint8_t* codes = sC + kv * kCSt * kCode;
-    const auto scale_of = [&](const Unit& un, int tile, int i) -> uint32_t {
-      const int row = tile * kKeys + r0 + 16 * i;
-      return row < p.P ? sf[(static_cast<long long>(row) * p.Hkv + un.h) * 4 + (chunk >> 1)] : 127u;
+    // A thread fetches the four scale bytes of one row a tile ahead, and they go round by shared
+    // memory: 128 loads a tile instead of 1024.
+    const uint32_t* sf4 = reinterpret_cast<const uint32_t*>(sf);
+    const auto scales_of = [&](const Unit& un, int tile) -> uint32_t {
+      const int row = tile * kKeys + tid;
+      return row < p.P ? sf4[static_cast<long long>(row) * p.Hkv + un.h] : 0u;  // past the end: zero codes
+    };
+    const auto keep = [&](uint32_t parity, uint32_t bytes) {
+      ex.scales[kv][parity][tid] = bytes;
+      if (!BF16)
+        ex.halves[kv][parity][tid] =
+            make_uint2(half_scale(bytes & 255u) | half_scale((bytes >> 8) & 255u) << 16,
+                       half_scale((bytes >> 16) & 255u) | half_scale(bytes >> 24) << 16);
     };
     uint32_t t = 0, tc = 0;
     bool ok = true;
     for (int u = blockIdx.x; u < total; u += gridDim.x) {
       const Unit un = unit_of(p, u);
-      uint32_t next[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) next[i] = un.pn > 0 ? scale_of(un, un.p0, i) : 0u;
+      if (un.pn > 0) {
+        keep(tc & 1u, scales_of(un, un.p0));
+        warpgroup_sync(3 + kv);
+      }
       for (int j = 0; j < un.pn; ++j, ++tc) {
         const uint32_t tt = t + j, st = tt % kSt, cs = tc % kCSt;
-        uint32_t sc[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          sc[i] = next[i];
-          next[i] = j + 1 < un.pn ? scale_of(un, un.p0 + j + 1, i) : 0u;
-        }
+        const uint32_t ahead = j + 1 < un.pn ? scales_of(un, un.p0 + j + 1) : 0u;
         ok = ok && __all_sync(0xffffffffu, mbar_wait(&bars[kCFull + 2 * kv + cs], (tc / kCSt) & 1u)) &&
              __all_sync(0xffffffffu, mbar_wait(&bars[kGrant + 2 * kv + cs], (tc / kCSt) & 1u));
-        const uint8_t* src = codes + cs * kCode + tid * 16;
-        uint8_t* dst = tiles + st * kTile + (chunk >> 2) * kBox + r0 * 128;
         if (ok) {
+          const uint8_t* src = codes + cs * kCode + tid * 8;
+          uint8_t* dst = tiles + st * kTile + (chunk >> 3) * kBox + r0 * 128 + (((chunk & 7) ^ r0) << 4);
+          const uint8_t* bytes = reinterpret_cast<const uint8_t*>(&ex.scales[kv][tc & 1u][r0]) + (chunk >> 2);
+          const uint16_t* halves = reinterpret_cast<const uint16_t*>(&ex.halves[kv][tc & 1u][r0]) + (chunk >> 2);
+          // fp16: in half precision, unless a scale of the warp's rows does not allow it (decided
+          // for the whole tile: a branch for each piece took a third of the time)
+          uint32_t h[16], worst = 0;
+          if (!BF16) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            uint4 o[2];
-            codes_to_16bit<BF16>(*reinterpret_cast<const uint4*>(src + i * 2048), sc[i], o);
-            const int x = (r0 + 16 * i) & 7, c = (chunk & 3) * 2;
-            *reinterpret_cast<uint4*>(dst + i * 2048 + ((c ^ x) << 4)) = o[0];
-            *reinterpret_cast<uint4*>(dst + i * 2048 + (((c + 1) ^ x) << 4)) = o[1];
+            for (int i = 0; i < 16; ++i) {
+              h[i] = halves[i * 32];
+              worst = max(worst, h[i]);
+            }
+          }
+          if (!BF16 && !__any_sync(0xffffffffu, worst == kNoHalf)) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              *reinterpret_cast<uint4*>(dst + i * 1024) =
+                  codes_to_16bit<BF16, !BF16>(*reinterpret_cast<const uint2*>(src + i * 1024), h[i]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              *reinterpret_cast<uint4*>(dst + i * 1024) =
+                  codes_to_16bit<BF16, false>(*reinterpret_cast<const uint2*>(src + i * 1024), bytes[i * 32]);
           }
         }
+        keep((tc & 1u) ^ 1u, ahead);
         fence_proxy_async_smem();
         warpgroup_sync(3 + kv);
         if (tid == 0 && ok) {
