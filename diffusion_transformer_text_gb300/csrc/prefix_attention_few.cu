@@ -47,12 +47,11 @@ struct Cfg {
 
 // mbarriers; [K, V] where a pair is meant
 enum : int {
-  kFull = 0,                     // [K, V][3] 16-bit tile in place
+  kFull = 0,                     // [K, V][3] 16-bit tile in place (producer; with kQ8 also 4 converting warps)
   kEmpty = kFull + 6,            // [K, V][3] ... read by its product
   kCFull = kEmpty + 6,           // [K, V][2] codes in place
-  kCEmpty = kCFull + 4,          // [K, V][2] ... turned into 16 bits
-  kGrant = kCEmpty + 4,          // [K, V][2] the 16-bit stage of a tile of codes is free
-  kVClean = kGrant + 4,          // [3] rows past own_len of a unit's last V tile cleared
+  kCEmpty = kCFull + 4,          // [K, V][2] ... turned into 16 bits (4 warps)
+  kVClean = kCEmpty + 4,         // [3] rows past own_len of a unit's last V tile cleared
   kQFull = kVClean + 3,
   kQEmpty = kQFull + kQBufs,
   kSFull = kQEmpty + kQBufs,
@@ -64,8 +63,13 @@ enum : int {
   kNumBars = kDrainPV + 1
 };
 constexpr int kBarSlots = (kNumBars + 1) & ~1;  // what follows is read in 16-byte pieces
+template <bool Q8>
 __device__ __forceinline__ uint32_t bar_count(int i) {
-  return (i >= kSFree && i < kSFree + kSBufs) || (i >= kPFull && i < kPFull + kSBufs) ? 4 : 1;
+  if (i < kFull + 6) return Q8 ? 5 : 1;
+  return (i >= kCEmpty && i < kCEmpty + 4) || (i >= kSFree && i < kSFree + kSBufs) ||
+                 (i >= kPFull && i < kPFull + kSBufs)
+             ? 4
+             : 1;
 }
 
 // per softmax warpgroup: maxima by [tile parity][warp][row], sums by [warp][row]; per warp:
@@ -77,8 +81,8 @@ struct Exchange {
   int lim[8][kR];
   uint32_t issued[3][5];
   uint32_t pad;
-  uint32_t scales[2][2][kKeys];  // [K, V][tile parity] a row's four scale bytes,
-  uint2 halves[2][2][kKeys];     // and their half_scale
+  uint32_t scales[8][2][32];  // [converting warp][tile parity] the four scale bytes of its rows,
+  uint2 halves[8][2][32];     // and their half_scale
 };
 template <bool Q8>
 constexpr int smem_bytes() {
@@ -181,7 +185,7 @@ __global__ void __launch_bounds__(Cfg<Q8>::kThreads, 1)
   };
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kNumBars; ++i) mbar_init(&bars[i], bar_count(i));
+    for (int i = 0; i < kNumBars; ++i) mbar_init(&bars[i], bar_count<Q8>(i));
     *abort_flag = 0;
     for (int i = 0; i < 15; ++i) ex.issued[i / 5][i % 5] = 0;
     fence_barrier_init();
@@ -215,7 +219,7 @@ __global__ void __launch_bounds__(Cfg<Q8>::kThreads, 1)
     // ---------------- producers: K tiles and Q (warp 0), V tiles (warp 2). Lane 0 works; warp 2
     // clears V rows past own_len as a whole, so every lane walks the units.
     const int kv = warp == 0 ? 0 : 1;
-    uint32_t t = 0, tc = 0, tg = 0, nq = 0;  // tiles; code tiles requested, granted; Q blocks
+    uint32_t t = 0, tc = 0, nq = 0;  // tiles; of which requested as codes; Q blocks
     uint64_t* full = &bars[kFull + 3 * kv];
     uint64_t* empty = &bars[kEmpty + 3 * kv];
     uint64_t* cfull = &bars[kCFull + 2 * kv];
@@ -241,9 +245,10 @@ __global__ void __launch_bounds__(Cfg<Q8>::kThreads, 1)
             issued[2][qb] = ++nq;
           }
         }
-        // Codes are requested a tile ahead of their turn. The 16-bit stage of every tile, turned
-        // from codes or loaded as it is, is waited for here and in order (a barrier's parity only
-        // tells the phases apart to who has seen them all), and granted to the converters.
+        // Codes are requested two tiles ahead of their turn. Of every tile, turned from codes or
+        // loaded as it is, the producer and the converting warps each wait for the 16-bit stage and
+        // then arrive on it: a barrier's parity tells the phases apart only to who sees them all,
+        // and none of them can be passed over this way.
         const auto request = [&](int j) {
           const uint32_t cs = tc % kCSt;
           if (!mbar_wait(&cempty[cs], ((tc / kCSt) & 1u) ^ 1u)) return false;
@@ -252,16 +257,15 @@ __global__ void __launch_bounds__(Cfg<Q8>::kThreads, 1)
           issued[kv][3 + cs] = ++tc;
           return true;
         };
-        if (Q8 && ok && un.pn > 0) ok = request(0);
+        if (Q8 && ok && un.pn > 0) ok = request(0) && (un.pn < 2 || request(1));
         for (int j = 0; ok && j < un.n; ++j) {
           const uint32_t tt = t + j, st = tt % kSt;
           const bool pre = j < un.pn;
-          if (Q8 && j + 1 < un.pn) ok = request(j + 1);
-          ok = ok && mbar_wait(&empty[st], ((tt / kSt) & 1u) ^ 1u);
+          ok = mbar_wait(&empty[st], ((tt / kSt) & 1u) ^ 1u);
           if (!ok) break;
           if (Q8 && pre) {
-            mbar_arrive(&bars[kGrant + 2 * kv + tg % kCSt]);
-            ++tg;
+            mbar_arrive(&full[st]);
+            if (j + 2 < un.pn) ok = request(j + 2);
           } else {
             const CUtensorMap* m = pre ? pre_map : own_map;
             const int row = (pre ? un.p0 + j : un.o0 + j - un.pn) * kKeys;
@@ -507,17 +511,19 @@ __global__ void __launch_bounds__(Cfg<Q8>::kThreads, 1)
     const uint8_t* sf = kv ? t8.v_sf : t8.k_sf;  // 4-byte aligned
     uint8_t* tiles = sT + kv * kSt * kTile;
     const uint8_t* codes = sC + kv * kCSt * kCode;
-    // A thread fetches the four scale bytes of one row a tile ahead, and they go round by shared
-    // memory: 128 loads a tile instead of 1024.
+    // The warps of a tile do not wait for each other. A warp's 32 rows are 2 w + (0, 1) + 8 i; lane
+    // 2 i + (0, 1) fetches that row's four scale bytes a tile ahead (one load a lane), and they go
+    // round by shared memory.
+    const int cw = warp - 12;
     const uint32_t* sf4 = reinterpret_cast<const uint32_t*>(sf);
     const auto scales_of = [&](const Unit& un, int tile) -> uint32_t {
-      const int row = tile * kKeys + tid;
+      const int row = tile * kKeys + 2 * (warp & 3) + (lane & 1) + 8 * (lane >> 1);
       return row < p.P ? sf4[static_cast<long long>(row) * p.Hkv + un.h] : 0u;  // past the end: zero codes
     };
     const auto keep = [&](uint32_t parity, uint32_t bytes) {
-      ex.scales[kv][parity][tid] = bytes;
+      ex.scales[cw][parity][lane] = bytes;
       if (!BF16)
-        ex.halves[kv][parity][tid] =
+        ex.halves[cw][parity][lane] =
             make_uint2(half_scale(bytes & 255u) | half_scale((bytes >> 8) & 255u) << 16,
                        half_scale((bytes >> 16) & 255u) | half_scale(bytes >> 24) << 16);
     };
@@ -527,47 +533,55 @@ __global__ void __launch_bounds__(Cfg<Q8>::kThreads, 1)
       const Unit un = unit_of(p, u);
       if (un.pn > 0) {
         keep(tc & 1u, scales_of(un, un.p0));
-        warpgroup_sync(3 + kv);
+        __syncwarp();
       }
-      for (int j = 0; j < un.pn; ++j, ++tc) {
+      for (int j = 0; j < un.n; ++j) {
         const uint32_t tt = t + j, st = tt % kSt, cs = tc % kCSt;
+        ok = ok && __all_sync(0xffffffffu, mbar_wait(&bars[kEmpty + 3 * kv + st], ((tt / kSt) & 1u) ^ 1u));
+        if (j >= un.pn) {  // an own tile: nothing to turn
+          if (lane == 0 && ok) mbar_arrive(&bars[kFull + 3 * kv + st]);
+          continue;
+        }
         const uint32_t ahead = j + 1 < un.pn ? scales_of(un, un.p0 + j + 1) : 0u;
-        ok = ok && __all_sync(0xffffffffu, mbar_wait(&bars[kCFull + 2 * kv + cs], (tc / kCSt) & 1u)) &&
-             __all_sync(0xffffffffu, mbar_wait(&bars[kGrant + 2 * kv + cs], (tc / kCSt) & 1u));
+        ok = ok && __all_sync(0xffffffffu, mbar_wait(&bars[kCFull + 2 * kv + cs], (tc / kCSt) & 1u));
         if (ok) {
           const uint8_t* src = codes + cs * kCode + tid * 8;
           uint8_t* dst = tiles + st * kTile + (chunk >> 3) * kBox + r0 * 128 + (((chunk & 7) ^ r0) << 4);
-          const uint8_t* bytes = reinterpret_cast<const uint8_t*>(&ex.scales[kv][tc & 1u][r0]) + (chunk >> 2);
-          const uint16_t* halves = reinterpret_cast<const uint16_t*>(&ex.halves[kv][tc & 1u][r0]) + (chunk >> 2);
-          // fp16: in half precision, unless a scale of the warp's rows does not allow it (decided
-          // for the whole tile: a branch for each piece took a third of the time)
-          uint32_t h[16], worst = 0;
-          if (!BF16) {
+          const uint8_t* bytes = reinterpret_cast<const uint8_t*>(&ex.scales[cw][tc & 1u][lane >> 4]) + (chunk >> 2);
+          const uint16_t* halves = reinterpret_cast<const uint16_t*>(&ex.halves[cw][tc & 1u][lane >> 4]) + (chunk >> 2);
+          // All loads before the first store: nothing tells the compiler that the two do not
+          // overlap, and a piece at a time took 110 cycles a piece.
+          uint2 c[16];
+          uint32_t h[16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              h[i] = halves[i * 32];
-              worst = max(worst, h[i]);
-            }
+          for (int i = 0; i < 16; ++i) {
+            c[i] = *reinterpret_cast<const uint2*>(src + i * 1024);
+            h[i] = BF16 ? static_cast<uint32_t>(bytes[i * 8]) : halves[i * 8];
           }
-          if (!BF16 && !__any_sync(0xffffffffu, worst == kNoHalf)) {
+          // fp16: in half precision, unless a scale of the warp's rows does not allow it (decided
+          // for the whole tile)
+          uint32_t worst = 0;
 #pragma unroll
+          for (int i = 0; i < 16; ++i) worst = max(worst, h[i]);
+          if (!BF16 && __any_sync(0xffffffffu, worst == kNoHalf)) {
+#pragma unroll 1
             for (int i = 0; i < 16; ++i)
               *reinterpret_cast<uint4*>(dst + i * 1024) =
-                  codes_to_16bit<BF16, !BF16>(*reinterpret_cast<const uint2*>(src + i * 1024), h[i]);
+                  codes_to_16bit<BF16, false>(*reinterpret_cast<const uint2*>(src + i * 1024), bytes[i * 8]);
           } else {
 #pragma unroll
             for (int i = 0; i < 16; ++i)
-              *reinterpret_cast<uint4*>(dst + i * 1024) =
-                  codes_to_16bit<BF16, false>(*reinterpret_cast<const uint2*>(src + i * 1024), bytes[i * 32]);
+              *reinterpret_cast<uint4*>(dst + i * 1024) = codes_to_16bit<BF16, !BF16>(c[i], h[i]);
           }
         }
         keep((tc & 1u) ^ 1u, ahead);
         fence_proxy_async_smem();
-        warpgroup_sync(3 + kv);
-        if (tid == 0 && ok) {
+        __syncwarp();
+        if (lane == 0 && ok) {
           mbar_arrive(&bars[kFull + 3 * kv + st]);
           mbar_arrive(&bars[kCEmpty + 2 * kv + cs]);
         }
+        ++tc;
       }
       t += un.n;
     }
