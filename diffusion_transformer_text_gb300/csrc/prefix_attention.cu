@@ -677,20 +677,23 @@ qi_status op_fail(qi_status st, const char* fmt, ...) {
 
 int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
-// Chooses the decomposition from sizes alone (own lengths, which only the device
-// knows, count as S). Time is counted in key tiles of the 128-row kernel (about 0.9 us):
-// a unit costs its tiles plus kUnitTiles for its Q load, pipeline fill and epilogue, and
-// splitting costs kMergeTiles for the partials and the second launch. The few-row kernel's
-// tiles and units cost less (kFewTile, kFewUnit), and it reads an 8-bit prefix as it is; the
-// others first turn it into 16 bits (kConvert tiles a 2^20 values: written and read again).
+// Chooses the decomposition from sizes alone (own lengths, which only the device knows, count
+// as S): the one whose busiest CTA has the least to do. Time is counted in units of a key
+// tile of the 128-row kernel, about 0.9 us: a unit costs its tiles plus a fill and an
+// epilogue, splitting costs kMergeTiles for the partials and the second launch. The few-row
+// kernel reads an 8-bit prefix as it is; the other first has it turned into 16 bits
+// (kConvert a 2^20 values: written and read again). Measured, 128-row against few-row
+// kernel: %PLAN%
 //
 // Order of the joint units: head-major, so that the CTAs running at one time share a few
 // heads' K/V in L2; with `causal`, whose units differ in length, last row blocks first
 // over all heads and sequences, so that the CTAs' sums of lengths agree (3 x 777 rows over
 // 2048 + 1201 keys, 4 key heads: %BYBLOCK%), as long as all K/V stay in half of the L2.
-constexpr float kUnitTiles = 3.f;
-constexpr float kMergeTiles = 5.f;
-constexpr float kFewTile = 0.6f, kFewUnit = 1.5f;
+struct Rate {
+  float tile, tile8, unit;  // a 16-bit tile, a tile of codes, a unit
+};
+constexpr Rate kFullRate{1.f, 1.f, 2.5f}, kFewRate{0.95f, 1.5f, 2.f};
+constexpr float kMergeTiles = 4.f, kPartRows = 5300.f;  // and a unit per so many partial rows written and read
 constexpr float kConvert = 0.5f;
 constexpr long long kL2Half = 64ll << 20;
 struct Sizes {
@@ -721,9 +724,10 @@ Plan make_plan(const Sizes& z, int sms) {
   };
   const float convert = z.from8 && z.P > 0 ? kConvert * static_cast<float>(z.P) * z.Hkv * kHeadDim / (1 << 20) : 0.f;
   // joint units, every number of chunks that keeps the grid within a few waves
-  const auto joint = [&](Plan c, float tile, float unit, bool always_split, float more) {
+  const auto joint = [&](Plan c, Rate r, bool always_split, float more) {
     const int n = c.pt + c.ot;
     const long long blocks = static_cast<long long>(z.Hkv) * z.B * c.nqb;
+    const float each = (c.pt * (z.from8 ? r.tile8 : r.tile) + c.ot * r.tile) / n;
     for (int nch = 1; nch <= n; ++nch) {
       if (nch > 1 && blocks * nch > 4ll * sms) break;  // (at most 4 x SMs rounds of this loop)
       c.ct = ceil_div(n, nch);
@@ -731,7 +735,8 @@ Plan make_plan(const Sizes& z, int sms) {
       c.nch = nch;
       c.split = always_split || nch > 1;
       const float waves = static_cast<float>((blocks * nch + sms - 1) / sms);
-      const float cost = waves * (c.ct * tile + unit) + (c.split ? kMergeTiles : 0.f) + more;
+      const float parts = c.split ? kMergeTiles + static_cast<float>(blocks * nch) * c.rows_o * c.per / kPartRows : 0.f;
+      const float cost = waves * (c.ct * each + r.unit) + parts + more;
       if (cost < best_cost && blocks * nch <= INT_MAX / 2) {
         best_cost = cost;
         c.units = static_cast<int>(blocks * nch);
@@ -739,8 +744,8 @@ Plan make_plan(const Sizes& z, int sms) {
       }
     }
   };
-  // the prefix once per rb sequences, own keys by sequence
-  const auto packed = [&](Plan c, float tile, float unit, float more) {
+  // the prefix once per rb sequences, own keys by sequence; CTA i has units i, i + SMs, ...
+  const auto packed = [&](Plan c, Rate r, float more) {
     c.split = 1;
     const long long blocks = static_cast<long long>(z.Hkv) * z.B;
     const int most = c.pt > c.ot ? c.pt : c.ot;
@@ -750,8 +755,17 @@ Plan make_plan(const Sizes& z, int sms) {
       c.nch = c.ot ? ceil_div(c.ot, ct) : 1;
       const long long up = static_cast<long long>(z.Hkv) * c.npb * c.nchp, uo = c.ot ? blocks * c.nch : 0;
       if (up + uo > INT_MAX / 2) continue;
-      const float tiles = static_cast<float>(static_cast<long long>(z.Hkv) * c.npb * c.pt + blocks * c.ot);
-      const float cost = (tiles * tile + static_cast<float>(up + uo) * unit) / sms + ct * tile / 2 + unit + kMergeTiles + more;
+      const float unit_p = r.unit + (z.from8 ? r.tile8 : r.tile) * c.pt / c.nchp;
+      const float unit_o = r.unit + r.tile * c.ot / c.nch;
+      float load = 0.f;
+      for (long long i : {0ll, up % sms, (up + uo) % sms - 1, static_cast<long long>(sms) - 1}) {
+        if (i < 0) continue;
+        const long long np = (up - i + sms - 1) / sms, all = (up + uo - i + sms - 1) / sms;
+        const float l = np * unit_p + (all - np) * unit_o;
+        load = l > load ? l : load;
+      }
+      const float parts = (static_cast<float>(up) * c.rows_p + static_cast<float>(uo) * c.rows_o) * c.per / kPartRows;
+      const float cost = load + kMergeTiles + parts + more;
       if (cost < best_cost) {
         best_cost = cost;
         c.units_p = static_cast<int>(up);
@@ -762,22 +776,22 @@ Plan make_plan(const Sizes& z, int sms) {
   };
   Plan c = a;
   rows_of(c, kRows, false);
-  joint(c, 1.f, kUnitTiles, false, convert);
+  joint(c, kFullRate, false, convert);
   const int rows_seq = z.T * a.G;
   // packed: only if two or more sequences' rows fit one block
   if (z.P > 0 && z.B > 1 && 2 * rows_seq <= kRows) {
     rows_of(c, kRows, true);
-    packed(c, 1.f, kUnitTiles, convert);
+    packed(c, kFullRate, convert);
   }
   if (rows_seq <= kFewRows) {
     c = a;
     c.few = 1;
     c.per = 2;
     rows_of(c, kFewRows, false);
-    joint(c, kFewTile, kFewUnit, true, 0.f);
+    joint(c, kFewRate, true, 0.f);
     if (z.P > 0 && z.B > 1) {
       rows_of(c, kFewRows, true);
-      packed(c, kFewTile, kFewUnit, 0.f);
+      packed(c, kFewRate, 0.f);
     }
   }
   return best;
