@@ -56,6 +56,21 @@ constexpr uint32_t kColP = 384;               // buffer b at kColP + 64 b, half 
 constexpr int kThreads = 512;
 constexpr uint32_t kRegsLow = 104, kRegsHigh = 152, kRegsEpi = 104;
 static_assert(kRegsLow + 2 * kRegsHigh + kRegsEpi == 4 * 128, "register split must equal the launch allotment");
+// setmaxnreg.dec may only lower and setmaxnreg.inc only raise the launch's 128
+static_assert(kRegsLow <= 128 && kRegsHigh >= 128 && kRegsEpi <= 128 && kRegsLow % 8 == 0 && kRegsHigh % 8 == 0 &&
+                  kRegsEpi % 8 == 0,
+              "setmaxnreg direction and granularity");
+
+// A unit's numbers for the softmax and epilogue warps, worked out once, by the K producer, which
+// is ahead of them: each warp doing it itself between two units held the next unit's first
+// tile up by 700 cycles.
+constexpr int kMessages = 4;
+struct __align__(16) Message {
+  int n, pn, p0, o0;
+  int t0, b0, len, rows;
+  int h, u;
+  long long slot;
+};
 
 // mbarriers, as in attention.cu
 enum : int {
@@ -76,16 +91,20 @@ enum : int {
   kOEmpty = kOFull + 1,
   kLFull = kOEmpty + 1,  // the unit's row sums and maxima in shared memory (8 softmax warps)
   kLFree = kLFull + 1,   // ... read by the epilogue (4 warps)
-  kDrainQK = kLFree + 1,
+  kUFull = kLFree + 1,   // [message] a unit's numbers in shared memory, from the K producer
+  kUEmpty = kUFull + kMessages,  // [message] ... read by the softmax and epilogue warps (12)
+  kDrainQK = kUEmpty + kMessages,
   kDrainPV = kDrainQK + 1,
   kNumBars = kDrainPV + 1
 };
 __device__ __forceinline__ uint32_t bar_count(int i) {
+  if (i >= kUEmpty && i < kUEmpty + kMessages) return 12;
   if (i == kSFree || i == kLFull) return 8;
   if ((i >= kPFull && i < kPFull + 4) || i == kOEmpty || i == kLFree) return 4;
   return 1;
 }
-constexpr int kSmem = (kQBufs + kKStages + kVStages) * kTile + 1024 + kNumBars * 8 + 16 + 2 * 2 * kRows * 4;
+constexpr int kSmem = (kQBufs + kKStages + kVStages) * kTile + 1024 + kNumBars * 8 + 16 + 2 * 2 * kRows * 4 + 16 +
+                      kMessages * static_cast<int>(sizeof(Message));
 static_assert(kSmem <= 227 * 1024, "shared memory over the per-block limit");
 
 template <bool BF16>
@@ -103,6 +122,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   float* lsum = reinterpret_cast<float*>(tmem_slot + 4);  // [half][kRows]
   float* msum = lsum + 2 * kRows;
+  Message* messages = reinterpret_cast<Message*>((reinterpret_cast<uintptr_t>(msum + 2 * kRows) + 15) & ~uintptr_t(15));
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -240,10 +260,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 0) {
       // ---------------- TMA producer of the K tiles and of each unit's Q rows
       uint32_t t = 0;
-      uint32_t nq = 0;
+      uint32_t nq = 0, nm = 0;
       bool ok = true;
       for (int u = blockIdx.x; ok && u < total; u += gridDim.x) {
         const Unit un = unit_of(p, u);
+        const uint32_t mb = nm % kMessages;
+        if (*abort_flag || !mbar_wait(&bars[kUEmpty + mb], ((nm / kMessages) & 1u) ^ 1u)) {
+          if (!*abort_flag) report_error(p.err, kErrTimeoutProducer);
+          *abort_flag = 1;
+          break;
+        }
+        messages[mb] = {un.n, un.pn, un.p0, un.o0, un.t0, un.b0, un.len, un.rows, un.h, u, un.slot};
+        mbar_arrive(&bars[kUFull + mb]);
+        ++nm;
         if (un.n == 0) continue;
         const uint32_t qb = nq % kQBufs;
         if (*abort_flag || !mbar_wait(&bars[kQEmpty + qb], ((nq / kQBufs) & 1u) ^ 1u)) {
@@ -330,11 +359,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tO = tmem + lane_off + kColO + 128u * h;
     const uint64_t sc2 = f2_pack(scale_log2, scale_log2);
     uint32_t t = 0;
-    uint32_t ku = 0;
+    uint32_t ku = 0, km = 0;
     bool ok = true;
-    for (int u = blockIdx.x; u < total; u += gridDim.x) {
-      if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
-      const Unit un = unit_of(p, u);
+    for (int u = blockIdx.x; u < total; u += gridDim.x, ++km) {
+      const uint32_t mb = km % kMessages;
+      ok = __all_sync(0xffffffffu, mbar_wait(&bars[kUFull + mb], (km / kMessages) & 1u));
+      if (!ok) break;
+      const Message un = messages[mb];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[kUEmpty + mb]);
       if (un.n == 0) continue;
       const int lim_own = own_lim(p, un.len, un.t0 + tok);
       // A warp whose 32 rows lie past the block's has nothing to compute: it only keeps the
@@ -343,10 +376,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool idle = quarter * 32 >= un.rows;
       float m_used = -INFINITY;
       float l = 0.f;
-      for (int j = 0; j < un.n; ++j) {
+      // keys of this half of the tile that the row sees, counted down by tile (few live values:
+      // the loop runs at its register limit, and the tile numbers kept instead cost 1.5 %)
+      int left = p.P - un.p0 * kKeys - h * 64;
+      const int left_own = lim_own - un.o0 * kKeys - h * 64;
+      const int n = un.n, pn = un.pn;
+      for (int j = 0; j < n; ++j) {
         const uint32_t tt = t + j;
         const uint32_t b = tt & 1u;
-        const bool last = j + 1 == un.n;
+        const bool last = j + 1 == n;
         ok = __all_sync(0xffffffffu, mbar_wait(&bars[kSFull], tt & 1u));
         if (!ok) break;
         if (idle) {
@@ -371,9 +409,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[kSFree]);
         // keys at or past the row's limit become -inf, whatever their scores are
-        const bool pre = j < un.pn;
-        const int left =
-            (pre ? p.P - (un.p0 + j) * kKeys : lim_own - (un.o0 + j - un.pn) * kKeys) - h * 64;
+        if (j == pn) left = left_own;
         if (__any_sync(0xffffffffu, left < 64)) {
 #pragma unroll
           for (int c = 0; c < 2; ++c)
@@ -381,6 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < 32; ++i)
               if (c * 32 + i >= left) r[c][i] = 0xff800000u;
         }
+        left -= kKeys;
         float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
         for (int c = 0; c < 2; ++c)
@@ -461,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (!ok) break;
-      t += un.n;
+      t += n;
       ++ku;
     }
     if (!ok) {
@@ -477,10 +514,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tok = quot(p.d_G, rit);
     const int g = rit - tok * p.pl.G;
     bool ok = true;
-    uint32_t ku = 0;
-    for (int u = blockIdx.x; ok && u < total; u += gridDim.x) {
-      if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
-      const Unit un = unit_of(p, u);
+    uint32_t ku = 0, km = 0;
+    for (int u = blockIdx.x; ok && u < total; u += gridDim.x, ++km) {
+      const uint32_t mb = km % kMessages;
+      ok = __all_sync(0xffffffffu, mbar_wait(&bars[kUFull + mb], (km / kMessages) & 1u));
+      if (!ok) break;
+      const Message un = messages[mb];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[kUEmpty + mb]);
       // where the row goes: token and sequence (a prefix block runs over sequences)
       int b = un.b0, tk = un.t0 + tok;
       if (u < p.pl.units_p) {
