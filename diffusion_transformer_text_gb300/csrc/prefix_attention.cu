@@ -107,7 +107,7 @@ constexpr int kSmem = (kQBufs + kKStages + kVStages) * kTile + 1024 + kNumBars *
                       kMessages * static_cast<int>(sizeof(Message));
 static_assert(kSmem <= 227 * 1024, "shared memory over the per-block limit");
 
-template <bool BF16>
+template <bool BF16, bool JOIN>
 __global__ void __launch_bounds__(kThreads, 1)
     prefix_attn_tc(const __grid_constant__ Maps tm, const __grid_constant__ Params p, float scale_log2) {
   constexpr uint32_t kIdescQK = BF16 ? idesc_bf16_f32(128, kKeys) : idesc_f16_f32(128, kKeys);
@@ -532,8 +532,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool mine = rit < un.rows && tk < p.T && b < p.B;
       uint16_t* orow = p.o + b * p.ob + tk * p.orow + static_cast<long long>(un.h * p.pl.G + g) * p.oh;
       if (un.n == 0) {
+        if (JOIN) *reinterpret_cast<float2*>(smem + kJoinMl + rit * 8) = make_float2(-INFINITY, 0.f);
         // no key at all: a joint unit that is its row's only one writes zeros
-        if (!p.pl.split && mine) {
+        if (!JOIN && !p.pl.split && mine) {
 #pragma unroll
           for (int i = 0; i < 16; ++i) reinterpret_cast<uint4*>(orow)[i] = make_uint4(0u, 0u, 0u, 0u);
         }
@@ -551,9 +552,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float a0 = mm == -INFINITY ? 1.f : fast_exp2(m0 - mm);
       const float a1 = mm == -INFINITY ? 1.f : fast_exp2(m1 - mm);
       const float den = l0 * a0 + l1 * a1;
-      const float inv = p.pl.split ? 1.f : (den == 0.f ? 0.f : 1.f / den);
+      const float inv = JOIN || p.pl.split ? 1.f : (den == 0.f ? 0.f : 1.f / den);
       const float w0 = a0 * inv, w1 = a1 * inv;
-      if (p.pl.split && mine) p.ml[un.slot + rit] = make_float2(mm, den);
+      if (!JOIN && p.pl.split && mine) p.ml[un.slot + rit] = make_float2(mm, den);
       ok = __all_sync(0xffffffffu, mbar_wait(&bars[kOFull], ku & 1u));
       if (!ok) break;
       if (quarter * 32 >= un.rows) {  // none of the warp's rows are the block's
@@ -563,6 +564,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         continue;
       }
       tc_fence_after();
+      if (JOIN) {
+        // (the unit is the CTA's only one and its products are done: the rings are free)
+        *reinterpret_cast<float2*>(smem + kJoinMl + rit * 8) = make_float2(mm, den);
+      }
       // 16 columns of both halves at a time, the next ones loading while these are stored
       const uint32_t tO = tmem + lane_off + kColO;
       const uint64_t w00 = f2_pack(w0, w0), w11 = f2_pack(w1, w1);
@@ -590,8 +595,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             f2_unpack(fma_f32x2(f2_pack(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), w00,
                                 mul_f32x2(f2_pack(__uint_as_float(y[2 * i]), __uint_as_float(y[2 * i + 1])), w11)),
                       ov[2 * i], ov[2 * i + 1]);
-          if (p.pl.split) {
-            float4* d = reinterpret_cast<float4*>(p.part + (un.slot + rit) * kHeadDim + c * 16);
+          if (JOIN || p.pl.split) {
+            float4* d = JOIN ? reinterpret_cast<float4*>(smem + (rit * kJoinPitch + c * 16) * 4)
+                             : reinterpret_cast<float4*>(p.part + (un.slot + rit) * kHeadDim + c * 16);
 #pragma unroll
             for (int i = 0; i < 4; ++i) d[i] = make_float4(ov[4 * i], ov[4 * i + 1], ov[4 * i + 2], ov[4 * i + 3]);
           } else {
@@ -616,6 +622,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
+  }
+  if (JOIN) {
+    __syncwarp();
+    cluster_sync();  // every CTA's part is in its shared memory
+    cluster_join<BF16>(p, unit_of(p, static_cast<int>(blockIdx.x)), smem, kRows);
+    cluster_sync();  // none leaves while another reads it
   }
 }
 
@@ -736,6 +748,8 @@ struct Rate {
 constexpr Rate kFullRate{1.f, 1.f, 2.5f}, kFewRate{0.95f, 1.5f, 2.f};
 constexpr float kMergeTiles = 4.f, kPartRows = 5300.f;  // and a unit per so many partial rows written and read
 constexpr float kConvert = 0.5f;
+constexpr float kStart = 3.f;      // of a kernel whose CTAs walk the units
+constexpr float kJoinTiles = 3.f;  // of a CTA in a cluster, and its join
 constexpr long long kL2Half = 64ll << 20;
 struct Sizes {
   int B, T, Hq, Hkv, P, S, causal;
@@ -777,8 +791,29 @@ Plan make_plan(const Sizes& z, int sms) {
       c.split = always_split || nch > 1;
       const float waves = static_cast<float>((blocks * nch + sms - 1) / sms);
       const float parts = c.split ? kMergeTiles + static_cast<float>(blocks * nch) * c.rows_o * c.per / kPartRows : 0.f;
-      const float cost = waves * (c.ct * each + r.unit) + parts + more;
+      const float cost = kStart + waves * (c.ct * each + r.unit) + parts + more;
       if (cost < best_cost && blocks * nch <= INT_MAX / 2) {
+        best_cost = cost;
+        c.units = static_cast<int>(blocks * nch);
+        best = c;
+      }
+    }
+  };
+  // joint units whose chunks join in a cluster: one unit per CTA; clusters of more than two leave
+  // some SMs of a processing cluster over
+  const auto joined = [&](Plan c, Rate r, int least, float more) {
+    const int n = c.pt + c.ot;
+    const long long blocks = static_cast<long long>(z.Hkv) * z.B * c.nqb;
+    const float each = (c.pt * (z.from8 ? r.tile8 : r.tile) + c.ot * r.tile) / n;
+    for (int nch = least; nch <= n && nch <= kJoinMost; ++nch) {
+      c.ct = ceil_div(n, nch);
+      if (ceil_div(n, c.ct) != nch || blocks * nch > INT_MAX / 2) continue;
+      c.nch = nch;
+      c.join = 1;
+      const int slots = nch <= 2 ? sms : sms * 5 / 6;
+      const float waves = static_cast<float>((blocks * nch + slots - 1) / slots);
+      const float cost = waves * (c.ct * each + r.unit + kJoinTiles) + more;
+      if (cost < best_cost) {
         best_cost = cost;
         c.units = static_cast<int>(blocks * nch);
         best = c;
@@ -806,7 +841,7 @@ Plan make_plan(const Sizes& z, int sms) {
         load = l > load ? l : load;
       }
       const float parts = (static_cast<float>(up) * c.rows_p + static_cast<float>(uo) * c.rows_o) * c.per / kPartRows;
-      const float cost = load + kMergeTiles + parts + more;
+      const float cost = kStart + load + kMergeTiles + parts + more;
       if (cost < best_cost) {
         best_cost = cost;
         c.units_p = static_cast<int>(up);
@@ -818,6 +853,7 @@ Plan make_plan(const Sizes& z, int sms) {
   Plan c = a;
   rows_of(c, kRows, false);
   joint(c, kFullRate, false, convert);
+  joined(c, kFullRate, 2, convert);
   const int rows_seq = z.T * a.G;
   // packed: only if two or more sequences' rows fit one block
   if (z.P > 0 && z.B > 1 && 2 * rows_seq <= kRows) {
@@ -830,6 +866,7 @@ Plan make_plan(const Sizes& z, int sms) {
     c.per = 2;
     rows_of(c, kFewRows, false);
     joint(c, kFewRate, true, 0.f);
+    joined(c, kFewRate, 1, 0.f);
     if (z.P > 0 && z.B > 1) {
       rows_of(c, kFewRows, true);
       packed(c, kFewRate, 0.f);
@@ -933,11 +970,17 @@ cudaError_t launch(const Maps& tm, const Maps8* t8, const Params& p, float scale
   if (p.pl.few) {
     e = launch_few(tm, t8, p, BF16, scale_log2, sms, stream);
   } else {
-    static std::atomic<unsigned long long> attr_done{0};
-    e = ensure_smem_limit(prefix_attn_tc<BF16>, kSmem, attr_done);
+    static std::atomic<unsigned long long> attr_done{0}, attr_done_join{0};
+    if (p.pl.join) {
+      e = ensure_smem_limit(prefix_attn_tc<BF16, true>, kSmem, attr_done_join);
+      if (e != cudaSuccess) return e;
+      return launch_clusters(prefix_attn_tc<BF16, true>, p.pl.nch, dim3(p.pl.units), dim3(kThreads), kSmem, stream, tm, p,
+                             scale_log2);
+    }
+    e = ensure_smem_limit(prefix_attn_tc<BF16, false>, kSmem, attr_done);
     if (e != cudaSuccess) return e;
     const int grid = p.pl.units < sms ? p.pl.units : sms;
-    e = launch_dependent(prefix_attn_tc<BF16>, dim3(grid), dim3(kThreads), kSmem, stream, tm, p, scale_log2);
+    e = launch_dependent(prefix_attn_tc<BF16, false>, dim3(grid), dim3(kThreads), kSmem, stream, tm, p, scale_log2);
   }
   if (e != cudaSuccess || !p.pl.split) return e;
   // Warps per row: as many as its parts keep busy, unless the rows alone fill the GPU (1024

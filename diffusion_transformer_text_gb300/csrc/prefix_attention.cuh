@@ -31,6 +31,7 @@ struct Plan {
   int rows_p;     // rows of a prefix block's partial
   int rows_o;     // rows of a joint / own block's partial
   int few;        // blocks of at most kFewRows rows, by launch_few
+  int join;       // joint units whose chunks are a cluster of CTAs and join their parts themselves
   int per;        // partials per unit
 };
 
@@ -167,6 +168,85 @@ struct Maps8 {
 constexpr int kFewRows = 16;
 cudaError_t launch_few(const Maps& tm, const Maps8* t8, const Params& p, bool bf16, float scale_log2, int sms,
                        cudaStream_t s);
+
+// ------------------------------------------------------------------ parts joined by a cluster
+//
+// With pl.join the chunks of a row block are the CTAs of one cluster, one unit each, and their
+// parts meet in distributed shared memory: no partials in memory and no second launch. Every
+// CTA leaves part s of its unit at smem: row r of O (unnormalised, fp32) at float
+// (s rows + r) kJoinPitch, its (maximum, sum) at kJoinMl + (s rows + r) 8 bytes; a part without
+// a key has (-inf, 0), and its O is not read. CTA c writes output rows c, c + n, ..., adding the
+// parts up in order.
+constexpr int kJoinPitch = kHeadDim + 4;
+constexpr int kJoinMl = 128 * kJoinPitch * 4;
+constexpr int kJoinMost = 8;  // CTAs of a cluster that every GPU of this kind can place
+
+template <bool BF16>
+__device__ __forceinline__ void cluster_join(const Params& p, const Unit& un, const uint8_t* smem, int rows) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const int n = p.pl.nch, per = p.pl.per, parts = n * per;  // at most 16
+  const uint32_t base = smem_u32(smem);
+  for (int i = static_cast<int>(cluster_ctarank()) + n * warp; i < un.rows; i += n * warps) {
+    float m = -INFINITY, l = 0.f;
+    if (lane < parts) {
+      const int c = per == 2 ? lane >> 1 : lane, s = per == 2 ? lane & 1 : 0;
+      const uint32_t a = mapa_shared(base + kJoinMl + (s * rows + i) * 8, static_cast<uint32_t>(c));
+      asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(m), "=f"(l) : "r"(a) : "memory");
+    }
+    float top = m;
+#pragma unroll
+    for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    const unsigned used = __ballot_sync(0xffffffffu, !(m == -INFINITY && l == 0.f));
+    // (m = -inf with another sum is a row of NaN scores, which stays one)
+    const float w = top == -INFINITY ? 1.f : fast_exp2(m - top);
+    float den = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = 0; k < parts; ++k) {
+      if (!((used >> k) & 1u)) continue;
+      const int c = per == 2 ? k >> 1 : k, s = per == 2 ? k & 1 : 0;
+      const uint32_t a =
+          mapa_shared(base + ((s * rows + i) * kJoinPitch + lane * 4) * 4, static_cast<uint32_t>(c));
+      float4 v;
+      asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                   : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                   : "r"(a)
+                   : "memory");
+      const float wk = __shfl_sync(0xffffffffu, w, k);
+      den += __shfl_sync(0xffffffffu, l, k) * wk;
+      acc.x += v.x * wk;
+      acc.y += v.y * wk;
+      acc.z += v.z * wk;
+      acc.w += v.w * wk;
+    }
+    const float inv = den == 0.f ? 0.f : 1.f / den;
+    const int tok = quot(p.d_G, i), g = i - tok * p.pl.G, t = un.t0 + tok;
+    if (t < p.T) {
+      uint16_t* orow = p.o + un.b0 * p.ob + t * p.orow + static_cast<long long>(un.h * p.pl.G + g) * p.oh;
+      reinterpret_cast<uint2*>(orow)[lane] =
+          make_uint2(pack16<BF16>(acc.x * inv, acc.y * inv), pack16<BF16>(acc.z * inv, acc.w * inv));
+    }
+  }
+}
+
+// launch_dependent with clusters of `cluster` CTAs
+template <typename... KArgs, typename... Args>
+cudaError_t launch_clusters(void (*kernel)(KArgs...), int cluster, dim3 grid, dim3 block, size_t smem,
+                            cudaStream_t stream, Args&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<Args&&>(args)...);
+}
 
 }  // namespace pa
 }  // namespace qi

@@ -81,6 +81,7 @@ struct Exchange {
   int lim[8][kR];
   uint32_t issued[3][5];
   uint32_t pad;
+  float2 ml[2][kR];  // JOIN: each warpgroup's maxima and sums
   uint32_t scales[8][2][32];  // [converting warp][tile parity] the four scale bytes of its rows,
   uint2 halves[8][2][32];     // and their half_scale
 };
@@ -156,7 +157,7 @@ __device__ __forceinline__ uint4 codes_to_16bit(uint2 c, uint32_t scale) {
   return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
-template <bool BF16, bool Q8>
+template <bool BF16, bool Q8, bool JOIN>
 __global__ void __launch_bounds__(Cfg<Q8>::kThreads, 1)
     prefix_attn_few(const __grid_constant__ Maps tm, const __grid_constant__ Maps8 t8, const __grid_constant__ Params p,
                     float scale_log2) {
@@ -188,6 +189,7 @@ __global__ void __launch_bounds__(Cfg<Q8>::kThreads, 1)
     for (int i = 0; i < kNumBars; ++i) mbar_init(&bars[i], bar_count<Q8>(i));
     *abort_flag = 0;
     for (int i = 0; i < 15; ++i) ex.issued[i / 5][i % 5] = 0;
+    for (int i = 0; i < 2 * kR; ++i) ex.ml[i / kR][i % kR] = make_float2(-INFINITY, 0.f);
     fence_barrier_init();
   }
   if (warp == 0 && lane == 0) {
@@ -482,8 +484,14 @@ __global__ void __launch_bounds__(Cfg<Q8>::kThreads, 1)
         if (lane == 0) store16f(ex.sum[s][quarter], l);
         warpgroup_sync(1 + s);
         const float den = (ex.sum[s][0][row16] + ex.sum[s][1][row16]) + (ex.sum[s][2][row16] + ex.sum[s][3][row16]);
-        if (quarter == 0 && lane < un.rows) p.ml[slot + lane] = make_float2(m_used, den);
+        if (quarter == 0 && lane < kR) {
+          if (JOIN)
+            ex.ml[s][lane] = make_float2(m_used, den);
+          else if (lane < un.rows)
+            p.ml[slot + lane] = make_float2(m_used, den);
+        }
         ok = ok && __all_sync(0xffffffffu, mbar_wait(&bars[kPDone + last % kSBufs], (last / kSBufs) & 1u));
+        if (JOIN) continue;  // O^T stays in tensor memory for the end of the kernel
         tc_fence_after();
         uint32_t o[kR];
         tmem_ld16(tO, o);
@@ -494,7 +502,7 @@ __global__ void __launch_bounds__(Cfg<Q8>::kThreads, 1)
         for (int i = 0; i < kR; ++i)
           if (i < un.rows) out[i * kHeadDim] = __uint_as_float(o[i]);
         // (the next unit's sums are stored after another warpgroup_sync)
-      } else if (quarter == 0 && lane < un.rows) {
+      } else if (!JOIN && quarter == 0 && lane < un.rows) {
         p.ml[slot + lane] = make_float2(-INFINITY, 0.f);  // no tile: merge_partials passes it over
       }
       t += un.n;
@@ -603,20 +611,49 @@ __global__ void __launch_bounds__(Cfg<Q8>::kThreads, 1)
       if (issued[2][i]) mbar_wait(&bars[kQFull + i], ((issued[2][i] - 1) / kQBufs) & 1u);
   }
   __syncthreads();
+  if (JOIN) {
+    // the unit was the CTA's only one and all is done: its parts go where the tiles were
+    if (warp >= 4 && warp < 12) {
+      const int s = (warp - 4) >> 2, dim = (warp & 3) * 32 + lane;
+      tc_fence_after();
+      uint32_t o[kR];
+      tmem_ld16(tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + kColO + 16u * s, o);
+      tmem_ld_wait();
+      tc_fence_before();
+#pragma unroll
+      for (int i = 0; i < kR; ++i)
+        *reinterpret_cast<uint32_t*>(smem + ((s * kR + i) * kJoinPitch + dim) * 4) = o[i];
+      if (dim < kR) *reinterpret_cast<float2*>(smem + kJoinMl + (s * kR + dim) * 8) = ex.ml[s][dim];
+    }
+    __syncthreads();
+  }
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
+  }
+  if (JOIN) {
+    __syncwarp();
+    cluster_sync();  // every CTA's parts are in its shared memory
+    cluster_join<BF16>(p, unit_of(p, static_cast<int>(blockIdx.x)), smem, kR);
+    cluster_sync();  // none leaves while another reads them
   }
 }
 
 template <bool BF16, bool Q8>
 cudaError_t launch_as(const Maps& tm, const Maps8& t8, const Params& p, float scale_log2, int sms, cudaStream_t stream) {
-  static std::atomic<unsigned long long> attr_done{0};
+  static std::atomic<unsigned long long> attr_done{0}, attr_done_join{0};
   constexpr int smem = smem_bytes<Q8>();
-  const cudaError_t e = ensure_smem_limit(prefix_attn_few<BF16, Q8>, smem, attr_done);
+  constexpr int threads = Cfg<Q8>::kThreads;
+  if (p.pl.join) {
+    const cudaError_t e = ensure_smem_limit(prefix_attn_few<BF16, Q8, true>, smem, attr_done_join);
+    if (e != cudaSuccess) return e;
+    return launch_clusters(prefix_attn_few<BF16, Q8, true>, p.pl.nch, dim3(p.pl.units), dim3(threads), smem, stream, tm,
+                           t8, p, scale_log2);
+  }
+  const cudaError_t e = ensure_smem_limit(prefix_attn_few<BF16, Q8, false>, smem, attr_done);
   if (e != cudaSuccess) return e;
   const int grid = p.pl.units < sms ? p.pl.units : sms;
-  return launch_dependent(prefix_attn_few<BF16, Q8>, dim3(grid), dim3(Cfg<Q8>::kThreads), smem, stream, tm, t8, p,
+  return launch_dependent(prefix_attn_few<BF16, Q8, false>, dim3(grid), dim3(threads), smem, stream, tm, t8, p,
                           scale_log2);
 }
 

@@ -266,11 +266,24 @@ def test_attention_refuses(qi):
         qi.prefix_attention(_normal(1, 6 * 8 * 128 + 4)[4:].view(6, 1, 8, 128), k, v, pk, pv)
     with pytest.raises(qi.QiError, match="INVALID_ARG"):  # one K row for all: stride 0
         qi.prefix_attention(q, k[:, :1].expand(-1, 200, -1, -1), v, pk, pv)
-    with pytest.raises(qi.QiError, match="workspace"):
-        buf = qi._PREFIX_ATTN.pack(0, 6, 1, 8, 2, 1500, 200, 0, 0.1, q.data_ptr(), 1024, 1024, 128, k.data_ptr(), 51200,
-                                   256, 128, v.data_ptr(), 51200, 256, 128, q.data_ptr(), 1024, 1024, 128, pk.data_ptr(),
-                                   0, 256, 128, pv.data_ptr(), 0, 256, 128, 0, 0, 0, 0, 0, 0, 0, 0)
-        qi._check(qi.lib().qi_prefix_attention(buf, None))
+    q, k, v, pk, pv = _batch(qi, B=32, P=8192)             # sizes that go by partial results
+    o = torch.zeros_like(q)
+    args = [0, 32, 1, 8, 2, 8192, 200, 0, 0.1]
+    for t in (q, k, v, o):
+        args += [t.data_ptr(), *t.stride()[:3]]
+    for t in (pk, pv):
+        args += [t.data_ptr(), 0, *t.stride()[:2]]
+    L = qi.lib()
+    need = L.qi_prefix_attention_workspace(qi._PREFIX_ATTN.pack(*args, *[0] * 8))
+    assert need > 0
+    ws = torch.empty(need + 256, dtype=torch.uint8, device="cuda")
+    for ptr, size in ((0, 0), (ws.data_ptr(), need - 1), (ws.data_ptr() + 8, need)):
+        with pytest.raises(qi.QiError, match="workspace"):
+            qi._check(L.qi_prefix_attention(qi._PREFIX_ATTN.pack(*args, 0, 0, 0, 0, 0, ptr, size, 0), None))
+    assert (o == 0).all()
+    st = torch.cuda.current_stream().cuda_stream
+    qi._check(L.qi_prefix_attention(qi._PREFIX_ATTN.pack(*args, 0, 0, 0, 0, 0, ws.data_ptr(), need, 0), st))
+    assert torch.equal(o, qi.prefix_attention(q, k, v, pk, pv, scale=0.1))
 
 
 # ---------------------------------------------------------------- 8-bit cache
