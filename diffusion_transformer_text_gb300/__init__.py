@@ -126,8 +126,8 @@ def lib() -> ctypes.CDLL:
         "qi_gemm_mxfp8": [P, P, P, P, P, P, I, I, I, P],
         "qi_dpmpp2m_update": [P, P, P, I, P, I, I, P],
         "qi_prefix_attention": [P, P],
-        "qi_kv8_write": [I, I, I, I, I, P, P, P, P, P, P, P, P, P],
-        "qi_kv8_read": [I, I, I, I, I, P, P, P, P, P, P, P, P, P],
+        "qi_kv8_write": [P, P],
+        "qi_kv8_read": [P, P],
         "qi_add_rmsnorm_mxfp8": [P, P],
     }
     for name, args in sig.items():
@@ -294,9 +294,10 @@ def gemv(x, W, b, silu_in: bool = False):
 # ---------------------------------------------------------------- batches from one prompt
 
 DT_F16, DT_BF16, DT_F32 = 0, 1, 2
-_TENSOR4 = struct.Struct("@Pqqq")                          # qi_tensor4
-_PREFIX_ATTN = struct.Struct("@8if" + "Pqqq" * 6 + "6PNP")  # qi_prefix_attn
-_ADD_RMSNORM = struct.Struct("@6ifPqPqPqPPP")              # qi_add_rmsnorm
+# qi_prefix_attn, qi_kv8 and qi_add_rmsnorm: what changes from call to call, then what a layout fixes
+_ATTN_HEAD, _ATTN_TAIL = struct.Struct("@13Pif"), struct.Struct("@N18q7ixxxx")
+_KV8_HEAD, _KV8_TAIL = struct.Struct("@8P"), struct.Struct("@6q5ixxxx")
+_NORM_HEAD, _NORM_TAIL = struct.Struct("@6Pif"), struct.Struct("@3q5ixxxx")
 _SCALE = 1.0 / math.sqrt(HEAD_DIM)
 # Layouts (types, devices, shapes and strides of all tensor arguments) that a call has checked, with
 # what it packs for them; the checks and the workspace size depend on nothing else, and take longer
@@ -391,7 +392,7 @@ def _elsewhere(t, stream):
 
 
 def _check_prefix_attention(key, q, k, v, prefix_k, prefix_v, prefix8, own_len, out, status):
-    """(leading sizes, strides by tensor, workspace bytes, output shape) of arguments in this layout."""
+    """(the fixed part of qi_prefix_attn, workspace bytes, output shape) of arguments in this layout."""
     import torch
     if q.dim() != 4 or q.shape[3] != HEAD_DIM:
         raise ValueError(f"q: want [B, T, Hq, {HEAD_DIM}], got {tuple(q.shape)}")
@@ -422,11 +423,11 @@ def _check_prefix_attention(key, q, k, v, prefix_k, prefix_v, prefix8, own_len, 
     os_ = (T * Hq * HEAD_DIM, Hq * HEAD_DIM, HEAD_DIM) if out is None else _strides4(out, q, shape, "out")
     _want(own_len, torch.int32, (B,), dev, "own_len")
     _want(status, torch.int32, (1,), dev, "status")
-    sizes = (dt, B, T, Hq, Hkv, P, S)
+    tail = (*qs, *ks, *vs, *os_, *pks, *pvs, dt, B, T, Hq, Hkv, P, S)
     p8 = int(prefix8 is not None and P > 0)
     need = lib().qi_prefix_attention_workspace(
-        _PREFIX_ATTN.pack(*sizes, 0, 1.0, *(0, 0, 0, 0) * 6, p8, 0, 0, 0, 0, 0, 0, 0))
-    return _remember(_attn_layouts, key, (sizes, qs, ks, vs, os_, pks, pvs, need, shape))
+        _ATTN_HEAD.pack(*[0] * 6, p8, *[0] * 6, 0, 1.0) + _ATTN_TAIL.pack(0, *tail))
+    return _remember(_attn_layouts, key, (_ATTN_TAIL.pack(need, *tail), need, shape))
 
 
 def prefix_attention(q, k, v, prefix_k=None, prefix_v=None, prefix8: KV8Cache | None = None, own_len=None,
@@ -446,19 +447,20 @@ def prefix_attention(q, k, v, prefix_k=None, prefix_v=None, prefix8: KV8Cache | 
         with _elsewhere(q, stream):
             return prefix_attention(q, k, v, prefix_k, prefix_v, prefix8, own_len, causal, scale, out, status)
     key = (q.dtype, q.device, q.shape, q.stride(), _layout(k), _layout(v), _layout(prefix_k), _layout(prefix_v),
-           None if prefix8 is None else (*map(_layout, prefix8),), _layout(own_len), _layout(out), _layout(status))
+           None if prefix8 is None else (*map(_layout, prefix8),), None if own_len is None else _layout(own_len),
+           None if out is None else _layout(out), None if status is None else _layout(status))
     plan = _attn_layouts.get(key)
     if plan is None:
         plan = _check_prefix_attention(key, q, k, v, prefix_k, prefix_v, prefix8, own_len, out, status)
-    sizes, qs, ks, vs, os_, pks, pvs, need, shape = plan
+    tail, need, shape = plan
     if out is None:
         out = q.new_empty(shape)
     ws = q.new_empty(need, dtype=torch.uint8) if need else None
     p8 = (0, 0, 0, 0) if prefix8 is None else [t.data_ptr() for t in prefix8]
-    st = _lib.qi_prefix_attention(_PREFIX_ATTN.pack(
-        *sizes, 1 if causal else 0, _SCALE if scale is None else scale, q.data_ptr(), *qs, _addr(k), *ks, _addr(v),
-        *vs, out.data_ptr(), *os_, _addr(prefix_k), *pks, _addr(prefix_v), *pvs, *p8, _addr(own_len), _addr(ws), need,
-        _addr(status)), torch._C._cuda_getCurrentRawStream(dev))
+    st = _lib.qi_prefix_attention(_ATTN_HEAD.pack(
+        q.data_ptr(), _addr(k), _addr(v), out.data_ptr(), _addr(prefix_k), _addr(prefix_v), *p8, _addr(own_len),
+        _addr(ws), _addr(status), 1 if causal else 0, _SCALE if scale is None else scale) + tail,
+        torch._C._cuda_getCurrentRawStream(dev))
     if st:
         _check(st)
     return out
@@ -481,7 +483,7 @@ def _check_kv8(key, cache, k, v, pos, lens):
     _want(pos, torch.int32, (B,), dev, "pos")
     _want(lens, torch.int32, (B,), dev, "lens")
     lib()
-    return _remember(_kv8_layouts, key, ((dt, B, T, S, H), *strides))
+    return _remember(_kv8_layouts, key, _KV8_TAIL.pack(*strides[0], *strides[1], dt, B, T, S, H))
 
 
 def _kv8_call(write, cache, k, v, pos, lens, dev):
@@ -489,14 +491,12 @@ def _kv8_call(write, cache, k, v, pos, lens, dev):
     ck, cv, ck_sf, cv_sf = cache
     key = (ck.dtype, ck.device, ck.shape, ck.stride(), _layout(cv), _layout(ck_sf), _layout(cv_sf), _layout(k),
            _layout(v), _layout(pos), _layout(lens))
-    plan = _kv8_layouts.get(key)
-    if plan is None:
-        plan = _check_kv8(key, cache, k, v, pos, lens)
-    sizes, ks, vs = plan
-    kt, vt = _TENSOR4.pack(k.data_ptr(), *ks), _TENSOR4.pack(v.data_ptr(), *vs)
-    c = (ck.data_ptr(), cv.data_ptr(), ck_sf.data_ptr(), cv_sf.data_ptr(), _addr(pos), _addr(lens))
-    raw = torch._C._cuda_getCurrentRawStream(dev)
-    st = _lib.qi_kv8_write(*sizes, kt, vt, *c, raw) if write else _lib.qi_kv8_read(*sizes, *c, kt, vt, raw)
+    tail = _kv8_layouts.get(key)
+    if tail is None:
+        tail = _check_kv8(key, cache, k, v, pos, lens)
+    st = (_lib.qi_kv8_write if write else _lib.qi_kv8_read)(
+        _KV8_HEAD.pack(k.data_ptr(), v.data_ptr(), ck.data_ptr(), cv.data_ptr(), ck_sf.data_ptr(), cv_sf.data_ptr(),
+                       _addr(pos), _addr(lens)) + tail, torch._C._cuda_getCurrentRawStream(dev))
     if st:
         _check(st)
 
@@ -536,7 +536,7 @@ def kv8_read(cache: KV8Cache, T: int, dtype, pos=None, lens=None, out=None, stre
 
 
 def _check_norm(key, x, delta, w, x_out, q, sf):
-    """(leading arguments, row strides, bytes of the scale chunks) of arguments in this layout."""
+    """(the fixed part of qi_add_rmsnorm, bytes of the scale chunks) of arguments in this layout."""
     import torch
     kinds = {torch.float16: DT_F16, torch.bfloat16: DT_BF16, torch.float32: DT_F32}
     if x.dim() != 2 or x.dtype not in kinds:
@@ -555,9 +555,10 @@ def _check_norm(key, x, delta, w, x_out, q, sf):
         _want(w, w.dtype if w.dtype in (torch.bfloat16, torch.float32) else torch.bfloat16, (K,), dev, "w")
     lib()
     stride = lambda t: K if t is None else t.stride(0)
-    return _remember(_norm_layouts, key, ((kinds[x.dtype], 0 if delta is None else kinds[delta.dtype], rows, K,
-                            int(w is not None and w.dtype == torch.float32)), stride(x), stride(delta), stride(x_out),
-                           chunks))
+    return _remember(_norm_layouts, key, (
+        _NORM_TAIL.pack(stride(x), stride(delta), stride(x_out), kinds[x.dtype],
+                        0 if delta is None else kinds[delta.dtype], rows, K,
+                        int(w is not None and w.dtype == torch.float32)), chunks))
 
 
 def add_rmsnorm_mxfp8(x, delta=None, w=None, plus_one: bool = False, eps: float = 1e-6, x_out=None, q=None, sf=None,
@@ -578,7 +579,7 @@ def add_rmsnorm_mxfp8(x, delta=None, w=None, plus_one: bool = False, eps: float 
     plan = _norm_layouts.get(key)
     if plan is None:
         plan = _check_norm(key, x, delta, w, x_out, q, sf)
-    head, xs, ds, os_, chunks = plan
+    tail, chunks = plan
     if x_out is None:
         x_out = x.new_empty(x.shape)
     if q is None:
@@ -586,8 +587,8 @@ def add_rmsnorm_mxfp8(x, delta=None, w=None, plus_one: bool = False, eps: float 
     if sf is None:
         sf = x.new_zeros(chunks, dtype=torch.uint8)
     st = _lib.qi_add_rmsnorm_mxfp8(
-        _ADD_RMSNORM.pack(*head, 1 if plus_one else 0, eps, x.data_ptr(), xs, _addr(delta), ds, x_out.data_ptr(), os_,
-                          _addr(w), q.data_ptr(), sf.data_ptr()), torch._C._cuda_getCurrentRawStream(dev))
+        _NORM_HEAD.pack(x.data_ptr(), _addr(delta), x_out.data_ptr(), _addr(w), q.data_ptr(), sf.data_ptr(),
+                        1 if plus_one else 0, eps) + tail, torch._C._cuda_getCurrentRawStream(dev))
     if st:
         _check(st)
     return x_out, q, sf

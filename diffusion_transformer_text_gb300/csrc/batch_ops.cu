@@ -170,7 +170,7 @@ __device__ __forceinline__ Kv8At kv8_at(const Kv8Args& a, int i, int n, int pos)
   x.row = x.t < n && row >= 0 && row < a.S ? row : -1;
   return x;
 }
-__device__ __forceinline__ long long kv8_offset(const qi_tensor4& t, const Kv8At& x) {
+__device__ __forceinline__ long long kv8_offset(const Tensor4& t, const Kv8At& x) {
   return x.t * t.row + x.h * t.head;
 }
 
@@ -509,35 +509,35 @@ bool good_stride(long long* s, int size) {
   return *s > 0 && *s % 8 == 0 && *s < (1ll << 38);
 }
 
-qi_status kv8_call(const char* name, int dtype, int B, int T, int S, int H, const qi_tensor4* k, const qi_tensor4* v,
-                   const uint8_t* k8, const uint8_t* v8, const uint8_t* k_sf, const uint8_t* v_sf, const int* pos,
-                   const int* lens, Kv8Args* a) {
-  if (!k || !v || !k->data || !v->data || !k8 || !v8 || !k_sf || !v_sf)
+qi_status kv8_call(const char* name, const qi_kv8* z, Kv8Args* a) {
+  if (!z || !z->k || !z->v || !z->k8 || !z->v8 || !z->k_sf || !z->v_sf)
     return op_fail(QI_ERR_INVALID_ARG, "%s: NULL argument", name);
-  if (dtype != QI_DT_F16 && dtype != QI_DT_BF16) return op_fail(QI_ERR_INVALID_ARG, "%s: dtype %d", name, dtype);
+  if (z->dtype != QI_DT_F16 && z->dtype != QI_DT_BF16)
+    return op_fail(QI_ERR_INVALID_ARG, "%s: dtype %d", name, z->dtype);
   constexpr int kMost = 1 << 24;
-  if (B < 1 || B > 65535 || T < 1 || T > kMost || S < 1 || S > kMost || H < 1 || H > 65535 ||
-      static_cast<long long>(T) * H >= (1ll << 27))
-    return op_fail(QI_ERR_SHAPE, "%s: B %d T %d S %d H %d", name, B, T, S, H);
-  a->B = B;
-  a->T = T;
-  a->S = S;
-  a->H = H;
-  a->k = *k;
-  a->v = *v;
-  for (qi_tensor4* t : {&a->k, &a->v})
-    if (misaligned(t->data, 16) || !good_stride(&t->batch, B) || !good_stride(&t->row, T) || !good_stride(&t->head, H))
+  if (z->B < 1 || z->B > 65535 || z->T < 1 || z->T > kMost || z->S < 1 || z->S > kMost || z->H < 1 || z->H > 65535 ||
+      static_cast<long long>(z->T) * z->H >= (1ll << 26))
+    return op_fail(QI_ERR_SHAPE, "%s: B %d T %d S %d H %d", name, z->B, z->T, z->S, z->H);
+  a->B = z->B;
+  a->T = z->T;
+  a->S = z->S;
+  a->H = z->H;
+  a->k = {z->k, z->k_stride.batch, z->k_stride.row, z->k_stride.head};
+  a->v = {z->v, z->v_stride.batch, z->v_stride.row, z->v_stride.head};
+  for (Tensor4* t : {&a->k, &a->v})
+    if (misaligned(t->data, 16) || !good_stride(&t->batch, z->B) || !good_stride(&t->row, z->T) ||
+        !good_stride(&t->head, z->H))
       return op_fail(QI_ERR_INVALID_ARG,
                      "%s: k and v need 16-byte alignment and strides that are positive multiples of 8", name);
-  if (misaligned(k8, 16) || misaligned(v8, 16) || misaligned(k_sf, 4) || misaligned(v_sf, 4) || misaligned(pos, 4) ||
-      misaligned(lens, 4))
+  if (misaligned(z->k8, 16) || misaligned(z->v8, 16) || misaligned(z->k_sf, 4) || misaligned(z->v_sf, 4) ||
+      misaligned(z->pos, 4) || misaligned(z->lens, 4))
     return op_fail(QI_ERR_INVALID_ARG, "%s: codes need 16-byte, scales, pos and lens 4-byte alignment", name);
-  a->k8 = const_cast<uint8_t*>(k8);
-  a->v8 = const_cast<uint8_t*>(v8);
-  a->k_sf = const_cast<uint8_t*>(k_sf);
-  a->v_sf = const_cast<uint8_t*>(v_sf);
-  a->pos = pos;
-  a->lens = lens;
+  a->k8 = z->k8;
+  a->v8 = z->v8;
+  a->k_sf = z->k_sf;
+  a->v_sf = z->v_sf;
+  a->pos = z->pos;
+  a->lens = z->lens;
   return QI_OK;
 }
 
@@ -554,24 +554,19 @@ cudaError_t launch_kv8_read(const Kv8Args& a, bool bf16, cudaStream_t s) {
 
 }  // namespace qi
 
-extern "C" qi_status qi_kv8_write(int dtype, int B, int T, int S, int H, const qi_tensor4* k, const qi_tensor4* v,
-                                  uint8_t* k8, uint8_t* v8, uint8_t* k_sf, uint8_t* v_sf, const int* pos,
-                                  const int* lens, qi_stream_t stream) {
+extern "C" qi_status qi_kv8_write(const qi_kv8* args, qi_stream_t stream) {
   qi::Kv8Args a{};
-  const qi_status st =
-      qi::kv8_call("qi_kv8_write", dtype, B, T, S, H, k, v, k8, v8, k_sf, v_sf, pos, lens, &a);
+  const qi_status st = qi::kv8_call("qi_kv8_write", args, &a);
   if (st != QI_OK) return st;
-  const cudaError_t e = qi::launch_kv8_write(a, dtype == QI_DT_BF16, reinterpret_cast<cudaStream_t>(stream));
+  const cudaError_t e = qi::launch_kv8_write(a, args->dtype == QI_DT_BF16, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? QI_OK : qi::op_fail(QI_ERR_CUDA, "qi_kv8_write: %s", cudaGetErrorString(e));
 }
 
-extern "C" qi_status qi_kv8_read(int dtype, int B, int T, int S, int H, const uint8_t* k8, const uint8_t* v8,
-                                 const uint8_t* k_sf, const uint8_t* v_sf, const int* pos, const int* lens,
-                                 const qi_tensor4* k, const qi_tensor4* v, qi_stream_t stream) {
+extern "C" qi_status qi_kv8_read(const qi_kv8* args, qi_stream_t stream) {
   qi::Kv8Args a{};
-  const qi_status st = qi::kv8_call("qi_kv8_read", dtype, B, T, S, H, k, v, k8, v8, k_sf, v_sf, pos, lens, &a);
+  const qi_status st = qi::kv8_call("qi_kv8_read", args, &a);
   if (st != QI_OK) return st;
-  const cudaError_t e = qi::launch_kv8_read(a, dtype == QI_DT_BF16, reinterpret_cast<cudaStream_t>(stream));
+  const cudaError_t e = qi::launch_kv8_read(a, args->dtype == QI_DT_BF16, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? QI_OK : qi::op_fail(QI_ERR_CUDA, "qi_kv8_read: %s", cudaGetErrorString(e));
 }
 

@@ -217,9 +217,13 @@ __device__ __forceinline__ int quot(const Div& v, int n) {
 // 8-bit K/V cache (batch_ops.cu): rows t < lens[b] of k and v [B, T, H, 128] (16 bits, element
 // strides) against rows pos[b] + t of the cache [B, S, H, 128] codes and [B, S, H, 4] scales;
 // rows outside 0 .. S-1 are passed over. pos NULL: 0; lens NULL: T.
+struct Tensor4 {
+  const void* data;
+  long long batch, row, head;
+};
 struct Kv8Args {
   int B, T, S, H;
-  qi_tensor4 k, v;
+  Tensor4 k, v;
   uint8_t* k8;
   uint8_t* v8;
   uint8_t* k_sf;

@@ -922,7 +922,7 @@ bool fix_stride(long long* s, int size) {
   return *s > 0 && *s % 8 == 0 && *s < (1ll << 38);
 }
 
-bool map_kv(CUtensorMap* m, const qi_tensor4& t, int heads, int rows, int batch) {
+bool map_kv(CUtensorMap* m, const Tensor4& t, int heads, int rows, int batch) {
   const unsigned long long dims[4] = {kHeadDim, static_cast<unsigned long long>(heads),
                                       static_cast<unsigned long long>(rows), static_cast<unsigned long long>(batch)};
   const unsigned long long str[3] = {static_cast<unsigned long long>(t.head) * 2,
@@ -940,7 +940,7 @@ bool map_codes(CUtensorMap* m, const uint8_t* codes, int heads, int rows) {
   return encode_map_nd(m, codes, true, 3, dims, str, box);
 }
 
-bool map_q(CUtensorMap* m, const qi_tensor4& t, int G, int Hkv, int T, int B, int tb, int rb) {
+bool map_q(CUtensorMap* m, const Tensor4& t, int G, int Hkv, int T, int B, int tb, int rb) {
   const unsigned long long dims[5] = {kHeadDim, static_cast<unsigned long long>(G),
                                       static_cast<unsigned long long>(Hkv), static_cast<unsigned long long>(T),
                                       static_cast<unsigned long long>(B)};
@@ -958,7 +958,7 @@ qi_status check_sizes(const qi_prefix_attn* a) {
   constexpr int kMost = 1 << 24;
   if (a->B < 1 || a->B > 65535 || a->T < 1 || a->T > kMost || a->Hkv < 1 || a->Hkv > 65535 || a->Hq < a->Hkv ||
       a->Hq % a->Hkv != 0 || a->Hq / a->Hkv > kRows || a->P < 0 || a->P > kMost || a->S < 0 || a->S > kMost ||
-      (a->P == 0 && a->S == 0) || static_cast<long long>(a->B) * a->T * a->Hq >= (1ll << 31))
+      (a->P == 0 && a->S == 0) || (a->pk8 && static_cast<long long>(a->P) * a->Hkv >= (1ll << 26)) || static_cast<long long>(a->B) * a->T * a->Hq >= (1ll << 31))
     return op_fail(QI_ERR_SHAPE, "qi_prefix_attention: B %d T %d Hq %d Hkv %d P %d S %d", a->B, a->T, a->Hq, a->Hkv,
                    a->P, a->S);
   return QI_OK;
@@ -1026,16 +1026,18 @@ extern "C" qi_status qi_prefix_attention(const qi_prefix_attn* a, qi_stream_t st
   qi_status st = check_sizes(a);
   if (st != QI_OK) return st;
   const bool from8 = a->pk8 || a->pv8 || a->pk_sf || a->pv_sf;
-  if (!a->q.data || !a->o.data || (a->S > 0 && (!a->k.data || !a->v.data)))
+  if (!a->q || !a->o || (a->S > 0 && (!a->k || !a->v)))
     return op_fail(QI_ERR_INVALID_ARG, "qi_prefix_attention: NULL q, o, k or v");
-  if (a->P > 0 && from8 && (!a->pk8 || !a->pv8 || !a->pk_sf || !a->pv_sf || a->pk.data || a->pv.data))
+  if (a->P > 0 && from8 && (!a->pk8 || !a->pv8 || !a->pk_sf || !a->pv_sf || a->pk || a->pv))
     return op_fail(QI_ERR_INVALID_ARG, "qi_prefix_attention: give the prefix either as pk, pv or as all of pk8, pv8, pk_sf, pv_sf");
-  if (a->P > 0 && !from8 && (!a->pk.data || !a->pv.data))
+  if (a->P > 0 && !from8 && (!a->pk || !a->pv))
     return op_fail(QI_ERR_INVALID_ARG, "qi_prefix_attention: NULL prefix");
   if (!(a->scale > 0.f) || !(a->scale < 3e38f))
     return op_fail(QI_ERR_INVALID_ARG, "qi_prefix_attention: scale must be positive and finite");
-  qi_tensor4 q = a->q, o = a->o, k = a->k, v = a->v, pk = a->pk, pv = a->pv;
-  auto good = [](qi_tensor4* t, int batch, int rows, int heads) {
+  const auto tensor = [](const void* data, const qi_strides& s) { return Tensor4{data, s.batch, s.row, s.head}; };
+  Tensor4 q = tensor(a->q, a->q_stride), o = tensor(a->o, a->o_stride), k = tensor(a->k, a->k_stride);
+  Tensor4 v = tensor(a->v, a->v_stride), pk = tensor(a->pk, a->pk_stride), pv = tensor(a->pv, a->pv_stride);
+  const auto good = [](Tensor4* t, int batch, int rows, int heads) {
     return (reinterpret_cast<uintptr_t>(t->data) & 15) == 0 && fix_stride(&t->batch, batch) &&
            fix_stride(&t->row, rows) && fix_stride(&t->head, heads);
   };
@@ -1050,6 +1052,8 @@ extern "C" qi_status qi_prefix_attention(const qi_prefix_attn* a, qi_stream_t st
       (((reinterpret_cast<uintptr_t>(a->pk8) | reinterpret_cast<uintptr_t>(a->pv8)) & 15) ||
        ((reinterpret_cast<uintptr_t>(a->pk_sf) | reinterpret_cast<uintptr_t>(a->pv_sf)) & 3)))
     return op_fail(QI_ERR_INVALID_ARG, "qi_prefix_attention: the 8-bit prefix needs 16-byte aligned codes and 4-byte aligned scales");
+  if ((reinterpret_cast<uintptr_t>(a->own_len) | reinterpret_cast<uintptr_t>(a->status)) & 3)
+    return op_fail(QI_ERR_INVALID_ARG, "qi_prefix_attention: own_len and status need 4-byte alignment");
   const int sms = device_sms();
   if (sms <= 0) return op_fail(QI_ERR_CUDA, "qi_prefix_attention: no CUDA device");
   const Plan pl = plan_for({a->B, a->T, a->Hq, a->Hkv, a->P, a->S, a->causal != 0, a->P > 0 && a->pk8 != nullptr}, sms);
@@ -1073,8 +1077,8 @@ extern "C" qi_status qi_prefix_attention(const qi_prefix_attn* a, qi_stream_t st
     r.k_sf = const_cast<uint8_t*>(a->pk_sf);
     r.v_sf = const_cast<uint8_t*>(a->pv_sf);
     const long long head = kHeadDim, row = static_cast<long long>(a->Hkv) * kHeadDim;
-    r.k = pk = qi_tensor4{ws + w.pk, row, row, head};
-    r.v = pv = qi_tensor4{ws + w.pv, row, row, head};
+    r.k = pk = Tensor4{ws + w.pk, row, row, head};
+    r.v = pv = Tensor4{ws + w.pv, row, row, head};
     const cudaError_t e = launch_kv8_read(r, bf16, s);
     if (e != cudaSuccess) return op_fail(QI_ERR_CUDA, "qi_prefix_attention: %s", cudaGetErrorString(e));
   }

@@ -497,13 +497,12 @@ qi_status qi_dit_profile_read(qi_dit* dit, double* ms, long long* launches);
 #define QI_DT_BF16 1
 #define QI_DT_F32 2
 
-/* A tensor [batch, row, head, 128] of 16-bit values: element strides of the first three
- * dimensions, the last one contiguous. data is 16-byte aligned; a stride is a positive
- * multiple of 8 (that of a dimension of size 1 is ignored). */
-typedef struct qi_tensor4 {
-  const void* data;
+/* Element strides of a tensor [batch, row, head, 128] of 16-bit values, whose last dimension
+ * is contiguous and whose first element is 16-byte aligned: positive multiples of 8 (that of
+ * a dimension of size 1 is ignored). */
+typedef struct qi_strides {
   long long batch, row, head;
-} qi_tensor4;
+} qi_strides;
 
 /* Attention of a batch that shares a prefix. For sequence b < B, query row t < T and
  * query head hq < Hq, with key head h = hq / (Hq / Hkv):
@@ -520,10 +519,10 @@ typedef struct qi_tensor4 {
  * dtype QI_DT_F16 or QI_DT_BF16 for q, o and every 16-bit K/V; scores, maxima, sums and O
  * are fp32, the probabilities are rounded to dtype as tensor-core operands. q and o are
  * [B, T, Hq, 128], o written with 16-byte stores and not overlapping any input.
- * The prefix is given either as pk, pv (batch stride ignored), or with pk.data = pv.data =
- * NULL as rows of an 8-bit cache (qi_kv8_write): codes pk8, pv8 [P, Hkv, 128] and scales
- * pk_sf, pv_sf [P, Hkv, 4], contiguous, codes 16-byte and scales 4-byte aligned; its values
- * are the codes times their scales, rounded to dtype.
+ * The prefix is given either as pk, pv (batch stride ignored), or with pk = pv = NULL as rows
+ * of an 8-bit cache (qi_kv8_write): codes pk8, pv8 [P, Hkv, 128] and scales pk_sf, pv_sf
+ * [P, Hkv, 4], contiguous, codes 16-byte and scales 4-byte aligned; its values are the codes
+ * times their scales, rounded to dtype.
  * ws: 256-byte aligned scratch of at least qi_prefix_attention_workspace(args) bytes (which
  * depends on the sizes, on whether pk8 is NULL and on the current device only; NULL if 0).
  * status: device int, or NULL: receives a non-zero code if a bounded wait in the kernel
@@ -531,19 +530,26 @@ typedef struct qi_tensor4 {
  * Results do not depend on the other sequences' contents, and repeat bit for bit.
  * Errors: INVALID_ARG (NULL, dtype, alignment, strides, scale not positive, workspace),
  * SHAPE (B, T, Hkv < 1, Hq % Hkv != 0, Hq / Hkv > 128, P + S = 0, B or Hkv > 65535, T, P or
- * S > 2^24, B T Hq >= 2^31), CUDA. */
+ * S > 2^24, B T Hq >= 2^31, P Hkv >= 2^26 in 8 bits), CUDA. */
 typedef struct qi_prefix_attn {
-  int dtype, B, T, Hq, Hkv, P, S, causal;
-  float scale;
-  qi_tensor4 q, k, v, o, pk, pv;
+  const void* q;
+  const void* k;
+  const void* v;
+  void* o;
+  const void* pk;
+  const void* pv;
   const uint8_t* pk8;
   const uint8_t* pv8;
   const uint8_t* pk_sf;
   const uint8_t* pv_sf;
   const int* own_len;
   void* ws;
-  size_t ws_bytes;
   int* status;
+  int causal;
+  float scale;
+  size_t ws_bytes;
+  qi_strides q_stride, k_stride, v_stride, o_stride, pk_stride, pv_stride;
+  int dtype, B, T, Hq, Hkv, P, S;
 } qi_prefix_attn;
 size_t qi_prefix_attention_workspace(const qi_prefix_attn* args); /* 0 also for bad sizes */
 qi_status qi_prefix_attention(const qi_prefix_attn* args, qi_stream_t stream);
@@ -560,13 +566,21 @@ qi_status qi_prefix_attention(const qi_prefix_attn* args, qi_stream_t stream);
  * T. Rows at or past lens[b] and rows whose cache row is outside 0 .. S - 1 are passed over:
  * nothing of them is read, and what is there stays as it was.
  * Errors: INVALID_ARG (NULL, dtype, alignment, strides), SHAPE (B, T, H, S < 1, B or H >
- * 65535, T or S > 2^24), CUDA. */
-qi_status qi_kv8_write(int dtype, int B, int T, int S, int H, const qi_tensor4* k, const qi_tensor4* v, uint8_t* k8,
-                       uint8_t* v8, uint8_t* k_sf, uint8_t* v_sf, const int* pos, const int* lens,
-                       qi_stream_t stream);
-qi_status qi_kv8_read(int dtype, int B, int T, int S, int H, const uint8_t* k8, const uint8_t* v8,
-                      const uint8_t* k_sf, const uint8_t* v_sf, const int* pos, const int* lens, const qi_tensor4* k,
-                      const qi_tensor4* v, qi_stream_t stream);
+ * 65535, T or S > 2^24, T H >= 2^26), CUDA. */
+typedef struct qi_kv8 {
+  void* k; /* read by qi_kv8_write, written by qi_kv8_read */
+  void* v;
+  uint8_t* k8;
+  uint8_t* v8;
+  uint8_t* k_sf;
+  uint8_t* v_sf;
+  const int* pos;
+  const int* lens;
+  qi_strides k_stride, v_stride;
+  int dtype, B, T, S, H;
+} qi_kv8;
+qi_status qi_kv8_write(const qi_kv8* args, qi_stream_t stream);
+qi_status qi_kv8_read(const qi_kv8* args, qi_stream_t stream);
 
 /* Residual addition, RMSNorm and the MXFP8 operand of the next block-scaled GEMM:
  *   x_out = round(x + delta), y = x_out / sqrt(mean(x_out^2) + eps) * gain,
@@ -582,17 +596,16 @@ qi_status qi_kv8_read(int dtype, int B, int T, int S, int H, const uint8_t* k8, 
  * those of rows past `rows` are left as they were.
  * Errors: INVALID_ARG (NULL, dtype, alignment, eps negative or not finite), SHAPE, CUDA. */
 typedef struct qi_add_rmsnorm {
-  int x_dtype, delta_dtype, rows, K, w_f32, plus_one;
-  float eps;
   const void* x;
-  long long x_stride;
   const void* delta;
-  long long delta_stride;
   void* x_out;
-  long long x_out_stride;
   const void* w;
   uint8_t* q;
   uint8_t* sf;
+  int plus_one;
+  float eps;
+  long long x_stride, delta_stride, x_out_stride;
+  int x_dtype, delta_dtype, rows, K, w_f32;
 } qi_add_rmsnorm;
 qi_status qi_add_rmsnorm_mxfp8(const qi_add_rmsnorm* args, qi_stream_t stream);
 

@@ -268,21 +268,22 @@ def test_attention_refuses(qi):
         qi.prefix_attention(q, k[:, :1].expand(-1, 200, -1, -1), v, pk, pv)
     q, k, v, pk, pv = _batch(qi, B=32, P=8192)             # sizes that go by partial results
     o = torch.zeros_like(q)
-    args = [0, 32, 1, 8, 2, 8192, 200, 0, 0.1]
-    for t in (q, k, v, o):
-        args += [t.data_ptr(), *t.stride()[:3]]
-    for t in (pk, pv):
-        args += [t.data_ptr(), 0, *t.stride()[:2]]
+    strides = [x for t in (q, k, v, o) for x in t.stride()[:3]] + [0, *pk.stride()[:2], 0, *pv.stride()[:2]]
     L = qi.lib()
-    need = L.qi_prefix_attention_workspace(qi._PREFIX_ATTN.pack(*args, *[0] * 8))
+
+    def args(ws, size):
+        head = qi._ATTN_HEAD.pack(*[t.data_ptr() for t in (q, k, v, o, pk, pv)], 0, 0, 0, 0, 0, ws, 0, 0, 0.1)
+        return head + qi._ATTN_TAIL.pack(size, *strides, 0, 32, 1, 8, 2, 8192, 200)
+
+    need = L.qi_prefix_attention_workspace(args(0, 0))
     assert need > 0
     ws = torch.empty(need + 256, dtype=torch.uint8, device="cuda")
     for ptr, size in ((0, 0), (ws.data_ptr(), need - 1), (ws.data_ptr() + 8, need)):
         with pytest.raises(qi.QiError, match="workspace"):
-            qi._check(L.qi_prefix_attention(qi._PREFIX_ATTN.pack(*args, 0, 0, 0, 0, 0, ptr, size, 0), None))
+            qi._check(L.qi_prefix_attention(args(ptr, size), None))
     assert (o == 0).all()
     st = torch.cuda.current_stream().cuda_stream
-    qi._check(L.qi_prefix_attention(qi._PREFIX_ATTN.pack(*args, 0, 0, 0, 0, 0, ws.data_ptr(), need, 0), st))
+    qi._check(L.qi_prefix_attention(args(ws.data_ptr(), need), st))
     assert torch.equal(o, qi.prefix_attention(q, k, v, pk, pv, scale=0.1))
 
 
