@@ -353,6 +353,8 @@ def _strides4(t, like, shape, name):
     """Batch, row and head strides of a 16-bit tensor `shape` = [batch, row, head, 128] (batch may be left out)."""
     if t.dtype != like.dtype or t.device != like.device or tuple(t.shape) != shape:
         raise ValueError(f"{name}: want {like.dtype} {like.device} {shape}, got {t.dtype} {t.device} {tuple(t.shape)}")
+    if not t.numel():  # (whatever its strides)
+        return 0, 0, 0
     st = t.stride()
     if st[-1] != 1:
         raise ValueError(f"{name}: the last dimension must be contiguous")
@@ -375,9 +377,10 @@ def _addr(t):
     return 0 if t is None else t.data_ptr()
 
 
-def _elsewhere(t, stream):
+def _elsewhere(t, stream, others=()):
     """A context in which t's device is current and `stream` (None: that device's current one) the current
-    stream, so that what a call allocates belongs to it. Raises for tensors that are not on a GPU."""
+    stream, so that what a call allocates belongs to it. The memory of t and of `others`, once freed, is not
+    reused before `stream` is through with what it was given until then. Raises for tensors that are not on a GPU."""
     import contextlib
     import torch
     if not t.is_cuda:
@@ -387,6 +390,9 @@ def _elsewhere(t, stream):
     stack = contextlib.ExitStack()
     stack.enter_context(torch.cuda.device(t.device))
     if stream is not None:
+        for x in (t, *others):
+            if x is not None and x.is_cuda:
+                x.record_stream(stream)
         stack.enter_context(torch.cuda.stream(stream))
     return stack
 
@@ -436,15 +442,16 @@ def prefix_attention(q, k, v, prefix_k=None, prefix_v=None, prefix8: KV8Cache | 
 
     q [B, T, Hq, 128]; k, v [B, S, Hkv, 128] (S may be 0, or k = v = None); prefix_k, prefix_v
     [P, Hkv, 128], or prefix8, an 8-bit cache's rows ([P, Hkv, ...], KV8Cache.prefix). float16 or
-    bfloat16, any strides with a contiguous last dimension. own_len: int32 [B] on the device, the own
-    rows in use (None: S). causal: query row t of T sees own rows up to own_len - T + t. scale: default
-    1 / sqrt(128). status: int32 [1] on the device that receives a non-zero code if a wait in the
-    kernel expires. stream: default the current one of q's device. Returns o [B, T, Hq, 128] (`out`, if
-    given)."""
+    bfloat16, the last dimension contiguous, other strides positive multiples of 8 (nothing expanded).
+    own_len: int32 [B] on the device, the own rows in use (None: S). causal: query row t of T sees own
+    rows up to own_len - T + t. scale: default 1 / sqrt(128). status: int32 [1] on the device that
+    receives a non-zero code if a wait in the kernel expires. stream: default the current one of q's
+    device; another one has to come after whatever wrote the arguments. Returns o [B, T, Hq, 128]
+    (`out`, if given)."""
     import torch
     dev = q.get_device()
     if stream is not None or dev < 0 or dev != torch._C._cuda_getDevice():
-        with _elsewhere(q, stream):
+        with _elsewhere(q, stream, (k, v, prefix_k, prefix_v, *(prefix8 or ()), own_len, out, status)):
             return prefix_attention(q, k, v, prefix_k, prefix_v, prefix8, own_len, causal, scale, out, status)
     key = (q.dtype, q.device, q.shape, q.stride(), _layout(k), _layout(v), _layout(prefix_k), _layout(prefix_v),
            None if prefix8 is None else (*map(_layout, prefix8),), None if own_len is None else _layout(own_len),
@@ -502,14 +509,14 @@ def _kv8_call(write, cache, k, v, pos, lens, dev):
 
 
 def kv8_write(cache: KV8Cache, k, v, pos=None, lens=None, stream=None):
-    """Quantises k, v [B, T, H, 128] (float16 or bfloat16, any strides with a contiguous last dimension)
+    """Quantises k, v [B, T, H, 128] (float16 or bfloat16, strides as for prefix_attention)
     into the cache: row t < lens[b] of sequence b becomes cache row pos[b] + t (int32 [B] on the device;
     None: 0 and T). Rows that fall outside the cache are passed over. stream: default the current one of
     the cache's device. Returns the cache."""
     import torch
     dev = cache.k.get_device()
     if stream is not None or dev < 0 or dev != torch._C._cuda_getDevice():
-        with _elsewhere(cache.k, stream):
+        with _elsewhere(cache.k, stream, (*cache[1:], k, v, pos, lens)):
             return kv8_write(cache, k, v, pos, lens)
     _kv8_call(True, cache, k, v, pos, lens, dev)
     return cache
@@ -522,7 +529,7 @@ def kv8_read(cache: KV8Cache, T: int, dtype, pos=None, lens=None, out=None, stre
     import torch
     dev = cache.k.get_device()
     if stream is not None or dev < 0 or dev != torch._C._cuda_getDevice():
-        with _elsewhere(cache.k, stream):
+        with _elsewhere(cache.k, stream, (*cache[1:], *(out or ()), pos, lens)):
             return kv8_read(cache, T, dtype, pos, lens, out)
     if out is None:
         B, S, H, _ = cache.k.shape
@@ -573,7 +580,7 @@ def add_rmsnorm_mxfp8(x, delta=None, w=None, plus_one: bool = False, eps: float 
     import torch
     dev = x.get_device()
     if stream is not None or dev < 0 or dev != torch._C._cuda_getDevice():
-        with _elsewhere(x, stream):
+        with _elsewhere(x, stream, (delta, w, x_out, q, sf)):
             return add_rmsnorm_mxfp8(x, delta, w, plus_one, eps, x_out, q, sf)
     key = (x.dtype, x.device, x.shape, x.stride(), _layout(delta), _layout(w), _layout(x_out), _layout(q), _layout(sf))
     plan = _norm_layouts.get(key)

@@ -1,9 +1,9 @@
 // Memory-bound operators of batches that share a prompt: the 8-bit K/V cache (write,
 // read back) and the residual RMSNorm that ends in an MXFP8 operand.
 //
-// Both work on groups of 8 consecutive values per thread (one 16-byte access of 16-bit
-// data), so a block of 32 values that shares a scale is four neighbouring lanes: its
-// largest magnitude takes two shuffles, and every load and store of a warp is contiguous.
+// All work on groups of 8 or 16 consecutive values per thread, so a block of 32 values that
+// shares a scale is four or two neighbouring lanes: its largest magnitude takes a shuffle or
+// two, and every load and store of a warp is contiguous.
 #include <cstdarg>
 #include <cstdio>
 
@@ -101,7 +101,7 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
   return lo | (hi << 16);
 }
 
-// The largest magnitude of 16 packed values, in fp32 (NaNs are passed over)
+// The largest magnitude of 16 packed values, in fp32 (NaNs are passed over; NaN if all are)
 __device__ __forceinline__ float absmax16(const uint32_t (&u)[8], const __half*) {
   __half2 m = __habs2(*reinterpret_cast<const __half2*>(&u[0]));
 #pragma unroll
@@ -122,7 +122,7 @@ template <typename T>
 __device__ __forceinline__ uint4 mx_quant16(uint4 a, uint4 b, uint32_t& scale) {
   const uint32_t u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
   float top = absmax16(u, static_cast<const T*>(nullptr));
-  top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+  top = fmaxf(fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1)), 0.f);  // (a block of NaNs counts as zero)
   const int e = mx_exponent(top);
   const float inv = pow2(-e);
   float v[16];
@@ -175,8 +175,9 @@ __device__ __forceinline__ long long kv8_offset(const Tensor4& t, const Kv8At& x
 }
 
 // Thread = kKv8Groups groups of 16 values of one (row, head) of K and the same of V; two lanes
-// share a scale. Bound by the ALU pipe and HBM together: 17.7 instructions a value with groups
-// of 8 and the position worked out for each, %KV8W% now (16 prompts of up to 2048 rows, 8 heads).
+// share a scale. Bound by issue (71 % of the issue slots) more than by HBM (51 %): with groups of
+// 8 and the position worked out for each, 17.7 instructions a value and 26.4 us; now 9.4 and
+// 20.3 us (16 prompts of up to 2048 rows, 8 heads; the bytes alone take 16.9 us).
 template <typename T>
 __global__ void __launch_bounds__(kKv8Threads) kv8_write_kernel(const __grid_constant__ Kv8Args a) {
   grid_dep_wait();
@@ -240,7 +241,7 @@ __device__ __forceinline__ void mx_values8(uint2 c, uint32_t scale, float (&v)[8
   }
 }
 
-// Bound by HBM: 4 prompts of 1999 rows of 32 heads in %KV8R%.
+// Bound by HBM: 4 prompts of 1999 rows of 32 heads in 22.2 us, 6.2 TB/s, 91 % of the copy rate.
 template <typename T>
 __global__ void __launch_bounds__(kKv8Threads) kv8_read_kernel(const __grid_constant__ Kv8Args a) {
   grid_dep_wait();
@@ -341,7 +342,11 @@ __device__ __forceinline__ F2 lanes_sum(F2 x, int lanes) {
 
 // One CTA per row. The sum goes to shared memory (as it is stored, in TX) between the two
 // passes over it: a thread reads back only what it wrote, so the one barrier is that of the
-// reduction, and there is none in a CTA of one warp. %NORM%
+// reduction, and there is none in a CTA of one warp. 4503 rows of 4096, fp32 with an fp16 delta:
+// 37.1 us at 128 threads a row, 80 % of the copy rate. The first pass alone (loads, the sum, its
+// store) takes 28.5 us and the arithmetic without stores 26: a CTA's reduction and second pass
+// overlap other CTAs' loads, but not wholly. 256 threads 37.4 us, 64 threads 48, one warp 66; rows
+// staged by cp.async a row ahead 48 (fewer resident CTAs).
 constexpr int kNormUnroll = 2;  // groups of 8 whose loads are issued together
 template <typename TX, typename TD>
 __global__ void add_rmsnorm_kernel(const __grid_constant__ NormParams p) {

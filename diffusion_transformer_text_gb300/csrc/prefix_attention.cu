@@ -19,8 +19,11 @@
 //           per sequence, where a joint unit would read the whole prefix for T G of
 //           the MMA's 128 rows.
 // Where the units would not fill the SMs, or leave a ragged last wave, a unit's
-// tiles are cut into chunks; each writes its unnormalised O with its maximum and
-// sum, and merge_partials joins a row's parts in a fixed order (no atomics).
+// tiles are cut into chunks. Up to kJoinMost chunks of a joint block can be one
+// cluster that adds its parts in distributed shared memory (cluster_join, JOIN: one
+// launch, one unit per CTA); otherwise each writes its unnormalised O with its
+// maximum and sum, and merge_partials joins a row's parts. Both in a fixed order, no
+// atomics. Blocks of at most 16 rows may go to the kernel of prefix_attention_few.cu.
 //
 // The inside of a unit is that of the block-causal kernel (attention.cu): one CTA
 // per SM, K and V rings filled by TMA, S and the two key halves' O in tensor
@@ -33,6 +36,13 @@
 // product, so that whatever the cache holds there (0 x NaN is NaN) cannot reach O.
 // P is rounded to the operands' 16-bit type, as the tensor cores need it: an error
 // of half a step of that type per term, as large as the rounding of the output.
+//
+// Measured: 4 x 4096 rows over 407 shared and 4096 own keys each, 32 heads: 938 us,
+// 1290 TFLOP/s, 67 % of the library product's rate. A tile takes about 1800 cycles, the two
+// products 1024 of them: S, softmax, P and P V follow one another for each half, and only the
+// other half's work overlaps them. Between two units 2500 cycles go to the epilogue's reads of
+// tensor memory, which is what small cases show. 32 single tokens over 8192 shared rows: 28.0
+// us with the merge, of which a unit's chain of tiles and the second launch are all.
 #include <climits>
 #include <cstdarg>
 #include <cstdio>
@@ -736,12 +746,17 @@ int ceil_div(int a, int b) { return (a + b - 1) / b; }
 // epilogue, splitting costs kMergeTiles for the partials and the second launch. The few-row
 // kernel reads an 8-bit prefix as it is; the other first has it turned into 16 bits
 // (kConvert a 2^20 values: written and read again). Measured, 128-row against few-row
-// kernel: %PLAN%
+// kernel, us (16 sequences, 32 key heads, 8192 prefix + 256 own keys, one token each):
+//   that, 16-bit prefix   44.6 / 38.8      8-bit prefix   76 / 41
+//   32 sequences, groups of 4, 8192 + 512, 16-bit   29.6 / 33.3      8-bit   36 / 73.6
+//   7 sequences of 5 tokens, 16 bits   12.8 / 11.6      8 sequences of 16 rows, 8 bits   27.0 / 49.9
+//   one sequence over 8192 prefix rows, 32 heads   28.7 / 26.0
+//   64 sequences, 2048 own keys   88.4 / 85.2      2 sequences, 8 heads, 300 + 40   8.8 / 6.7
 //
 // Order of the joint units: head-major, so that the CTAs running at one time share a few
 // heads' K/V in L2; with `causal`, whose units differ in length, last row blocks first
 // over all heads and sequences, so that the CTAs' sums of lengths agree (3 x 777 rows over
-// 2048 + 1201 keys, 4 key heads: %BYBLOCK%), as long as all K/V stay in half of the L2.
+// 2048 + 1201 keys, 4 key heads: 90.4 us, head-major 97.0), as long as all K/V stay in half of the L2.
 struct Rate {
   float tile, tile8, unit;  // a 16-bit tile, a tile of codes, a unit
 };
@@ -958,7 +973,8 @@ qi_status check_sizes(const qi_prefix_attn* a) {
   constexpr int kMost = 1 << 24;
   if (a->B < 1 || a->B > 65535 || a->T < 1 || a->T > kMost || a->Hkv < 1 || a->Hkv > 65535 || a->Hq < a->Hkv ||
       a->Hq % a->Hkv != 0 || a->Hq / a->Hkv > kRows || a->P < 0 || a->P > kMost || a->S < 0 || a->S > kMost ||
-      (a->P == 0 && a->S == 0) || (a->pk8 && static_cast<long long>(a->P) * a->Hkv >= (1ll << 26)) || static_cast<long long>(a->B) * a->T * a->Hq >= (1ll << 31))
+      (a->P == 0 && a->S == 0) || (a->pk8 && static_cast<long long>(a->P) * a->Hkv >= (1ll << 26)) ||
+      static_cast<long long>(a->B) * a->T * a->Hq >= (1ll << 31))
     return op_fail(QI_ERR_SHAPE, "qi_prefix_attention: B %d T %d Hq %d Hkv %d P %d S %d", a->B, a->T, a->Hq, a->Hkv,
                    a->P, a->S);
   return QI_OK;
@@ -984,7 +1000,7 @@ cudaError_t launch(const Maps& tm, const Maps8* t8, const Params& p, float scale
   }
   if (e != cudaSuccess || !p.pl.split) return e;
   // Warps per row: as many as its parts keep busy, unless the rows alone fill the GPU (1024
-  // rows of 16 parts: %MERGE%)
+  // rows of 16 parts, with the attention before it: 31.6 us at one warp a row, 29.4 at 4 or 8)
   const long long rows = static_cast<long long>(p.B) * p.T * p.Hq;
   const int parts = (p.pl.packed ? p.pl.nchp + p.pl.nch : p.pl.nch) * p.pl.per;
   const int w = rows > 16384 || parts < 4 ? 1 : parts < 16 ? 4 : 8;

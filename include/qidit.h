@@ -586,9 +586,10 @@ qi_status qi_kv8_read(const qi_kv8* args, qi_stream_t stream);
  *   x_out = round(x + delta), y = x_out / sqrt(mean(x_out^2) + eps) * gain,
  *   (q, sf) = MXFP8(y) as qi_quant_mxfp8 lays it out for qi_gemm_mxfp8.
  * x, x_out: [rows, K] of x_dtype; delta: [rows, K] of delta_dtype, or NULL (x_out, if given,
- * is then a copy of x); row strides in elements. x_out may be x itself, or NULL if the sum
- * is not wanted. The norm is that of the stored sum, rounded to x_dtype. gain: w [K] (fp32
+ * is then a copy of x); row strides in elements. x_out may be x itself (or delta, of the same
+ * type and stride), or NULL if the sum is not wanted. The norm is that of the stored sum, rounded to x_dtype. gain: w [K] (fp32
  * if w_f32, else bf16 bits), 1 + w if plus_one (the ZeroCenterRMSNorm form), 1 if w is NULL.
+ * The sum of squares has to stay finite in fp32, as in any fp32 norm.
  * The statistics and the products carry an error term beside each fp32 value, so that y is
  * the fp32 rounding of its exact value but for the last bits of rsqrt's correction.
  * K a multiple of 128 up to 16384, pointers and row strides in bytes multiples of 16, w
