@@ -90,8 +90,6 @@ struct Exchange {
   uint32_t issued[3][5];
   uint32_t pad;
   float2 ml[2][kR];  // JOIN: each warpgroup's maxima and sums
-  uint32_t scales[8][2][32];  // [converting warp][tile parity] the four scale bytes of its rows,
-  uint2 halves[8][2][32];     // and their half_scale
 };
 template <bool Q8>
 constexpr int smem_bytes() {
@@ -517,41 +515,25 @@ __global__ void __launch_bounds__(Cfg<Q8>::kThreads, 1)
     }
     if (!ok && lane == 0) give_up(kErrTimeoutEpilogue);
   } else if constexpr (Q8) {
-    // ---------------- codes to 16 bits: warps 12..15 K, 16..19 V. Sixteen lanes per row, 8 codes
-    // each: a 16-byte piece of the swizzled tile per lane, eight lanes to a 128-byte line (with 16
-    // codes a lane, two pieces, the stores met in the banks: 54 us, 42 with one; 16 sequences over
-    // 8192 prefix rows, 32 key heads). A tile takes about 2400 cycles, 1000 of them here, between
-    // the codes' arrival and the product that needs them.
+    // ---------------- codes to 16 bits: warps 12..15 K, 16..19 V. A lane turns one row (key): its
+    // four scale bytes stay with it, and eight lanes' pieces of one column lie in eight different
+    // 16-byte places of a 128-byte line, of the codes (swizzled as the 16-bit tiles are) and of the
+    // tile alike, so neither access meets itself in the banks.
     const int kv = warp >= 16 ? 1 : 0;
-    const int tid = (warp & 3) * 32 + lane;
-    const int chunk = tid & 15, r0 = tid >> 4;  // rows r0 + 8 i
-    const uint8_t* sf = kv ? t8.v_sf : t8.k_sf;  // 4-byte aligned
-    uint8_t* tiles = sT + kv * kSt * kTile;
-    const uint8_t* codes = sC + kv * kCSt * kCode;
-    // The warps of a tile do not wait for each other. A warp's 32 rows are 2 w + (0, 1) + 8 i; lane
-    // 2 i + (0, 1) fetches that row's four scale bytes a tile ahead (one load a lane), and they go
-    // round by shared memory.
-    const int cw = warp - 12;
-    const uint32_t* sf4 = reinterpret_cast<const uint32_t*>(sf);
+    const int row = (warp & 3) * 32 + lane;
+    const uint32_t turn = static_cast<uint32_t>(row & 7) << 4;
+    const uint32_t* sf4 = reinterpret_cast<const uint32_t*>(kv ? t8.v_sf : t8.k_sf);  // 4-byte aligned
+    uint8_t* tiles = sT + kv * kSt * kTile + row * 128;
+    const uint8_t* codes = sC + kv * kCSt * kCode + row * 128;
     const auto scales_of = [&](const Unit& un, int tile) -> uint32_t {
-      const int row = tile * kKeys + 2 * (warp & 3) + (lane & 1) + 8 * (lane >> 1);
-      return row < p.P ? sf4[static_cast<long long>(row) * p.Hkv + un.h] : 0u;  // past the end: zero codes
-    };
-    const auto keep = [&](uint32_t parity, uint32_t bytes) {
-      ex.scales[cw][parity][lane] = bytes;
-      if (!BF16)
-        ex.halves[cw][parity][lane] =
-            make_uint2(half_scale(bytes & 255u) | half_scale((bytes >> 8) & 255u) << 16,
-                       half_scale((bytes >> 16) & 255u) | half_scale(bytes >> 24) << 16);
+      const int r = tile * kKeys + row;
+      return r < p.P ? sf4[static_cast<long long>(r) * p.Hkv + un.h] : 0u;  // past the end: zero codes
     };
     uint32_t t = 0, tc = 0;
     bool ok = true;
     for (int u = blockIdx.x; u < total; u += gridDim.x) {
       const Unit un = unit_of(p, u);
-      if (un.pn > 0) {
-        keep(tc & 1u, scales_of(un, un.p0));
-        __syncwarp();
-      }
+      uint32_t bytes = un.pn > 0 ? scales_of(un, un.p0) : 0u;
       for (int j = 0; j < un.n; ++j) {
         const uint32_t tt = t + j, st = tt % kSt, cs = tc % kCSt;
         ok = ok && __all_sync(0xffffffffu, mbar_wait(&bars[kEmpty + 3 * kv + st], ((tt / kSt) & 1u) ^ 1u));
@@ -562,36 +544,40 @@ __global__ void __launch_bounds__(Cfg<Q8>::kThreads, 1)
         const uint32_t ahead = j + 1 < un.pn ? scales_of(un, un.p0 + j + 1) : 0u;
         ok = ok && __all_sync(0xffffffffu, mbar_wait(&bars[kCFull + 2 * kv + cs], (tc / kCSt) & 1u));
         if (ok) {
-          const uint8_t* src = codes + cs * kCode + tid * 8;
-          uint8_t* dst = tiles + st * kTile + (chunk >> 3) * kBox + r0 * 128 + (((chunk & 7) ^ r0) << 4);
-          const uint8_t* bytes = reinterpret_cast<const uint8_t*>(&ex.scales[cw][tc & 1u][lane >> 4]) + (chunk >> 2);
-          const uint16_t* halves = reinterpret_cast<const uint16_t*>(&ex.halves[cw][tc & 1u][lane >> 4]) + (chunk >> 2);
-          // All loads before the first store: nothing tells the compiler that the two do not
-          // overlap, and a piece at a time took 110 cycles a piece.
-          uint2 c[16];
-          uint32_t h[16];
+          const uint8_t* src = codes + cs * kCode;
+          uint8_t* dst = tiles + st * kTile;
+          // (all loads before the first store: nothing tells the compiler that the two do not overlap)
+          uint4 c[8];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            c[i] = *reinterpret_cast<const uint2*>(src + i * 1024);
-            h[i] = BF16 ? static_cast<uint32_t>(bytes[i * 8]) : halves[i * 8];
+          for (int i = 0; i < 8; ++i) c[i] = *reinterpret_cast<const uint4*>(src + ((i << 4) ^ turn));
+          // fp16: in half precision, unless a scale of the warp's rows does not allow it
+          uint32_t h[4], worst = 0;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t byte = (bytes >> (8 * i)) & 255u;
+            h[i] = BF16 ? byte : half_scale(byte);
+            worst = max(worst, h[i]);
           }
-          // fp16: in half precision, unless a scale of the warp's rows does not allow it (decided
-          // for the whole tile)
-          uint32_t worst = 0;
-#pragma unroll
-          for (int i = 0; i < 16; ++i) worst = max(worst, h[i]);
+          const auto put = [&](int i, uint4 lo, uint4 hi) {  // pieces 2 i and 2 i + 1
+            uint8_t* box = dst + (i >> 2) * kBox;
+            *reinterpret_cast<uint4*>(box + (((2 * i & 7) << 4) ^ turn)) = lo;
+            *reinterpret_cast<uint4*>(box + (((2 * i & 7) + 1) << 4 ^ turn)) = hi;
+          };
           if (!BF16 && __any_sync(0xffffffffu, worst == kNoHalf)) {
-#pragma unroll 1
-            for (int i = 0; i < 16; ++i)
-              *reinterpret_cast<uint4*>(dst + i * 1024) =
-                  codes_to_16bit<BF16, false>(*reinterpret_cast<const uint2*>(src + i * 1024), bytes[i * 8]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const uint32_t byte = (bytes >> (8 * (i >> 1))) & 255u;
+              put(i, codes_to_16bit<BF16, false>(make_uint2(c[i].x, c[i].y), byte),
+                  codes_to_16bit<BF16, false>(make_uint2(c[i].z, c[i].w), byte));
+            }
           } else {
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-              *reinterpret_cast<uint4*>(dst + i * 1024) = codes_to_16bit<BF16, !BF16>(c[i], h[i]);
+            for (int i = 0; i < 8; ++i)
+              put(i, codes_to_16bit<BF16, !BF16>(make_uint2(c[i].x, c[i].y), h[i >> 1]),
+                  codes_to_16bit<BF16, !BF16>(make_uint2(c[i].z, c[i].w), h[i >> 1]));
           }
         }
-        keep((tc & 1u) ^ 1u, ahead);
+        bytes = ahead;
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0 && ok) {
