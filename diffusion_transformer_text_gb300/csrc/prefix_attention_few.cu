@@ -128,6 +128,13 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, u
       : "memory");
 }
 
+// One lane of a converged warp, always the same
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(one));
+  return one != 0;
+}
+
 // 2^e as a half, for the exponents with which code * 2^e can be formed in half precision (codes
 // have 4 significant bits: the product is exact or, below 2^-14, rounded once); kNoHalf else.
 constexpr uint32_t kNoHalf = 0xFFFFu;
@@ -308,8 +315,8 @@ __global__ void __launch_bounds__(Cfg<Q8>::kThreads, 1)
       }
     }
   } else if (warp == 1) {
-    // ---------------- S^T issuer
-    if (lane == 0) {
+    // ---------------- S^T issuer. The warp walks as a whole, so that the descriptors are uniform.
+    {
       const uint64_t kdesc0 = sw128_kmajor_desc(smem_u32(sT));
       const uint64_t qdesc0 = sw128_kmajor_desc(smem_u32(sQ));
       uint32_t t = 0, ku = 0;
@@ -318,35 +325,41 @@ __global__ void __launch_bounds__(Cfg<Q8>::kThreads, 1)
         const Unit un = unit_of(p, u);
         if (un.n == 0) continue;
         const uint32_t qb = ku % kQBufs;
-        ok = !*abort_flag && mbar_wait(&bars[kQFull + qb], (ku / kQBufs) & 1u);
+        ok = __all_sync(0xffffffffu, !*abort_flag && mbar_wait(&bars[kQFull + qb], (ku / kQBufs) & 1u));
         if (!ok) break;
         const uint64_t qd = qdesc0 + ((qb * kQTile) >> 4);
         for (int j = 0; j < un.n; ++j, ++t) {
           const uint32_t st = t % kSt, sb = t % kSBufs;
-          ok = mbar_wait(&bars[kSFree + sb], ((t / kSBufs) & 1u) ^ 1u) &&
-               mbar_wait(&bars[kFull + st], (t / kSt) & 1u);
+          ok = __all_sync(0xffffffffu, mbar_wait(&bars[kSFree + sb], ((t / kSBufs) & 1u) ^ 1u) &&
+                                           mbar_wait(&bars[kFull + st], (t / kSt) & 1u));
           if (!ok) break;
           tc_fence_after();
           const uint64_t kd = kdesc0 + ((st * kTile) >> 4);
+          if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < kHeadDim / 16; ++k)
-            mma_ss(tmem + kColS + 16 * sb, kd + (((k >> 2) * kBox + (k & 3) * 32) >> 4),
-                   qd + (((k >> 2) * kQBox + (k & 3) * 32) >> 4), kIdescS, k > 0 ? 1u : 0u);
-          mma_commit(&bars[kSFull + sb]);
-          mma_commit(&bars[kEmpty + st]);
+            for (int k = 0; k < kHeadDim / 16; ++k)
+              mma_ss(tmem + kColS + 16 * sb, kd + (((k >> 2) * kBox + (k & 3) * 32) >> 4),
+                     qd + (((k >> 2) * kQBox + (k & 3) * 32) >> 4), kIdescS, k > 0 ? 1u : 0u);
+            mma_commit(&bars[kSFull + sb]);
+            mma_commit(&bars[kEmpty + st]);
+            if (j + 1 == un.n) mma_commit(&bars[kQEmpty + qb]);
+          }
+          __syncwarp();
         }
         if (!ok) break;
-        mma_commit(&bars[kQEmpty + qb]);
         ++ku;
       }
-      if (!ok) give_up(kErrTimeoutMma);
-      mma_commit(&bars[kDrainQK]);
-      if (!mbar_wait(&bars[kDrainQK], 0)) report_error(p.err, kErrTimeoutDrain);
+      if (elect_one()) {
+        if (!ok) give_up(kErrTimeoutMma);
+        mma_commit(&bars[kDrainQK]);
+        if (!mbar_wait(&bars[kDrainQK], 0)) report_error(p.err, kErrTimeoutDrain);
+      }
+      __syncwarp();
     }
   } else if (warp == 3) {
     // ---------------- O^T issuer: the first tile of each warpgroup in a unit overwrites its O^T
     // (which it has read: its P comes after)
-    if (lane == 0) {
+    {
       const uint64_t vdesc0 = sw128_mnmajor_desc(smem_u32(sT + kSt * kTile), kBox, 1024);
       const uint64_t pdesc0 = sw128_kmajor_desc(smem_u32(sP));
       uint32_t t = 0, cleared = 0;
@@ -360,22 +373,29 @@ __global__ void __launch_bounds__(Cfg<Q8>::kThreads, 1)
             ok = ok && mbar_wait(&bars[kVClean + st], (cleared >> st) & 1u);
             cleared ^= 1u << st;  // the stage's phase
           }
-          ok = ok && mbar_wait(&bars[kPFull + sb], (t / kSBufs) & 1u);
+          ok = __all_sync(0xffffffffu, ok && mbar_wait(&bars[kPFull + sb], (t / kSBufs) & 1u));
           if (!ok) break;
           tc_fence_after();
           const uint64_t vd = vdesc0 + ((st * kTile) >> 4);
           const uint64_t pd = pdesc0 + ((sb * kQTile) >> 4);
+          if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < kKeys / 16; ++k)
-            mma_ss(tmem + kColO + 16 * (t & 1u), vd + ((k * 2048) >> 4),
-                   pd + (((k >> 2) * kQBox + (k & 3) * 32) >> 4), kIdescO, (j > 1 || k > 0) ? 1u : 0u);
-          mma_commit(&bars[kPDone + sb]);
-          mma_commit(&bars[kEmpty + 3 + st]);
+            for (int k = 0; k < kKeys / 16; ++k)
+              mma_ss(tmem + kColO + 16 * (t & 1u), vd + ((k * 2048) >> 4),
+                     pd + (((k >> 2) * kQBox + (k & 3) * 32) >> 4), kIdescO, (j > 1 || k > 0) ? 1u : 0u);
+            mma_commit(&bars[kPDone + sb]);
+            mma_commit(&bars[kEmpty + 3 + st]);
+          }
+          __syncwarp();
         }
+        if (!ok) break;
       }
-      if (!ok) give_up(kErrTimeoutMma);
-      mma_commit(&bars[kDrainPV]);
-      if (!mbar_wait(&bars[kDrainPV], 0)) report_error(p.err, kErrTimeoutDrain);
+      if (elect_one()) {
+        if (!ok) give_up(kErrTimeoutMma);
+        mma_commit(&bars[kDrainPV]);
+        if (!mbar_wait(&bars[kDrainPV], 0)) report_error(p.err, kErrTimeoutDrain);
+      }
+      __syncwarp();
     }
   } else if (warp < 12) {
     // ---------------- softmax: warpgroup s takes the tiles of parity s; thread = one key
