@@ -221,11 +221,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (uint32_t i = t > kVStages ? t - kVStages : 0; i < t; ++i)
           if (!mbar_wait(&bars[kVFull + i % kVStages], (i / kVStages) & 1u)) report_error(p.err, kErrTimeoutDrain);
       }
-    } else if (lane != 0) {
-      // one thread per warp works in these
     } else if (warp == 3) {
       // ---------------- P V issuer: nothing between its waits but what it must decide; a
-      // flag read for every tile here cost 4 % of a 1024^2 image's time
+      // flag read for every tile here cost 4 % of a 1024^2 image's time. The issuing warps walk
+      // as a whole, so that the descriptors are uniform; one lane issues.
       const uint64_t vdesc0 = sw128_mnmajor_desc(smem_u32(sV), kBox, 1024);
       uint32_t t = 0;
       uint32_t ku = 0, cleared = 0;
@@ -233,7 +232,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int u = blockIdx.x; ok && u < total; u += gridDim.x) {
         const Unit un = unit_of(p, u);
         if (un.n == 0) continue;
-        ok = !*abort_flag;
+        ok = __all_sync(0xffffffffu, !*abort_flag);
         if (!ok) break;
         for (int j = 0; j < un.n; ++j, ++t) {
           const uint32_t b = t & 1u;
@@ -244,31 +243,39 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = ok && mbar_wait(&bars[kVClean + st], (cleared >> st) & 1u);
             cleared ^= 1u << st;  // the stage's phase
           }
-          if (!ok) break;
           const uint64_t vd = vdesc0 + ((st * kTile) >> 4);
           for (int h = 0; h < 2; ++h) {
-            ok = mbar_wait(&bars[kPFull + b * 2 + h], (t >> 1) & 1u);
+            ok = __all_sync(0xffffffffu, ok && mbar_wait(&bars[kPFull + b * 2 + h], (t >> 1) & 1u));
             if (!ok) break;
             tc_fence_after();
+            if (elect_one()) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mma_ts(tmem + kColO + 128u * h, tmem + kColP + b * 64 + h * 32 + k * 8,
-                     vd + ((static_cast<uint32_t>(4 * h + k) * 2048) >> 4), kIdescPV, (j > 0 || k > 0) ? 1u : 0u);
-            mma_commit(&bars[kPvDone + b * 2 + h]);
+              for (int k = 0; k < 4; ++k)
+                mma_ts(tmem + kColO + 128u * h, tmem + kColP + b * 64 + h * 32 + k * 8,
+                       vd + ((static_cast<uint32_t>(4 * h + k) * 2048) >> 4), kIdescPV, (j > 0 || k > 0) ? 1u : 0u);
+              mma_commit(&bars[kPvDone + b * 2 + h]);
+              if (h == 1) {
+                mma_commit(&bars[kVEmpty + st]);
+                if (j + 1 == un.n) mma_commit(&bars[kOFull]);
+              }
+            }
+            __syncwarp();
           }
           if (!ok) break;
-          mma_commit(&bars[kVEmpty + st]);
         }
         if (!ok) break;
-        mma_commit(&bars[kOFull]);
         ++ku;
       }
-      if (!ok && !*abort_flag) report_error(p.err, kErrTimeoutMma);
-      if (!ok) *abort_flag = 1;
-      mma_commit(&bars[kDrainPV]);
-      if (!mbar_wait(&bars[kDrainPV], 0)) report_error(p.err, kErrTimeoutDrain);
+      if (elect_one()) {
+        if (!ok && !*abort_flag) report_error(p.err, kErrTimeoutMma);
+        if (!ok) *abort_flag = 1;
+        mma_commit(&bars[kDrainPV]);
+        if (!mbar_wait(&bars[kDrainPV], 0)) report_error(p.err, kErrTimeoutDrain);
+      }
+      __syncwarp();
     } else if (warp == 0) {
-      // ---------------- TMA producer of the K tiles and of each unit's Q rows
+      // ---------------- TMA producer of the K tiles and of each unit's Q rows (lane 0)
+      if (lane == 0) {
       uint32_t t = 0;
       uint32_t nq = 0, nm = 0;
       bool ok = true;
@@ -316,6 +323,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!mbar_wait(&bars[kKFull + i % kKStages], (i / kKStages) & 1u)) report_error(p.err, kErrTimeoutDrain);
       for (uint32_t i = nq > kQBufs ? nq - kQBufs : 0; i < nq; ++i)
         if (!mbar_wait(&bars[kQFull + i % kQBufs], (i / kQBufs) & 1u)) report_error(p.err, kErrTimeoutDrain);
+      }
+      __syncwarp();
     } else {
       // ---------------- Q K^T issuer
       const uint64_t qdesc0 = sw128_kmajor_desc(smem_u32(sQ));
@@ -327,35 +336,41 @@ __global__ void __launch_bounds__(kThreads, 1)
         const Unit un = unit_of(p, u);
         if (un.n == 0) continue;
         const uint32_t qb = ku % kQBufs;
-        ok = !*abort_flag && mbar_wait(&bars[kQFull + qb], (ku / kQBufs) & 1u);
+        ok = __all_sync(0xffffffffu, !*abort_flag && mbar_wait(&bars[kQFull + qb], (ku / kQBufs) & 1u));
         if (!ok) break;
         tc_fence_after();
         const uint64_t qdesc = qdesc0 + ((qb * kTile) >> 4);
         for (int j = 0; j < un.n; ++j, ++t) {
           const uint32_t st = t % kKStages;
-          ok = (t < 1 || mbar_wait(&bars[kSFree], (t - 1) & 1u)) &&
-               mbar_wait(&bars[kKFull + st], (t / kKStages) & 1u);
+          ok = __all_sync(0xffffffffu, (t < 1 || mbar_wait(&bars[kSFree], (t - 1) & 1u)) &&
+                                           mbar_wait(&bars[kKFull + st], (t / kKStages) & 1u));
           if (!ok) break;
           tc_fence_after();
           const uint64_t kd = kdesc0 + ((st * kTile) >> 4);
+          if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < kHeadDim / 16; ++k) {
-            const uint32_t off = static_cast<uint32_t>(((k >> 2) * kBox + (k & 3) * 32) >> 4);
-            mma_ss(tmem + kColS, qdesc + off, kd + off, kIdescQK, k > 0 ? 1u : 0u);
+            for (int k = 0; k < kHeadDim / 16; ++k) {
+              const uint32_t off = static_cast<uint32_t>(((k >> 2) * kBox + (k & 3) * 32) >> 4);
+              mma_ss(tmem + kColS, qdesc + off, kd + off, kIdescQK, k > 0 ? 1u : 0u);
+            }
+            mma_commit(&bars[kSFull]);
+            mma_commit(&bars[kKEmpty + st]);
+            if (j + 1 == un.n) mma_commit(&bars[kQEmpty + qb]);
           }
-          mma_commit(&bars[kSFull]);
-          mma_commit(&bars[kKEmpty + st]);
+          __syncwarp();
         }
         if (!ok) break;
-        mma_commit(&bars[kQEmpty + qb]);
         ++ku;
       }
-      if (!ok) {
-        report_error(p.err, kErrTimeoutMma);
-        *abort_flag = 1;
+      if (elect_one()) {
+        if (!ok) {
+          report_error(p.err, kErrTimeoutMma);
+          *abort_flag = 1;
+        }
+        mma_commit(&bars[kDrainQK]);
+        if (!mbar_wait(&bars[kDrainQK], 0)) report_error(p.err, kErrTimeoutDrain);
       }
-      mma_commit(&bars[kDrainQK]);
-      if (!mbar_wait(&bars[kDrainQK], 0)) report_error(p.err, kErrTimeoutDrain);
+      __syncwarp();
     }
   } else if (warp < 12) {
     regs_acquire<kRegsHigh>();

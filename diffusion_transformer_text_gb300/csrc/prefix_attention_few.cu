@@ -128,13 +128,6 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, u
       : "memory");
 }
 
-// One lane of a converged warp, always the same
-__device__ __forceinline__ bool elect_one() {
-  uint32_t one;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(one));
-  return one != 0;
-}
-
 // 2^e as a half, for the exponents with which code * 2^e can be formed in half precision (codes
 // have 4 significant bits: the product is exact or, below 2^-14, rounded once); kNoHalf else.
 constexpr uint32_t kNoHalf = 0xFFFFu;
