@@ -398,7 +398,7 @@ def _elsewhere(t, stream, others=()):
 
 
 def _check_prefix_attention(key, q, k, v, prefix_k, prefix_v, prefix8, own_len, out, status):
-    """(the fixed part of qi_prefix_attn, workspace bytes, output shape) of arguments in this layout."""
+    """(the fixed part of qi_prefix_attn, workspace bytes) of arguments in this layout."""
     import torch
     if q.dim() != 4 or q.shape[3] != HEAD_DIM:
         raise ValueError(f"q: want [B, T, Hq, {HEAD_DIM}], got {tuple(q.shape)}")
@@ -433,7 +433,7 @@ def _check_prefix_attention(key, q, k, v, prefix_k, prefix_v, prefix8, own_len, 
     p8 = int(prefix8 is not None and P > 0)
     need = lib().qi_prefix_attention_workspace(
         _ATTN_HEAD.pack(*[0] * 6, p8, *[0] * 6, 0, 1.0) + _ATTN_TAIL.pack(0, *tail))
-    return _remember(_attn_layouts, key, (_ATTN_TAIL.pack(need, *tail), need, shape))
+    return _remember(_attn_layouts, key, (_ATTN_TAIL.pack(need, *tail), need))
 
 
 def prefix_attention(q, k, v, prefix_k=None, prefix_v=None, prefix8: KV8Cache | None = None, own_len=None,
@@ -459,10 +459,10 @@ def prefix_attention(q, k, v, prefix_k=None, prefix_v=None, prefix8: KV8Cache | 
     plan = _attn_layouts.get(key)
     if plan is None:
         plan = _check_prefix_attention(key, q, k, v, prefix_k, prefix_v, prefix8, own_len, out, status)
-    tail, need, shape = plan
+    tail, need = plan
     if out is None:
-        out = q.new_empty(shape)
-    ws = q.new_empty(need, dtype=torch.uint8) if need else None
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
     p8 = (0, 0, 0, 0) if prefix8 is None else [t.data_ptr() for t in prefix8]
     st = _lib.qi_prefix_attention(_ATTN_HEAD.pack(
         q.data_ptr(), _addr(k), _addr(v), out.data_ptr(), _addr(prefix_k), _addr(prefix_v), *p8, _addr(own_len),
@@ -588,11 +588,11 @@ def add_rmsnorm_mxfp8(x, delta=None, w=None, plus_one: bool = False, eps: float 
         plan = _check_norm(key, x, delta, w, x_out, q, sf)
     tail, chunks = plan
     if x_out is None:
-        x_out = x.new_empty(x.shape)
+        x_out = torch.empty_like(x, memory_format=torch.contiguous_format)
     if q is None:
-        q = x.new_empty(x.shape, dtype=torch.uint8)
+        q = torch.empty(x.shape, dtype=torch.uint8, device=x.device)
     if sf is None:
-        sf = x.new_zeros(chunks, dtype=torch.uint8)
+        sf = torch.zeros(chunks, dtype=torch.uint8, device=x.device)
     st = _lib.qi_add_rmsnorm_mxfp8(
         _NORM_HEAD.pack(x.data_ptr(), _addr(delta), x_out.data_ptr(), _addr(w), q.data_ptr(), sf.data_ptr(),
                         1 if plus_one else 0, eps) + tail, torch._C._cuda_getCurrentRawStream(dev))
