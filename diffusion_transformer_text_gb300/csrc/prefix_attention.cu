@@ -37,12 +37,13 @@
 // P is rounded to the operands' 16-bit type, as the tensor cores need it: an error
 // of half a step of that type per term, as large as the rounding of the output.
 //
-// Measured: 4 x 4096 rows over 407 shared and 4096 own keys each, 32 heads: 938 us,
-// 1290 TFLOP/s, 67 % of the library product's rate. A tile takes about 1800 cycles, the two
-// products 1024 of them: S, softmax, P and P V follow one another for each half, and only the
-// other half's work overlaps them. Between two units 2500 cycles go to the epilogue's reads of
-// tensor memory, which is what small cases show. 32 single tokens over 8192 shared rows: 28.0
-// us with the merge, of which a unit's chain of tiles and the second launch are all.
+// Measured: 4 x 4096 rows over 407 shared and 4096 own keys each, 32 heads: 940 us,
+// 1290 TFLOP/s, 67 % of the library product's rate, the clock at its power limit. A tile takes
+// 1600 to 1800 cycles, the two products 1024 of them: S, softmax, P and P V follow one another
+// for each half, and only the other half's work overlaps them. Between two units 2500 cycles go
+// to the epilogue's reads of tensor memory, which is what small cases show: 3 x 777 causal rows
+// over 2048 + 1201 keys, 4 key heads, 86.5 us, 61 %. 32 single tokens over 8192 shared rows, 8
+// key heads: 27.3 us with the merge, a unit's chain of tiles and the second launch, 44 % of HBM.
 #include <climits>
 #include <cstdarg>
 #include <cstdio>
@@ -224,7 +225,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 3) {
       // ---------------- P V issuer: nothing between its waits but what it must decide; a
       // flag read for every tile here cost 4 % of a 1024^2 image's time. The issuing warps walk
-      // as a whole, so that the descriptors are uniform; one lane issues.
+      // as a whole, so that the descriptors are uniform, and one lane issues: by a lane alone the
+      // causal case above took 91.2 us.
       const uint64_t vdesc0 = sw128_mnmajor_desc(smem_u32(sV), kBox, 1024);
       uint32_t t = 0;
       uint32_t ku = 0, cleared = 0;
@@ -762,16 +764,18 @@ int ceil_div(int a, int b) { return (a + b - 1) / b; }
 // kernel reads an 8-bit prefix as it is; the other first has it turned into 16 bits
 // (kConvert a 2^20 values: written and read again). Measured, 128-row against few-row
 // kernel, us (16 sequences, 32 key heads, 8192 prefix + 256 own keys, one token each):
-//   that, 16-bit prefix   44.6 / 38.8      8-bit prefix   76 / 41
-//   32 sequences, groups of 4, 8192 + 512, 16-bit   29.6 / 33.3      8-bit   36 / 73.6
-//   7 sequences of 5 tokens, 16 bits   12.8 / 11.6      8 sequences of 16 rows, 8 bits   27.0 / 49.9
-//   one sequence over 8192 prefix rows, 32 heads   28.7 / 26.0
-//   64 sequences, 2048 own keys   88.4 / 85.2      2 sequences, 8 heads, 300 + 40   8.8 / 6.7
+//   that, 16-bit prefix   43.7 / 38.1      8-bit prefix   75 / 40.6
+//   32 sequences, groups of 4, 8192 + 512, 16-bit   29.3 / 31.7      8-bit   34.6 / 61.7
+//   7 sequences of 5 tokens, 16 bits   12.6 / 11.0      8 sequences of 16 rows, 8 bits   26.1 / 44.1
+//   one sequence over 8192 prefix rows, 32 heads   28.0 / 26.2
+//   64 sequences, 2048 own keys   87.6 / 86.7      2 sequences, 8 heads, 300 + 40   7.4 / 6.4
+// and a cluster's join against partials and a merge (few-row kernel): the 7 sequences 11.0 / 11.9,
+// 4 sequences of 4 tokens, groups of 4, 1000 + 1000 keys 10.1 / 9.8, the last 6.4 / 7.0.
 //
 // Order of the joint units: head-major, so that the CTAs running at one time share a few
 // heads' K/V in L2; with `causal`, whose units differ in length, last row blocks first
 // over all heads and sequences, so that the CTAs' sums of lengths agree (3 x 777 rows over
-// 2048 + 1201 keys, 4 key heads: 90.4 us, head-major 97.0), as long as all K/V stay in half of the L2.
+// 2048 + 1201 keys, 4 key heads: 90.4 us, head-major 97.0, when chosen), as long as all K/V stay in half of the L2.
 struct Rate {
   float tile, tile8, unit;  // a 16-bit tile, a tile of codes, a unit
 };

@@ -26,10 +26,13 @@
 // early: a wait that expires only makes them skip the work.
 //
 // Measured, 16 sequences of one token over 8192 prefix + 256 own keys, 32 key heads: 16 bits
-// 38.8 us with the merge (the packed 128-row kernel 44.6), 4.7 TB/s; 8-bit prefix 42.6 us,
-// 2.8 TB/s (76 us with the prefix turned into 16 bits in memory first). The chain
-// of one tile (load, convert, S^T, softmax, O^T) bounds it, two tiles in flight: the issue
-// slots are 39 % used, DRAM 40 %, the tensor pipe 4 %.
+// 38.1 us with the merge (the packed 128-row kernel 43.7), 4.8 TB/s; 8-bit prefix 40.6 us,
+// 2.9 TB/s (75 us with the prefix turned into 16 bits in memory first). One sequence over
+// 131072 prefix rows: 16 bits 304 us, the copy rate; 8 bits 287 us, 57 % of it. There a tile of
+// codes takes 2300 cycles where HBM would give it in 1400: converting it keeps four warps
+// apiece for K and V busy for about 1800, 500 of them with the conversions themselves, the
+// rest with waits for their stages and with shared memory, which carries the codes in and out
+// and the 16-bit tiles in and out.
 #include "prefix_attention.cuh"
 
 namespace qi {
@@ -308,7 +311,9 @@ __global__ void __launch_bounds__(Cfg<Q8>::kThreads, 1)
       }
     }
   } else if (warp == 1) {
-    // ---------------- S^T issuer. The warp walks as a whole, so that the descriptors are uniform.
+    // ---------------- S^T issuer. The issuing warps walk as a whole, so that the descriptors are
+    // uniform: by a lane alone a product was issued 900 cycles after its operands were there (the
+    // other warps' instructions came first), now 400; 7 sequences of 5 tokens 11.5 us, now 10.9.
     {
       const uint64_t kdesc0 = sw128_kmajor_desc(smem_u32(sT));
       const uint64_t qdesc0 = sw128_kmajor_desc(smem_u32(sQ));
@@ -531,7 +536,9 @@ __global__ void __launch_bounds__(Cfg<Q8>::kThreads, 1)
     // ---------------- codes to 16 bits: warps 12..15 K, 16..19 V. A lane turns one row (key): its
     // four scale bytes stay with it, and eight lanes' pieces of one column lie in eight different
     // 16-byte places of a 128-byte line, of the codes (swizzled as the 16-bit tiles are) and of the
-    // tile alike, so neither access meets itself in the banks.
+    // tile alike, so neither access meets itself in the banks. (Sixteen lanes a row, the scales by
+    // way of shared memory: 3 to 6 % slower. K by way of tensor memory: 8 % slower. Half of the
+    // codes by integer instructions instead of the converter: 17 % slower.)
     const int kv = warp >= 16 ? 1 : 0;
     const int row = (warp & 3) * 32 + lane;
     const uint32_t turn = static_cast<uint32_t>(row & 7) << 4;
