@@ -622,17 +622,30 @@ __global__ void __launch_bounds__(kThreads, 1)
             f2_unpack(fma_f32x2(f2_pack(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), w00,
                                 mul_f32x2(f2_pack(__uint_as_float(y[2 * i]), __uint_as_float(y[2 * i + 1])), w11)),
                       ov[2 * i], ov[2 * i + 1]);
-          if (JOIN || p.pl.split) {
-            float4* d = JOIN ? reinterpret_cast<float4*>(smem + (rit * kJoinPitch + c * 16) * 4)
-                             : reinterpret_cast<float4*>(p.part + (un.slot + rit) * kHeadDim + c * 16);
+          if (JOIN) {
+            float4* d = reinterpret_cast<float4*>(smem + (rit * kJoinPitch + c * 16) * 4);
 #pragma unroll
             for (int i = 0; i < 4; ++i) d[i] = make_float4(ov[4 * i], ov[4 * i + 1], ov[4 * i + 2], ov[4 * i + 3]);
-          } else {
-            uint4* d = reinterpret_cast<uint4*>(orow + c * 16);
+          } else if (p.pl.split) {
+            float* d = p.part + (un.slot + rit) * kHeadDim + c * 16;
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-              d[i] = make_uint4(pack16<BF16>(ov[8 * i], ov[8 * i + 1]), pack16<BF16>(ov[8 * i + 2], ov[8 * i + 3]),
-                                pack16<BF16>(ov[8 * i + 4], ov[8 * i + 5]), pack16<BF16>(ov[8 * i + 6], ov[8 * i + 7]));
+            for (int i = 0; i < 2; ++i) {
+              uint32_t r[8];
+#pragma unroll
+              for (int k = 0; k < 8; ++k) r[k] = __float_as_uint(ov[8 * i + k]);
+              store32(d + 8 * i, r);
+            }
+          } else {
+            uint32_t r[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) r[k] = pack16<BF16>(ov[2 * k], ov[2 * k + 1]);
+            if (p.o32) {
+              store32(orow + c * 16, r);
+            } else {
+              uint4* d = reinterpret_cast<uint4*>(orow + c * 16);
+              d[0] = make_uint4(r[0], r[1], r[2], r[3]);
+              d[1] = make_uint4(r[4], r[5], r[6], r[7]);
+            }
           }
         }
       }
@@ -1161,6 +1174,7 @@ extern "C" qi_status qi_prefix_attention(const qi_prefix_attn* a, qi_stream_t st
   p.ob = o.batch;
   p.orow = o.row;
   p.oh = o.head;
+  p.o32 = ((reinterpret_cast<uintptr_t>(o.data) & 31) | ((o.batch | o.row | o.head) & 15)) == 0;
   p.part = reinterpret_cast<float*>(ws + w.part);
   p.ml = reinterpret_cast<float2*>(ws + w.ml);
   p.err = a->status;

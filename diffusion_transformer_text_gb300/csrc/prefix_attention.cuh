@@ -43,6 +43,7 @@ struct Params {
   const int* own_len;
   uint16_t* o;
   long long ob, orow, oh;  // element strides of o
+  int o32;                 // o and its strides allow 32-byte stores
   float* part;             // partial O rows, 128 floats each
   float2* ml;              // (maximum in base-2 units, sum) of each partial row
   int* err;
@@ -149,6 +150,13 @@ __device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
   uint64_t d;
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
+}
+
+// 32 bytes, 32-byte aligned
+__device__ __forceinline__ void store32(void* dst, const uint32_t (&r)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+               "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
 }
 
 template <bool BF16>
