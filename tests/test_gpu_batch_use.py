@@ -364,3 +364,46 @@ def test_attention_masked_places_hold_anything(qi):
             for s, n in enumerate(a["own_len"].tolist()):
                 b["k"][s, n:], b["v"][s, n:] = fill, -fill
             assert torch.equal(qi.prefix_attention(**b), want), (c, fill)
+
+
+@pytest.mark.parametrize("c", KINDS, ids=IDS)
+def test_attention_of_tensors_at_any_16_bytes(qi, c):
+    """Every tensor 16 bytes off a 32-byte boundary, outputs with rows and heads at odd multiples of 16 bytes."""
+    import torch
+
+    def off(t, pad=0):
+        wide = torch.zeros(*t.shape[:-1], t.shape[-1] + pad, dtype=t.dtype, device=t.device)
+        base = torch.zeros(wide.numel() + 8, dtype=t.dtype, device=t.device)[8:].view(wide.shape)[..., :t.shape[-1]]
+        base.copy_(t)
+        return base
+
+    a = _case(qi, c, 77)
+    want = qi.prefix_attention(**a)
+    b = {n: off(x, 8) if torch.is_tensor(x) and x.dim() > 1 else x for n, x in a.items()}
+    for pad in (0, 8, 24):
+        out = off(torch.zeros_like(want), pad)
+        assert out.data_ptr() % 32 == 16
+        assert torch.equal(qi.prefix_attention(out=out, **b), want)
+        assert torch.equal(out, want)
+
+
+def test_kv8_and_norm_of_tensors_at_any_16_bytes(qi):
+    import torch
+    k, v = _normal(1, 2, 9, 3, 128), _normal(2, 2, 9, 3, 128)
+    want = qi.kv8_write(qi.kv8_cache(2, 9, 3), k, v)
+    buf = torch.zeros(8 + 2 * 9 * 3 * 136, dtype=k.dtype, device="cuda")
+    far = buf[8:].view(2, 9, 3, 136)[..., :128]
+    far.copy_(k)
+    got = qi.kv8_write(qi.kv8_cache(2, 9, 3), far, v)
+    assert all(torch.equal(x, y) for x, y in zip(got, want))
+    far.zero_()
+    rk, _ = qi.kv8_read(want, 9, torch.float16, out=(far, torch.empty_like(v)))
+    assert torch.equal(rk, qi.kv8_read(want, 9, torch.float16)[0]) and buf[:8].count_nonzero() == 0
+    assert buf[8:].view(2, 9, 3, 136)[..., 128:].count_nonzero() == 0
+    for dt in ("fp32", "bf16"):
+        x, d = _normal(3, 5, 256, dtype=dt), _normal(4, 5, 256, dtype="fp32")
+        n = 16 // x.element_size()
+        fx = torch.zeros(n + 5 * (256 + n), dtype=x.dtype, device="cuda")[n:].view(5, 256 + n)[:, :256]
+        fx.copy_(x)
+        want = qi.add_rmsnorm_mxfp8(x, d)
+        assert all(torch.equal(g, w) for g, w in zip(qi.add_rmsnorm_mxfp8(fx, d, x_out=fx), want))
