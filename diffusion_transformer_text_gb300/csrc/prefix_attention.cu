@@ -65,7 +65,7 @@ constexpr uint32_t kColO = 0;                 // O_h at kColO + 128 h
 constexpr uint32_t kColS = 256;
 constexpr uint32_t kColP = 384;               // buffer b at kColP + 64 b, half h at + 32 h
 constexpr int kThreads = 512;
-constexpr uint32_t kRegsLow = 104, kRegsHigh = 152, kRegsEpi = 104;
+constexpr uint32_t kRegsLow = 96, kRegsHigh = 160, kRegsEpi = 96;
 static_assert(kRegsLow + 2 * kRegsHigh + kRegsEpi == 4 * 128, "register split must equal the launch allotment");
 // setmaxnreg.dec may only lower and setmaxnreg.inc only raise the launch's 128
 static_assert(kRegsLow <= 128 && kRegsHigh >= 128 && kRegsEpi <= 128 && kRegsLow % 8 == 0 && kRegsHigh % 8 == 0 &&
