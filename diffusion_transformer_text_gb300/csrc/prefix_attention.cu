@@ -37,12 +37,14 @@
 // P is rounded to the operands' 16-bit type, as the tensor cores need it: an error
 // of half a step of that type per term, as large as the rounding of the output.
 //
-// Measured: 4 x 4096 rows over 407 shared and 4096 own keys each, 32 heads: 940 us,
-// 1290 TFLOP/s, 67 % of the library product's rate, the clock at its power limit. A tile takes
-// 1600 to 1800 cycles, the two products 1024 of them: S, softmax, P and P V follow one another
-// for each half, and only the other half's work overlaps them. Between two units 2500 cycles go
-// to the epilogue's reads of tensor memory, which is what small cases show: 3 x 777 causal rows
-// over 2048 + 1201 keys, 4 key heads, 85.6 us, 62 %. 32 single tokens over 8192 shared rows, 8
+// Measured: 4 x 4096 rows over 407 shared and 4096 own keys each, 32 heads: 900 to 930 us,
+// 1300 to 1340 TFLOP/s, 68 % of the library product's rate, the clock at its power limit. A
+// tile takes 1770 cycles from one S to the next: Q K^T is issued about 500 after S has been
+// read, runs for 512 and more beside the other product, and is seen 150 later; the softmax
+// (65 to load S, 310 for the maximum, 660 for the exponentials, 300 to wait for P's place and
+// to store it) fills 1350 of them. Between two units 2500 cycles go to the epilogue's reads of
+// tensor memory, which is what small cases show: 3 x 777 causal rows over 2048 + 1201 keys, 4
+// key heads, 84.7 us, 62 %. 32 single tokens over 8192 shared rows, 8
 // key heads: 26.6 us with the merge, a unit's chain of tiles and the second launch, 46 % of HBM.
 #include <climits>
 #include <cstdarg>
@@ -65,6 +67,7 @@ constexpr uint32_t kColO = 0;                 // O_h at kColO + 128 h
 constexpr uint32_t kColS = 256;
 constexpr uint32_t kColP = 384;               // buffer b at kColP + 64 b, half h at + 32 h
 constexpr int kThreads = 512;
+// (152 for the softmax warps, with which they spill: 1 to 2.5 % slower; 168: 1 to 3 %)
 constexpr uint32_t kRegsLow = 96, kRegsHigh = 160, kRegsEpi = 96;
 static_assert(kRegsLow + 2 * kRegsHigh + kRegsEpi == 4 * 128, "register split must equal the launch allotment");
 // setmaxnreg.dec may only lower and setmaxnreg.inc only raise the launch's 128
