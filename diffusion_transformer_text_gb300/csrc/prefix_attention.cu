@@ -776,10 +776,12 @@ int ceil_div(int a, int b) { return (a + b - 1) / b; }
 // Chooses the decomposition from sizes alone (own lengths, which only the device knows, count
 // as S): the one whose busiest CTA has the least to do. Time is counted in units of a key
 // tile of the 128-row kernel, about 0.9 us: a unit costs its tiles plus a fill and an
-// epilogue, splitting costs kMergeTiles for the partials and the second launch. The few-row
-// kernel reads an 8-bit prefix as it is; the other first has it turned into 16 bits
-// (kConvert a 2^20 values: written and read again). Measured, 128-row against few-row
-// kernel, us (16 sequences, 32 key heads, 8192 prefix + 256 own keys, one token each):
+// epilogue that grows with its rows, splitting costs kMergeTiles for the partials and the
+// second launch, a cluster's join by its rows. The few-row kernel reads an 8-bit prefix as it
+// is; the other first has it turned into 16 bits (a launch, and kConvert a 2^20 values:
+// written and read again). Over 90 random calls the choice was within 3 % (geometric mean;
+// 55 % at worst, where a few-row tile comes from L2 in half the time) of the best of joint,
+// packed and joined units of both kernels. Measured, 128-row against few-row kernel, us (16 sequences, 32 key heads, 8192 prefix + 256 own keys, one token each):
 //   that, 16-bit prefix   43.7 / 38.1      8-bit prefix   75 / 40.6
 //   32 sequences, groups of 4, 8192 + 512, 16-bit   29.3 / 31.7      8-bit   34.6 / 61.7
 //   7 sequences of 5 tokens, 16 bits   12.6 / 11.0      8 sequences of 16 rows, 8 bits   26.1 / 44.1
@@ -793,13 +795,14 @@ int ceil_div(int a, int b) { return (a + b - 1) / b; }
 // over all heads and sequences, so that the CTAs' sums of lengths agree (3 x 777 rows over
 // 2048 + 1201 keys, 4 key heads: 90.4 us, head-major 97.0, when chosen), as long as all K/V stay in half of the L2.
 struct Rate {
-  float tile, tile8, unit;  // a 16-bit tile, a tile of codes, a unit
+  float tile, tile8, unit, row;  // a 16-bit tile, a tile of codes, a unit, each of its rows
+  float of(int rows) const { return unit + row * static_cast<float>(rows); }
 };
-constexpr Rate kFullRate{1.f, 1.f, 2.5f}, kFewRate{0.95f, 1.5f, 2.f};
+constexpr Rate kFullRate{1.f, 1.f, 1.5f, 1.f / 128}, kFewRate{0.95f, 1.5f, 0.6f, 0.09f};
 constexpr float kMergeTiles = 4.f, kPartRows = 5300.f;  // and a unit per so many partial rows written and read
-constexpr float kConvert = 0.5f;
+constexpr float kConvert = 0.5f, kConvertStart = 2.5f;
 constexpr float kStart = 3.f;      // of a kernel whose CTAs walk the units
-constexpr float kJoinTiles = 3.f;  // of a CTA in a cluster, and its join
+constexpr float kJoinTiles = 2.6f, kJoinRow = 1.f / 32;  // start of a CTA in a cluster and its join; each row
 constexpr long long kL2Half = 64ll << 20;
 struct Sizes {
   int B, T, Hq, Hkv, P, S, causal;
@@ -827,7 +830,7 @@ Plan make_plan(const Sizes& z, int sms) {
       c.rows_p = c.rb * c.rows_o;
     }
   };
-  const float convert = z.from8 && z.P > 0 ? kConvert * static_cast<float>(z.P) * z.Hkv * kHeadDim / (1 << 20) : 0.f;
+  const float convert = z.from8 && z.P > 0 ? kConvertStart + kConvert * static_cast<float>(z.P) * z.Hkv * kHeadDim / (1 << 20) : 0.f;
   // joint units, every number of chunks that keeps the grid within a few waves
   const auto joint = [&](Plan c, Rate r, bool always_split, float more) {
     const int n = c.pt + c.ot;
@@ -841,7 +844,7 @@ Plan make_plan(const Sizes& z, int sms) {
       c.split = always_split || nch > 1;
       const float waves = static_cast<float>((blocks * nch + sms - 1) / sms);
       const float parts = c.split ? kMergeTiles + static_cast<float>(blocks * nch) * c.rows_o * c.per / kPartRows : 0.f;
-      const float cost = kStart + waves * (c.ct * each + r.unit) + parts + more;
+      const float cost = kStart + waves * (c.ct * each + r.of(c.rows_o)) + parts + more;
       if (cost < best_cost && blocks * nch <= INT_MAX / 2) {
         best_cost = cost;
         c.units = static_cast<int>(blocks * nch);
@@ -850,7 +853,7 @@ Plan make_plan(const Sizes& z, int sms) {
     }
   };
   // joint units whose chunks join in a cluster: one unit per CTA; clusters of more than two leave
-  // some SMs of a processing cluster over
+  // some SMs of a processing cluster over (of 152: 138 to 144 CTAs in clusters of 3 to 6, 105 of 7)
   const auto joined = [&](Plan c, Rate r, int least, float more) {
     const int n = c.pt + c.ot;
     const long long blocks = static_cast<long long>(z.Hkv) * z.B * c.nqb;
@@ -860,9 +863,9 @@ Plan make_plan(const Sizes& z, int sms) {
       if (ceil_div(n, c.ct) != nch || blocks * nch > INT_MAX / 2) continue;
       c.nch = nch;
       c.join = 1;
-      const int slots = nch <= 2 ? sms : sms * 5 / 6;
+      const int slots = nch <= 2 ? sms : nch <= 6 ? sms * 9 / 10 : sms * 2 / 3;
       const float waves = static_cast<float>((blocks * nch + slots - 1) / slots);
-      const float cost = waves * (c.ct * each + r.unit + kJoinTiles) + more;
+      const float cost = waves * (c.ct * each + r.of(c.rows_o) + kJoinTiles + kJoinRow * static_cast<float>(c.rows_o)) + more;
       if (cost < best_cost) {
         best_cost = cost;
         c.units = static_cast<int>(blocks * nch);
@@ -881,8 +884,8 @@ Plan make_plan(const Sizes& z, int sms) {
       c.nch = c.ot ? ceil_div(c.ot, ct) : 1;
       const long long up = static_cast<long long>(z.Hkv) * c.npb * c.nchp, uo = c.ot ? blocks * c.nch : 0;
       if (up + uo > INT_MAX / 2) continue;
-      const float unit_p = r.unit + (z.from8 ? r.tile8 : r.tile) * c.pt / c.nchp;
-      const float unit_o = r.unit + r.tile * c.ot / c.nch;
+      const float unit_p = r.of(c.rows_p) + (z.from8 ? r.tile8 : r.tile) * c.pt / c.nchp;
+      const float unit_o = r.of(c.rows_o) + r.tile * c.ot / c.nch;
       float load = 0.f;
       for (long long i : {0ll, up % sms, (up + uo) % sms - 1, static_cast<long long>(sms) - 1}) {
         if (i < 0) continue;
