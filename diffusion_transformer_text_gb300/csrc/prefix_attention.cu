@@ -781,8 +781,8 @@ int ceil_div(int a, int b) { return (a + b - 1) / b; }
 // is; the other first has it turned into 16 bits (a launch, and kConvert a 2^20 values:
 // written and read again). Over 90 random calls the choice was within 3 % (geometric mean;
 // 55 % at worst, where a few-row tile comes from L2 in half the time) of the best of joint,
-// packed and joined units of both kernels. Measured, 128-row against few-row kernel, us (16 sequences, 32 key heads, 8192 prefix + 256 own keys, one token each):
-//   that, 16-bit prefix   43.7 / 38.1      8-bit prefix   75 / 40.6
+// packed and joined units of both kernels. Measured, 128-row against few-row kernel, us:
+//   16 sequences, 32 key heads, 8192 + 256, 16-bit prefix   43.7 / 38.1      8-bit   75 / 40.6
 //   32 sequences, groups of 4, 8192 + 512, 16-bit   29.3 / 31.7      8-bit   34.6 / 61.7
 //   7 sequences of 5 tokens, 16 bits   12.6 / 11.0      8 sequences of 16 rows, 8 bits   26.1 / 44.1
 //   one sequence over 8192 prefix rows, 32 heads   28.0 / 26.2
@@ -793,13 +793,14 @@ int ceil_div(int a, int b) { return (a + b - 1) / b; }
 // Order of the joint units: head-major, so that the CTAs running at one time share a few
 // heads' K/V in L2; with `causal`, whose units differ in length, last row blocks first
 // over all heads and sequences, so that the CTAs' sums of lengths agree (3 x 777 rows over
-// 2048 + 1201 keys, 4 key heads: 90.4 us, head-major 97.0, when chosen), as long as all K/V stay in half of the L2.
+// 2048 + 1201 keys, 4 key heads: 90.4 us, head-major 97.0, when chosen), as long as all K/V
+// stay in half of the L2.
 struct Rate {
   float tile, tile8, unit, row;  // a 16-bit tile, a tile of codes, a unit, each of its rows
   float of(int rows) const { return unit + row * static_cast<float>(rows); }
 };
-constexpr Rate kFullRate{1.f, 1.f, 1.5f, 1.f / 128}, kFewRate{0.95f, 1.5f, 0.6f, 0.09f};
-constexpr float kMergeTiles = 4.f, kPartRows = 5300.f;  // and a unit per so many partial rows written and read
+constexpr Rate kFullRate{1.f, 1.f, 1.5f, 1.f / 128}, kFewRate{0.7f, 1.5f, 0.6f, 0.09f};
+constexpr float kMergeTiles = 3.f, kPartRows = 5300.f;  // and a unit per so many partial rows written and read
 constexpr float kConvert = 0.5f, kConvertStart = 2.5f;
 constexpr float kStart = 3.f;      // of a kernel whose CTAs walk the units
 constexpr float kJoinTiles = 2.6f, kJoinRow = 1.f / 32;  // start of a CTA in a cluster and its join; each row

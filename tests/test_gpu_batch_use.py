@@ -12,8 +12,8 @@ from test_gpu_batch import _bound, _check_attention, _normal, _np, qi  # noqa: F
 
 pytestmark = pytest.mark.gpu
 
-# sizes by what the attention makes of them: few rows joined in a cluster, few rows packed with partials,
-# few rows split with partials, 128 rows packed with partials, 128 rows joint, 128 rows joined
+# sizes by what the attention makes of them: few rows joined in a cluster, packed with partials, joined from
+# many tiles; 128 rows packed with partials, joint, joined; few rows in 53 chunks with partials, 128 rows too
 KINDS = [
     dict(B=1, T=1, Hq=32, Hkv=32, P=22, S=17),
     dict(B=16, T=1, Hq=32, Hkv=32, P=2100, S=256),
@@ -21,6 +21,8 @@ KINDS = [
     dict(B=32, T=1, Hq=32, Hkv=8, P=4000, S=300),
     dict(B=2, T=300, Hq=32, Hkv=8, P=140, S=300),
     dict(B=2, T=40, Hq=8, Hkv=2, P=900, S=700),
+    dict(B=1, T=1, Hq=8, Hkv=2, P=20000, S=64),
+    dict(B=1, T=30, Hq=8, Hkv=2, P=20000, S=64),
 ]
 IDS = ["-".join(str(x) for x in c.values()) for c in KINDS]
 
@@ -184,6 +186,8 @@ def test_freed_while_another_stream_still_reads(qi):
     dict(B=3, T=17, Hq=1, Hkv=1, P=1, S=5000, lens=[17, 16, 5000], causal=True, layout="bhsd"),
     dict(B=12, T=1, Hq=8, Hkv=8, P=3000, S=600, lens=[0] * 12),
     dict(B=300, T=1, Hq=2, Hkv=2, P=129, S=3, lens=[i % 4 for i in range(300)]),
+    dict(B=1, T=1, Hq=8, Hkv=2, P=9000, S=64, lens=[63], causal=True),
+    dict(B=1, T=30, Hq=8, Hkv=2, P=9000, S=64, lens=[20], causal=True),
 ], ids=lambda c: f"B{c['B']}-T{c['T']}-P{c['P']}-S{c['S']}")
 def test_attention_few_keys_of_many(qi, c, dtype):
     _check_attention(qi, dtype=dtype, seed=c["S"] + c["B"], **c)
