@@ -447,7 +447,7 @@ def prefix_attention(q, k, v, prefix_k=None, prefix_v=None, prefix8: KV8Cache | 
     rows up to own_len - T + t. scale: default 1 / sqrt(128). status: int32 [1] on the device that
     receives a non-zero code if a wait in the kernel expires. stream: default the current one of q's
     device; another one has to come after whatever wrote the arguments. Returns o [B, T, Hq, 128]
-    (`out`, if given)."""
+    (`out`, if given, which must not overlap the arguments). No gradients."""
     import torch
     dev = q.get_device()
     if stream is not None or dev < 0 or dev != torch._C._cuda_getDevice():
@@ -592,7 +592,9 @@ def add_rmsnorm_mxfp8(x, delta=None, w=None, plus_one: bool = False, eps: float 
     if q is None:
         q = torch.empty(x.shape, dtype=torch.uint8, device=x.device)
     if sf is None:
-        sf = torch.zeros(chunks, dtype=torch.uint8, device=x.device)
+        # (the bytes of rows that fill the last 128 up are not written)
+        make = torch.zeros if x.shape[0] % 128 else torch.empty
+        sf = make(chunks, dtype=torch.uint8, device=x.device)
     st = _lib.qi_add_rmsnorm_mxfp8(
         _NORM_HEAD.pack(x.data_ptr(), _addr(delta), x_out.data_ptr(), _addr(w), q.data_ptr(), sf.data_ptr(),
                         1 if plus_one else 0, eps) + tail, torch._C._cuda_getCurrentRawStream(dev))

@@ -411,3 +411,18 @@ def test_kv8_and_norm_of_tensors_at_any_16_bytes(qi):
         fx.copy_(x)
         want = qi.add_rmsnorm_mxfp8(x, d)
         assert all(torch.equal(g, w) for g, w in zip(qi.add_rmsnorm_mxfp8(fx, d, x_out=fx), want))
+
+
+def test_add_rmsnorm_into_its_arguments_and_new_scales(qi):
+    """x_out may be x or delta; the scales that a call makes itself are complete, whole groups of 128 rows or not."""
+    import torch
+    for rows in (5, 128, 256, 300):
+        x, d = _normal(rows, rows, 384), _normal(rows + 1, rows, 384)
+        torch.full((rows * 384 // 32 + 70000,), 255, dtype=torch.uint8, device="cuda")   # dirties what comes next
+        want = qi.add_rmsnorm_mxfp8(x, d)
+        sf = torch.zeros(((rows + 127) // 128) * 3 * 512, dtype=torch.uint8, device="cuda")
+        for n in ("x", "d"):
+            a, b = x.clone(), d.clone()
+            to = a if n == "x" else b
+            got = qi.add_rmsnorm_mxfp8(a, b, x_out=to, sf=sf.zero_())
+            assert got[0] is to and all(torch.equal(g, w) for g, w in zip(got, want))
