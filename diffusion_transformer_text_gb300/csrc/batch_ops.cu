@@ -454,7 +454,8 @@ __global__ void add_rmsnorm_kernel(const __grid_constant__ NormParams p) {
         const float q = __fmul_rn(v[k], rs.hi);
         const float qe = __fmaf_rn(v[k], rs.hi, -q) + v[k] * rs.lo;
         const float z = __fmul_rn(q, h.hi);
-        y[k] = round_odd(two_sum(z, __fmaf_rn(q, h.hi, -z) + (qe * h.hi + q * h.lo)));
+        // (an infinite gain or a product past fp32's range stays an infinity: it has no error term)
+        y[k] = isfinite(z) ? round_odd(two_sum(z, __fmaf_rn(q, h.hi, -z) + (qe * h.hi + q * h.lo))) : z;
       }
       e = mx_exponent8(y, top);
       inv = pow2(-e);

@@ -589,7 +589,8 @@ qi_status qi_kv8_read(const qi_kv8* args, qi_stream_t stream);
  * is then a copy of x); row strides in elements. x_out may be x itself (or delta, of the same
  * type and stride), or NULL if the sum is not wanted. The norm is that of the stored sum, rounded to x_dtype. gain: w [K] (fp32
  * if w_f32, else bf16 bits), 1 + w if plus_one (the ZeroCenterRMSNorm form), 1 if w is NULL.
- * The sum of squares has to stay finite in fp32, as in any fp32 norm.
+ * The sum of squares has to stay finite in fp32, as in any fp32 norm. A y that overflows, or an
+ * infinite gain, gives the codes and scale of an infinity, as qi_quant_mxfp8's.
  * The statistics and the products carry an error term beside each fp32 value, so that y is
  * the fp32 rounding of its exact value but for the last bits of rsqrt's correction.
  * K a multiple of 128 up to 16384, pointers and row strides in bytes multiples of 16, w
