@@ -325,6 +325,14 @@ __device__ __forceinline__ float round_odd(F2 x) {
   return __uint_as_float(x.lo == 0.f || (b & 1u) ? b : b + step);
 }
 
+// a if x is a number, else b. As one select: from the operator ?: the compiler makes a branch for each
+// value, which 2000 rows of 12288 columns show as 84 us instead of 76.
+__device__ __forceinline__ float if_number(float x, float a, float b) {
+  float r;
+  asm("{\n\t.reg .pred p;\n\tsetp.num.f32 p, %1, %1;\n\tselp.f32 %0, %2, %3, p;\n\t}" : "=f"(r) : "f"(x), "f"(a), "f"(b));
+  return r;
+}
+
 constexpr uint32_t kNear = 16;  // fp32 steps around a border
 
 struct NormParams {
@@ -454,8 +462,10 @@ __global__ void add_rmsnorm_kernel(const __grid_constant__ NormParams p) {
         const float q = __fmul_rn(v[k], rs.hi);
         const float qe = __fmaf_rn(v[k], rs.hi, -q) + v[k] * rs.lo;
         const float z = __fmul_rn(q, h.hi);
-        // (an infinite gain or a product past fp32's range stays an infinity: it has no error term)
-        y[k] = isfinite(z) ? round_odd(two_sum(z, __fmaf_rn(q, h.hi, -z) + (qe * h.hi + q * h.lo))) : z;
+        // (an infinite gain or a product past fp32's range stays an infinity: the sum with its error term
+        // is no number)
+        const F2 t = two_sum(z, __fmaf_rn(q, h.hi, -z) + (qe * h.hi + q * h.lo));
+        y[k] = if_number(t.hi, round_odd(t), z);
       }
       e = mx_exponent8(y, top);
       inv = pow2(-e);
