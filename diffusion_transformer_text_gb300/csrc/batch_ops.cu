@@ -290,9 +290,11 @@ cudaError_t launch_kv8(void (*kernel)(Kv8Args), Kv8Args a, int parts, int per_bl
 // Where it matters (a value next to a border between two codes, see below) y keeps its error
 // term up to the quantiser and is then rounded to odd (the last bit set if anything was lost),
 // which makes the rounding to E4M3, and the block's exponent, those of the unrounded value:
-// codes differ from the exact ones only by the error of the mean square. That is summed in
-// plain fp32 within a thread (its up to 64 roundings are unbiased and there are hundreds of
-// threads) and with error terms across threads, so it is off by about 2^-27.
+// codes differ from the exact ones only by the error of the mean square. Squares are added in
+// plain fp32 by twos (two roundings of a sum of terms >= 0), those sums with error terms, so the
+// mean is off by less than 2^-23 of itself whatever the row, and y by less than 2^-24. (Chains of
+// plain fp32 over all of a thread's values, which a channel far above the others robs of their
+// squares: up to 2^-19 at 16384 columns.)
 struct F2 {
   float hi, lo;
 };
@@ -305,6 +307,15 @@ __device__ __forceinline__ F2 add(F2 a, F2 b) {
   F2 s = two_sum(a.hi, b.hi);
   s.lo += a.lo + b.lo;
   return s;
+}
+// two of them at once: (hi, lo) += x
+__device__ __forceinline__ void add_two_sum(uint64_t& hi, uint64_t& lo, uint64_t x) {
+  const uint64_t minus = f2_pack(-1.f, -1.f);
+  const uint64_t s = add_f32x2(hi, x);
+  const uint64_t xx = fma_f32x2(hi, minus, s);  // (a product with -1 is exact: these are differences)
+  const uint64_t hh = fma_f32x2(xx, minus, s);
+  lo = add_f32x2(lo, add_f32x2(fma_f32x2(hh, minus, hi), fma_f32x2(xx, minus, x)));
+  hi = s;
 }
 // 1 / sqrt(m), m = hi + lo > 0: rsqrtf and one Newton step of which only the correction is kept
 __device__ __forceinline__ F2 inv_sqrt(F2 m) {
@@ -371,7 +382,7 @@ __global__ void add_rmsnorm_kernel(const __grid_constant__ NormParams p) {
   const uint4* x = reinterpret_cast<const uint4*>(static_cast<const TX*>(a.x) + r * a.x_stride);
   const uint4* d = a.delta ? reinterpret_cast<const uint4*>(static_cast<const TD*>(a.delta) + r * a.delta_stride) : nullptr;
   TX* xo = a.x_out ? static_cast<TX*>(a.x_out) + r * a.x_out_stride : nullptr;
-  float sq[4] = {};
+  uint64_t sq = 0ull, sq_lo = 0ull;  // two sums and their error terms
   for (int c0 = threadIdx.x; c0 < groups8; c0 += kNormUnroll * threads) {
     uint4 xr[kNormUnroll][kX], dr[kNormUnroll][kD];
 #pragma unroll
@@ -405,11 +416,17 @@ __global__ void add_rmsnorm_kernel(const __grid_constant__ NormParams p) {
           if (xo) reinterpret_cast<uint4*>(xo)[c * kX + j] = xr[i][j];
         }
 #pragma unroll
-        for (int k = 0; k < 8; ++k) sq[k & 3] = __fmaf_rn(v[k], v[k], sq[k & 3]);
+        for (int h = 0; h < 2; ++h) {
+          const uint64_t lo = f2_pack(v[2 * h], v[2 * h + 1]), hi = f2_pack(v[2 * h + 4], v[2 * h + 5]);
+          add_two_sum(sq, sq_lo, fma_f32x2(hi, hi, mul_f32x2(lo, lo)));
+        }
       }
     }
   }
-  F2 sum = lanes_sum(add(two_sum(sq[0], sq[1]), two_sum(sq[2], sq[3])), 32);
+  F2 even, odd;
+  f2_unpack(sq, even.hi, odd.hi);
+  f2_unpack(sq_lo, even.lo, odd.lo);
+  F2 sum = lanes_sum(add(even, odd), 32);
   if (threads > 32) {
     if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = sum;
     __syncthreads();
@@ -442,8 +459,8 @@ __global__ void add_rmsnorm_kernel(const __grid_constant__ NormParams p) {
           load8(static_cast<const __nv_bfloat16*>(a.w) + c * 8, g);
       }
     }
-    // y in fp32: roundings of r1, of 1 + w and of the two products, at most 2 fp32 steps and
-    // 2^-27 of the statistics off, that is within kNear steps with room to spare
+    // y in fp32: roundings of r1, of 1 + w and of the two products, at most 2 fp32 steps and one
+    // of the statistics off, that is within kNear steps with room to spare
     float y[8], top;
 #pragma unroll
     for (int k = 0; k < 8; ++k) y[k] = v[k] * r1 * (g[k] + bias);

@@ -591,8 +591,9 @@ qi_status qi_kv8_read(const qi_kv8* args, qi_stream_t stream);
  * if w_f32, else bf16 bits), 1 + w if plus_one (the ZeroCenterRMSNorm form), 1 if w is NULL.
  * The sum of squares has to stay finite in fp32, as in any fp32 norm. A y that overflows, or an
  * infinite gain, gives the codes and scale of an infinity, as qi_quant_mxfp8's.
- * The statistics and the products carry an error term beside each fp32 value, so that y is
- * the fp32 rounding of its exact value but for the last bits of rsqrt's correction.
+ * The mean of the squares is within 2^-23 of itself for any row whose squares do not underflow
+ * (they are added by twos in fp32, the rest carries error terms), so the codes and scales are
+ * those of a y within 2^-24 of its exact value.
  * K a multiple of 128 up to 16384, pointers and row strides in bytes multiples of 16, w
  * 16-byte aligned; sf holds ceil(rows / 128) * (K / 128) * 512 bytes, 4-byte aligned, of which
  * those of rows past `rows` are left as they were.
