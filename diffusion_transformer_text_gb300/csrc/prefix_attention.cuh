@@ -11,6 +11,12 @@ constexpr int kKeys = 128;           // keys per tile
 constexpr int kBox = 128 * 64 * 2;   // 128 rows x 64 dims, 128-byte swizzle (16 KB)
 constexpr int kTile = 2 * kBox;      // K or V tile (32 KB)
 constexpr float kRescaleLog2 = 8.0f; // rescale O only when its maximum grows by > 2^8
+// Probabilities are 2^(s - m) with m the running maximum less kLift: fp16 ones lie between 2^7 and
+// 2^15 times their ratio to the row's largest, so that the type's range below 1 serves the small ones
+// too. Without it those below 2^-25 became zero, and thousands of such keys behind one of great
+// weight and small value (a sink) left the row without its sum. The factor cancels in O / sum.
+template <bool BF16>
+constexpr float kLift = BF16 ? 0.f : 7.f;
 
 // The decomposition, decided on the host from sizes alone.
 struct Plan {

@@ -449,8 +449,8 @@ __global__ void __launch_bounds__(Cfg<Q8>::kThreads, 1)
         for (int i = 0; i < kR; ++i) w[i] = redux_max(x[i]);
         if (lane == 0) store16f(ex.top[s][turn][quarter], w);
         warpgroup_sync(1 + s);
-        const float mx = fmaxf(fmaxf(ex.top[s][turn][0][row16], ex.top[s][turn][1][row16]),
-                               fmaxf(ex.top[s][turn][2][row16], ex.top[s][turn][3][row16])) * scale_log2;
+        const float mx = fmaf(fmaxf(fmaxf(ex.top[s][turn][0][row16], ex.top[s][turn][1][row16]),
+                                    fmaxf(ex.top[s][turn][2][row16], ex.top[s][turn][3][row16])), scale_log2, -kLift<BF16>);
         turn ^= 1u;
         const float m_new = fmaxf(m_used, mx);
         if (cnt == 0) {

@@ -517,8 +517,9 @@ typedef struct qi_strides {
  * attention to an encoder's states); with S = 0 over the prefix alone.
  *
  * dtype QI_DT_F16 or QI_DT_BF16 for q, o and every 16-bit K/V; scores, maxima, sums and O
- * are fp32, the probabilities are rounded to dtype as tensor-core operands. q and o are
- * [B, T, Hq, 128], o written with 16-byte stores and not overlapping any input.
+ * are fp32, the probabilities are rounded to dtype as tensor-core operands (in fp16 by at most
+ * half a step, or 2^-32 of the row's largest where that is more). q and o are [B, T, Hq, 128],
+ * o written with 16-byte stores and not overlapping any input.
  * The prefix is given either as pk, pv (batch stride ignored), or with pk = pv = NULL as rows
  * of an 8-bit cache (qi_kv8_write): codes pk8, pv8 [P, Hkv, 128] and scales pk_sf, pv_sf
  * [P, Hkv, 4], contiguous, codes 16-byte and scales 4-byte aligned; its values are the codes

@@ -2,8 +2,9 @@
 import numpy as np
 import pytest
 
+from oracle import batch as ob
 from oracle import mx as omx
-from test_gpu_batch import _normal, _sf, qi  # noqa: F401
+from test_gpu_batch import _normal, _np, _sf, qi  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -72,3 +73,44 @@ def test_add_rmsnorm_of_a_dominant_channel(qi, kind, K, rows):
     val = omx.dequantize(omx.E4M3_TABLE[q.cpu().numpy()], e)
     off_by = (val != omx.dequantize(lo, le)) & sure
     assert not off_by.any(), f"{off_by[0].sum()} of {K} codes off"
+
+
+@pytest.mark.parametrize("bits", [16, 8])
+@pytest.mark.parametrize("B,T,Hq,Hkv,P,S", [(1, 1, 4, 2, 9000, 20), (2, 40, 2, 1, 9000, 64), (24, 1, 8, 2, 6000, 50),
+                                            (2, 5, 3, 1, 700, 6000), (1, 200, 1, 1, 300, 7000)])
+def test_attention_behind_keys_that_take_all(qi, B, T, Hq, Hkv, P, S, bits):
+    """fp16: a few keys of every row have about 2^26 times the weight of each other one and the value zero
+    (sinks); the output is what the thousands of others leave. A probability enters the product as w 2^7 or
+    more, w its ratio to the row's largest, in fp16: one below 2^-21 is off by at most 2^-25 2^-7 = 2^-32, n keys
+    by n 2^-32 max|v| over the sum, at least 0.7 of the number of sinks (in 8 bits 14.25 becomes 14: 2^-0.45 of
+    the weight); the other terms are those of the bound in test_gpu_batch."""
+    import torch
+    q = _normal(1, B, T, Hq, 128, std=0.05)
+    k, v = _normal(2, B, S, Hkv, 128, std=0.05), _normal(3, B, S, Hkv, 128, std=0.1) + 1
+    pk, pv = _normal(4, P, Hkv, 128, std=0.05), _normal(5, P, Hkv, 128, std=0.1) + 1
+    q[..., 7] = 14.25                                    # 14.25^2 / sqrt(128) log2 e = 25.9
+    sinks = 0
+    for key, val, rows in ((pk, pv, P), (k.transpose(0, 1), v.transpose(0, 1), S)):
+        key[..., 7] = 0
+        at = [i for i in range(rows) if i % 1024 in (3, 67, 131, 195)]   # in each half of two tiles in eight
+        key[at], val[at] = 0, 0
+        key[at, ..., 7] = 14.25
+        sinks += len(at)
+    kw = dict(prefix_k=pk, prefix_v=pv)
+    if bits == 8:
+        cache = qi.kv8_write(qi.kv8_cache(1, P, Hkv), pk[None], pv[None])
+        kw = dict(prefix8=cache.prefix(0, P))
+        pk, pv = (t[0] for t in qi.kv8_read(cache, P, torch.float16))
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    o = _np(qi.prefix_attention(q, k, v, status=status, **kw))
+    assert status.item() == 0
+    args = [_np(x) for x in (q, k, v, pk, pv)]
+    scale = 1 / np.sqrt(128)
+    ref, A = ob.prefix_attention(*args, None, False, scale)
+    n, vmax = P + S, max(np.abs(args[2]).max(), np.abs(args[4]).max())
+    mag = scale * np.abs(args[0]).max() * 14.25 + scale * 128 * 0.3 * 0.3   # a score's sum of magnitudes, at most
+    tol = (2.0 ** -11 * (A + np.abs(ref)) * (1 + 2.0 ** -8) + 2 * (mag * (128 * 2.0 ** -23 + 3 * 2.0 ** -24) + 2.0 ** -22) * A
+           + (2 * n * 2.0 ** -23 + 8 * 2.0 ** -22) * A + n * 2.0 ** -32 * vmax / (0.7 * sinks) + 2.0 ** -25)
+    assert (tol < 0.1 * np.abs(ref).max()).all()         # (the tail is far above what the bound allows)
+    err = np.abs(o - ref)
+    assert (err <= tol).all(), f"max error {err.max():.3e}, {(err / tol).max():.2f} of the bound"
