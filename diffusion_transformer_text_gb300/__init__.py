@@ -45,7 +45,8 @@ SYMBOLS = (
     "qi_dit_profile_read", "qi_last_error", "qi_gemm_bf16", "qi_attention_f16", "qi_gemm_bf16_noalloc", "qi_gemv_bf16",
     "qi_dit_step_cfg", "qi_dpmpp2m_coeffs", "qi_dpmpp2m_update", "qi_dit_step_fbcache", "qi_dit_fbcache_reset",
     "qi_dit_set_mxfp8", "qi_quant_mxfp8", "qi_gemm_mxfp8", "qi_debug_inject", "qi_dit_euler_step", "qi_dit_set_range_probe",
-    "qi_prefix_attention", "qi_prefix_attention_workspace", "qi_kv8_write", "qi_kv8_read", "qi_add_rmsnorm_mxfp8",
+    "qi_prefix_attention", "qi_prefix_attention_workspace", "qi_prefix_attention_check", "qi_kv8_write", "qi_kv8_read",
+    "qi_add_rmsnorm_mxfp8",
 )
 
 
@@ -126,6 +127,7 @@ def lib() -> ctypes.CDLL:
         "qi_gemm_mxfp8": [P, P, P, P, P, P, I, I, I, P],
         "qi_dpmpp2m_update": [P, P, P, I, P, I, I, P],
         "qi_prefix_attention": [P, P],
+        "qi_prefix_attention_check": [P],
         "qi_kv8_write": [P, P],
         "qi_kv8_read": [P, P],
         "qi_add_rmsnorm_mxfp8": [P, P],
@@ -256,7 +258,7 @@ def dpmpp2m_update(x, vel, d_prev, sigmas, i: int):
 
 def debug_inject(kind: int, arg: int = 0, dit=None):
     """Test hook: 1 = fail the arg-th next device allocation; 2 = stall the next block GEMM
-    of `dit` until its bounded wait expires; 0 = cancel."""
+    of `dit` until its bounded wait expires; 3 = the same for the next prefix_attention; 0 = cancel."""
     _check(lib().qi_debug_inject(dit._h if dit is not None else None, kind, arg))
 
 
@@ -445,7 +447,8 @@ def prefix_attention(q, k, v, prefix_k=None, prefix_v=None, prefix8: KV8Cache | 
     bfloat16, the last dimension contiguous, other strides positive multiples of 8 (nothing expanded).
     own_len: int32 [B] on the device, the own rows in use (None: S). causal: query row t of T sees own
     rows up to own_len - T + t. scale: default 1 / sqrt(128). status: int32 [1] on the device that
-    receives a non-zero code if a wait in the kernel expires. stream: default the current one of q's
+    receives a non-zero code if a wait in the kernel expires (the result is then undefined); without
+    it prefix_attention_check tells. stream: default the current one of q's
     device; another one has to come after whatever wrote the arguments. Returns o [B, T, Hq, 128]
     (`out`, if given, which must not overlap the arguments). No gradients."""
     import torch
@@ -471,6 +474,15 @@ def prefix_attention(q, k, v, prefix_k=None, prefix_v=None, prefix8: KV8Cache | 
     if st:
         _check(st)
     return out
+
+
+def prefix_attention_check(stream=None):
+    """Waits for `stream` (default: the current one) and raises QiError if a wait in a kernel has expired since
+    the last check, in a prefix_attention call without `status` on the stream's device."""
+    import torch
+    s = stream if stream is not None else torch.cuda.current_stream()
+    with torch.cuda.device(s.device):
+        _check(lib().qi_prefix_attention_check(s.cuda_stream))
 
 
 def _check_kv8(key, cache, k, v, pos, lens):

@@ -194,6 +194,9 @@ bool encode_map16(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols
 bool encode_map_nd(CUtensorMap* m, const void* base, bool bytes, int rank, const unsigned long long* dims,
                    const unsigned long long* strides, const unsigned* box);
 
+// Test hook: the next qi_prefix_attention waits for what never comes (prefix_attention.cu).
+extern std::atomic<bool> g_stall_prefix_attention;
+
 // SMs of the current device, looked up once per device; 0 if there is none (prefix_attention.cu).
 int device_sms();
 

@@ -995,14 +995,15 @@ bool map_codes(CUtensorMap* m, const uint8_t* codes, int heads, int rows) {
   return encode_map_nd(m, codes, true, 3, dims, str, box);
 }
 
-bool map_q(CUtensorMap* m, const Tensor4& t, int G, int Hkv, int T, int B, int tb, int rb) {
+// `stall` (test hook): the boxes bring half of the bytes that the kernels wait for, so Q never comes
+bool map_q(CUtensorMap* m, const Tensor4& t, int G, int Hkv, int T, int B, int tb, int rb, bool stall) {
   const unsigned long long dims[5] = {kHeadDim, static_cast<unsigned long long>(G),
                                       static_cast<unsigned long long>(Hkv), static_cast<unsigned long long>(T),
                                       static_cast<unsigned long long>(B)};
   const unsigned long long str[4] = {
       static_cast<unsigned long long>(t.head) * 2, static_cast<unsigned long long>(t.head) * G * 2,
       static_cast<unsigned long long>(t.row) * 2, static_cast<unsigned long long>(t.batch) * 2};
-  const unsigned box[5] = {64, static_cast<unsigned>(G), 1, static_cast<unsigned>(tb), static_cast<unsigned>(rb)};
+  const unsigned box[5] = {stall ? 32u : 64u, static_cast<unsigned>(G), 1, static_cast<unsigned>(tb), static_cast<unsigned>(rb)};
   return encode_map_nd(m, t.data, false, 5, dims, str, box);
 }
 
@@ -1048,6 +1049,29 @@ cudaError_t launch(const Maps& tm, const Maps8* t8, const Params& p, float scale
   const long long per = kMergeWarps / w;
   return launch_dependent(kernel, dim3(static_cast<unsigned>((rows + per - 1) / per)), dim3(kMergeWarps * 32), 0, stream,
                           p);
+}
+
+}  // namespace
+
+std::atomic<bool> g_stall_prefix_attention{false};
+
+namespace {
+
+// What launches without a status word report into, one on each device; its address is looked up once
+// per device. (Told to the kernels like a caller's word: a choice between the two within them, at
+// places that never run, made the 8-bit decode 12 % slower.)
+__device__ int g_expired;
+cudaError_t expired_word(int** word) {
+  static std::atomic<int*> cached[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const bool slot = dev >= 0 && dev < 64;
+  *word = slot ? cached[dev].load(std::memory_order_relaxed) : nullptr;
+  if (*word) return cudaSuccess;
+  e = cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_expired);
+  if (e == cudaSuccess && slot) cached[dev].store(*word, std::memory_order_relaxed);
+  return e;
 }
 
 }  // namespace
@@ -1139,8 +1163,9 @@ extern "C" qi_status qi_prefix_attention(const qi_prefix_attn* a, qi_stream_t st
     if (e != cudaSuccess) return op_fail(QI_ERR_CUDA, "qi_prefix_attention: %s", cudaGetErrorString(e));
   }
   Maps tm;
-  bool ok = map_q(&tm.qo, q, pl.G, a->Hkv, a->T, a->B, pl.tb, 1) &&
-            (pl.packed ? map_q(&tm.qp, q, pl.G, a->Hkv, a->T, a->B, pl.tb, pl.rb) : (tm.qp = tm.qo, true));
+  const bool stall = g_stall_prefix_attention.exchange(false);
+  bool ok = map_q(&tm.qo, q, pl.G, a->Hkv, a->T, a->B, pl.tb, 1, stall) &&
+            (pl.packed ? map_q(&tm.qp, q, pl.G, a->Hkv, a->T, a->B, pl.tb, pl.rb, stall) : (tm.qp = tm.qo, true));
   Maps8 t8;
   const Maps8* use8 = nullptr;
   if (pre8 && !convert) {
@@ -1186,8 +1211,31 @@ extern "C" qi_status qi_prefix_attention(const qi_prefix_attn* a, qi_stream_t st
   p.part = reinterpret_cast<float*>(ws + w.part);
   p.ml = reinterpret_cast<float2*>(ws + w.ml);
   p.err = a->status;
+  if (!p.err) {
+    const cudaError_t e = expired_word(&p.err);
+    if (e != cudaSuccess) return op_fail(QI_ERR_CUDA, "qi_prefix_attention: %s", cudaGetErrorString(e));
+  }
   const float scale_log2 = a->scale * 1.4426950408889634f;
   const cudaError_t e = bf16 ? launch<true>(tm, use8, p, scale_log2, sms, s) : launch<false>(tm, use8, p, scale_log2, sms, s);
   if (e != cudaSuccess) return op_fail(QI_ERR_CUDA, "qi_prefix_attention: %s", cudaGetErrorString(e));
+  return QI_OK;
+}
+
+extern "C" qi_status qi_prefix_attention_check(qi_stream_t stream) {
+  using namespace qi;
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  int* word = nullptr;
+  int code = 0;
+  cudaError_t e = cudaStreamSynchronize(s);
+  if (e == cudaSuccess) e = expired_word(&word);
+  if (e == cudaSuccess) e = cudaMemcpyAsync(&code, word, sizeof(int), cudaMemcpyDeviceToHost, s);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  if (e == cudaSuccess && code != 0) {
+    e = cudaMemsetAsync(word, 0, sizeof(int), s);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  }
+  if (e != cudaSuccess) return op_fail(QI_ERR_CUDA, "qi_prefix_attention_check: %s", cudaGetErrorString(e));
+  if (code != 0)
+    return op_fail(QI_ERR_DEVICE_TIMEOUT, "qi_prefix_attention: a kernel's bounded wait expired (device code %d)", code);
   return QI_OK;
 }

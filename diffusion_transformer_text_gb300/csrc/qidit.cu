@@ -1334,6 +1334,7 @@ qi_status qi_debug_inject(qi_dit* d, int kind, int arg) {
   switch (kind) {
     case 0:
       g_fail_alloc.store(0);
+      qi::g_stall_prefix_attention.store(false);
       if (d) d->inject_stall = 0;
       return QI_OK;
     case 1:
@@ -1343,6 +1344,9 @@ qi_status qi_debug_inject(qi_dit* d, int kind, int arg) {
     case 2:
       if (!d) return fail(QI_ERR_INVALID_ARG, "qi_debug_inject: kind 2 needs a handle");
       d->inject_stall = 1;
+      return QI_OK;
+    case 3:
+      qi::g_stall_prefix_attention.store(true);
       return QI_OK;
   }
   return fail(QI_ERR_INVALID_ARG, "qi_debug_inject: kind %d", kind);

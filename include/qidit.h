@@ -366,6 +366,9 @@ qi_status qi_gemm_bf16(qi_dit* dit, const uint16_t* A, const uint16_t* B, float*
  *   The pass's result is then undefined; qi_dit_check (or the next call that
  *   synchronises) returns QI_ERR_DEVICE_TIMEOUT and clears the word, and later
  *   calls run normally.
+ * kind 3: the next qi_prefix_attention launch (process-wide, dit may be NULL) waits for bytes of Q
+ *   that never come; its waits run out and report into its status word, or to
+ *   qi_prefix_attention_check.
  * kind 0: cancel pending injections (of `dit`, if given).
  * Errors: INVALID_ARG (unknown kind, arg < 1 for kind 1, NULL dit for kind 2). */
 qi_status qi_debug_inject(qi_dit* dit, int kind, int arg);
@@ -526,8 +529,9 @@ typedef struct qi_strides {
  * times their scales, rounded to dtype.
  * ws: 256-byte aligned scratch of at least qi_prefix_attention_workspace(args) bytes (which
  * depends on the sizes, on whether pk8 is NULL and on the current device only; NULL if 0).
- * status: device int, or NULL: receives a non-zero code if a bounded wait in the kernel
- * expires (the result is then undefined); never cleared by the library.
+ * status: device int that receives a non-zero code if a bounded wait in the kernel expires (the
+ * result is then undefined); never cleared by the library. NULL: a word that the library has on
+ * each device, for qi_prefix_attention_check.
  * Results do not depend on the other sequences' contents, and repeat bit for bit.
  * Errors: INVALID_ARG (NULL, dtype, alignment, strides, scale not positive, workspace),
  * SHAPE (B, T, Hkv < 1, Hq % Hkv != 0, Hq / Hkv > 128, P + S = 0, B or Hkv > 65535, T, P or
@@ -554,6 +558,9 @@ typedef struct qi_prefix_attn {
 } qi_prefix_attn;
 size_t qi_prefix_attention_workspace(const qi_prefix_attn* args); /* 0 also for bad sizes */
 qi_status qi_prefix_attention(const qi_prefix_attn* args, qi_stream_t stream);
+/* Synchronises `stream`; DEVICE_TIMEOUT if a bounded wait expired since the last check in a call on
+ * the current device whose status was NULL (and clears the word). */
+qi_status qi_prefix_attention_check(qi_stream_t stream);
 
 /* The 8-bit K/V cache: MXFP8 (as qi_quant_mxfp8) along the head dimension. k8, v8: E4M3
  * codes [B, S, H, 128]; k_sf, v_sf: UE8M0 scale bytes [B, S, H, 4], one per 32 values; all

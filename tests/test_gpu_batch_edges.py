@@ -1,10 +1,15 @@
 """The batch operators at the edges of their arithmetic. Helpers are those of test_gpu_batch."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 
 from oracle import batch as ob
 from oracle import mx as omx
 from test_gpu_batch import _normal, _np, _sf, qi  # noqa: F401
+from test_gpu_batch_use import KINDS, _case
 
 pytestmark = pytest.mark.gpu
 
@@ -114,3 +119,56 @@ def test_attention_behind_keys_that_take_all(qi, B, T, Hq, Hkv, P, S, bits):
     assert (tol < 0.1 * np.abs(ref).max()).all()         # (the tail is far above what the bound allows)
     err = np.abs(o - ref)
     assert (err <= tol).all(), f"max error {err.max():.3e}, {(err / tol).max():.2f} of the bound"
+
+
+# few rows joined in a cluster, with partials from codes; 128 rows joined
+@pytest.mark.parametrize("kind,bits", [(0, 16), (1, 8), (5, 8)])
+def test_an_expired_wait_is_told(qi, kind, bits):
+    """A launch that waits for bytes of Q that never come gives up after its limit of two seconds a wait. Without a
+    status word the check tells, once; with one the word does, and the check has nothing to say. What follows
+    runs as before."""
+    import torch
+    a = _case(qi, KINDS[kind], 3, bits=bits)
+    want = qi.prefix_attention(**a)
+    qi.prefix_attention_check()
+    st = torch.cuda.Stream()
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    qi.debug_inject(3)
+    qi.prefix_attention(stream=st, **a)
+    with pytest.raises(qi.QiError, match="DEVICE_TIMEOUT"):
+        qi.prefix_attention_check(st)
+    qi.prefix_attention_check(st)
+    qi.debug_inject(3)
+    qi.prefix_attention(status=status, **a)
+    assert status.item() != 0
+    qi.prefix_attention_check()
+    qi.debug_inject(3)
+    qi.debug_inject(0)
+    assert torch.equal(qi.prefix_attention(**a), want)
+    qi.prefix_attention_check()
+
+
+def test_the_first_call_of_a_process_captured(qi):
+    """Nothing that the library does once per process or device stands in the way of a capture."""
+    code = """
+import torch, diffusion_transformer_text_gb300 as qi
+q, k, v = (torch.randn(2, n, 4, 128, device="cuda").half() for n in (1, 50, 50))
+pk = torch.randn(1, 300, 4, 128, device="cuda").half()
+x = torch.randn(8, 512, device="cuda")
+cache = qi.kv8_cache(1, 300, 4)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    qi.kv8_write(cache, pk, pk)
+    got = [qi.prefix_attention(q, k, v, prefix8=cache.prefix(0, 300)), *qi.add_rmsnorm_mxfp8(x)]
+g.replay()
+torch.cuda.synchronize()
+want = [qi.prefix_attention(q, k, v, prefix8=cache.prefix(0, 300)), *qi.add_rmsnorm_mxfp8(x)]
+qi.prefix_attention_check()
+assert all(torch.equal(a, b) for a, b in zip(got, want))
+print("same")
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
+                       capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip() == "same", r.stderr[-2000:]
