@@ -1207,7 +1207,9 @@ extern "C" qi_status qi_prefix_attention(const qi_prefix_attn* a, qi_stream_t st
   p.ob = o.batch;
   p.orow = o.row;
   p.oh = o.head;
-  p.o32 = ((reinterpret_cast<uintptr_t>(o.data) & 31) | ((o.batch | o.row | o.head) & 15)) == 0;
+  // (only strides that are followed: fix_stride has replaced the others)
+  const auto by32 = [](long long stride, int size) { return size == 1 || stride % 16 == 0; };
+  p.o32 = (reinterpret_cast<uintptr_t>(o.data) & 31) == 0 && by32(o.batch, a->B) && by32(o.row, a->T) && by32(o.head, a->Hq);
   p.part = reinterpret_cast<float*>(ws + w.part);
   p.ml = reinterpret_cast<float2*>(ws + w.ml);
   p.err = a->status;

@@ -172,3 +172,21 @@ print("same")
     r = subprocess.run([sys.executable, "-c", code], cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
                        capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and r.stdout.strip() == "same", r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("c", [dict(B=1, T=300, Hq=4, Hkv=2, P=140, S=300), dict(B=1, T=1, Hq=8, Hkv=2, P=2000, S=64),
+                               dict(B=3, T=1, Hq=128, Hkv=1, P=30, S=70), dict(B=2, T=200, Hq=1, Hkv=1, P=50, S=200)])
+def test_strides_of_dimensions_of_size_one(qi, c):
+    """They are never followed, so they may be anything, and say nothing about where the outputs lie: on and
+    off 32-byte boundaries the results are the same."""
+    import torch
+    a = _case(qi, c, 9)
+    want = qi.prefix_attention(**a)
+    for start in (0, 8):
+        buf = torch.zeros(want.numel() + 16, dtype=want.dtype, device="cuda")
+        for odd in (0, 3, 8, 2 ** 40):
+            st = [odd if n == 1 else s for n, s in zip(want.shape, want.stride())]
+            out = buf[start:].as_strided(want.shape, (*st[:3], 1))
+            assert torch.equal(qi.prefix_attention(out=out, **a), want)
+            assert buf[:start].count_nonzero() == 0 and buf[start + want.numel():].count_nonzero() == 0
+            buf.zero_()
