@@ -190,3 +190,35 @@ def test_strides_of_dimensions_of_size_one(qi, c):
             assert torch.equal(qi.prefix_attention(out=out, **a), want)
             assert buf[:start].count_nonzero() == 0 and buf[start + want.numel():].count_nonzero() == 0
             buf.zero_()
+
+
+def test_threads_whose_errors_count(qi):
+    """Four threads, each on a stream of its own, all operators: every round is compared, and an error in a
+    thread is the test's."""
+    import torch
+    from concurrent.futures import ThreadPoolExecutor
+
+    def together(a, x, kv):
+        cache = qi.kv8_write(qi.kv8_cache(2, 64, 4), kv, kv)
+        return (qi.prefix_attention(**a), *qi.add_rmsnorm_mxfp8(x), *cache, *qi.kv8_read(cache, 64, torch.bfloat16))
+
+    work = [(_case(qi, c, 7 * i, bits=8 if i % 2 else 16), _normal(i, 40 + i, 1024, dtype="fp32"),
+             _normal(i + 1, 2, 30 + i, 4, 128)) for i, c in enumerate(KINDS)]
+    want = [together(*w) for w in work]
+    torch.cuda.synchronize()
+
+    def run(i):
+        st = torch.cuda.Stream()
+        same = 0
+        for n in range(20):
+            j = (i + n) % len(work)
+            with torch.cuda.stream(st):
+                got = together(*work[j])
+            st.synchronize()
+            same += all(torch.equal(g, w) for g, w in zip(got, want[j]))
+            with pytest.raises(ValueError):               # a refusal is raised in its own thread
+                qi.prefix_attention(work[j][0]["q"][..., :64], None, None)
+        return same
+
+    with ThreadPoolExecutor(4) as pool:
+        assert [f.result(timeout=120) for f in [pool.submit(run, i) for i in range(4)]] == [20] * 4
