@@ -222,3 +222,19 @@ def test_threads_whose_errors_count(qi):
 
     with ThreadPoolExecutor(4) as pool:
         assert [f.result(timeout=120) for f in [pool.submit(run, i) for i in range(4)]] == [20] * 4
+
+
+@pytest.mark.parametrize("rows", [3, 700])
+@pytest.mark.parametrize("with_delta", [False, True])
+def test_norm_without_the_sum(qi, rows, with_delta):
+    """The library's call with x_out = NULL: the same codes and scales, and x as it was."""
+    import torch
+    K = 512
+    x, d, w = _normal(1, rows, K, dtype="fp32"), _normal(2, rows, K), _normal(3, K, dtype="bf16")
+    d = d if with_delta else None
+    _, q0, sf0 = qi.add_rmsnorm_mxfp8(x, d, w)
+    q, sf, x0 = torch.zeros_like(q0), torch.zeros_like(sf0), x.clone()
+    args = qi._NORM_HEAD.pack(x.data_ptr(), d.data_ptr() if with_delta else 0, 0, w.data_ptr(), q.data_ptr(), sf.data_ptr(), 0, 1e-6)
+    args += qi._NORM_TAIL.pack(K, K, K, qi.DT_F32, qi.DT_F16, rows, K, 0)
+    qi._check(qi.lib().qi_add_rmsnorm_mxfp8(args, torch.cuda.current_stream().cuda_stream))
+    assert torch.equal(q, q0) and torch.equal(sf, sf0) and torch.equal(x, x0)
