@@ -238,3 +238,25 @@ def test_norm_without_the_sum(qi, rows, with_delta):
     args += qi._NORM_TAIL.pack(K, K, K, qi.DT_F32, qi.DT_F16, rows, K, 0)
     qi._check(qi.lib().qi_add_rmsnorm_mxfp8(args, torch.cuda.current_stream().cuda_stream))
     assert torch.equal(q, q0) and torch.equal(sf, sf0) and torch.equal(x, x0)
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("bits", [16, 8])
+@pytest.mark.parametrize("B,T,Hq,Hkv,P,S", [(16, 1, 150, 150, 1000, 100), (4, 1, 200, 200, 1000, 20)])
+def test_weights_of_few_rows_add_up_to_one(qi, B, T, Hq, Hkv, P, S, bits, dtype):
+    """Blocks of at most 16 rows with several key tiles each, all values the same: so is every output, bit for
+    bit, whatever the weights (some rows have most of theirs on one key of a later tile). Fp32 sums of terms of
+    one sign: n / 16 < 70 product steps of at most 4 2^-23 each, n / 128 additions a thread and 20 joins, below
+    2^-14 together; half a step of the types at a value just below 2 is 2^-12 of it or more."""
+    import torch
+    val = 2 - 2.0 ** (-10 if dtype == "fp16" else -7)
+    q, k = _normal(1, B, T, Hq, 128, std=3.0, dtype=dtype), _normal(2, B, S, Hkv, 128, std=1.3, dtype=dtype)
+    pk = _normal(3, P, Hkv, 128, std=1.3, dtype=dtype)
+    if bits == 8:
+        val = 1.75                                        # the largest code, 448, times 2^-8
+        cache = qi.kv8_write(qi.kv8_cache(1, P, Hkv), pk[None], torch.full_like(pk[None], val))
+        kw = dict(prefix8=cache.prefix(0, P))
+    else:
+        kw = dict(prefix_k=pk, prefix_v=torch.full_like(pk, val))
+    o = qi.prefix_attention(q, k, torch.full_like(k, val), **kw)
+    assert (o == val).all(), f"{(o != val).float().mean().item():.4f} of the outputs are not {val}"
