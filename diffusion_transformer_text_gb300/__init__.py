@@ -582,7 +582,7 @@ def _check_norm(key, x, delta, w, x_out, q, sf):
 
 def add_rmsnorm_mxfp8(x, delta=None, w=None, plus_one: bool = False, eps: float = 1e-6, x_out=None, q=None, sf=None,
                       stream=None):
-    """x_out = x + delta in x's type, then MXFP8 of RMSNorm(x_out) * gain along the last axis.
+    """x_out = x + delta (in fp32, rounded to x's type), then MXFP8 of RMSNorm(x_out) * gain along the last axis.
 
     x [rows, K] float32, float16 or bfloat16, delta [rows, K] of any of them (None: no addition), rows
     any multiple of 16 bytes apart; w [K] bfloat16 or float32: gain w, or 1 + w with plus_one. Returns

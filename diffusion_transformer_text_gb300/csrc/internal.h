@@ -188,9 +188,10 @@ cudaError_t launch_attention(const AttnParams& p, cudaStream_t stream);
 // columns with 128-byte swizzle; rows past `rows` read as zero (qidit.cu).
 bool encode_map16(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint32_t box_rows, bool bf16);
 
-// TMA map of `rank` dimensions (first innermost, contiguous) of 16-bit values with 128-byte
-// swizzle, or of bytes without one; byte strides of the other dimensions; what lies outside
-// the dimensions reads as zero (qidit.cu).
+// TMA map of `rank` dimensions (first innermost, contiguous) of 16-bit values or of bytes, both with
+// the 128-byte swizzle (a box's innermost extent is at most 128 bytes, its place in shared memory
+// 1024-byte aligned); byte strides of the other dimensions; what lies outside the dimensions reads as
+// zero (qidit.cu).
 bool encode_map_nd(CUtensorMap* m, const void* base, bool bytes, int rank, const unsigned long long* dims,
                    const unsigned long long* strides, const unsigned* box);
 

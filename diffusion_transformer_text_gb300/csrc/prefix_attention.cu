@@ -38,15 +38,15 @@
 // of half a step of that type per term, as large as the rounding of the output (in
 // fp16, of at most 2^-32 of the row's largest P where P is below 2^-21 of it; kLift).
 //
-// Measured: 4 x 4096 rows over 407 shared and 4096 own keys each, 32 heads: 900 to 930 us,
-// 1300 to 1340 TFLOP/s, 68 % of the library product's rate, the clock at its power limit. A
+// Measured: 4 x 4096 rows over 407 shared and 4096 own keys each, 32 heads: 900 to 960 us,
+// 1260 to 1340 TFLOP/s, 65 to 70 % of the library product's rate, the clock at its power limit. A
 // tile takes 1770 cycles from one S to the next: Q K^T is issued about 500 after S has been
 // read, runs for 512 and more beside the other product, and is seen 150 later; the softmax
 // (65 to load S, 310 for the maximum, 660 for the exponentials, 300 to wait for P's place and
 // to store it) fills 1350 of them. Between two units 2500 cycles go to the epilogue's reads of
 // tensor memory, which is what small cases show: 3 x 777 causal rows over 2048 + 1201 keys, 4
-// key heads, 84.7 us, 62 %. 32 single tokens over 8192 shared rows, 8
-// key heads: 26.6 us with the merge, a unit's chain of tiles and the second launch, 46 % of HBM.
+// key heads, 84.5 us, 62 %. 32 single tokens over 8192 shared rows, 8
+// key heads: 26.6 us with the merge, 46 % of HBM: the CTAs with a prefix unit have 15 tiles, the others 8.
 #include <climits>
 #include <cstdarg>
 #include <cstdio>

@@ -171,7 +171,8 @@ struct Maps {
 };
 
 
-// The 8-bit prefix: maps over the codes (dim, key head, row) without swizzle, scale bytes.
+// The 8-bit prefix: maps over the codes (dim, key head, row; 16-byte piece i of row r lands at i ^ (r % 8)),
+// scale bytes.
 struct Maps8 {
   CUtensorMap k, v;
   const uint8_t* k_sf;

@@ -26,7 +26,7 @@
 // early: a wait that expires only makes them skip the work.
 //
 // Measured, 16 sequences of one token over 8192 prefix + 256 own keys, 32 key heads: 16 bits
-// 38.1 us with the merge (the packed 128-row kernel 43.7), 4.8 TB/s; 8-bit prefix 40.6 us,
+// 38.1 us with the merge (the packed 128-row kernel 43.7), 4.8 TB/s; 8-bit prefix 40.4 us,
 // 2.9 TB/s (75 us with the prefix turned into 16 bits in memory first). One sequence over
 // 131072 prefix rows: 16 bits 304 us, the copy rate; 8 bits 287 us, 57 % of it. There a tile of
 // codes takes 2300 cycles where HBM would give it in 1400: converting it keeps four warps

@@ -591,7 +591,7 @@ qi_status qi_kv8_write(const qi_kv8* args, qi_stream_t stream);
 qi_status qi_kv8_read(const qi_kv8* args, qi_stream_t stream);
 
 /* Residual addition, RMSNorm and the MXFP8 operand of the next block-scaled GEMM:
- *   x_out = round(x + delta), y = x_out / sqrt(mean(x_out^2) + eps) * gain,
+ *   x_out = x + delta in fp32, rounded to x_dtype, y = x_out / sqrt(mean(x_out^2) + eps) * gain,
  *   (q, sf) = MXFP8(y) as qi_quant_mxfp8 lays it out for qi_gemm_mxfp8.
  * x, x_out: [rows, K] of x_dtype; delta: [rows, K] of delta_dtype, or NULL (x_out, if given,
  * is then a copy of x); row strides in elements. x_out may be x itself (or delta, of the same
