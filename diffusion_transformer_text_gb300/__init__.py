@@ -46,7 +46,7 @@ SYMBOLS = (
     "qi_dit_step_cfg", "qi_dpmpp2m_coeffs", "qi_dpmpp2m_update", "qi_dit_step_fbcache", "qi_dit_fbcache_reset",
     "qi_dit_set_mxfp8", "qi_quant_mxfp8", "qi_gemm_mxfp8", "qi_debug_inject", "qi_dit_euler_step", "qi_dit_set_range_probe",
     "qi_prefix_attention", "qi_prefix_attention_workspace", "qi_prefix_attention_check", "qi_kv8_write", "qi_kv8_read",
-    "qi_add_rmsnorm_mxfp8",
+    "qi_add_rmsnorm_mxfp8", "qi_qk_norm_rope", "qi_paged_attention", "qi_paged_attention_workspace",
 )
 
 
@@ -131,6 +131,8 @@ def lib() -> ctypes.CDLL:
         "qi_kv8_write": [P, P],
         "qi_kv8_read": [P, P],
         "qi_add_rmsnorm_mxfp8": [P, P],
+        "qi_qk_norm_rope": [P, P],
+        "qi_paged_attention": [P, P],
     }
     for name, args in sig.items():
         fn = getattr(L, name)
@@ -140,6 +142,8 @@ def lib() -> ctypes.CDLL:
     L.qi_kv_cache_bytes.restype = S
     L.qi_prefix_attention_workspace.argtypes = [P]
     L.qi_prefix_attention_workspace.restype = S
+    L.qi_paged_attention_workspace.argtypes = [P]
+    L.qi_paged_attention_workspace.restype = S
     L.qi_last_error.argtypes = []
     L.qi_last_error.restype = ctypes.c_char_p
     _lib = L
@@ -613,6 +617,261 @@ def add_rmsnorm_mxfp8(x, delta=None, w=None, plus_one: bool = False, eps: float 
     if st:
         _check(st)
     return x_out, q, sf
+
+
+# ---------------------------------------------------------------- sequences in pages
+
+# qi_qk_rope and qi_paged_attn: what changes from call to call, then what a layout fixes
+_ROPE_HEAD, _ROPE_TAIL = struct.Struct("@13Pif"), struct.Struct("@19q16i")
+_PAGED_HEAD, _PAGED_TAIL = struct.Struct("@9Pif"), struct.Struct("@N13q9ixxxx")
+_rope_layouts: dict = {}
+_paged_layouts: dict = {}
+
+
+class PagedKV(NamedTuple):
+    """K/V in pages: k, v [pages, rows, H, 128] (rows a power of two from 16 up; heads may lie outside rows).
+    `paged_kv` makes an empty one. Which pages are whose says a table, int32 [B, width] on the device: row i
+    of sequence b is row i % rows of page table[b, i // rows]."""
+    k: "object"
+    v: "object"
+
+
+class Rope(NamedTuple):
+    """A rotation: turns int64 [pairs], 2^64ths of a circle a position; pairs of each axis; halves as in `rope`."""
+    turns: "object"
+    pairs: tuple
+    halves: bool
+
+
+def paged_kv(pages: int, rows: int, heads: int, dtype=None, device="cuda") -> PagedKV:
+    """A cache of `pages` pages of zeros, `rows` rows each (a power of two from 16 up); dtype: float16 or
+    bfloat16 (default)."""
+    import torch
+    if rows < 16 or rows & (rows - 1):
+        raise ValueError(f"rows: want a power of two from 16 up, got {rows}")
+    return PagedKV(*(torch.zeros(pages, rows, heads, HEAD_DIM, dtype=torch.bfloat16 if dtype is None else dtype, device=device)
+                     for _ in range(2)))
+
+
+def rope(axes=(16, 56, 56), theta: float = 10000.0, freqs=None, halves: bool = False, device="cuda") -> Rope:
+    """A rotation for qk_norm_rope. axes: dims of each axis of the positions (even, 128 at most in all; one
+    to four of them; dims past their sum are not rotated); pair k of an axis of d dims turns by theta^(-2k/d)
+    a position, or by `freqs`, radians a position of all pairs in order. Pairs are neighbours, or, with halves,
+    dim c and dim c + (half the rotated dims) (which are then a multiple of 16)."""
+    import torch
+    if not 1 <= len(axes) <= 4 or any(d < 2 or d % 2 for d in axes) or sum(axes) > HEAD_DIM:
+        raise ValueError(f"axes: want one to four even numbers that add up to {HEAD_DIM} at most, got {tuple(axes)}")
+    if halves and sum(axes) % 16:
+        raise ValueError(f"halves: want a multiple of 16 rotated dims, got {sum(axes)}")
+    if freqs is None:
+        if not theta > 0:
+            raise ValueError(f"theta: {theta}")
+        freqs = [theta ** (-2.0 * k / d) for d in axes for k in range(d // 2)]
+    freqs = [float(f) for f in freqs]
+    if len(freqs) * 2 != sum(axes) or not all(math.isfinite(f) for f in freqs):
+        raise ValueError(f"freqs: want {sum(axes) // 2} finite numbers, got {len(freqs)}")
+    turns = [int(math.ldexp(f / (2.0 * math.pi), 64)) % 2 ** 64 for f in freqs]
+    turns = torch.tensor([t - 2 ** 64 if t >= 2 ** 63 else t for t in turns], dtype=torch.int64, device=device)
+    return Rope(turns, tuple(d // 2 for d in axes), bool(halves))
+
+
+def _strided(t, dtype, shape, dev, name):
+    """Strides of [.., row, head, 128] of a tensor of this type, shape and device."""
+    if t.dtype != dtype or t.device != dev or tuple(t.shape) != shape:
+        raise ValueError(f"{name}: want {dtype} {dev} {shape}, got {t.dtype} {t.device} {tuple(t.shape)}")
+    if t.stride(3) != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    return t.stride()[:3]
+
+
+def _table(table, B, dev):
+    """(width, stride between rows) of a page table."""
+    import torch
+    if table.dtype != torch.int32 or table.device != dev or table.dim() != 2 or table.shape[0] != B or table.shape[1] < 1:
+        raise ValueError(f"table: want int32 {dev} [{B}, width], got {table.dtype} {table.device} {tuple(table.shape)}")
+    if table.shape[1] > 1 and table.stride(1) != 1:
+        raise ValueError("table: rows must be contiguous")
+    return table.shape[1], table.stride(0)
+
+
+def _check_rope(key, q, k, v, rope, pos, q_w, k_w, outs, cache, table, start, lens, dtype):
+    import torch
+    kinds = {torch.float16: DT_F16, torch.bfloat16: DT_BF16, torch.float32: DT_F32}
+    given = [t for t in (q, k, v) if t is not None]
+    for t, n in ((q, "q"), (k, "k"), (v, "v")):
+        if t is not None and (t.dim() != 4 or t.shape[3] != HEAD_DIM or t.dtype not in kinds):
+            raise ValueError(f"{n}: want [B, T, heads, {HEAD_DIM}] of a floating type, got {t.dtype} {tuple(t.shape)}")
+    x = given[0]
+    dev, (B, T) = x.device, x.shape[:2]
+    if dtype not in (torch.float16, torch.bfloat16) or x.dtype not in (dtype, torch.float32):
+        raise ValueError(f"dtype: want float16 or bfloat16, that of the arguments or from float32, got {dtype} from {x.dtype}")
+    if (cache is None) != (table is None):
+        raise ValueError("cache and table come together")
+    Hq = 0 if q is None else q.shape[2]
+    Hkv = k.shape[2] if k is not None else v.shape[2] if v is not None else 0
+    heads = (Hq, Hkv, Hkv)
+    ins, dst = [], []
+    for t, o, h, n in zip((q, k, v), outs, heads, "qkv"):
+        ins.append((0, 0, 0) if t is None else _strided(t, x.dtype, (B, T, h, HEAD_DIM), dev, n))
+        if o is not None and t is None:
+            raise ValueError(f"out: one for {n}, which is not given")
+        if o is None or (cache is not None and n != "q"):
+            dst.append((T * h * HEAD_DIM, h * HEAD_DIM, HEAD_DIM))
+        else:
+            dst.append(_strided(o, dtype, (B, T, h, HEAD_DIM), dev, n + "_out"))
+    pages = rows = width = stride = 0
+    if cache is not None:
+        if Hkv == 0 or any(o is not None for o in outs[1:]):
+            raise ValueError("cache: wants k or v, and no other outputs for them")
+        if cache.k.dim() != 4:
+            raise ValueError(f"cache: want [pages, rows, H, {HEAD_DIM}], got {tuple(cache.k.shape)}")
+        pages, rows = cache.k.shape[:2]
+        dst[1:] = [_strided(t, dtype, (pages, rows, Hkv, HEAD_DIM), dev, "cache") for t in cache]
+        width, stride = _table(table, B, dev)
+    for w, t, n in ((q_w, q, "q_w"), (k_w, k, "k_w")):
+        if w is not None and t is None:
+            raise ValueError(f"{n}: for heads that are not given")
+        if w is not None:
+            _want(w, w.dtype if w.dtype in (torch.bfloat16, torch.float32) else torch.bfloat16, (HEAD_DIM,), dev, n)
+    if q_w is not None and k_w is not None and q_w.dtype != k_w.dtype:
+        raise ValueError(f"q_w and k_w of one type, got {q_w.dtype} and {k_w.dtype}")
+    pairs, halves = (), False
+    if rope is not None:
+        pairs, halves = rope.pairs, rope.halves
+        _want(rope.turns, torch.int64, (sum(pairs),), dev, "rope.turns")
+    if pos is not None:
+        if not pairs:
+            raise ValueError("pos without a rotation")
+        if len(pairs) > 1 or pos.dim() != 2:
+            _want(pos, torch.int32, (B, T, len(pairs)), dev, "pos")
+        else:
+            _want(pos, torch.int32, (B, T), dev, "pos")
+    _want(start, torch.int32, (B,), dev, "start")
+    _want(lens, torch.int32, (B,), dev, "lens")
+    w = q_w if q_w is not None else k_w
+    lib()
+    return _remember(_rope_layouts, key, _ROPE_TAIL.pack(
+        *ins[0], *ins[1], *ins[2], *dst[0], *dst[1], *dst[2], stride, kinds[x.dtype], kinds[dtype],
+        int(w is not None and w.dtype == torch.float32), B, T, Hq, Hkv, len(pairs),
+        *(*pairs, 0, 0, 0, 0)[:4], int(halves), pages, rows, width))
+
+
+def qk_norm_rope(q, k, v=None, rope: Rope | None = None, pos=None, q_w=None, k_w=None, plus_one: bool = False,
+                 eps: float = 1e-6, dtype=None, out=None, cache: PagedKV | None = None, table=None, start=None,
+                 lens=None, stream=None):
+    """RMSNorm of every head of q and k, their rotation, and q, k and v in the attention's type, in one pass.
+
+    q [B, T, Hq, 128], k and v [B, T, Hkv, 128] as the projection leaves them: float32, float16 or bfloat16, all
+    of one type, the last dimension contiguous, other strides positive multiples of 16 bytes; any of them may be
+    None. q_w, k_w [128] bfloat16 or float32: gains of the norm (1 + w with plus_one); None: no norm. rope:
+    the rotation (None: none) at pos, int32 [B, T, axes] (or [B, T] with one axis), or at start[b] + t on
+    every axis. dtype of the outputs: float16 or bfloat16; default that of q, bfloat16 for float32.
+    out: (q_out, k_out, v_out), any of them None; q_out may be q. cache, table: K and V go to the cache's rows
+    start[b] + t instead, rows that the table does not reach or whose page number is none passed over. start
+    (None: 0) and lens (rows of each sequence; None: T), int32 [B] on the device; rows at or past lens[b] are
+    neither read nor written (and are zero in outputs that are made here). stream: default the current one of q's
+    device. Returns (q_out, k_out, v_out), None for what was not given or went to the cache. No gradients."""
+    import torch
+    x = q if q is not None else k if k is not None else v
+    if x is None:
+        raise ValueError("none of q, k and v")
+    dev = x.get_device()
+    if stream is not None or dev < 0 or dev != torch._C._cuda_getDevice():
+        with _elsewhere(x, stream, (q, k, v, rope and rope.turns, pos, q_w, k_w, *(out or ()), *(cache or ()), table,
+                                    start, lens)):
+            return qk_norm_rope(q, k, v, rope, pos, q_w, k_w, plus_one, eps, dtype, out, cache, table, start, lens)
+    if dtype is None:
+        dtype = torch.bfloat16 if x.dtype == torch.float32 else x.dtype
+    outs = (None, None, None) if out is None else out
+    qo, ko, vo = outs
+    key = (_layout(q), _layout(k), _layout(v), None if rope is None else (_layout(rope.turns), rope.pairs, rope.halves),
+           _layout(pos), _layout(q_w), _layout(k_w), dtype, _layout(qo), _layout(ko), _layout(vo),
+           None if cache is None else (_layout(cache.k), _layout(cache.v)), _layout(table), _layout(start), _layout(lens))
+    tail = _rope_layouts.get(key)
+    if tail is None:
+        tail = _check_rope(key, q, k, v, rope, pos, q_w, k_w, outs, cache, table, start, lens, dtype)
+    make = torch.empty if lens is None else torch.zeros
+    if q is not None and qo is None:
+        qo = make(q.shape, dtype=dtype, device=q.device)
+    if cache is None:
+        if k is not None and ko is None:
+            ko = make(k.shape, dtype=dtype, device=k.device)
+        if v is not None and vo is None:
+            vo = make(v.shape, dtype=dtype, device=v.device)
+        ka, va = _addr(ko), _addr(vo)
+    else:
+        ka, va = cache.k.data_ptr(), cache.v.data_ptr()
+    st = _lib.qi_qk_norm_rope(_ROPE_HEAD.pack(
+        _addr(q), _addr(k), _addr(v), _addr(qo), ka, va, _addr(q_w), _addr(k_w), _addr(pos),
+        0 if rope is None else rope.turns.data_ptr(), _addr(start), _addr(lens), _addr(table), 1 if plus_one else 0,
+        eps) + tail, torch._C._cuda_getCurrentRawStream(dev))
+    if st:
+        _check(st)
+    return qo, ko, vo
+
+
+def _check_paged(key, q, cache, table, kv_len, q_len, max_len, causal, out, status):
+    """(the fixed part of qi_paged_attn, workspace bytes) of arguments in this layout."""
+    import torch
+    if q.dim() != 4 or q.shape[3] != HEAD_DIM:
+        raise ValueError(f"q: want [B, T, Hq, {HEAD_DIM}], got {tuple(q.shape)}")
+    dt, dev = _dt16(q, "q"), q.device
+    B, T, Hq, _ = q.shape
+    if cache.k.dim() != 4:
+        raise ValueError(f"cache: want [pages, rows, Hkv, {HEAD_DIM}], got {tuple(cache.k.shape)}")
+    pages, rows, Hkv, _ = cache.k.shape
+    ks, vs = (_strided(t, q.dtype, (pages, rows, Hkv, HEAD_DIM), dev, "cache") for t in cache)
+    qs = _strided(q, q.dtype, (B, T, Hq, HEAD_DIM), dev, "q")
+    os_ = (T * Hq * HEAD_DIM, Hq * HEAD_DIM, HEAD_DIM) if out is None else _strided(out, q.dtype, (B, T, Hq, HEAD_DIM), dev, "out")
+    width, stride = _table(table, B, dev)
+    if kv_len is None:
+        raise ValueError("kv_len: want int32 [B]")
+    _want(kv_len, torch.int32, (B,), dev, "kv_len")
+    _want(q_len, torch.int32, (B,), dev, "q_len")
+    _want(status, torch.int32, (1,), dev, "status")
+    longest = min(width * rows, 1 << 24) if max_len is None else max_len
+    tail = (*qs, *ks, *vs, *os_, stride, dt, B, T, Hq, Hkv, pages, rows, width, longest)
+    need = lib().qi_paged_attention_workspace(
+        _PAGED_HEAD.pack(*[0] * 9, 1 if causal else 0, 1.0) + _PAGED_TAIL.pack(0, *tail))
+    return _remember(_paged_layouts, key, (_PAGED_TAIL.pack(need, *tail), need))
+
+
+def paged_attention(q, cache: PagedKV, table, kv_len, q_len=None, causal: bool = True, scale: float | None = None,
+                    max_len: int | None = None, out=None, status=None, stream=None):
+    """Attention of each sequence's new tokens over its rows of a cache in pages.
+
+    q [B, T, Hq, 128]; cache of the same type, float16 or bfloat16; table int32 [B, width]; kv_len int32 [B], rows
+    of each sequence in the cache, the new tokens' among them; q_len int32 [B], its query rows (None: T; the
+    others stay as they are in `out` and are zero without it), all on the device. causal: query row t sees rows up
+    to kv_len - q_len + t, else all kv_len. max_len: an upper bound of kv_len known on the host (default: the table's
+    reach), by which the work is cut. scale: default 1 / sqrt(128). A page number that is none reads as zeros; a row
+    that sees nothing is zero. status, stream and strides as for prefix_attention, whose check
+    (prefix_attention_check) tells of expired waits. Returns o [B, T, Hq, 128]. No gradients."""
+    import torch
+    dev = q.get_device()
+    if stream is not None or dev < 0 or dev != torch._C._cuda_getDevice():
+        with _elsewhere(q, stream, (*cache, table, kv_len, q_len, out, status)):
+            return paged_attention(q, cache, table, kv_len, q_len, causal, scale, max_len, out, status)
+    ck, cv = cache
+    causal = bool(causal)
+    key = (q.dtype, q.device, q.shape, q.stride(), _layout(ck), _layout(cv), _layout(table), _layout(kv_len),
+           None if q_len is None else _layout(q_len), max_len, causal, None if out is None else _layout(out),
+           None if status is None else _layout(status))
+    plan = _paged_layouts.get(key)
+    if plan is None:
+        plan = _check_paged(key, q, cache, table, kv_len, q_len, max_len, causal, out, status)
+    tail, need = plan
+    if out is None:
+        out = torch.empty_like(q, memory_format=torch.contiguous_format) if q_len is None else torch.zeros(
+            q.shape, dtype=q.dtype, device=q.device)
+    ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
+    st = _lib.qi_paged_attention(_PAGED_HEAD.pack(
+        q.data_ptr(), ck.data_ptr(), cv.data_ptr(), out.data_ptr(), table.data_ptr(), kv_len.data_ptr(), _addr(q_len),
+        _addr(ws), _addr(status), 1 if causal else 0, _SCALE if scale is None else scale) + tail,
+        torch._C._cuda_getCurrentRawStream(dev))
+    if st:
+        _check(st)
+    return out
 
 
 # ---------------------------------------------------------------- the DiT

@@ -81,7 +81,7 @@ static_assert(kRegsLow <= 128 && kRegsHigh >= 128 && kRegsEpi <= 128 && kRegsLow
 // tile up by 700 cycles.
 constexpr int kMessages = 4;
 struct __align__(16) Message {
-  int n, pn, p0, o0;
+  int n, pn, p0, o0;  // p0: with pages, which have no prefix, the sequence's query rows
   int t0, b0, len, rows;
   int h, u;
   long long slot;
@@ -122,9 +122,9 @@ constexpr int kSmem = (kQBufs + kKStages + kVStages) * kTile + 1024 + kNumBars *
                       kMessages * static_cast<int>(sizeof(Message));
 static_assert(kSmem <= 227 * 1024, "shared memory over the per-block limit");
 
-template <bool BF16, bool JOIN>
+template <bool BF16, bool JOIN, typename P>
 __global__ void __launch_bounds__(kThreads, 1)
-    prefix_attn_tc(const __grid_constant__ Maps tm, const __grid_constant__ Params p, float scale_log2) {
+    prefix_attn_tc(const __grid_constant__ Maps tm, const __grid_constant__ P p, float scale_log2) {
   constexpr uint32_t kIdescQK = BF16 ? idesc_bf16_f32(128, kKeys) : idesc_f16_f32(128, kKeys);
   constexpr uint32_t kIdescPV = BF16 ? idesc_bf16_f32_bmn(128, 128) : idesc_f16_f32_bmn(128, 128);
   extern __shared__ uint8_t smem_raw[];
@@ -179,7 +179,28 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       for (int u = blockIdx.x; u < total; u += gridDim.x) {
         const Unit un = unit_of(p, u);
-        if (lane == 0 && ok) {
+        if constexpr (kPaged<P>) {
+          // by pages, a lane a box: a tile's pages are looked up while the one before it waits for its stage
+          ok = __shfl_sync(0xffffffffu, static_cast<int>(ok), 0);
+          int next = page_of(p, un, un.o0 * kKeys, lane);
+          for (int j = 0; ok && j < un.n; ++j) {
+            const uint32_t tt = t + j, st = tt % kVStages;
+            const int key0 = (un.o0 + j) * kKeys, id = next;
+            if (j + 1 < un.n) next = page_of(p, un, key0 + kKeys, lane);
+            ok = __all_sync(0xffffffffu, !*abort_flag && mbar_wait(&bars[kVEmpty + st], ((tt / kVStages) & 1u) ^ 1u));
+            if (!ok) {
+              if (lane == 0) {
+                if (!*abort_flag) report_error(p.err, kErrTimeoutProducer);
+                *abort_flag = 1;
+              }
+              t = tt;  // tiles issued, for the drain below
+              break;
+            }
+            if (lane == 0) mbar_arrive_expect_tx(&bars[kVFull + st], kTile);
+            __syncwarp();
+            load_pages(p, &tm.v, sV + st * kTile, &bars[kVFull + st], un.h, key0, id, lane);
+          }
+        } else if (lane == 0 && ok) {
           for (int j = 0; j < un.n; ++j) {
             const uint32_t tt = t + j, st = tt % kVStages;
             if (*abort_flag || !mbar_wait(&bars[kVEmpty + st], ((tt / kVStages) & 1u) ^ 1u)) {
@@ -280,13 +301,50 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
     } else if (warp == 0) {
-      // ---------------- TMA producer of the K tiles and of each unit's Q rows (lane 0)
-      if (lane == 0) {
+      // ---------------- TMA producer of the K tiles and of each unit's Q rows (lane 0; with pages the
+      // whole warp, a lane a box)
+      if (kPaged<P> || lane == 0) {
       uint32_t t = 0;
       uint32_t nq = 0, nm = 0;
       bool ok = true;
       for (int u = blockIdx.x; ok && u < total; u += gridDim.x) {
         const Unit un = unit_of(p, u);
+if constexpr (kPaged<P>) {
+          const uint32_t mb = nm % kMessages, qb = nq % kQBufs;
+          ok = __all_sync(0xffffffffu, !*abort_flag && mbar_wait(&bars[kUEmpty + mb], ((nm / kMessages) & 1u) ^ 1u));
+          if (ok && lane == 0) {
+            messages[mb] = {un.n, 0, un.tq, un.o0, un.t0, un.b0, un.len, un.rows, un.h, u, un.slot};
+            mbar_arrive(&bars[kUFull + mb]);
+          }
+          ++nm;
+          if (ok && un.n > 0) {
+            ok = __all_sync(0xffffffffu, !*abort_flag && mbar_wait(&bars[kQEmpty + qb], ((nq / kQBufs) & 1u) ^ 1u));
+            if (ok) {
+              if (lane == 0) {
+                mbar_arrive_expect_tx(&bars[kQFull + qb], static_cast<uint32_t>(un.rows) * 256u);
+                tma_load_5d(sQ + qb * kTile, &tm.qo, &bars[kQFull + qb], 0, 0, un.h, un.t0, un.b0);
+                tma_load_5d(sQ + qb * kTile + kBox, &tm.qo, &bars[kQFull + qb], 64, 0, un.h, un.t0, un.b0);
+              }
+              ++nq;
+            }
+            int next = page_of(p, un, un.o0 * kKeys, lane);
+            for (int j = 0; ok && j < un.n; ++j) {
+              const uint32_t st = t % kKStages;
+              const int key0 = (un.o0 + j) * kKeys, id = next;
+              if (j + 1 < un.n) next = page_of(p, un, key0 + kKeys, lane);
+              ok = __all_sync(0xffffffffu, !*abort_flag && mbar_wait(&bars[kKEmpty + st], ((t / kKStages) & 1u) ^ 1u));
+              if (!ok) break;
+              if (lane == 0) mbar_arrive_expect_tx(&bars[kKFull + st], kTile);
+              __syncwarp();
+              load_pages(p, &tm.k, sK + st * kTile, &bars[kKFull + st], un.h, key0, id, lane);
+              ++t;
+            }
+          }
+          if (!ok && lane == 0) {
+            if (!*abort_flag) report_error(p.err, kErrTimeoutProducer);
+            *abort_flag = 1;
+          }
+        } else {
         const uint32_t mb = nm % kMessages;
         if (*abort_flag || !mbar_wait(&bars[kUEmpty + mb], ((nm / kMessages) & 1u) ^ 1u)) {
           if (!*abort_flag) report_error(p.err, kErrTimeoutProducer);
@@ -324,10 +382,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           tma_load_4d(sK + st * kTile, m, &bars[kKFull + st], 0, un.h, row, bs);
           tma_load_4d(sK + st * kTile + kBox, m, &bars[kKFull + st], 64, un.h, row, bs);
         }
+        }
       }
-      for (uint32_t i = t > kKStages ? t - kKStages : 0; i < t; ++i)
+      for (uint32_t i = t > kKStages ? t - kKStages : 0; lane == 0 && i < t; ++i)
         if (!mbar_wait(&bars[kKFull + i % kKStages], (i / kKStages) & 1u)) report_error(p.err, kErrTimeoutDrain);
-      for (uint32_t i = nq > kQBufs ? nq - kQBufs : 0; i < nq; ++i)
+      for (uint32_t i = nq > kQBufs ? nq - kQBufs : 0; lane == 0 && i < nq; ++i)
         if (!mbar_wait(&bars[kQFull + i % kQBufs], (i / kQBufs) & 1u)) report_error(p.err, kErrTimeoutDrain);
       }
       __syncwarp();
@@ -400,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars[kUEmpty + mb]);
       if (un.n == 0) continue;
-      const int lim_own = own_lim(p, un.len, un.t0 + tok);
+      const int lim_own = own_lim(p, un.len, un.t0 + tok, kPaged<P> ? un.p0 : p.T);
       // A warp whose 32 rows lie past the block's has nothing to compute: it only keeps the
       // barriers' counts (its lanes of S, P and O hold whatever they held). It still waits
       // for every S, so it is never a phase ahead of the other warps on a P buffer.
@@ -409,9 +468,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       float l = 0.f;
       // keys of this half of the tile that the row sees, counted down by tile (few live values:
       // the loop runs at its register limit, and the tile numbers kept instead cost 1.5 %)
-      int left = p.P - un.p0 * kKeys - h * 64;
+      int left = kPaged<P> ? 0 : p.P - un.p0 * kKeys - h * 64;
       const int left_own = lim_own - un.o0 * kKeys - h * 64;
-      const int n = un.n, pn = un.pn;
+      const int n = un.n, pn = kPaged<P> ? 0 : un.pn;
       for (int j = 0; j < n; ++j) {
         const uint32_t tt = t + j;
         const uint32_t b = tt & 1u;
@@ -555,12 +614,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(&bars[kUEmpty + mb]);
       // where the row goes: token and sequence (a prefix block runs over sequences)
       int b = un.b0, tk = un.t0 + tok;
-      if (u < p.pl.units_p) {
+      if (!kPaged<P> && u < p.pl.units_p) {
         const int q = quot(p.d_T, tok);
         b += q;
         tk = tok - q * p.T;
       }
-      const bool mine = rit < un.rows && tk < p.T && b < p.B;
+      const bool mine = rit < un.rows && tk < (kPaged<P> ? un.p0 : p.T) && b < p.B;
       uint16_t* orow = p.o + b * p.ob + tk * p.orow + static_cast<long long>(un.h * p.pl.G + g) * p.oh;
       if (un.n == 0) {
         if (JOIN) *reinterpret_cast<float2*>(smem + kJoinMl + rit * 8) = make_float2(-INFINITY, 0.f);
@@ -681,21 +740,23 @@ __global__ void __launch_bounds__(kThreads, 1)
 // told from the lengths, as the units told them. What comes before the wait reads only what
 // was complete before the attention kernel began.
 constexpr int kMergeWarps = 8;
-template <bool BF16, int W>
-__global__ void __launch_bounds__(kMergeWarps * 32) merge_partials(const __grid_constant__ Params p) {
+template <bool BF16, int W, typename P>
+__global__ void __launch_bounds__(kMergeWarps * 32) merge_partials(const __grid_constant__ P p) {
   __shared__ float4 sacc[kMergeWarps][32];
   __shared__ float sden[kMergeWarps];
   const Plan& pl = p.pl;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int w = warp % W;
   const long long row = static_cast<long long>(blockIdx.x) * (kMergeWarps / W) + warp / W;
-  const bool in = row < static_cast<long long>(p.B) * p.T * p.Hq;  // below 2^31
+  bool in = row < static_cast<long long>(p.B) * p.T * p.Hq;  // below 2^31
   const int r = in ? static_cast<int>(row) : 0;
   const int bt = quot(p.d_Hq, r), hq = r - bt * p.Hq;
   const int b = quot(p.d_T, bt), t = bt - b * p.T;
   const int h = quot(p.d_G, hq), g = hq - h * pl.G;
   const int qb = quot(p.d_tb, t);
-  const int ot = own_tiles(p, own_len_of(p, b), qb * pl.tb, pl.tb);
+  const int tq = query_rows(p, b);
+  if (kPaged<P>) in = in && t < tq;  // rows past a sequence's stay as they are
+  const int ot = own_tiles(p, own_len_of(p, b), qb * pl.tb, pl.tb, tq);
   const long long hb = static_cast<long long>(h) * p.B + b;
   const long long unit_o =
       (pl.by_block ? (pl.nqb - 1 - qb) * static_cast<long long>(p.Hkv) * p.B + hb : hb * pl.nqb + qb) * pl.nch;
@@ -987,6 +1048,16 @@ bool map_kv(CUtensorMap* m, const Tensor4& t, int heads, int rows, int batch) {
   return encode_map_nd(m, t.data, false, 4, dims, str, box);
 }
 
+bool map_pages(CUtensorMap* m, const Tensor4& t, int heads, int page_rows, int pages) {
+  const unsigned long long dims[4] = {kHeadDim, static_cast<unsigned long long>(heads),
+                                      static_cast<unsigned long long>(page_rows), static_cast<unsigned long long>(pages)};
+  const unsigned long long str[3] = {static_cast<unsigned long long>(t.head) * 2,
+                                     static_cast<unsigned long long>(t.row) * 2,
+                                     static_cast<unsigned long long>(t.batch) * 2};
+  const unsigned box[4] = {64, 1, static_cast<unsigned>(page_rows < kKeys ? page_rows : kKeys), 1};
+  return encode_map_nd(m, t.data, false, 4, dims, str, box);
+}
+
 bool map_codes(CUtensorMap* m, const uint8_t* codes, int heads, int rows) {
   const unsigned long long dims[3] = {kHeadDim, static_cast<unsigned long long>(heads),
                                       static_cast<unsigned long long>(rows)};
@@ -1021,23 +1092,26 @@ qi_status check_sizes(const qi_prefix_attn* a) {
   return QI_OK;
 }
 
-template <bool BF16>
-cudaError_t launch(const Maps& tm, const Maps8* t8, const Params& p, float scale_log2, int sms, cudaStream_t stream) {
+template <bool BF16, typename P>
+cudaError_t launch(const Maps& tm, const Maps8* t8, const P& p, float scale_log2, int sms, cudaStream_t stream) {
   cudaError_t e;
   if (p.pl.few) {
-    e = launch_few(tm, t8, p, BF16, scale_log2, sms, stream);
+    if constexpr (kPaged<P>)
+      e = launch_few(tm, p, BF16, scale_log2, sms, stream);
+    else
+      e = launch_few(tm, t8, p, BF16, scale_log2, sms, stream);
   } else {
     static std::atomic<unsigned long long> attr_done{0}, attr_done_join{0};
     if (p.pl.join) {
-      e = ensure_smem_limit(prefix_attn_tc<BF16, true>, kSmem, attr_done_join);
+      e = ensure_smem_limit(prefix_attn_tc<BF16, true, P>, kSmem, attr_done_join);
       if (e != cudaSuccess) return e;
-      return launch_clusters(prefix_attn_tc<BF16, true>, p.pl.nch, dim3(p.pl.units), dim3(kThreads), kSmem, stream, tm, p,
-                             scale_log2);
+      return launch_clusters(prefix_attn_tc<BF16, true, P>, p.pl.nch, dim3(p.pl.units), dim3(kThreads), kSmem, stream,
+                             tm, p, scale_log2);
     }
-    e = ensure_smem_limit(prefix_attn_tc<BF16, false>, kSmem, attr_done);
+    e = ensure_smem_limit(prefix_attn_tc<BF16, false, P>, kSmem, attr_done);
     if (e != cudaSuccess) return e;
     const int grid = p.pl.units < sms ? p.pl.units : sms;
-    e = launch_dependent(prefix_attn_tc<BF16, false>, dim3(grid), dim3(kThreads), kSmem, stream, tm, p, scale_log2);
+    e = launch_dependent(prefix_attn_tc<BF16, false, P>, dim3(grid), dim3(kThreads), kSmem, stream, tm, p, scale_log2);
   }
   if (e != cudaSuccess || !p.pl.split) return e;
   // Warps per row: as many as its parts keep busy, unless the rows alone fill the GPU (1024
@@ -1045,10 +1119,43 @@ cudaError_t launch(const Maps& tm, const Maps8* t8, const Params& p, float scale
   const long long rows = static_cast<long long>(p.B) * p.T * p.Hq;
   const int parts = (p.pl.packed ? p.pl.nchp + p.pl.nch : p.pl.nch) * p.pl.per;
   const int w = rows > 16384 || parts < 4 ? 1 : parts < 16 ? 4 : 8;
-  const auto kernel = w == 1 ? merge_partials<BF16, 1> : w == 4 ? merge_partials<BF16, 4> : merge_partials<BF16, 8>;
+  const auto kernel = w == 1   ? merge_partials<BF16, 1, P>
+                      : w == 4 ? merge_partials<BF16, 4, P>
+                               : merge_partials<BF16, 8, P>;
   const long long per = kMergeWarps / w;
   return launch_dependent(kernel, dim3(static_cast<unsigned>((rows + per - 1) / per)), dim3(kMergeWarps * 32), 0, stream,
                           p);
+}
+
+// What does not come from where the keys are
+void fill_params(Params* p, const Plan& pl, const Sizes& z, const Tensor4& o) {
+  p->pl = pl;
+  p->d_nch = make_div(pl.nch);
+  p->d_nchp = make_div(pl.packed ? pl.nchp : 1);
+  p->d_nqb = make_div(pl.nqb);
+  p->d_npb = make_div(pl.packed ? pl.npb : 1);
+  p->d_tb = make_div(pl.tb);
+  p->d_rb = make_div(pl.rb);
+  p->d_ct = make_div(pl.ct);
+  p->d_Hq = make_div(z.Hq);
+  p->d_B = make_div(z.B);
+  p->d_hb = make_div(z.Hkv * z.B);
+  p->d_G = make_div(pl.G);
+  p->d_T = make_div(z.T);
+  p->B = z.B;
+  p->T = z.T;
+  p->Hq = z.Hq;
+  p->Hkv = z.Hkv;
+  p->P = z.P;
+  p->S = z.S;
+  p->causal = z.causal;
+  p->o = static_cast<uint16_t*>(const_cast<void*>(o.data));
+  p->ob = o.batch;
+  p->orow = o.row;
+  p->oh = o.head;
+  // (only strides that are followed: fix_stride has replaced the others)
+  const auto by32 = [](long long stride, int size) { return size == 1 || stride % 16 == 0; };
+  p->o32 = (reinterpret_cast<uintptr_t>(o.data) & 31) == 0 && by32(o.batch, z.B) && by32(o.row, z.T) && by32(o.head, z.Hq);
 }
 
 }  // namespace
@@ -1182,34 +1289,8 @@ extern "C" qi_status qi_prefix_attention(const qi_prefix_attn* a, qi_stream_t st
   if (a->P == 0) tm.pk = tm.k, tm.pv = tm.v;  // never loaded from
   if (a->S == 0) tm.k = tm.pk, tm.v = tm.pv;
   Params p{};
-  p.pl = pl;
-  p.d_nch = make_div(pl.nch);
-  p.d_nchp = make_div(pl.packed ? pl.nchp : 1);
-  p.d_nqb = make_div(pl.nqb);
-  p.d_npb = make_div(pl.packed ? pl.npb : 1);
-  p.d_tb = make_div(pl.tb);
-  p.d_rb = make_div(pl.rb);
-  p.d_ct = make_div(pl.ct);
-  p.d_Hq = make_div(a->Hq);
-  p.d_B = make_div(a->B);
-  p.d_hb = make_div(a->Hkv * a->B);
-  p.d_G = make_div(pl.G);
-  p.d_T = make_div(a->T);
-  p.B = a->B;
-  p.T = a->T;
-  p.Hq = a->Hq;
-  p.Hkv = a->Hkv;
-  p.P = a->P;
-  p.S = a->S;
-  p.causal = a->causal != 0;
+  fill_params(&p, pl, {a->B, a->T, a->Hq, a->Hkv, a->P, a->S, a->causal != 0, false}, o);
   p.own_len = a->S > 0 ? a->own_len : nullptr;
-  p.o = static_cast<uint16_t*>(const_cast<void*>(o.data));
-  p.ob = o.batch;
-  p.orow = o.row;
-  p.oh = o.head;
-  // (only strides that are followed: fix_stride has replaced the others)
-  const auto by32 = [](long long stride, int size) { return size == 1 || stride % 16 == 0; };
-  p.o32 = (reinterpret_cast<uintptr_t>(o.data) & 31) == 0 && by32(o.batch, a->B) && by32(o.row, a->T) && by32(o.head, a->Hq);
   p.part = reinterpret_cast<float*>(ws + w.part);
   p.ml = reinterpret_cast<float2*>(ws + w.ml);
   p.err = a->status;
@@ -1240,4 +1321,101 @@ extern "C" qi_status qi_prefix_attention_check(qi_stream_t stream) {
   if (code != 0)
     return op_fail(QI_ERR_DEVICE_TIMEOUT, "qi_prefix_attention: a kernel's bounded wait expired (device code %d)", code);
   return QI_OK;
+}
+
+namespace qi {
+namespace {
+
+// a call's sizes, checked but for what the plan makes of them
+qi_status check_paged(const qi_paged_attn* a) {
+  constexpr const char* kName = "qi_paged_attention";
+  if (!a) return op_fail(QI_ERR_INVALID_ARG, "%s: NULL argument", kName);
+  if (a->dtype != QI_DT_F16 && a->dtype != QI_DT_BF16) return op_fail(QI_ERR_INVALID_ARG, "%s: dtype %d", kName, a->dtype);
+  constexpr int kMost = 1 << 24;
+  const int n = a->page_rows;
+  if (a->B < 1 || a->B > 65535 || a->T < 1 || a->T > kMost || a->Hkv < 1 || a->Hkv > 65535 || a->Hq < a->Hkv ||
+      a->Hq % a->Hkv != 0 || a->Hq / a->Hkv > kRows || static_cast<long long>(a->B) * a->T * a->Hq >= (1ll << 31))
+    return op_fail(QI_ERR_SHAPE, "%s: B %d T %d Hq %d Hkv %d", kName, a->B, a->T, a->Hq, a->Hkv);
+  if (n < 16 || n > 65536 || (n & (n - 1)) != 0 || a->pages < 1 || a->table_width < 1 || a->max_len < 1 ||
+      a->max_len > kMost || a->max_len > static_cast<long long>(a->table_width) * n)
+    return op_fail(QI_ERR_SHAPE, "%s: pages %d of %d rows, table of %d, max_len %d", kName, a->pages, n, a->table_width,
+                   a->max_len);
+  return QI_OK;
+}
+Sizes paged_sizes(const qi_paged_attn* a) {
+  return {a->B, a->T, a->Hq, a->Hkv, 0, a->max_len, a->causal != 0, false};
+}
+
+}  // namespace
+}  // namespace qi
+
+extern "C" size_t qi_paged_attention_workspace(const qi_paged_attn* a) {
+  using namespace qi;
+  if (check_paged(a) != QI_OK) return 0;
+  const int sms = device_sms();
+  if (sms <= 0) return 0;
+  return ws_layout(plan_for(paged_sizes(a), sms), 0, a->Hkv, false).total;
+}
+
+extern "C" qi_status qi_paged_attention(const qi_paged_attn* a, qi_stream_t stream) {
+  using namespace qi;
+  constexpr const char* kName = "qi_paged_attention";
+  const qi_status st = check_paged(a);
+  if (st != QI_OK) return st;
+  if (!a->q || !a->k || !a->v || !a->o || !a->table || !a->kv_len)
+    return op_fail(QI_ERR_INVALID_ARG, "%s: NULL q, k, v, o, table or kv_len", kName);
+  if (!(a->scale > 0.f) || !(a->scale < 3e38f))
+    return op_fail(QI_ERR_INVALID_ARG, "%s: scale must be positive and finite", kName);
+  const auto tensor = [](const void* data, const qi_strides& s) { return Tensor4{data, s.batch, s.row, s.head}; };
+  Tensor4 q = tensor(a->q, a->q_stride), o = tensor(a->o, a->o_stride);
+  Tensor4 k = tensor(a->k, a->k_stride), v = tensor(a->v, a->v_stride);
+  const auto good = [](Tensor4* t, int batch, int rows, int heads) {
+    return (reinterpret_cast<uintptr_t>(t->data) & 15) == 0 && fix_stride(&t->batch, batch) &&
+           fix_stride(&t->row, rows) && fix_stride(&t->head, heads);
+  };
+  if (!good(&q, a->B, a->T, a->Hq) || !good(&o, a->B, a->T, a->Hq) || !good(&k, a->pages, a->page_rows, a->Hkv) ||
+      !good(&v, a->pages, a->page_rows, a->Hkv))
+    return op_fail(QI_ERR_INVALID_ARG, "%s: tensors need 16-byte alignment and strides that are positive multiples of 8",
+                   kName);
+  if ((reinterpret_cast<uintptr_t>(a->table) | reinterpret_cast<uintptr_t>(a->kv_len) |
+       reinterpret_cast<uintptr_t>(a->q_len) | reinterpret_cast<uintptr_t>(a->status)) & 3)
+    return op_fail(QI_ERR_INVALID_ARG, "%s: table, kv_len, q_len and status need 4-byte alignment", kName);
+  if (a->B > 1 && (a->table_stride < a->table_width || a->table_stride >= (1ll << 38)))
+    return op_fail(QI_ERR_INVALID_ARG, "%s: table rows %lld apart", kName, a->table_stride);
+  const int sms = device_sms();
+  if (sms <= 0) return op_fail(QI_ERR_CUDA, "%s: no CUDA device", kName);
+  const Sizes z = paged_sizes(a);
+  const Plan pl = plan_for(z, sms);
+  if (pl.units <= 0) return op_fail(QI_ERR_SHAPE, "%s: too many rows and heads", kName);
+  const WsLayout w = ws_layout(pl, 0, a->Hkv, false);
+  if (w.total > 0 && (!a->ws || a->ws_bytes < w.total || (reinterpret_cast<uintptr_t>(a->ws) & 255)))
+    return op_fail(QI_ERR_INVALID_ARG, "%s: needs a 256-byte aligned workspace of %zu bytes", kName, w.total);
+  Maps tm;
+  if (!map_q(&tm.qo, q, pl.G, a->Hkv, a->T, a->B, pl.tb, 1, g_stall_prefix_attention.exchange(false)) ||
+      !map_pages(&tm.k, k, a->Hkv, a->page_rows, a->pages) || !map_pages(&tm.v, v, a->Hkv, a->page_rows, a->pages))
+    return op_fail(QI_ERR_INVALID_ARG, "%s: tensor map encoding failed (strides?)", kName);
+  tm.qp = tm.qo;  // no prefix: never loaded from
+  tm.pk = tm.k;
+  tm.pv = tm.v;
+  PagedParams p{};
+  fill_params(&p, pl, z, o);
+  p.own_len = a->kv_len;
+  p.q_len = a->q_len;
+  p.table = a->table;
+  p.table_stride = a->B > 1 ? a->table_stride : 0;
+  p.pages = a->pages;
+  while ((1 << p.page_log) < a->page_rows) ++p.page_log;
+  uint8_t* ws = static_cast<uint8_t*>(a->ws);
+  p.part = reinterpret_cast<float*>(ws + w.part);
+  p.ml = reinterpret_cast<float2*>(ws + w.ml);
+  p.err = a->status;
+  if (!p.err) {
+    const cudaError_t e = expired_word(&p.err);
+    if (e != cudaSuccess) return op_fail(QI_ERR_CUDA, "%s: %s", kName, cudaGetErrorString(e));
+  }
+  const float scale_log2 = a->scale * 1.4426950408889634f;
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const cudaError_t e = a->dtype == QI_DT_BF16 ? launch<true>(tm, nullptr, p, scale_log2, sms, s)
+                                               : launch<false>(tm, nullptr, p, scale_log2, sms, s);
+  return e == cudaSuccess ? QI_OK : op_fail(QI_ERR_CUDA, "%s: %s", kName, cudaGetErrorString(e));
 }

@@ -1,4 +1,5 @@
-// What the kernels of the shared-prefix attention have in common: the decomposition into
+// What the kernels of the shared-prefix attention, and of the attention over a cache in pages
+// (the same kernels, their keys fetched page by page), have in common: the decomposition into
 // units, TMA loads over the caller's strides, and the tensor maps.
 #pragma once
 #include "internal.h"
@@ -55,8 +56,21 @@ struct Params {
   int* err;
 };
 
+// A cache in pages: no prefix, and own keys where the table says; S is the largest length.
+struct PagedParams : Params {
+  const int* table;  // page of key i of sequence b: table[b table_stride + (i >> page_log)]
+  long long table_stride;
+  const int* q_len;  // query rows of each sequence, or NULL: T
+  int page_log, pages;
+};
+template <typename P>
+constexpr bool kPaged = false;
+template <>
+constexpr bool kPaged<PagedParams> = true;
+
 struct Unit {
   int h, b0, t0;
+  int tq;          // query rows of sequence b0
   int p0, pn;      // prefix tiles [p0, p0 + pn)
   int o0, on;      // own tiles of sequence b0
   int n;           // pn + on
@@ -69,18 +83,27 @@ struct Unit {
 __device__ __forceinline__ int own_len_of(const Params& p, int b) {
   return p.own_len ? min(max(p.own_len[b], 0), p.S) : p.S;
 }
-// own keys that token t of a sequence with `len` own keys sees
-__device__ __forceinline__ int own_lim(const Params& p, int len, int t) {
-  return p.causal ? min(max(len - p.T + t + 1, 0), len) : len;
+template <typename P>
+__device__ __forceinline__ int query_rows(const P& p, int b) {
+  if constexpr (kPaged<P>) return p.q_len ? min(max(p.q_len[b], 0), p.T) : p.T;
+  return p.T;
 }
-__device__ __forceinline__ int own_tiles(const Params& p, int len, int t0, int tb) {
-  return (own_lim(p, len, min(t0 + tb, p.T) - 1) + kKeys - 1) / kKeys;
+// own keys that token t of a sequence with `len` own keys and tq query rows sees
+__device__ __forceinline__ int own_lim(const Params& p, int len, int t, int tq) {
+  return p.causal ? min(max(len - tq + t + 1, 0), len) : len;
+}
+template <typename P>
+__device__ __forceinline__ int own_tiles(const P& p, int len, int t0, int tb, int tq) {
+  if (kPaged<P> && t0 >= tq) return 0;  // no row of the block
+  return (own_lim(p, len, min(t0 + tb, tq) - 1, tq) + kKeys - 1) / kKeys;
 }
 
-__device__ __forceinline__ Unit unit_of(const Params& p, int u) {
+template <typename P>
+__device__ __forceinline__ Unit unit_of(const P& p, int u) {
   const Plan& pl = p.pl;
   Unit x;
   x.p0 = x.pn = x.o0 = x.on = x.len = 0;
+  x.tq = p.T;
   x.clear = false;
   if (u < pl.units_p) {  // packed: prefix
     const int r = quot(p.d_nchp, u), c = u - r * pl.nchp;
@@ -110,7 +133,8 @@ __device__ __forceinline__ Unit unit_of(const Params& p, int u) {
     x.t0 = qb * pl.tb;
     x.len = own_len_of(p, x.b0);
     const int pt = pl.packed ? 0 : pl.pt;
-    const int tiles = pt + own_tiles(p, x.len, x.t0, pl.tb);
+    x.tq = query_rows(p, x.b0);
+    const int tiles = pt + own_tiles(p, x.len, x.t0, pl.tb, x.tq);
     const int lo = c * pl.ct;
     const int hi = min(lo + pl.ct, tiles);
     if (lo < hi) {
@@ -118,7 +142,8 @@ __device__ __forceinline__ Unit unit_of(const Params& p, int u) {
       x.pn = min(hi, pt) - x.p0;
       x.o0 = max(lo, pt) - pt;
       x.on = max(hi, pt) - pt - x.o0;
-      x.clear = x.on > 0 && x.len < (x.o0 + x.on) * kKeys && x.len < p.S;
+      // (rows past S read as zero, but not those of a page)
+      x.clear = x.on > 0 && x.len < (x.o0 + x.on) * kKeys && (kPaged<P> || x.len < p.S);
     }
     x.rows = pl.rows_o;
     x.slot = (static_cast<long long>(pl.units_p) * pl.rows_p + static_cast<long long>(v) * pl.rows_o) * pl.per;
@@ -143,6 +168,24 @@ __device__ __forceinline__ void tma_load_5d(void* dst, const CUtensorMap* map, u
       " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(smem_u32(dst)),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(g), "r"(h), "r"(t), "r"(b)
       : "memory");
+}
+
+// The page that lane `lane` fetches for the tile of keys key0 .. key0 + 127 of a sequence: a tile is 128 >>
+// page_log pages (or part of one), each two boxes of 64 dims, a lane a box. Pages behind the sequence and
+// numbers that are none become `pages`, past the map's end, and read as zeros.
+__device__ __forceinline__ int page_boxes(const PagedParams& p) { return p.page_log < 7 ? 256 >> p.page_log : 2; }
+__device__ __forceinline__ int page_of(const PagedParams& p, const Unit& un, int key0, int lane) {
+  const int key = key0 + ((lane >> 1) << p.page_log);
+  if (lane >= page_boxes(p) || key >= un.len) return p.pages;
+  const int id = p.table[un.b0 * p.table_stride + (key >> p.page_log)];
+  return static_cast<unsigned>(id) < static_cast<unsigned>(p.pages) ? id : p.pages;
+}
+// ... and its load, by the warp's lanes; `tile` has room for all boxes
+__device__ __forceinline__ void load_pages(const PagedParams& p, const CUtensorMap* map, uint8_t* tile, uint64_t* bar,
+                                           int h, int key0, int id, int lane) {
+  if (lane < page_boxes(p))
+    tma_load_4d(tile + (lane & 1) * kBox + ((lane >> 1) << (p.page_log + 7)), map, bar, (lane & 1) * 64, h,
+                key0 & ((1 << p.page_log) - 1), id);
 }
 
 // One lane of a converged warp, always the same
@@ -184,6 +227,7 @@ struct Maps8 {
 constexpr int kFewRows = 16;
 cudaError_t launch_few(const Maps& tm, const Maps8* t8, const Params& p, bool bf16, float scale_log2, int sms,
                        cudaStream_t s);
+cudaError_t launch_few(const Maps& tm, const PagedParams& p, bool bf16, float scale_log2, int sms, cudaStream_t s);
 
 // ------------------------------------------------------------------ parts joined by a cluster
 //
@@ -197,8 +241,8 @@ constexpr int kJoinPitch = kHeadDim + 4;
 constexpr int kJoinMl = 128 * kJoinPitch * 4;
 constexpr int kJoinMost = 8;  // CTAs of a cluster that every GPU of this kind can place
 
-template <bool BF16>
-__device__ __forceinline__ void cluster_join(const Params& p, const Unit& un, const uint8_t* smem, int rows) {
+template <bool BF16, typename P>
+__device__ __forceinline__ void cluster_join(const P& p, const Unit& un, const uint8_t* smem, int rows) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   const int n = p.pl.nch, per = p.pl.per, parts = n * per;  // at most 16
   const uint32_t base = smem_u32(smem);
@@ -236,7 +280,7 @@ __device__ __forceinline__ void cluster_join(const Params& p, const Unit& un, co
     }
     const float inv = den == 0.f ? 0.f : 1.f / den;
     const int tok = quot(p.d_G, i), g = i - tok * p.pl.G, t = un.t0 + tok;
-    if (t < p.T) {
+    if (t < un.tq) {
       uint16_t* orow = p.o + un.b0 * p.ob + t * p.orow + static_cast<long long>(un.h * p.pl.G + g) * p.oh;
       reinterpret_cast<uint2*>(orow)[lane] =
           make_uint2(pack16<BF16>(acc.x * inv, acc.y * inv), pack16<BF16>(acc.z * inv, acc.w * inv));

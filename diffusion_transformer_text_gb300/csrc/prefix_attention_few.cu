@@ -178,9 +178,9 @@ __device__ __forceinline__ uint4 codes_to_16bit(uint2 c, uint32_t scale) {
   return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
-template <bool BF16, bool Q8, bool JOIN>
+template <bool BF16, bool Q8, bool JOIN, typename P>
 __global__ void __launch_bounds__(Cfg<Q8>::kThreads, 1)
-    prefix_attn_few(const __grid_constant__ Maps tm, const __grid_constant__ Maps8 t8, const __grid_constant__ Params p,
+    prefix_attn_few(const __grid_constant__ Maps tm, const __grid_constant__ Maps8 t8, const __grid_constant__ P p,
                     float scale_log2) {
   using C = Cfg<Q8>;
   constexpr int kSt = C::kSt, kCSt = Q8 ? 2 : 1;
@@ -256,7 +256,37 @@ __global__ void __launch_bounds__(Cfg<Q8>::kThreads, 1)
     for (int u = blockIdx.x; u < total; u += gridDim.x) {
       const Unit un = unit_of(p, u);
       if (un.n == 0) continue;
-      if (lane == 0 && ok) {
+      if constexpr (kPaged<P>) {
+        // keys by pages, a lane a box: the whole warp walks the tiles, and a tile's pages are looked up
+        // while the one before it waits for its stage
+        if (lane == 0 && ok && kv == 0) {
+          const uint32_t qb = nq % kQBufs;
+          ok = !*abort_flag && mbar_wait(&bars[kQEmpty + qb], ((nq / kQBufs) & 1u) ^ 1u);
+          if (ok) {
+            mbar_arrive_expect_tx(&bars[kQFull + qb], static_cast<uint32_t>(un.rows) * 256u);
+            tma_load_5d(sQ + qb * kQTile, &tm.qo, &bars[kQFull + qb], 0, 0, un.h, un.t0, un.b0);
+            tma_load_5d(sQ + qb * kQTile + kQBox, &tm.qo, &bars[kQFull + qb], 64, 0, un.h, un.t0, un.b0);
+            issued[2][qb] = ++nq;
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, static_cast<int>(ok), 0);
+        int next = page_of(p, un, un.o0 * kKeys, lane);
+        for (int j = 0; ok && j < un.n; ++j) {
+          const uint32_t tt = t + j, st = tt % kSt;
+          const int key0 = (un.o0 + j) * kKeys, id = next;
+          if (j + 1 < un.n) next = page_of(p, un, key0 + kKeys, lane);
+          ok = __all_sync(0xffffffffu, mbar_wait(&empty[st], ((tt / kSt) & 1u) ^ 1u));
+          if (!ok) break;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&full[st], kTile);
+            issued[kv][st] = tt + 1;
+          }
+          __syncwarp();
+          load_pages(p, own_map, tiles + st * kTile, &full[st], un.h, key0, id, lane);
+        }
+        if (!ok && lane == 0) give_up(kErrTimeoutProducer);
+        __syncwarp();
+      } else if (lane == 0 && ok) {
         if (kv == 0) {
           const uint32_t qb = nq % kQBufs;
           ok = !*abort_flag && mbar_wait(&bars[kQEmpty + qb], ((nq / kQBufs) & 1u) ^ 1u);
@@ -424,8 +454,8 @@ __global__ void __launch_bounds__(Cfg<Q8>::kThreads, 1)
     for (int u = blockIdx.x; u < total; u += gridDim.x) {
       const Unit un = unit_of(p, u);
       if (un.n == 0) continue;
-      const int lim16 = own_lim(p, un.len, un.t0 + tok16);
-      const int lim_least = own_lim(p, un.len, un.t0);
+      const int lim16 = own_lim(p, un.len, un.t0 + tok16, un.tq);
+      const int lim_least = own_lim(p, un.len, un.t0, un.tq);
       if (lane < kR) ex.lim[sw][lane] = lim16;
       __syncwarp();
       float m_used = -INFINITY;
@@ -665,21 +695,21 @@ __global__ void __launch_bounds__(Cfg<Q8>::kThreads, 1)
   }
 }
 
-template <bool BF16, bool Q8>
-cudaError_t launch_as(const Maps& tm, const Maps8& t8, const Params& p, float scale_log2, int sms, cudaStream_t stream) {
+template <bool BF16, bool Q8, typename P>
+cudaError_t launch_as(const Maps& tm, const Maps8& t8, const P& p, float scale_log2, int sms, cudaStream_t stream) {
   static std::atomic<unsigned long long> attr_done{0}, attr_done_join{0};
   constexpr int smem = smem_bytes<Q8>();
   constexpr int threads = Cfg<Q8>::kThreads;
   if (p.pl.join) {
-    const cudaError_t e = ensure_smem_limit(prefix_attn_few<BF16, Q8, true>, smem, attr_done_join);
+    const cudaError_t e = ensure_smem_limit(prefix_attn_few<BF16, Q8, true, P>, smem, attr_done_join);
     if (e != cudaSuccess) return e;
-    return launch_clusters(prefix_attn_few<BF16, Q8, true>, p.pl.nch, dim3(p.pl.units), dim3(threads), smem, stream, tm,
-                           t8, p, scale_log2);
+    return launch_clusters(prefix_attn_few<BF16, Q8, true, P>, p.pl.nch, dim3(p.pl.units), dim3(threads), smem, stream,
+                           tm, t8, p, scale_log2);
   }
-  const cudaError_t e = ensure_smem_limit(prefix_attn_few<BF16, Q8, false>, smem, attr_done);
+  const cudaError_t e = ensure_smem_limit(prefix_attn_few<BF16, Q8, false, P>, smem, attr_done);
   if (e != cudaSuccess) return e;
   const int grid = p.pl.units < sms ? p.pl.units : sms;
-  return launch_dependent(prefix_attn_few<BF16, Q8, false>, dim3(grid), dim3(threads), smem, stream, tm, t8, p,
+  return launch_dependent(prefix_attn_few<BF16, Q8, false, P>, dim3(grid), dim3(threads), smem, stream, tm, t8, p,
                           scale_log2);
 }
 
@@ -692,6 +722,12 @@ cudaError_t pa::launch_few(const Maps& tm, const Maps8* t8, const Params& p, boo
     return bf16 ? launch_as<true, true>(tm, *t8, p, scale_log2, sms, s)
                 : launch_as<false, true>(tm, *t8, p, scale_log2, sms, s);
   }
+  return bf16 ? launch_as<true, false>(tm, none, p, scale_log2, sms, s)
+              : launch_as<false, false>(tm, none, p, scale_log2, sms, s);
+}
+
+cudaError_t pa::launch_few(const Maps& tm, const PagedParams& p, bool bf16, float scale_log2, int sms, cudaStream_t s) {
+  static const Maps8 none{};
   return bf16 ? launch_as<true, false>(tm, none, p, scale_log2, sms, s)
               : launch_as<false, false>(tm, none, p, scale_log2, sms, s);
 }

@@ -620,6 +620,99 @@ typedef struct qi_add_rmsnorm {
 } qi_add_rmsnorm;
 qi_status qi_add_rmsnorm_mxfp8(const qi_add_rmsnorm* args, qi_stream_t stream);
 
+/* ------------------------------------------------------------------ sequences in pages
+ *
+ * Between the projection and attention, and attention over a cache whose sequences grow and
+ * end at different times: K and V lie in pages of page_rows rows, a power of two from 16 to
+ * 65536, and row i of sequence b is row i % page_rows of page table[b][i / page_rows]. The
+ * conventions of the section above hold: no handle, nothing allocated, everything that says
+ * how long a sequence is read when the kernels run, calls in flight on any streams as long
+ * as no two that overlap share an output or a workspace. */
+
+/* RMSNorm of every head, rotation by positions, and the store of Q, K and V in 16 bits: for row
+ * t of sequence b (t < lens[b]; NULL: all T), every head of q and k, with y = x / sqrt(mean(x^2)
+ * + eps) * gain over its 128 values (gain q_w or k_w [128], fp32 if w_f32, else bf16 bits; 1 + it
+ * if plus_one; a NULL gain: no norm, y = x), and for pair c < C = pairs[0] + .. + pairs[axes - 1]
+ * with the dims (i, j) = (2c, 2c + 1), or (c, c + C) with `halves` (C a multiple of 8 then):
+ *   out_i = y_i cos a - y_j sin a,   out_j = y_j cos a + y_i sin a,   a = 2 pi pos turns[c] / 2^64,
+ * the other dims out = y; v is only stored. fp32 throughout (the squares of a head have to stay
+ * finite in it), rounded once to dtype. The pairs of the axes follow one another; pos is int32 [B, T,
+ * axes], the token's position on each; NULL: start[b] + t on all (start NULL: 0). The angle is exact
+ * modulo a circle at any position, so it differs from that of qi_rope_tables' rows, which round it to
+ * fp32, by up to 2^-23 of itself. turns: int64 device array [C], 2^64ths of a circle a position, modulo 2^64.
+ *
+ * q, k, v: [B, T, Hq or Hkv or Hkv, 128] of in_dtype (dtype, or QI_DT_F32); any of them may be
+ * NULL and is passed over. Outputs of dtype (QI_DT_F16 or QI_DT_BF16), 16-byte aligned, strides
+ * positive multiples of 16 bytes: q_out [B, T, Hq, 128], which may be q itself; k_out and v_out
+ * likewise, or, with a table, the pages [pages, page_rows, Hkv, 128] (page stride in `batch`): row t
+ * goes to cache row start[b] + t. Rows that the table of table_width pages a sequence (rows table_stride
+ * apart) does not reach, and page numbers outside 0 .. pages - 1, are passed over: K and V of such a
+ * row are not written, its Q is. No two rows may go to one place. Rows at or past lens[b] are neither
+ * read nor written.
+ * Errors: INVALID_ARG (NULL, dtype, alignment, strides, eps), SHAPE (B, T < 1, B > 65535, T > 2^24, heads,
+ * B T (Hq + 2 Hkv) >= 2^31, axes, pairs, page_rows, table_width), CUDA. */
+typedef struct qi_qk_rope {
+  const void* q;
+  const void* k;
+  const void* v;
+  void* q_out;
+  void* k_out;
+  void* v_out;
+  const void* q_w;
+  const void* k_w;
+  const int* pos;
+  const int64_t* turns;
+  const int* start;
+  const int* lens;
+  const int* table;
+  int plus_one;
+  float eps;
+  qi_strides q_stride, k_stride, v_stride, q_out_stride, k_out_stride, v_out_stride;
+  long long table_stride;
+  int in_dtype, dtype, w_f32, B, T, Hq, Hkv, axes, pairs[4], halves, pages, page_rows, table_width;
+} qi_qk_rope;
+qi_status qi_qk_norm_rope(const qi_qk_rope* args, qi_stream_t stream);
+
+/* Attention of a chunk of new tokens over a cache in pages: a token in decoding, drafted tokens, a
+ * piece of a prompt, an image behind its prompt. For sequence b, query row t < q_len[b] and query
+ * head hq, with key head hq / (Hq / Hkv): o[b,t,hq] = softmax over j < lim of scale q[b,t,hq].key_j,
+ * times value_j, over rows j of the sequence's pages, lim = kv_len[b], or with `causal` kv_len[b] -
+ * q_len[b] + t + 1 (the new tokens are the cache's last rows; the last one sees them all), each
+ * clamped to 0 .. kv_len[b]. A row that sees no key is zero. kv_len (device int32 [B]) is clamped to
+ * 0 .. max_len, q_len (device int32 [B], NULL: all T) to 0 .. T, both read when the kernels run; rows
+ * of q at or past q_len[b] may hold anything, those of o stay as they are. max_len, at most
+ * table_width * page_rows, is what the work is cut by: the nearer to the longest kv_len, the better.
+ *
+ * k, v: the pages [pages, page_rows, Hkv, 128] (page stride in `batch`; heads may lie outside
+ * rows); table: device int32 [B, table_width], rows table_stride apart, of which the first
+ * ceil(kv_len[b] / page_rows) entries are read. A page number outside 0 .. pages - 1 stands for a page
+ * of zeros. Rows of a page behind the sequence's last may hold anything, rows before it must be
+ * finite. A page may serve several sequences. q, o [B, T, Hq, 128] as for qi_prefix_attention, whose
+ * types, roundings and rules for ws and status hold here (NULL status: the same word, told by
+ * qi_prefix_attention_check). Results do not depend on what the other sequences hold, and repeat bit for bit.
+ * Errors: INVALID_ARG (NULL, dtype, alignment, strides, scale not positive, workspace), SHAPE (B, T,
+ * Hkv < 1, Hq % Hkv != 0, Hq / Hkv > 128, B or Hkv > 65535, T or max_len > 2^24, B T Hq >= 2^31,
+ * page_rows, pages, table_width, max_len), CUDA. */
+typedef struct qi_paged_attn {
+  const void* q;
+  const void* k;
+  const void* v;
+  void* o;
+  const int* table;
+  const int* kv_len;
+  const int* q_len;
+  void* ws;
+  int* status;
+  int causal;
+  float scale;
+  size_t ws_bytes;
+  qi_strides q_stride, k_stride, v_stride, o_stride;
+  long long table_stride;
+  int dtype, B, T, Hq, Hkv, pages, page_rows, table_width, max_len;
+} qi_paged_attn;
+size_t qi_paged_attention_workspace(const qi_paged_attn* args); /* 0 also for bad sizes */
+qi_status qi_paged_attention(const qi_paged_attn* args, qi_stream_t stream);
+
 /* Message for the calling thread's last failed call ("" if none). */
 const char* qi_last_error(void);
 

@@ -14,6 +14,8 @@ attention  block-causal attention: masked dense, two-segment, brute force
 dit        timestep embedding, shared modulation, block, full DiT, output head
 fbcache    first-block cache ("Fast mode") around the DiT pass (MLX page)
 mx         MXFP8 block-scaled operands and the block with MXFP8 GEMMs
+batch      batches from one prompt: attention over a shared prefix, residual norm
+paged      sequences in pages: norm and rotation of heads, attention over pages
 
 Everything is numpy float32 (bf16 weights widened exactly); the brute-force
 checkers use Python float64 loops on tiny shapes.
