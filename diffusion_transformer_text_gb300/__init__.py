@@ -765,8 +765,8 @@ def qk_norm_rope(q, k, v=None, rope: Rope | None = None, pos=None, q_w=None, k_w
     of one type, the last dimension contiguous, other strides positive multiples of 16 bytes; any of them may be
     None. q_w, k_w [128] bfloat16 or float32: gains of the norm (1 + w with plus_one); None: no norm. rope:
     the rotation (None: none) at pos, int32 [B, T, axes] (or [B, T] with one axis), or at start[b] + t on
-    every axis. dtype of the outputs: float16 or bfloat16; default that of q, bfloat16 for float32.
-    out: (q_out, k_out, v_out), any of them None; q_out may be q. cache, table: K and V go to the cache's rows
+    every axis. dtype of the outputs: float16 or bfloat16; default that of the cache or of `out`, else that
+    of q, bfloat16 for float32. out: (q_out, k_out, v_out), any of them None; q_out may be q. cache, table: K and V go to the cache's rows
     start[b] + t instead, rows that the table does not reach or whose page number is none passed over. start
     (None: 0) and lens (rows of each sequence; None: T), int32 [B] on the device; rows at or past lens[b] are
     neither read nor written (and are zero in outputs that are made here). stream: default the current one of q's
@@ -780,10 +780,11 @@ def qk_norm_rope(q, k, v=None, rope: Rope | None = None, pos=None, q_w=None, k_w
         with _elsewhere(x, stream, (q, k, v, rope and rope.turns, pos, q_w, k_w, *(out or ()), *(cache or ()), table,
                                     start, lens)):
             return qk_norm_rope(q, k, v, rope, pos, q_w, k_w, plus_one, eps, dtype, out, cache, table, start, lens)
-    if dtype is None:
-        dtype = torch.bfloat16 if x.dtype == torch.float32 else x.dtype
     outs = (None, None, None) if out is None else out
     qo, ko, vo = outs
+    if dtype is None:
+        like = cache.k if cache is not None else qo if qo is not None else ko if ko is not None else vo
+        dtype = like.dtype if like is not None else torch.bfloat16 if x.dtype == torch.float32 else x.dtype
     key = (_layout(q), _layout(k), _layout(v), None if rope is None else (_layout(rope.turns), rope.pairs, rope.halves),
            _layout(pos), _layout(q_w), _layout(k_w), dtype, _layout(qo), _layout(ko), _layout(vo),
            None if cache is None else (_layout(cache.k), _layout(cache.v)), _layout(table), _layout(start), _layout(lens))
