@@ -768,8 +768,8 @@ def qk_norm_rope(q, k, v=None, rope: Rope | None = None, pos=None, q_w=None, k_w
     every axis. dtype of the outputs: float16 or bfloat16; default that of the cache or of `out`, else that
     of q, bfloat16 for float32. out: (q_out, k_out, v_out), any of them None; q_out may be q. cache, table: K and V go to the cache's rows
     start[b] + t instead, rows that the table does not reach or whose page number is none passed over. start
-    (None: 0) and lens (rows of each sequence; None: T), int32 [B] on the device; rows at or past lens[b] are
-    neither read nor written (and are zero in outputs that are made here). stream: default the current one of q's
+    (None: 0) and lens (rows of each sequence; None: T), int32 [B] on the device; rows at or past lens[b] may
+    hold anything and are not written (and are zero in outputs that are made here). stream: default the current one of q's
     device. Returns (q_out, k_out, v_out), None for what was not given or went to the cache. No gradients."""
     import torch
     x = q if q is not None else k if k is not None else v

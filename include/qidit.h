@@ -647,8 +647,8 @@ qi_status qi_add_rmsnorm_mxfp8(const qi_add_rmsnorm* args, qi_stream_t stream);
  * likewise, or, with a table, the pages [pages, page_rows, Hkv, 128] (page stride in `batch`): row t
  * goes to cache row start[b] + t. Rows that the table of table_width pages a sequence (rows table_stride
  * apart) does not reach, and page numbers outside 0 .. pages - 1, are passed over: K and V of such a
- * row are not written, its Q is. No two rows may go to one place. Rows at or past lens[b] are neither
- * read nor written.
+ * row are not written, its Q is. No two rows may go to one place. Rows at or past lens[b] may hold
+ * anything and are not written.
  * Errors: INVALID_ARG (NULL, dtype, alignment, strides, eps), SHAPE (B, T < 1, B > 65535, T > 2^24, heads,
  * B T (Hq + 2 Hkv) >= 2^31, axes, pairs, page_rows, table_width), CUDA. */
 typedef struct qi_qk_rope {
