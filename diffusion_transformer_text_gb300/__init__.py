@@ -833,7 +833,7 @@ def _check_paged(key, q, cache, table, kv_len, q_len, max_len, causal, out, stat
     longest = min(width * rows, 1 << 24) if max_len is None else max_len
     tail = (*qs, *ks, *vs, *os_, stride, dt, B, T, Hq, Hkv, pages, rows, width, longest)
     need = lib().qi_paged_attention_workspace(
-        _PAGED_HEAD.pack(*[0] * 9, 1 if causal else 0, 1.0) + _PAGED_TAIL.pack(0, *tail))
+        _PAGED_HEAD.pack(*[0] * 6, 0 if q_len is None else 1, 0, 0, 1 if causal else 0, 1.0) + _PAGED_TAIL.pack(0, *tail))
     return _remember(_paged_layouts, key, (_PAGED_TAIL.pack(need, *tail), need))
 
 

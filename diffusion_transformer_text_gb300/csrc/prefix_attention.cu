@@ -118,9 +118,12 @@ __device__ __forceinline__ uint32_t bar_count(int i) {
   if ((i >= kPFull && i < kPFull + 4) || i == kOEmpty || i == kLFree) return 4;
   return 1;
 }
-constexpr int kSmem = (kQBufs + kKStages + kVStages) * kTile + 1024 + kNumBars * 8 + 16 + 2 * 2 * kRows * 4 + 16 +
-                      kMessages * static_cast<int>(sizeof(Message));
-static_assert(kSmem <= 227 * 1024, "shared memory over the per-block limit");
+constexpr int kSmemBase = (kQBufs + kKStages + kVStages) * kTile + 1024 + kNumBars * 8 + 16 + 2 * 2 * kRows * 4 + 16 +
+                          kMessages * static_cast<int>(sizeof(Message));
+using FlowFull = Flow<2048>;
+template <typename P>
+constexpr int kSmem = kSmemBase + (kFlow<P> ? static_cast<int>(sizeof(FlowFull)) : 0);
+static_assert(kSmem<FlowParams> <= 227 * 1024 && kThreads >= kFlowThreads, "shared memory over the per-block limit");
 
 template <bool BF16, bool JOIN, typename P>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -141,7 +144,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const int total = p.pl.units;
+  FlowFull* pieces = reinterpret_cast<FlowFull*>(messages + kMessages);
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kNumBars; ++i) mbar_init(&bars[i], bar_count(i));
@@ -168,6 +171,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tmem_slot;
   grid_dep_wait();
   grid_dep_launch_dependents();
+  if constexpr (kFlow<P>) {
+    flow_pieces(p, *pieces);
+  }
 
   if (warp < 4) {
     regs_release<kRegsLow>();
@@ -177,8 +183,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // only stops its waits and loads, so the warp meets at every cleared tile.
       uint32_t t = 0;
       bool ok = true;
-      for (int u = blockIdx.x; u < total; u += gridDim.x) {
-        const Unit un = unit_of(p, u);
+      for (Walk<P, FlowFull> w(p, pieces); w.more(p); w.step(p)) {
+        const Unit un = w.unit(p);
         if constexpr (kPaged<P>) {
           // by pages, a lane a box: a tile's pages are looked up while the one before it waits for its stage
           ok = __shfl_sync(0xffffffffu, static_cast<int>(ok), 0);
@@ -256,8 +262,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t t = 0;
       uint32_t ku = 0, cleared = 0;
       bool ok = true;
-      for (int u = blockIdx.x; ok && u < total; u += gridDim.x) {
-        const Unit un = unit_of(p, u);
+      for (Walk<P, FlowFull> w(p, pieces); ok && w.more(p); w.step(p)) {
+        const Unit un = w.unit(p);
         if (un.n == 0) continue;
         ok = __all_sync(0xffffffffu, !*abort_flag);
         if (!ok) break;
@@ -307,8 +313,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t t = 0;
       uint32_t nq = 0, nm = 0;
       bool ok = true;
-      for (int u = blockIdx.x; ok && u < total; u += gridDim.x) {
-        const Unit un = unit_of(p, u);
+      for (Walk<P, FlowFull> w(p, pieces); ok && w.more(p); w.step(p)) {
+        const Unit un = w.unit(p);
+        const int u = w.u;
 if constexpr (kPaged<P>) {
           const uint32_t mb = nm % kMessages, qb = nq % kQBufs;
           ok = __all_sync(0xffffffffu, !*abort_flag && mbar_wait(&bars[kUEmpty + mb], ((nm / kMessages) & 1u) ^ 1u));
@@ -384,6 +391,14 @@ if constexpr (kPaged<P>) {
         }
         }
       }
+      if constexpr (kFlow<P>) {  // no more units
+        const uint32_t mb = nm % kMessages;
+        ok = __all_sync(0xffffffffu, ok && !*abort_flag && mbar_wait(&bars[kUEmpty + mb], ((nm / kMessages) & 1u) ^ 1u));
+        if (ok && lane == 0) {
+          messages[mb].n = -1;
+          mbar_arrive(&bars[kUFull + mb]);
+        }
+      }
       for (uint32_t i = t > kKStages ? t - kKStages : 0; lane == 0 && i < t; ++i)
         if (!mbar_wait(&bars[kKFull + i % kKStages], (i / kKStages) & 1u)) report_error(p.err, kErrTimeoutDrain);
       for (uint32_t i = nq > kQBufs ? nq - kQBufs : 0; lane == 0 && i < nq; ++i)
@@ -397,8 +412,8 @@ if constexpr (kPaged<P>) {
       uint32_t t = 0;
       uint32_t ku = 0;
       bool ok = true;
-      for (int u = blockIdx.x; ok && u < total; u += gridDim.x) {
-        const Unit un = unit_of(p, u);
+      for (Walk<P, FlowFull> w(p, pieces); ok && w.more(p); w.step(p)) {
+        const Unit un = w.unit(p);
         if (un.n == 0) continue;
         const uint32_t qb = ku % kQBufs;
         ok = __all_sync(0xffffffffu, !*abort_flag && mbar_wait(&bars[kQFull + qb], (ku / kQBufs) & 1u));
@@ -451,11 +466,12 @@ if constexpr (kPaged<P>) {
     uint32_t t = 0;
     uint32_t ku = 0, km = 0;
     bool ok = true;
-    for (int u = blockIdx.x; u < total; u += gridDim.x, ++km) {
+    for (int u = blockIdx.x; kFlow<P> || u < p.pl.units; u += gridDim.x, ++km) {
       const uint32_t mb = km % kMessages;
       ok = __all_sync(0xffffffffu, mbar_wait(&bars[kUFull + mb], (km / kMessages) & 1u));
       if (!ok) break;
       const Message un = messages[mb];
+      if (kFlow<P> && un.n < 0) break;
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars[kUEmpty + mb]);
       if (un.n == 0) continue;
@@ -605,11 +621,13 @@ if constexpr (kPaged<P>) {
     const int g = rit - tok * p.pl.G;
     bool ok = true;
     uint32_t ku = 0, km = 0;
-    for (int u = blockIdx.x; ok && u < total; u += gridDim.x, ++km) {
+    for (int u = blockIdx.x; ok && (kFlow<P> || u < p.pl.units); u += gridDim.x, ++km) {
       const uint32_t mb = km % kMessages;
       ok = __all_sync(0xffffffffu, mbar_wait(&bars[kUFull + mb], (km / kMessages) & 1u));
       if (!ok) break;
       const Message un = messages[mb];
+      if (kFlow<P> && un.n < 0) break;
+      const bool part = kFlow<P> ? un.slot >= 0 : p.pl.split;  // (unless JOIN) the rows are not all the keys'
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars[kUEmpty + mb]);
       // where the row goes: token and sequence (a prefix block runs over sequences)
@@ -624,7 +642,7 @@ if constexpr (kPaged<P>) {
       if (un.n == 0) {
         if (JOIN) *reinterpret_cast<float2*>(smem + kJoinMl + rit * 8) = make_float2(-INFINITY, 0.f);
         // no key at all: a joint unit that is its row's only one writes zeros
-        if (!JOIN && !p.pl.split && mine) {
+        if (!JOIN && !part && mine) {
 #pragma unroll
           for (int i = 0; i < 16; ++i) reinterpret_cast<uint4*>(orow)[i] = make_uint4(0u, 0u, 0u, 0u);
         }
@@ -642,9 +660,9 @@ if constexpr (kPaged<P>) {
       const float a0 = mm == -INFINITY ? 1.f : fast_exp2(m0 - mm);
       const float a1 = mm == -INFINITY ? 1.f : fast_exp2(m1 - mm);
       const float den = l0 * a0 + l1 * a1;
-      const float inv = JOIN || p.pl.split ? 1.f : (den == 0.f ? 0.f : 1.f / den);
+      const float inv = JOIN || part ? 1.f : (den == 0.f ? 0.f : 1.f / den);
       const float w0 = a0 * inv, w1 = a1 * inv;
-      if (!JOIN && p.pl.split && mine) p.ml[un.slot + rit] = make_float2(mm, den);
+      if (!JOIN && part && mine) p.ml[un.slot + rit] = make_float2(mm, den);
       ok = __all_sync(0xffffffffu, mbar_wait(&bars[kOFull], ku & 1u));
       if (!ok) break;
       if (quarter * 32 >= un.rows) {  // none of the warp's rows are the block's
@@ -689,7 +707,7 @@ if constexpr (kPaged<P>) {
             float4* d = reinterpret_cast<float4*>(smem + (rit * kJoinPitch + c * 16) * 4);
 #pragma unroll
             for (int i = 0; i < 4; ++i) d[i] = make_float4(ov[4 * i], ov[4 * i + 1], ov[4 * i + 2], ov[4 * i + 3]);
-          } else if (p.pl.split) {
+          } else if (part) {
             float* d = p.part + (un.slot + rit) * kHeadDim + c * 16;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -821,6 +839,96 @@ __global__ void __launch_bounds__(kMergeWarps * 32) merge_partials(const __grid_
       make_uint2(pack16<BF16>(acc.x * inv, acc.y * inv), pack16<BF16>(acc.z * inv, acc.w * inv));
 }
 
+// Joins the parts of a block that was cut (see Flow): block x has the one that piece x took over and ended.
+// A warp has ROWS rows, their loads in flight together, and W warps a row where parts are many: warp w takes
+// parts w, w + W, .., and the W sums are added in order.
+template <bool BF16, int ROWS, int W>
+__global__ void __launch_bounds__(kMergeWarps * 32) merge_flow(const __grid_constant__ FlowParams p) {
+  __shared__ float4 sacc[W > 1 ? kMergeWarps : 1][32];
+  __shared__ float sden[kMergeWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, w = warp % W, last = static_cast<int>(blockIdx.x);
+  const int r0 = (static_cast<int>(blockIdx.y) * (kMergeWarps / W) + warp / W) * ROWS;
+  grid_dep_wait();
+  grid_dep_launch_dependents();
+  const int4 end = p.rec[2 * last];
+  if (end.x < 0 || !end.z) return;  // (the whole block)
+  const int first = end.w, parts = last - first + 1;
+  // part k: what piece `first` left, then what piece first + k took over (none, if it is empty)
+  const auto slot = [&](int k) {
+    return (2ll * (first + k) + (k == 0 ? 1 : 0)) * p.pl.rows_o;
+  };
+  const auto used = [&](int k) {
+    if (k == 0) return true;
+    const int4 x = p.rec[2 * (first + k)];
+    return x.x == end.x && x.y == end.y;
+  };
+  const int b = quot(p.d_nqb, end.x), t0 = (end.x - b * p.pl.nqb) * p.pl.tb, tq = query_rows(p, b);
+  float m[ROWS], den[ROWS];
+  float4 acc[ROWS];
+#pragma unroll
+  for (int i = 0; i < ROWS; ++i) {
+    m[i] = -INFINITY;
+    den[i] = 0.f;
+    acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  for (int k = lane; k < parts; k += 32) {
+    const bool u = used(k);
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i)
+      if (r0 + i < p.pl.rows_o) {
+        const float x = p.ml[slot(k) + r0 + i].x;  // (what an empty piece's holds is not used)
+        m[i] = u ? fmaxf(m[i], x) : m[i];
+      }
+  }
+#pragma unroll
+  for (int i = 0; i < ROWS; ++i)
+#pragma unroll
+    for (int d = 16; d; d >>= 1) m[i] = fmaxf(m[i], __shfl_xor_sync(0xffffffffu, m[i], d));
+#pragma unroll 2
+  for (int k = w; k < parts; k += W) {
+    if (!used(k)) continue;
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+      if (r0 + i >= p.pl.rows_o) break;
+      const long long s = slot(k) + r0 + i;
+      const float2 ml = p.ml[s];
+      const float4 v = reinterpret_cast<const float4*>(p.part + s * kHeadDim)[lane];
+      // (a part in which the row sees no key; m = -inf with another sum is a row of NaN scores, which stays one)
+      const bool none = ml.x == -INFINITY && ml.y == 0.f;
+      const float a = m[i] == -INFINITY ? 1.f : fast_exp2(ml.x - m[i]);
+      den[i] += none ? 0.f : ml.y * a;
+      acc[i].x += none ? 0.f : v.x * a;
+      acc[i].y += none ? 0.f : v.y * a;
+      acc[i].z += none ? 0.f : v.z * a;
+      acc[i].w += none ? 0.f : v.w * a;
+    }
+  }
+  if (W > 1) {  // (ROWS is 1)
+    sacc[warp][lane] = acc[0];
+    if (lane == 0) sden[warp] = den[0];
+    __syncthreads();
+    if (w != 0) return;
+#pragma unroll
+    for (int i = 1; i < W; ++i) {
+      const float4 v = sacc[warp + i][lane];
+      den[0] += sden[warp + i];
+      acc[0].x += v.x;
+      acc[0].y += v.y;
+      acc[0].z += v.z;
+      acc[0].w += v.w;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < ROWS; ++i) {
+    const int r = r0 + i, tok = quot(p.d_G, r), t = t0 + tok;
+    if (r >= p.pl.rows_o || t >= tq) break;
+    const float inv = den[i] == 0.f ? 0.f : 1.f / den[i];
+    uint16_t* orow = p.o + b * p.ob + t * p.orow + static_cast<long long>(end.y * p.pl.G + r - tok * p.pl.G) * p.oh;
+    reinterpret_cast<uint2*>(orow)[lane] = make_uint2(pack16<BF16>(acc[i].x * inv, acc[i].y * inv),
+                                                      pack16<BF16>(acc[i].z * inv, acc[i].w * inv));
+  }
+}
+
 // ---------------------------------------------------------------- host
 
 qi_status op_fail(qi_status st, const char* fmt, ...) {
@@ -867,9 +975,14 @@ constexpr float kConvert = 0.5f, kConvertStart = 2.5f;
 constexpr float kStart = 3.f;      // of a kernel whose CTAs walk the units
 constexpr float kJoinTiles = 2.6f, kJoinRow = 1.f / 32;  // start of a CTA in a cluster and its join; each row
 constexpr long long kL2Half = 64ll << 20;
+constexpr int kFullCost = 2, kFewCost = 2;  // of a unit, in tiles, where pieces are cut
+constexpr float kFlowStart = 5.f;           // cutting them, and a second launch
+constexpr float kPiece = 128.f;             // tiles of a piece where blocks share keys
+constexpr float kEvenFrom = 48.f;           // tiles a CTA from which unequal chunks are worth cutting
+constexpr int kFewTiles = 4;                // so few in a unit, and their number does not matter
 struct Sizes {
   int B, T, Hq, Hkv, P, S, causal;
-  bool from8;
+  bool from8, paged, ragged;  // ragged: of a cache in pages, whose chunks have lengths of their own
 };
 Plan make_plan(const Sizes& z, int sms) {
   Plan a{};
@@ -894,6 +1007,9 @@ Plan make_plan(const Sizes& z, int sms) {
     }
   };
   const float convert = z.from8 && z.P > 0 ? kConvertStart + kConvert * static_cast<float>(z.P) * z.Hkv * kHeadDim / (1 << 20) : 0.f;
+const bool even =
+      z.paged && (z.T <= kRows / a.G ||
+                  (z.ragged && static_cast<float>(ceil_div(z.T, kRows / a.G)) * z.B * z.Hkv * (a.ot + kFullCost) > kEvenFrom * sms));
   // joint units, every number of chunks that keeps the grid within a few waves
   const auto joint = [&](Plan c, Rate r, bool always_split, float more) {
     const int n = c.pt + c.ot;
@@ -901,6 +1017,7 @@ Plan make_plan(const Sizes& z, int sms) {
     const float each = (c.pt * (z.from8 ? r.tile8 : r.tile) + c.ot * r.tile) / n;
     for (int nch = 1; nch <= n; ++nch) {
       if (nch > 1 && blocks * nch > 4ll * sms) break;  // (at most 4 x SMs rounds of this loop)
+      if (even && (nch > 1 || (blocks > sms && n > kFewTiles))) break;
       c.ct = ceil_div(n, nch);
       if (ceil_div(n, c.ct) != nch) continue;
       c.nch = nch;
@@ -928,6 +1045,7 @@ Plan make_plan(const Sizes& z, int sms) {
       c.join = 1;
       const int slots = nch <= 2 ? sms : nch <= 6 ? sms * 9 / 10 : sms * 2 / 3;
       const float waves = static_cast<float>((blocks * nch + slots - 1) / slots);
+      if (even && waves > 1.f) continue;
       const float cost = waves * (c.ct * each + r.of(c.rows_o) + kJoinTiles + kJoinRow * static_cast<float>(c.rows_o)) + more;
       if (cost < best_cost) {
         best_cost = cost;
@@ -966,10 +1084,30 @@ Plan make_plan(const Sizes& z, int sms) {
       }
     }
   };
+  // Even pieces of a cache in pages, where the sequences' shares of the work are known on the device alone
+  // (single tokens, chunks of lengths of their own), in rounds of about kPiece tiles where row blocks share keys.
+  // Chunks of one length keep units of equal length: CTAs that walk neighbouring row blocks from the same
+  // key on meet in the L2, and pieces do not (3 x 2461 causal rows, 16 key heads: 139 us, in pieces 168).
+  const auto flow = [&](Plan c, Rate r) {
+    const long long blocks = static_cast<long long>(z.B) * c.nqb * z.Hkv;
+    if (!even || blocks > INT_MAX) return;
+    c.nch = c.ct = 1;
+    c.cost = c.few ? kFewCost : kFullCost;
+    const float each = static_cast<float>(blocks) * (c.ot * r.tile + r.of(c.rows_o)) / sms;
+    const float cost = kStart + kFlowStart + each + kMergeTiles;
+    if (cost < best_cost) {
+      best_cost = cost;
+      c.units = blocks * c.ot < sms ? static_cast<int>(blocks * c.ot) : sms;
+      c.flow = c.nqb > 1 ? static_cast<int>(each / kPiece + 0.5f) : 1;
+      c.flow = c.flow < 1 ? 1 : c.flow > kMostRounds ? kMostRounds : c.flow;
+      best = c;
+    }
+  };
   Plan c = a;
   rows_of(c, kRows, false);
+  flow(c, kFullRate);
   joint(c, kFullRate, false, convert);
-  joined(c, kFullRate, 2, convert);
+  joined(c, kFullRate, z.paged ? 1 : 2, convert);
   const int rows_seq = z.T * a.G;
   // packed: only if two or more sequences' rows fit one block
   if (z.P > 0 && z.B > 1 && 2 * rows_seq <= kRows) {
@@ -981,7 +1119,10 @@ Plan make_plan(const Sizes& z, int sms) {
     c.few = 1;
     c.per = 2;
     rows_of(c, kFewRows, false);
-    joint(c, kFewRate, true, 0.f);
+    if (!z.paged) joint(c, kFewRate, true, 0.f);
+    c.per = 1;
+    flow(c, kFewRate);
+    c.per = 2;
     joined(c, kFewRate, 1, 0.f);
     if (z.P > 0 && z.B > 1) {
       rows_of(c, kFewRows, true);
@@ -1001,24 +1142,25 @@ Plan plan_for(const Sizes& z, int sms) {
   };
   static thread_local Entry kept[16];
   unsigned h = static_cast<unsigned>(z.B);
-  for (int v : {z.T, z.Hq, z.Hkv, z.P, z.S, z.causal * 2 + (z.from8 ? 1 : 0), sms})
+  for (int v : {z.T, z.Hq, z.Hkv, z.P, z.S, z.causal * 16 + (z.from8 ? 1 : 0) + (z.paged ? 2 : 0) + (z.ragged ? 8 : 0), sms})
     h = h * 0x9E3779B1u + static_cast<unsigned>(v);
   Entry& e = kept[(h ^ (h >> 16)) & 15u];
   if (e.sms != sms || e.z.B != z.B || e.z.T != z.T || e.z.Hq != z.Hq || e.z.Hkv != z.Hkv || e.z.P != z.P ||
-      e.z.S != z.S || e.z.causal != z.causal || e.z.from8 != z.from8)
+      e.z.S != z.S || e.z.causal != z.causal || e.z.from8 != z.from8 || e.z.paged != z.paged || e.z.ragged != z.ragged)
     e = Entry{z, sms, make_plan(z, sms)};
   return e.plan;
 }
 
 size_t align256(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
 size_t partial_rows(const Plan& pl) {
+  if (pl.flow) return static_cast<size_t>(pl.units) * pl.flow * 2 * pl.rows_o;
   return pl.split ? (static_cast<size_t>(pl.units_p) * pl.rows_p +
                      static_cast<size_t>(pl.units - pl.units_p) * pl.rows_o) * pl.per
                   : 0;
 }
-// workspace: the prefix in 16 bits (8-bit prefix only), partial O rows, their (max, sum)
+// workspace: the prefix in 16 bits (8-bit prefix only), partial O rows, their (max, sum), pieces' records
 struct WsLayout {
-  size_t pk, pv, part, ml, total;
+  size_t pk, pv, part, ml, rec, total;
 };
 WsLayout ws_layout(const Plan& pl, int P, int Hkv, bool from8) {
   WsLayout w{};
@@ -1028,7 +1170,8 @@ WsLayout ws_layout(const Plan& pl, int P, int Hkv, bool from8) {
   w.pv = pre;
   w.part = 2 * pre;
   w.ml = w.part + align256(rows * kHeadDim * 4);
-  w.total = w.ml + align256(rows * 8);
+  w.rec = w.ml + align256(rows * 8);
+  w.total = w.rec + (pl.flow ? align256(static_cast<size_t>(pl.units) * pl.flow * 2 * sizeof(int4)) : 0);
   return w;
 }
 
@@ -1093,27 +1236,23 @@ qi_status check_sizes(const qi_prefix_attn* a) {
 }
 
 template <bool BF16, typename P>
-cudaError_t launch(const Maps& tm, const Maps8* t8, const P& p, float scale_log2, int sms, cudaStream_t stream) {
-  cudaError_t e;
-  if (p.pl.few) {
-    if constexpr (kPaged<P>)
-      e = launch_few(tm, p, BF16, scale_log2, sms, stream);
-    else
-      e = launch_few(tm, t8, p, BF16, scale_log2, sms, stream);
-  } else {
-    static std::atomic<unsigned long long> attr_done{0}, attr_done_join{0};
-    if (p.pl.join) {
-      e = ensure_smem_limit(prefix_attn_tc<BF16, true, P>, kSmem, attr_done_join);
-      if (e != cudaSuccess) return e;
-      return launch_clusters(prefix_attn_tc<BF16, true, P>, p.pl.nch, dim3(p.pl.units), dim3(kThreads), kSmem, stream,
-                             tm, p, scale_log2);
-    }
-    e = ensure_smem_limit(prefix_attn_tc<BF16, false, P>, kSmem, attr_done);
-    if (e != cudaSuccess) return e;
-    const int grid = p.pl.units < sms ? p.pl.units : sms;
-    e = launch_dependent(prefix_attn_tc<BF16, false, P>, dim3(grid), dim3(kThreads), kSmem, stream, tm, p, scale_log2);
-  }
-  if (e != cudaSuccess || !p.pl.split) return e;
+cudaError_t launch_join(const Maps& tm, const P& p, float scale_log2, cudaStream_t stream) {
+  static std::atomic<unsigned long long> attr_done{0};
+  const cudaError_t e = ensure_smem_limit(prefix_attn_tc<BF16, true, P>, kSmem<P>, attr_done);
+  if (e != cudaSuccess) return e;
+  return launch_clusters(prefix_attn_tc<BF16, true, P>, p.pl.nch, dim3(p.pl.units), dim3(kThreads), kSmem<P>, stream, tm,
+                         p, scale_log2);
+}
+template <bool BF16, typename P>
+cudaError_t launch_walk(const Maps& tm, const P& p, float scale_log2, int grid, cudaStream_t stream) {
+  static std::atomic<unsigned long long> attr_done{0};
+  const cudaError_t e = ensure_smem_limit(prefix_attn_tc<BF16, false, P>, kSmem<P>, attr_done);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(prefix_attn_tc<BF16, false, P>, dim3(grid), dim3(kThreads), kSmem<P>, stream, tm, p, scale_log2);
+}
+
+template <bool BF16, typename P>
+cudaError_t launch_merge(const P& p, cudaStream_t stream) {
   // Warps per row: as many as its parts keep busy, unless the rows alone fill the GPU (1024
   // rows of 16 parts, with the attention before it: 31.6 us at one warp a row, 29.4 at 4 or 8)
   const long long rows = static_cast<long long>(p.B) * p.T * p.Hq;
@@ -1125,6 +1264,40 @@ cudaError_t launch(const Maps& tm, const Maps8* t8, const P& p, float scale_log2
   const long long per = kMergeWarps / w;
   return launch_dependent(kernel, dim3(static_cast<unsigned>((rows + per - 1) / per)), dim3(kMergeWarps * 32), 0, stream,
                           p);
+}
+
+template <bool BF16>
+cudaError_t launch(const Maps& tm, const Maps8* t8, const Params& p, float scale_log2, int sms, cudaStream_t stream) {
+  cudaError_t e;
+  if (p.pl.few)
+    e = launch_few(tm, t8, p, BF16, scale_log2, sms, stream);
+  else if (p.pl.join)
+    e = launch_join<BF16>(tm, p, scale_log2, stream);
+  else
+    e = launch_walk<BF16>(tm, p, scale_log2, p.pl.units < sms ? p.pl.units : sms, stream);
+  return e != cudaSuccess || !p.pl.split ? e : launch_merge<BF16>(p, stream);
+}
+
+template <bool BF16>
+cudaError_t launch_paged(const Maps& tm, const FlowParams& f, float scale_log2, int sms, cudaStream_t stream) {
+  const Plan& pl = f.pl;
+  const PagedParams& p = f;
+  if (pl.join)
+    return pl.few ? launch_few(tm, p, BF16, scale_log2, stream) : launch_join<BF16>(tm, p, scale_log2, stream);
+  if (!pl.flow) {
+    const cudaError_t e = launch_walk<BF16>(tm, p, scale_log2, pl.units < sms ? pl.units : sms, stream);
+    return e != cudaSuccess || !pl.split ? e : launch_merge<BF16>(p, stream);
+  }
+  const cudaError_t e = pl.few ? launch_few(tm, f, BF16, scale_log2, stream)
+                               : launch_walk<BF16>(tm, f, scale_log2, pl.units, stream);
+  const int pieces = pl.units * pl.flow;
+  if (e != cudaSuccess || pieces == 1) return e;
+  // few rows may have many parts, many rows have two or three
+  constexpr int kRowsEach = 4, kWarpsEach = 4;
+  const auto kernel = pl.few ? merge_flow<BF16, 1, kWarpsEach> : merge_flow<BF16, kRowsEach, 1>;
+  const int each = pl.few ? kMergeWarps / kWarpsEach : kMergeWarps * kRowsEach;
+  return launch_dependent(kernel, dim3(pieces, static_cast<unsigned>(ceil_div(pl.rows_o, each))), dim3(kMergeWarps * 32), 0,
+                          stream, f);
 }
 
 // What does not come from where the keys are
@@ -1204,7 +1377,7 @@ extern "C" size_t qi_prefix_attention_workspace(const qi_prefix_attn* a) {
   if (check_sizes(a) != QI_OK) return 0;
   const int sms = device_sms();
   if (sms <= 0) return 0;
-  const Plan pl = plan_for({a->B, a->T, a->Hq, a->Hkv, a->P, a->S, a->causal != 0, a->P > 0 && a->pk8 != nullptr}, sms);
+  const Plan pl = plan_for({a->B, a->T, a->Hq, a->Hkv, a->P, a->S, a->causal != 0, a->P > 0 && a->pk8 != nullptr, false, false}, sms);
   return ws_layout(pl, a->P, a->Hkv, a->P > 0 && a->pk8 != nullptr).total;
 }
 
@@ -1243,7 +1416,7 @@ extern "C" qi_status qi_prefix_attention(const qi_prefix_attn* a, qi_stream_t st
     return op_fail(QI_ERR_INVALID_ARG, "qi_prefix_attention: own_len and status need 4-byte alignment");
   const int sms = device_sms();
   if (sms <= 0) return op_fail(QI_ERR_CUDA, "qi_prefix_attention: no CUDA device");
-  const Plan pl = plan_for({a->B, a->T, a->Hq, a->Hkv, a->P, a->S, a->causal != 0, a->P > 0 && a->pk8 != nullptr}, sms);
+  const Plan pl = plan_for({a->B, a->T, a->Hq, a->Hkv, a->P, a->S, a->causal != 0, a->P > 0 && a->pk8 != nullptr, false, false}, sms);
   if (pl.units <= 0) return op_fail(QI_ERR_SHAPE, "qi_prefix_attention: too many rows and heads");
   const bool pre8 = a->P > 0 && from8;
   const bool convert = pre8 && !pl.few;  // the prefix goes through 16 bits in the workspace
@@ -1289,7 +1462,7 @@ extern "C" qi_status qi_prefix_attention(const qi_prefix_attn* a, qi_stream_t st
   if (a->P == 0) tm.pk = tm.k, tm.pv = tm.v;  // never loaded from
   if (a->S == 0) tm.k = tm.pk, tm.v = tm.pv;
   Params p{};
-  fill_params(&p, pl, {a->B, a->T, a->Hq, a->Hkv, a->P, a->S, a->causal != 0, false}, o);
+  fill_params(&p, pl, {a->B, a->T, a->Hq, a->Hkv, a->P, a->S, a->causal != 0, false, false, false}, o);
   p.own_len = a->S > 0 ? a->own_len : nullptr;
   p.part = reinterpret_cast<float*>(ws + w.part);
   p.ml = reinterpret_cast<float2*>(ws + w.ml);
@@ -1343,7 +1516,7 @@ qi_status check_paged(const qi_paged_attn* a) {
   return QI_OK;
 }
 Sizes paged_sizes(const qi_paged_attn* a) {
-  return {a->B, a->T, a->Hq, a->Hkv, 0, a->max_len, a->causal != 0, false};
+  return {a->B, a->T, a->Hq, a->Hkv, 0, a->max_len, a->causal != 0, false, true, a->q_len != nullptr};
 }
 
 }  // namespace
@@ -1397,7 +1570,7 @@ extern "C" qi_status qi_paged_attention(const qi_paged_attn* a, qi_stream_t stre
   tm.qp = tm.qo;  // no prefix: never loaded from
   tm.pk = tm.k;
   tm.pv = tm.v;
-  PagedParams p{};
+  FlowParams p{};
   fill_params(&p, pl, z, o);
   p.own_len = a->kv_len;
   p.q_len = a->q_len;
@@ -1415,7 +1588,10 @@ extern "C" qi_status qi_paged_attention(const qi_paged_attn* a, qi_stream_t stre
   }
   const float scale_log2 = a->scale * 1.4426950408889634f;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t e = a->dtype == QI_DT_BF16 ? launch<true>(tm, nullptr, p, scale_log2, sms, s)
-                                               : launch<false>(tm, nullptr, p, scale_log2, sms, s);
+  p.rec = reinterpret_cast<int4*>(ws + w.rec);
+  p.per_slot = ceil_div(a->B * pl.nqb, pl.few ? kFlowSlotsFew : FlowFull::kSlots);
+  p.d_slot = make_div(p.per_slot);
+  const cudaError_t e = a->dtype == QI_DT_BF16 ? launch_paged<true>(tm, p, scale_log2, sms, s)
+                                               : launch_paged<false>(tm, p, scale_log2, sms, s);
   return e == cudaSuccess ? QI_OK : op_fail(QI_ERR_CUDA, "%s: %s", kName, cudaGetErrorString(e));
 }

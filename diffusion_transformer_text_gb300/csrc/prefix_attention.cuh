@@ -40,6 +40,8 @@ struct Plan {
   int few;        // blocks of at most kFewRows rows, by launch_few
   int join;       // joint units whose chunks are a cluster of CTAs and join their parts themselves
   int per;        // partials per unit
+  int flow;       // a cache in pages: even pieces of all tiles, cut on the device (FlowParams); each CTA's
+  int cost;       // ... of a unit, in tiles, beside its own
 };
 
 struct Params {
@@ -63,10 +65,22 @@ struct PagedParams : Params {
   const int* q_len;  // query rows of each sequence, or NULL: T
   int page_log, pages;
 };
+// ... whose tiles are dealt out when the kernel runs: every CTA gets the same share of all sequences' tiles
+struct FlowParams : PagedParams {
+  int per_slot;  // (sequence, row block) pairs to a sum
+  Div d_slot;    // ... as a divisor
+  int4* rec;     // what each piece begins and ends with, two a piece (see Flow)
+};
 template <typename P>
 constexpr bool kPaged = false;
 template <>
 constexpr bool kPaged<PagedParams> = true;
+template <>
+constexpr bool kPaged<FlowParams> = true;
+template <typename P>
+constexpr bool kFlow = false;
+template <>
+constexpr bool kFlow<FlowParams> = true;
 
 struct Unit {
   int h, b0, t0;
@@ -77,7 +91,7 @@ struct Unit {
   int len;         // own keys of sequence b0
   int rows;        // rows of the block (the MMA's other rows are ignored)
   bool clear;      // the last tile holds own rows at or past len
-  long long slot;  // first partial row
+  long long slot;  // first partial row; of a share (FlowParams): -1 if the unit is a whole block
 };
 
 __device__ __forceinline__ int own_len_of(const Params& p, int b) {
@@ -152,6 +166,221 @@ __device__ __forceinline__ Unit unit_of(const P& p, int u) {
   return x;
 }
 
+// ------------------------------------------------------------------ even pieces of a cache in pages
+//
+// Sequences differ in length, and only the device knows by how much: units cut on the host for the
+// longest leave some CTAs idle and others with a wave more. With FlowParams all blocks (sequence, head, row
+// block) lie behind one another on a line, each as long as its tiles and a unit's overhead (pl.cost), which
+// is cut into pl.flow x gridDim equal pieces: CTA c takes pieces c, c + gridDim, ..: whole blocks, whose rows
+// it writes, and at either end a part of one, which it leaves as partials for merge_flow. A cut closer than
+// kLeast tiles to an end of its block moves there. Every CTA works its cuts out for itself, from sums over the
+// sequences. More rounds than one keep the CTAs, at any one time, on a stretch of the line whose keys stay
+// in the L2 while the row blocks that share them pass by: one round over 60 MB of keys, row blocks before
+// heads, took each CTA twice the time a tile (3 x 2461 causal rows, 16 key heads: 205 us, units cut on the
+// host 139).
+constexpr int kLeast = 2;
+constexpr int kFlowThreads = 384;  // that add up: the smaller kernel's
+constexpr int kMostRounds = 8;
+
+struct FlowCut {
+  int b, h, qb, j;  // sequence, head, row block, tile
+};
+__device__ __forceinline__ bool before(const FlowCut& x, const FlowCut& y) {
+  return x.b != y.b ? x.b < y.b : x.h != y.h ? x.h < y.h : x.qb != y.qb ? x.qb < y.qb : x.j < y.j;
+}
+template <int SLOTS>
+struct Flow {
+  static constexpr int kSlots = SLOTS;
+  long long sum[SLOTS + 1];  // of one head's costs of all pairs before a slot's first, and of all
+  long long warp_sum[kFlowThreads / 32];
+  FlowCut cut[2 * kMostRounds];  // begin and end of the CTA's pieces
+  int first[kMostRounds];        // the piece in which the block that a piece begins in began
+};
+// partial rows of piece v: of the block that it takes over, 2 v; of the one that it leaves, 2 v + 1.
+// rec[2 v] = (pair, head, whether that block ends here, piece that it began in), pair -1: none;
+// rec[2 v + 1] = (pair, head, -, -) of the one left
+
+// tiles of a pair, and whether it has rows at all
+__device__ __forceinline__ int flow_tiles(const FlowParams& p, int e, bool& live) {
+  const int b = quot(p.d_nqb, e), t0 = (e - b * p.pl.nqb) * p.pl.tb, tq = query_rows(p, b);
+  live = t0 < tq;
+  return live ? own_tiles(p, own_len_of(p, b), t0, p.pl.tb, tq) : 0;
+}
+__device__ __forceinline__ int flow_cost(const FlowParams& p, int e) {
+  bool live;
+  const int n = flow_tiles(p, e, live);
+  return live ? n + p.pl.cost : 0;
+}
+// costs of the pairs before pair e
+template <typename F>
+__device__ __forceinline__ long long flow_upto(const FlowParams& p, const F& f, int e) {
+  const int slot = quot(p.d_slot, e);
+  long long s = f.sum[slot];
+  for (int x = slot * p.per_slot; x < e; ++x) s += flow_cost(p, x);
+  return s;
+}
+// where on a line of `all` piece v of n begins
+__device__ __forceinline__ long long flow_at(long long all, int v, int n) {
+  return all / n * v + all % n * v / n;
+}
+
+template <typename F>
+__device__ __forceinline__ FlowCut flow_cut(const FlowParams& p, const F& f, int v, int n, int* first) {
+  const int nqb = p.pl.nqb, cost = p.pl.cost;
+  const long long all = flow_upto(p, f, p.B * nqb) * p.Hkv, pos = flow_at(all, v, n);
+  if (pos >= all) return {p.B, 0, 0, 0};
+  int lo = 0, hi = p.B;  // the sequence: the last one that begins at or before pos
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (flow_upto(p, f, mid * nqb) * p.Hkv <= pos)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  FlowCut x{lo, 0, 0, 0};
+  const int e0 = x.b * nqb;
+  const long long base = flow_upto(p, f, e0), head = flow_upto(p, f, e0 + nqb) - base;
+  long long rest = pos - base * p.Hkv;
+  x.h = static_cast<int>(rest / head);
+  rest -= x.h * head;
+  lo = 0, hi = nqb;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (flow_upto(p, f, e0 + mid) - base <= rest)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  x.qb = lo;
+  rest -= flow_upto(p, f, e0 + lo) - base;
+  const int tiles = flow_cost(p, e0 + lo) - cost;
+  x.j = static_cast<int>(rest) - cost;
+  if (x.j < kLeast) {
+    x.j = 0;
+  } else if (tiles - x.j < kLeast) {
+    x.j = 0;
+    if (++x.qb == nqb) {
+      x.qb = 0;
+      if (++x.h == p.Hkv) x.h = 0, ++x.b;
+    }
+  }
+  if (x.j > 0 && first) {
+    // the first cut that stays within the block, and the piece before it
+    const long long least = pos - rest + cost + kLeast;
+    int w = static_cast<int>(static_cast<double>(least) * n / static_cast<double>(all));
+    while (flow_at(all, w, n) < least) ++w;
+    while (w > 0 && flow_at(all, w - 1, n) >= least) --w;
+    *first = w - 1;
+  }
+  return x;
+}
+
+// The CTA's pieces; all of its threads, of which the first kFlowThreads add up
+template <typename F>
+__device__ __forceinline__ void flow_pieces(const FlowParams& p, F& f) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int pairs = p.B * p.pl.nqb, slots = quot(p.d_slot, pairs + p.per_slot - 1);
+  const int each = (slots + kFlowThreads - 1) / kFlowThreads, s0 = tid * each;
+  long long mine = 0, upto = 0;
+  if (tid < kFlowThreads) {
+    for (int s = s0; s < s0 + each && s < slots; ++s) {
+      f.sum[s] = mine;
+      for (int e = s * p.per_slot; e < (s + 1) * p.per_slot && e < pairs; ++e) mine += flow_cost(p, e);
+    }
+    upto = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const long long x = __shfl_up_sync(0xffffffffu, upto, d);
+      if (lane >= d) upto += x;
+    }
+    if (lane == 31) f.warp_sum[warp] = upto;
+  }
+  __syncthreads();
+  if (tid < kFlowThreads) {
+    long long at = upto - mine;
+    for (int w = 0; w < warp; ++w) at += f.warp_sum[w];
+    for (int s = s0; s < s0 + each && s < slots; ++s) f.sum[s] += at;
+    if (tid == kFlowThreads - 1) f.sum[slots] = at + mine;
+  }
+  __syncthreads();
+  const int n = p.pl.flow * static_cast<int>(gridDim.x);
+  if ((tid & 3) == 0 && tid < 8 * p.pl.flow) {
+    const int k = tid >> 2, v = (k >> 1) * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x);
+    f.cut[k] = flow_cut(p, f, v + (k & 1), n, (k & 1) ? nullptr : &f.first[k >> 1]);
+  }
+  __syncthreads();
+  if (tid < p.pl.flow) {
+    const int v = tid * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x);
+    const FlowCut a = f.cut[2 * tid], z = f.cut[2 * tid + 1];
+    const bool one = a.b == z.b && a.h == z.h && a.qb == z.qb;  // the piece ends in the block that it begins in
+    const bool takes = a.j > 0 && !(one && a.j == z.j), leaves = z.j > 0 && !(one && a.j > 0);
+    p.rec[2 * v] = make_int4(takes ? a.b * p.pl.nqb + a.qb : -1, a.h, one ? 0 : 1, takes ? f.first[tid] : 0);
+    p.rec[2 * v + 1] = make_int4(leaves ? z.b * p.pl.nqb + z.qb : -1, z.h, 0, 0);
+  }
+}
+
+// The units of a CTA: unit blockIdx, blockIdx + grid, .., or those of its pieces
+template <typename P, typename F>
+struct Walk {
+  int u;
+  __device__ __forceinline__ Walk(const P&, const F*) : u(blockIdx.x) {}
+  __device__ __forceinline__ bool more(const P& p) const { return u < p.pl.units; }
+  __device__ __forceinline__ Unit unit(const P& p) const { return unit_of(p, u); }
+  __device__ __forceinline__ void step(const P&) { u += gridDim.x; }
+};
+template <typename F>
+struct Walk<FlowParams, F> {
+  const F* f;
+  int round = 0;
+  FlowCut at, to;
+  bool ends;  // the unit is the block's last
+  int u = 0;
+  __device__ __forceinline__ Walk(const FlowParams&, const F* flow) : f(flow), at(flow->cut[0]), to(flow->cut[1]) {}
+  __device__ __forceinline__ bool more(const FlowParams& p) {
+    for (;;) {
+      while (before(at, to)) {
+        const int tq = query_rows(p, at.b);
+        if (at.qb * p.pl.tb < tq) return true;
+        // no more rows
+        at.qb = at.j = 0;
+        if (tq == 0 || ++at.h == p.Hkv) at.h = 0, ++at.b;
+      }
+      if (++round >= p.pl.flow) return false;
+      at = f->cut[2 * round];
+      to = f->cut[2 * round + 1];
+    }
+  }
+  __device__ __forceinline__ Unit unit(const FlowParams& p) {
+    Unit x;
+    x.b0 = at.b;
+    x.h = at.h;
+    x.t0 = at.qb * p.pl.tb;
+    x.tq = query_rows(p, x.b0);
+    x.len = own_len_of(p, x.b0);
+    x.p0 = x.pn = 0;
+    ends = !(at.b == to.b && at.h == to.h && at.qb == to.qb);
+    const int stop = ends ? own_tiles(p, x.len, x.t0, p.pl.tb, x.tq) : to.j;
+    x.o0 = at.j;
+    x.n = x.on = stop - at.j;
+    x.clear = x.on > 0 && x.len < stop * kKeys;
+    x.rows = p.pl.rows_o;
+    const long long v = static_cast<long long>(round) * gridDim.x + blockIdx.x;
+    x.slot = at.j == 0 && ends ? -1 : (2 * v + (at.j == 0 ? 1 : 0)) * p.pl.rows_o;
+    return x;
+  }
+  __device__ __forceinline__ void step(const FlowParams& p) {
+    if (!ends) {
+      at = to;
+    } else {
+      at.j = 0;
+      if (++at.qb == p.pl.nqb) {
+        at.qb = 0;
+        if (++at.h == p.Hkv) at.h = 0, ++at.b;
+      }
+    }
+  }
+};
+
 // 4-D tiled load: (dim, head, row, sequence); 5-D: (dim, head of the group, key head, token, sequence)
 __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int h, int row,
                                             int b) {
@@ -225,9 +454,11 @@ struct Maps8 {
 // Blocks of at most kFewRows rows (prefix_attention_few.cu); t8 NULL: 16-bit prefix. Each unit
 // writes two partials; merge_partials joins them.
 constexpr int kFewRows = 16;
+constexpr int kFlowSlotsFew = 512;
 cudaError_t launch_few(const Maps& tm, const Maps8* t8, const Params& p, bool bf16, float scale_log2, int sms,
                        cudaStream_t s);
-cudaError_t launch_few(const Maps& tm, const PagedParams& p, bool bf16, float scale_log2, int sms, cudaStream_t s);
+cudaError_t launch_few(const Maps& tm, const PagedParams& p, bool bf16, float scale_log2, cudaStream_t s);  // pl.join
+cudaError_t launch_few(const Maps& tm, const FlowParams& p, bool bf16, float scale_log2, cudaStream_t s);
 
 // ------------------------------------------------------------------ parts joined by a cluster
 //

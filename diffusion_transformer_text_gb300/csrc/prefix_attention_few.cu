@@ -94,13 +94,14 @@ struct Exchange {
   uint32_t pad;
   float2 ml[2][kR];  // JOIN: each warpgroup's maxima and sums
 };
-template <bool Q8>
+template <bool Q8, typename P = Params>
 constexpr int smem_bytes() {
   using C = Cfg<Q8>;
   return 2 * C::kSt * kTile + 2 * C::kCSt * kCode + kQBufs * kQTile + kSBufs * kQTile + 1024 + kBarSlots * 8 + 16 +
-         static_cast<int>(sizeof(Exchange));
+         static_cast<int>(sizeof(Exchange)) + (kFlow<P> ? static_cast<int>(sizeof(Flow<kFlowSlotsFew>)) : 0);
 }
-static_assert(smem_bytes<true>() <= 227 * 1024 && smem_bytes<false>() <= 227 * 1024, "shared memory per block");
+static_assert(smem_bytes<true>() <= 227 * 1024 && smem_bytes<false, FlowParams>() <= 227 * 1024, "shared memory per block");
+static_assert(Cfg<false>::kThreads >= kFlowThreads, "threads that add shares up");
 
 __device__ __forceinline__ void warpgroup_sync(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
 
@@ -178,6 +179,14 @@ __device__ __forceinline__ uint4 codes_to_16bit(uint2 c, uint32_t scale) {
   return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
+// where row i of a unit's block goes, or NULL
+__device__ __forceinline__ uint16_t* out_row(const FlowParams& p, const Unit& un, int i) {
+  const int tok = quot(p.d_G, i), t = un.t0 + tok;
+  return i < un.rows && t < un.tq
+             ? p.o + un.b0 * p.ob + t * p.orow + static_cast<long long>(un.h * p.pl.G + i - tok * p.pl.G) * p.oh
+             : nullptr;
+}
+
 template <bool BF16, bool Q8, bool JOIN, typename P>
 __global__ void __launch_bounds__(Cfg<Q8>::kThreads, 1)
     prefix_attn_few(const __grid_constant__ Maps tm, const __grid_constant__ Maps8 t8, const __grid_constant__ P p,
@@ -200,7 +209,8 @@ __global__ void __launch_bounds__(Cfg<Q8>::kThreads, 1)
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const int total = p.pl.units;
+  using F = Flow<kFlowSlotsFew>;
+  F* pieces = reinterpret_cast<F*>(&ex + 1);
   const auto give_up = [&](int code) {
     if (!*abort_flag) report_error(p.err, code);
     *abort_flag = 1;
@@ -237,6 +247,9 @@ __global__ void __launch_bounds__(Cfg<Q8>::kThreads, 1)
   const uint32_t tmem = *tmem_slot;
   grid_dep_wait();
   grid_dep_launch_dependents();
+  if constexpr (kFlow<P>) {
+    flow_pieces(p, *pieces);
+  }
 
   if (warp == 0 || warp == 2) {
     // ---------------- producers: K tiles and Q (warp 0), V tiles (warp 2). Lane 0 works; warp 2
@@ -253,8 +266,9 @@ __global__ void __launch_bounds__(Cfg<Q8>::kThreads, 1)
     const CUtensorMap* own_map = kv ? &tm.v : &tm.k;
     const CUtensorMap* code_map = kv ? &t8.v : &t8.k;
     bool ok = true;
-    for (int u = blockIdx.x; u < total; u += gridDim.x) {
-      const Unit un = unit_of(p, u);
+    for (Walk<P, F> w(p, pieces); w.more(p); w.step(p)) {
+      const Unit un = w.unit(p);
+      const int u = w.u;
       if (un.n == 0) continue;
       if constexpr (kPaged<P>) {
         // keys by pages, a lane a box: the whole warp walks the tiles, and a tile's pages are looked up
@@ -361,8 +375,8 @@ __global__ void __launch_bounds__(Cfg<Q8>::kThreads, 1)
       const uint64_t qdesc0 = sw128_kmajor_desc(smem_u32(sQ));
       uint32_t t = 0, ku = 0;
       bool ok = true;
-      for (int u = blockIdx.x; ok && u < total; u += gridDim.x) {
-        const Unit un = unit_of(p, u);
+      for (Walk<P, F> w(p, pieces); ok && w.more(p); w.step(p)) {
+        const Unit un = w.unit(p);
         if (un.n == 0) continue;
         const uint32_t qb = ku % kQBufs;
         ok = __all_sync(0xffffffffu, !*abort_flag && mbar_wait(&bars[kQFull + qb], (ku / kQBufs) & 1u));
@@ -404,8 +418,8 @@ __global__ void __launch_bounds__(Cfg<Q8>::kThreads, 1)
       const uint64_t pdesc0 = sw128_kmajor_desc(smem_u32(sP));
       uint32_t t = 0, cleared = 0;
       bool ok = true;
-      for (int u = blockIdx.x; ok && u < total; u += gridDim.x) {
-        const Unit un = unit_of(p, u);
+      for (Walk<P, F> w(p, pieces); ok && w.more(p); w.step(p)) {
+        const Unit un = w.unit(p);
         for (int j = 0; j < un.n; ++j, ++t) {
           const uint32_t st = t % kSt, sb = t % kSBufs;
           ok = mbar_wait(&bars[kFull + 3 + st], (t / kSt) & 1u);
@@ -451,8 +465,17 @@ __global__ void __launch_bounds__(Cfg<Q8>::kThreads, 1)
     const uint32_t piece = static_cast<uint32_t>((key & 63) >> 3);
     uint32_t t = 0, turn = 0;
     bool ok = true;
-    for (int u = blockIdx.x; u < total; u += gridDim.x) {
-      const Unit un = unit_of(p, u);
+    for (Walk<P, F> walk(p, pieces); walk.more(p); walk.step(p)) {
+      const Unit un = walk.unit(p);
+      if constexpr (kFlow<P>) {
+        if (un.n == 0 && s == 0) {  // rows without a key
+#pragma unroll
+          for (int i = 0; i < kR; ++i) {
+            uint16_t* orow = out_row(p, un, i);
+            if (orow) orow[key] = 0;
+          }
+        }
+      }
       if (un.n == 0) continue;
       const int lim16 = own_lim(p, un.len, un.t0 + tok16, un.tq);
       const int lim_least = own_lim(p, un.len, un.t0, un.tq);
@@ -540,7 +563,75 @@ __global__ void __launch_bounds__(Cfg<Q8>::kThreads, 1)
       }
       // this warpgroup's part of the block's rows
       const long long slot = un.slot + s * un.rows;
-      if (cnt > 0) {
+      if constexpr (kFlow<P>) {
+        // The two parts meet here: warpgroup 1 leaves its O^T where its P was (whose products are done), and
+        // warpgroup 0 writes the rows, or their part of a block that other shares have the rest of.
+        float den = 0.f;
+        if (cnt > 0) {
+#pragma unroll
+          for (int d = 16; d; d >>= 1)
+#pragma unroll
+            for (int i = 0; i < kR; ++i) l[i] += __shfl_xor_sync(0xffffffffu, l[i], d);
+          if (lane == 0) store16f(ex.sum[s][quarter], l);
+          warpgroup_sync(1 + s);
+          den = (ex.sum[s][0][row16] + ex.sum[s][1][row16]) + (ex.sum[s][2][row16] + ex.sum[s][3][row16]);
+          ok = ok && __all_sync(0xffffffffu, mbar_wait(&bars[kPDone + last % kSBufs], (last / kSBufs) & 1u));
+          tc_fence_after();
+        }
+        uint32_t o[kR];
+        if (cnt > 0) {
+          tmem_ld16(tO, o);
+          tmem_ld_wait();
+          tc_fence_before();
+        } else {
+#pragma unroll
+          for (int i = 0; i < kR; ++i) o[i] = 0u;
+        }
+        // row i at buffer 1 or 3, whose products are warpgroup 1's alone
+        float* const park = reinterpret_cast<float*>(sP + kQTile) + key;
+        if (s == 1) {
+#pragma unroll
+          for (int i = 0; i < kR; ++i) park[(i >> 3) * (2 * kQTile / 4) + (i & 7) * kHeadDim] = __uint_as_float(o[i]);
+          if (quarter == 0 && lane < kR) ex.ml[1][lane] = make_float2(m_used, den);
+          asm volatile("bar.sync 3, 256;" ::: "memory");
+          asm volatile("bar.sync 4, 256;" ::: "memory");  // it has been read
+        } else {
+          asm volatile("bar.sync 3, 256;" ::: "memory");
+          const float2 ml1 = ex.ml[1][row16];
+          const float top = fmaxf(m_used, ml1.x);
+          // (a part without a key has m = -inf and weight 0; m = -inf with another sum is a row of NaN scores)
+          const float a0 = top == -INFINITY ? 1.f : fast_exp2(m_used - top);
+          const float a1 = top == -INFINITY ? 1.f : fast_exp2(ml1.x - top);
+          const float sum = den * a0 + ml1.y * a1;
+          const bool part = un.slot >= 0;
+          const float inv = part ? 1.f : (sum == 0.f ? 0.f : 1.f / sum);
+          if (lane < kR) {
+            ex.nm[sw][lane] = a0 * inv;
+            ex.alpha[sw][lane] = a1 * inv;
+            if (part && quarter == 0 && lane < un.rows) p.ml[un.slot + lane] = make_float2(top, sum);
+          }
+          __syncwarp();
+          float w0[kR], w1[kR], v[kR];
+          load16f(ex.nm[sw], w0);
+          load16f(ex.alpha[sw], w1);
+#pragma unroll
+          for (int i = 0; i < kR; ++i)
+            v[i] = fmaf(__uint_as_float(o[i]), w0[i], park[(i >> 3) * (2 * kQTile / 4) + (i & 7) * kHeadDim] * w1[i]);
+          asm volatile("bar.arrive 4, 256;" ::: "memory");
+          if (part) {
+            float* out = p.part + un.slot * kHeadDim + key;
+#pragma unroll
+            for (int i = 0; i < kR; ++i)
+              if (i < un.rows) out[i * kHeadDim] = v[i];
+          } else {
+#pragma unroll
+            for (int i = 0; i < kR; ++i) {
+              uint16_t* orow = out_row(p, un, i);
+              if (orow) orow[key] = static_cast<uint16_t>(pack16<BF16>(v[i], 0.f));
+            }
+          }
+        }
+      } else if (cnt > 0) {
         // sums over the warp's lanes
 #pragma unroll
         for (int d = 16; d; d >>= 1)
@@ -592,8 +683,8 @@ __global__ void __launch_bounds__(Cfg<Q8>::kThreads, 1)
     };
     uint32_t t = 0, tc = 0;
     bool ok = true;
-    for (int u = blockIdx.x; u < total; u += gridDim.x) {
-      const Unit un = unit_of(p, u);
+    for (Walk<P, F> w(p, pieces); w.more(p); w.step(p)) {
+      const Unit un = w.unit(p);
       uint32_t bytes = un.pn > 0 ? scales_of(un, un.p0) : 0u;
       for (int j = 0; j < un.n; ++j) {
         const uint32_t tt = t + j, st = tt % kSt, cs = tc % kCSt;
@@ -696,21 +787,27 @@ __global__ void __launch_bounds__(Cfg<Q8>::kThreads, 1)
 }
 
 template <bool BF16, bool Q8, typename P>
-cudaError_t launch_as(const Maps& tm, const Maps8& t8, const P& p, float scale_log2, int sms, cudaStream_t stream) {
-  static std::atomic<unsigned long long> attr_done{0}, attr_done_join{0};
-  constexpr int smem = smem_bytes<Q8>();
-  constexpr int threads = Cfg<Q8>::kThreads;
-  if (p.pl.join) {
-    const cudaError_t e = ensure_smem_limit(prefix_attn_few<BF16, Q8, true, P>, smem, attr_done_join);
-    if (e != cudaSuccess) return e;
-    return launch_clusters(prefix_attn_few<BF16, Q8, true, P>, p.pl.nch, dim3(p.pl.units), dim3(threads), smem, stream,
-                           tm, t8, p, scale_log2);
-  }
+cudaError_t launch_join(const Maps& tm, const Maps8& t8, const P& p, float scale_log2, cudaStream_t stream) {
+  static std::atomic<unsigned long long> attr_done{0};
+  constexpr int smem = smem_bytes<Q8, P>();
+  const cudaError_t e = ensure_smem_limit(prefix_attn_few<BF16, Q8, true, P>, smem, attr_done);
+  if (e != cudaSuccess) return e;
+  return launch_clusters(prefix_attn_few<BF16, Q8, true, P>, p.pl.nch, dim3(p.pl.units), dim3(Cfg<Q8>::kThreads), smem,
+                         stream, tm, t8, p, scale_log2);
+}
+template <bool BF16, bool Q8, typename P>
+cudaError_t launch_walk(const Maps& tm, const Maps8& t8, const P& p, float scale_log2, int grid, cudaStream_t stream) {
+  static std::atomic<unsigned long long> attr_done{0};
+  constexpr int smem = smem_bytes<Q8, P>();
   const cudaError_t e = ensure_smem_limit(prefix_attn_few<BF16, Q8, false, P>, smem, attr_done);
   if (e != cudaSuccess) return e;
-  const int grid = p.pl.units < sms ? p.pl.units : sms;
-  return launch_dependent(prefix_attn_few<BF16, Q8, false, P>, dim3(grid), dim3(threads), smem, stream, tm, t8, p,
+  return launch_dependent(prefix_attn_few<BF16, Q8, false, P>, dim3(grid), dim3(Cfg<Q8>::kThreads), smem, stream, tm, t8, p,
                           scale_log2);
+}
+template <bool BF16, bool Q8>
+cudaError_t launch_as(const Maps& tm, const Maps8& t8, const Params& p, float scale_log2, int sms, cudaStream_t stream) {
+  return p.pl.join ? launch_join<BF16, Q8>(tm, t8, p, scale_log2, stream)
+                   : launch_walk<BF16, Q8>(tm, t8, p, scale_log2, p.pl.units < sms ? p.pl.units : sms, stream);
 }
 
 }  // namespace
@@ -725,11 +822,14 @@ cudaError_t pa::launch_few(const Maps& tm, const Maps8* t8, const Params& p, boo
   return bf16 ? launch_as<true, false>(tm, none, p, scale_log2, sms, s)
               : launch_as<false, false>(tm, none, p, scale_log2, sms, s);
 }
-
-cudaError_t pa::launch_few(const Maps& tm, const PagedParams& p, bool bf16, float scale_log2, int sms, cudaStream_t s) {
+cudaError_t pa::launch_few(const Maps& tm, const PagedParams& p, bool bf16, float scale_log2, cudaStream_t s) {
   static const Maps8 none{};
-  return bf16 ? launch_as<true, false>(tm, none, p, scale_log2, sms, s)
-              : launch_as<false, false>(tm, none, p, scale_log2, sms, s);
+  return bf16 ? launch_join<true, false>(tm, none, p, scale_log2, s) : launch_join<false, false>(tm, none, p, scale_log2, s);
+}
+cudaError_t pa::launch_few(const Maps& tm, const FlowParams& p, bool bf16, float scale_log2, cudaStream_t s) {
+  static const Maps8 none{};
+  return bf16 ? launch_walk<true, false>(tm, none, p, scale_log2, p.pl.units, s)
+              : launch_walk<false, false>(tm, none, p, scale_log2, p.pl.units, s);
 }
 
 }  // namespace qi

@@ -710,7 +710,7 @@ typedef struct qi_paged_attn {
   long long table_stride;
   int dtype, B, T, Hq, Hkv, pages, page_rows, table_width, max_len;
 } qi_paged_attn;
-size_t qi_paged_attention_workspace(const qi_paged_attn* args); /* 0 also for bad sizes */
+size_t qi_paged_attention_workspace(const qi_paged_attn* args); /* by the sizes, by whether q_len is NULL; 0 also for bad sizes */
 qi_status qi_paged_attention(const qi_paged_attn* args, qi_stream_t stream);
 
 /* Message for the calling thread's last failed call ("" if none). */
