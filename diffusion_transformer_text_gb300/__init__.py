@@ -15,7 +15,7 @@ from typing import NamedTuple
 
 import numpy as np
 
-from .build import LIB, build  # noqa: F401  (build() compiles the library)
+from .build import LIB, TENSORS, build  # noqa: F401  (build() compiles the library)
 
 HIDDEN = 4096
 HEADS = 32
@@ -80,17 +80,26 @@ class SchedParams(ctypes.Structure):
 
 
 _lib = None
+_describe = None  # qi_tensors.describe, once lib() has run
 
 
 def lib() -> ctypes.CDLL:
     """Load libqidit.so (built in-tree by build()); raises if it is absent."""
-    global _lib
+    global _lib, _describe
     if _lib is not None:
         return _lib
     path = os.environ.get("QIDIT_LIB", LIB)
     if not os.path.exists(path):
         raise RuntimeError(f"{path} is missing: run diffusion_transformer_text_gb300.build() first")
     L = ctypes.CDLL(path)
+    if not os.path.exists(TENSORS):
+        raise RuntimeError(f"{TENSORS} is missing: run diffusion_transformer_text_gb300.build() first")
+    import importlib.util
+    import torch  # noqa: F401  (what the module is linked to)
+    spec = importlib.util.spec_from_file_location("qi_tensors", TENSORS)
+    tensors = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(tensors)
+    _describe = tensors.describe
     P, I, F, U, S = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_uint, ctypes.c_size_t
     sig = {
         "qi_dit_create": [ctypes.POINTER(DitConfig), I, ctypes.POINTER(P)],
@@ -621,9 +630,11 @@ def add_rmsnorm_mxfp8(x, delta=None, w=None, plus_one: bool = False, eps: float 
 
 # ---------------------------------------------------------------- sequences in pages
 
-# qi_qk_rope and qi_paged_attn: what changes from call to call, then what a layout fixes
-_ROPE_HEAD, _ROPE_TAIL = struct.Struct("@13Pif"), struct.Struct("@19q16i")
-_PAGED_HEAD, _PAGED_TAIL = struct.Struct("@9Pif"), struct.Struct("@N13q9ixxxx")
+# qi_qk_rope and qi_paged_attn: behind the tensors' addresses (13 and 9) what else changes from call to call, then
+# what a layout fixes
+_ROPE_HEAD, _ROPE_TAIL = struct.Struct("@if"), struct.Struct("@19q16i")
+_PAGED_HEAD, _PAGED_TAIL = struct.Struct("@if"), struct.Struct("@N13q9ixxxx")
+_POINTER = struct.Struct("@P")
 _rope_layouts: dict = {}
 _paged_layouts: dict = {}
 
@@ -695,6 +706,7 @@ def _table(table, B, dev):
 
 
 def _check_rope(key, q, k, v, rope, pos, q_w, k_w, outs, cache, table, start, lens, dtype):
+    """(device, type of the outputs, the fixed part of qi_qk_rope) of arguments in this layout."""
     import torch
     kinds = {torch.float16: DT_F16, torch.bfloat16: DT_BF16, torch.float32: DT_F32}
     given = [t for t in (q, k, v) if t is not None]
@@ -703,6 +715,9 @@ def _check_rope(key, q, k, v, rope, pos, q_w, k_w, outs, cache, table, start, le
             raise ValueError(f"{n}: want [B, T, heads, {HEAD_DIM}] of a floating type, got {t.dtype} {tuple(t.shape)}")
     x = given[0]
     dev, (B, T) = x.device, x.shape[:2]
+    if dtype is None:
+        like = cache.k if cache is not None else next((o for o in outs if o is not None), None)
+        dtype = like.dtype if like is not None else torch.bfloat16 if x.dtype == torch.float32 else x.dtype
     if dtype not in (torch.float16, torch.bfloat16) or x.dtype not in (dtype, torch.float32):
         raise ValueError(f"dtype: want float16 or bfloat16, that of the arguments or from float32, got {dtype} from {x.dtype}")
     if (cache is None) != (table is None):
@@ -721,8 +736,8 @@ def _check_rope(key, q, k, v, rope, pos, q_w, k_w, outs, cache, table, start, le
             dst.append(_strided(o, dtype, (B, T, h, HEAD_DIM), dev, n + "_out"))
     pages = rows = width = stride = 0
     if cache is not None:
-        if Hkv == 0 or any(o is not None for o in outs[1:]):
-            raise ValueError("cache: wants k or v, and no other outputs for them")
+        if Hkv == 0:
+            raise ValueError("cache: wants k or v")
         if cache.k.dim() != 4:
             raise ValueError(f"cache: want [pages, rows, H, {HEAD_DIM}], got {tuple(cache.k.shape)}")
         pages, rows = cache.k.shape[:2]
@@ -749,11 +764,10 @@ def _check_rope(key, q, k, v, rope, pos, q_w, k_w, outs, cache, table, start, le
     _want(start, torch.int32, (B,), dev, "start")
     _want(lens, torch.int32, (B,), dev, "lens")
     w = q_w if q_w is not None else k_w
-    lib()
-    return _remember(_rope_layouts, key, _ROPE_TAIL.pack(
+    return _remember(_rope_layouts, key, (dev.index, dtype, _ROPE_TAIL.pack(
         *ins[0], *ins[1], *ins[2], *dst[0], *dst[1], *dst[2], stride, kinds[x.dtype], kinds[dtype],
         int(w is not None and w.dtype == torch.float32), B, T, Hq, Hkv, len(pairs),
-        *(*pairs, 0, 0, 0, 0)[:4], int(halves), pages, rows, width))
+        *(*pairs, 0, 0, 0, 0)[:4], int(halves), pages, rows, width)))
 
 
 def qk_norm_rope(q, k, v=None, rope: Rope | None = None, pos=None, q_w=None, k_w=None, plus_one: bool = False,
@@ -772,47 +786,44 @@ def qk_norm_rope(q, k, v=None, rope: Rope | None = None, pos=None, q_w=None, k_w
     hold anything and are not written (and are zero in outputs that are made here). stream: default the current one of q's
     device. Returns (q_out, k_out, v_out), None for what was not given or went to the cache. No gradients."""
     import torch
-    x = q if q is not None else k if k is not None else v
-    if x is None:
-        raise ValueError("none of q, k and v")
-    dev = x.get_device()
-    if stream is not None or dev < 0 or dev != torch._C._cuda_getDevice():
-        with _elsewhere(x, stream, (q, k, v, rope and rope.turns, pos, q_w, k_w, *(out or ()), *(cache or ()), table,
-                                    start, lens)):
-            return qk_norm_rope(q, k, v, rope, pos, q_w, k_w, plus_one, eps, dtype, out, cache, table, start, lens)
+    if _lib is None:
+        lib()
     outs = (None, None, None) if out is None else out
     qo, ko, vo = outs
-    if dtype is None:
-        like = cache.k if cache is not None else qo if qo is not None else ko if ko is not None else vo
-        dtype = like.dtype if like is not None else torch.bfloat16 if x.dtype == torch.float32 else x.dtype
-    key = (_layout(q), _layout(k), _layout(v), None if rope is None else (_layout(rope.turns), rope.pairs, rope.halves),
-           _layout(pos), _layout(q_w), _layout(k_w), dtype, _layout(qo), _layout(ko), _layout(vo),
-           None if cache is None else (_layout(cache.k), _layout(cache.v)), _layout(table), _layout(start), _layout(lens))
-    tail = _rope_layouts.get(key)
-    if tail is None:
-        tail = _check_rope(key, q, k, v, rope, pos, q_w, k_w, outs, cache, table, start, lens, dtype)
-    make = torch.empty if lens is None else torch.zeros
-    if q is not None and qo is None:
-        qo = make(q.shape, dtype=dtype, device=q.device)
     if cache is None:
-        if k is not None and ko is None:
-            ko = make(k.shape, dtype=dtype, device=k.device)
-        if v is not None and vo is None:
-            vo = make(v.shape, dtype=dtype, device=v.device)
-        ka, va = _addr(ko), _addr(vo)
+        ck, cv = ko, vo
     else:
-        ka, va = cache.k.data_ptr(), cache.v.data_ptr()
-    st = _lib.qi_qk_norm_rope(_ROPE_HEAD.pack(
-        _addr(q), _addr(k), _addr(v), _addr(qo), ka, va, _addr(q_w), _addr(k_w), _addr(pos),
-        0 if rope is None else rope.turns.data_ptr(), _addr(start), _addr(lens), _addr(table), 1 if plus_one else 0,
-        eps) + tail, torch._C._cuda_getCurrentRawStream(dev))
+        ck, cv = cache
+        if ko is not None or vo is not None:
+            raise ValueError("cache: wants no other outputs of k and v")
+    turns, pairs, halves = (None, None, None) if rope is None else rope
+    layout, addresses = _describe(q, k, v, qo, ck, cv, q_w, k_w, pos, turns, start, lens, table)
+    key = (layout, pairs, halves, dtype, cache is None)
+    plan = None if stream is not None else _rope_layouts.get(key)
+    if plan is None or plan[0] != torch._C._cuda_getDevice():
+        x = q if q is not None else k if k is not None else v
+        if x is None:
+            raise ValueError("none of q, k and v")
+        if stream is not None or x.get_device() < 0 or x.get_device() != torch._C._cuda_getDevice():
+            with _elsewhere(x, stream, (q, k, v, turns, pos, q_w, k_w, qo, ck, cv, table, start, lens)):
+                return qk_norm_rope(q, k, v, rope, pos, q_w, k_w, plus_one, eps, dtype, out, cache, table, start, lens)
+        plan = _check_rope(key, q, k, v, rope, pos, q_w, k_w, outs, cache, table, start, lens, dtype)
+    dev, kind, tail = plan
+    if qo is None and q is not None or cache is None and (ko is None and k is not None or vo is None and v is not None):
+        make = torch.empty if lens is None else torch.zeros
+        new = [o if o is not None or t is None else make(t.shape, dtype=kind, device=t.device)
+               for t, o in ((q, qo), (k, ck), (v, cv))]
+        qo, ck, cv = new
+        addresses = _describe(q, k, v, qo, ck, cv, q_w, k_w, pos, turns, start, lens, table)[1]
+    st = _lib.qi_qk_norm_rope(addresses + _ROPE_HEAD.pack(1 if plus_one else 0, eps) + tail,
+                              torch._C._cuda_getCurrentRawStream(dev))
     if st:
         _check(st)
-    return qo, ko, vo
+    return (qo, ck, cv) if cache is None else (qo, None, None)
 
 
 def _check_paged(key, q, cache, table, kv_len, q_len, max_len, causal, out, status):
-    """(the fixed part of qi_paged_attn, workspace bytes) of arguments in this layout."""
+    """(device, the fixed part of qi_paged_attn, workspace bytes) of arguments in this layout."""
     import torch
     if q.dim() != 4 or q.shape[3] != HEAD_DIM:
         raise ValueError(f"q: want [B, T, Hq, {HEAD_DIM}], got {tuple(q.shape)}")
@@ -832,9 +843,11 @@ def _check_paged(key, q, cache, table, kv_len, q_len, max_len, causal, out, stat
     _want(status, torch.int32, (1,), dev, "status")
     longest = min(width * rows, 1 << 24) if max_len is None else max_len
     tail = (*qs, *ks, *vs, *os_, stride, dt, B, T, Hq, Hkv, pages, rows, width, longest)
-    need = lib().qi_paged_attention_workspace(
-        _PAGED_HEAD.pack(*[0] * 6, 0 if q_len is None else 1, 0, 0, 1 if causal else 0, 1.0) + _PAGED_TAIL.pack(0, *tail))
-    return _remember(_paged_layouts, key, (_PAGED_TAIL.pack(need, *tail), need))
+    # (the workspace depends on the sizes and on whether there is a q_len)
+    need = _lib.qi_paged_attention_workspace(
+        bytes(48) + _POINTER.pack(0 if q_len is None else 1) + bytes(16) + _PAGED_HEAD.pack(1 if causal else 0, 1.0)
+        + _PAGED_TAIL.pack(0, *tail))
+    return _remember(_paged_layouts, key, (dev.index, _PAGED_TAIL.pack(need, *tail), need))
 
 
 def paged_attention(q, cache: PagedKV, table, kv_len, q_len=None, causal: bool = True, scale: float | None = None,
@@ -849,27 +862,27 @@ def paged_attention(q, cache: PagedKV, table, kv_len, q_len=None, causal: bool =
     that sees nothing is zero. status, stream and strides as for prefix_attention, whose check
     (prefix_attention_check) tells of expired waits. Returns o [B, T, Hq, 128]. No gradients."""
     import torch
-    dev = q.get_device()
-    if stream is not None or dev < 0 or dev != torch._C._cuda_getDevice():
-        with _elsewhere(q, stream, (*cache, table, kv_len, q_len, out, status)):
-            return paged_attention(q, cache, table, kv_len, q_len, causal, scale, max_len, out, status)
+    if _lib is None:
+        lib()
     ck, cv = cache
-    causal = bool(causal)
-    key = (q.dtype, q.device, q.shape, q.stride(), _layout(ck), _layout(cv), _layout(table), _layout(kv_len),
-           None if q_len is None else _layout(q_len), max_len, causal, None if out is None else _layout(out),
-           None if status is None else _layout(status))
-    plan = _paged_layouts.get(key)
-    if plan is None:
+    layout, addresses = _describe(q, ck, cv, out, table, kv_len, q_len, None, status)
+    key = (layout, max_len, bool(causal))
+    plan = None if stream is not None else _paged_layouts.get(key)
+    if plan is None or plan[0] != torch._C._cuda_getDevice():
+        if stream is not None or q.get_device() < 0 or q.get_device() != torch._C._cuda_getDevice():
+            with _elsewhere(q, stream, (ck, cv, table, kv_len, q_len, out, status)):
+                return paged_attention(q, cache, table, kv_len, q_len, causal, scale, max_len, out, status)
         plan = _check_paged(key, q, cache, table, kv_len, q_len, max_len, causal, out, status)
-    tail, need = plan
+    dev, tail, need = plan
     if out is None:
         out = torch.empty_like(q, memory_format=torch.contiguous_format) if q_len is None else torch.zeros(
             q.shape, dtype=q.dtype, device=q.device)
-    ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
-    st = _lib.qi_paged_attention(_PAGED_HEAD.pack(
-        q.data_ptr(), ck.data_ptr(), cv.data_ptr(), out.data_ptr(), table.data_ptr(), kv_len.data_ptr(), _addr(q_len),
-        _addr(ws), _addr(status), 1 if causal else 0, _SCALE if scale is None else scale) + tail,
-        torch._C._cuda_getCurrentRawStream(dev))
+        addresses = _describe(q, ck, cv, out, table, kv_len, q_len, None, status)[1]
+    if need:
+        ws = torch.empty(need, dtype=torch.uint8, device=q.device)
+        addresses = addresses[:56] + _POINTER.pack(ws.data_ptr()) + addresses[64:]
+    st = _lib.qi_paged_attention(addresses + _PAGED_HEAD.pack(1 if causal else 0, _SCALE if scale is None else scale) + tail,
+                                 torch._C._cuda_getCurrentRawStream(dev))
     if st:
         _check(st)
     return out

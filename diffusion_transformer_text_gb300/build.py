@@ -3,7 +3,8 @@
     python -m diffusion_transformer_text_gb300.build [--force]
 
 Translation units compile in parallel; the output goes to
-diffusion_transformer_text_gb300/_build/libqidit.so (git-ignored).
+diffusion_transformer_text_gb300/_build/libqidit.so (git-ignored). Beside it goes qi_tensors.so, the
+part of the Python binding that is compiled against PyTorch's headers.
 """
 from __future__ import annotations
 
@@ -12,6 +13,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -19,6 +21,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libqidit.so")
+TENSORS = os.path.join(BUILD, "qi_tensors.so")  # the binding's reader of tensor arguments (csrc/tensors.cpp)
 SOURCES = ["qidit.cu", "gemm.cu", "attention.cu", "kernels_small.cu", "gemm_noalloc.cu", "prefix_attention.cu",
            "prefix_attention_few.cu", "batch_ops.cu", "rope_ops.cu"]
 HEADERS = ["ptx.cuh", "internal.h", "prefix_attention.cuh", "values.cuh"]
@@ -34,15 +37,44 @@ def nvcc() -> str:
     raise RuntimeError("nvcc not found: the CUDA 13 toolkit is required to build libqidit.so")
 
 
+def _torch_dir() -> str:
+    import importlib.util
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not spec.submodule_search_locations:
+        raise RuntimeError("PyTorch not found: the binding is compiled against its headers")
+    return list(spec.submodule_search_locations)[0]
+
+
+def _torch_version() -> str:
+    with open(os.path.join(_torch_dir(), "version.py")) as f:
+        return f.read()
+
+
+def _build_tensors() -> None:
+    """qi_tensors.so, a CPython module over PyTorch's headers (host code only)."""
+    t, py = _torch_dir(), sysconfig.get_paths()["include"]
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    tmp = TENSORS + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-I" + py, "-I" + os.path.join(t, "include"),
+           "-I" + os.path.join(t, "include", "torch", "csrc", "api", "include"), "-I" + os.path.join(cuda, "include"),
+           os.path.join(CSRC, "tensors.cpp"), "-o", tmp, "-L" + os.path.join(t, "lib"), "-ltorch_python", "-ltorch_cpu",
+           "-lc10", "-Wl,-rpath," + os.path.join(t, "lib")]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on tensors.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, TENSORS)
+
+
 def _fingerprint() -> str:
     h = hashlib.sha256()
-    for name in SOURCES + HEADERS:
+    for name in SOURCES + HEADERS + ["tensors.cpp"]:
         with open(os.path.join(CSRC, name), "rb") as f:
             h.update(name.encode() + f.read())
     with open(os.path.join(ROOT, "include", "qidit.h"), "rb") as f:
         h.update(f.read())
     h.update(" ".join(ARCH + FLAGS).encode())
     h.update(os.uname().machine.encode())
+    h.update(sys.version.encode() + _torch_version().encode())
     return h.hexdigest()
 
 
@@ -51,7 +83,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     stamp = os.path.join(BUILD, "libqidit.stamp")
     fp = _fingerprint()
-    if not force and os.path.exists(LIB) and os.path.exists(stamp):
+    if not force and os.path.exists(LIB) and os.path.exists(TENSORS) and os.path.exists(stamp):
         with open(stamp) as f:
             if f.read().strip() == fp:
                 return LIB
@@ -65,8 +97,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
             raise RuntimeError(f"nvcc failed on {src}:\n{r.stdout}\n{r.stderr}")
         return obj, r.stderr
 
-    with ThreadPoolExecutor(len(SOURCES)) as ex:
+    with ThreadPoolExecutor(len(SOURCES) + 1) as ex:
+        tensors = ex.submit(_build_tensors)
         results = list(ex.map(compile_one, SOURCES))
+        tensors.result()
     if verbose:
         for _, log in results:
             sys.stderr.write(log)

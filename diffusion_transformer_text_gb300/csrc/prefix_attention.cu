@@ -977,7 +977,7 @@ constexpr float kJoinTiles = 2.6f, kJoinRow = 1.f / 32;  // start of a CTA in a 
 constexpr long long kL2Half = 64ll << 20;
 constexpr int kFullCost = 2, kFewCost = 2;  // of a unit, in tiles, where pieces are cut
 constexpr float kFlowStart = 5.f;           // cutting them, and a second launch
-constexpr float kPiece = 128.f;             // tiles of a piece where blocks share keys
+constexpr float kPiece = 256.f;             // tiles of a piece where blocks share keys
 constexpr float kEvenFrom = 48.f;           // tiles a CTA from which unequal chunks are worth cutting
 constexpr int kFewTiles = 4;                // so few in a unit, and their number does not matter
 struct Sizes {
@@ -1009,7 +1009,7 @@ Plan make_plan(const Sizes& z, int sms) {
   const float convert = z.from8 && z.P > 0 ? kConvertStart + kConvert * static_cast<float>(z.P) * z.Hkv * kHeadDim / (1 << 20) : 0.f;
 const bool even =
       z.paged && (z.T <= kRows / a.G ||
-                  (z.ragged && static_cast<float>(ceil_div(z.T, kRows / a.G)) * z.B * z.Hkv * (a.ot + kFullCost) > kEvenFrom * sms));
+                  (z.ragged && z.B > 1 && static_cast<float>(ceil_div(z.T, kRows / a.G)) * z.B * z.Hkv * (a.ot + kFullCost) > kEvenFrom * sms));
   // joint units, every number of chunks that keeps the grid within a few waves
   const auto joint = [&](Plan c, Rate r, bool always_split, float more) {
     const int n = c.pt + c.ot;

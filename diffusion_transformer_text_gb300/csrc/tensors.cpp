@@ -1,0 +1,66 @@
+// What the binding reads of its tensor arguments, in one call: describe(t0, t1, ..) gives (layouts, addresses),
+// two byte strings. Layouts: of each argument its type, device, shape and strides (None: a mark of its own), so
+// that equal strings mean that the checks of one call hold for the other; addresses: 64 bits each, 0 for None. By
+// Python attributes alone that took 5 us for 13 tensors, more than the launch they are for; this takes 0.3.
+#define PY_SSIZE_T_CLEAN
+#include <Python.h>
+
+#include <torch/csrc/autograd/python_variable.h>
+
+#include <cstdint>
+#include <exception>
+
+namespace {
+
+constexpr Py_ssize_t kMostTensors = 24;
+constexpr int64_t kMostDims = 8;
+
+PyObject* describe(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  if (n > kMostTensors) {
+    PyErr_SetString(PyExc_ValueError, "too many tensors");
+    return nullptr;
+  }
+  int64_t layout[kMostTensors * (1 + 2 * kMostDims)], address[kMostTensors];
+  Py_ssize_t used = 0;
+  try {
+    for (Py_ssize_t i = 0; i < n; ++i) {
+      if (args[i] == Py_None) {
+        layout[used++] = -1;
+        address[i] = 0;
+        continue;
+      }
+      if (!THPVariable_Check(args[i])) {
+        PyErr_Format(PyExc_TypeError, "want a tensor, got %s", Py_TYPE(args[i])->tp_name);
+        return nullptr;
+      }
+      const at::Tensor& t = THPVariable_Unpack(args[i]);
+      if (t.layout() != at::kStrided || t.dim() > kMostDims) {
+        PyErr_SetString(PyExc_ValueError, "want a dense tensor of at most 8 dimensions");
+        return nullptr;
+      }
+      const c10::Device device = t.device();
+      layout[used++] = static_cast<int64_t>(t.scalar_type()) | static_cast<int64_t>(device.type()) << 8 |
+                       static_cast<int64_t>(device.index() + 1) << 16 | t.dim() << 32;
+      for (int64_t d = 0; d < t.dim(); ++d) {
+        layout[used++] = t.size(d);
+        layout[used++] = t.stride(d);
+      }
+      address[i] = static_cast<int64_t>(reinterpret_cast<uintptr_t>(t.data_ptr()));
+    }
+  } catch (const std::exception& e) {
+    PyErr_SetString(PyExc_ValueError, e.what());
+    return nullptr;
+  }
+  return Py_BuildValue("(y#y#)", reinterpret_cast<const char*>(layout), used * static_cast<Py_ssize_t>(sizeof(int64_t)),
+                       reinterpret_cast<const char*>(address), n * static_cast<Py_ssize_t>(sizeof(int64_t)));
+}
+
+PyMethodDef methods[] = {
+    {"describe", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(describe)), METH_FASTCALL,
+     "(layouts, addresses) of tensors"},
+    {nullptr, nullptr, 0, nullptr}};
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "qi_tensors", nullptr, -1, methods};
+
+}  // namespace
+
+PyMODINIT_FUNC PyInit_qi_tensors() { return PyModule_Create(&module); }

@@ -1,5 +1,6 @@
 """Refusals of the paged operators. Arguments are checked before any device work, so this runs without a GPU."""
 import math
+import struct
 
 import pytest
 
@@ -23,8 +24,8 @@ def _rope(qi, **kw):
              pages=5, rows=32, width=4)
     assert set(kw) <= set(f)
     f.update(kw)
-    buf = qi._ROPE_HEAD.pack(*[f[n] for n in ("q", "k", "v", "qo", "ko", "vo", "q_w", "k_w", "pos", "turns", "start",
-                                              "lens", "table", "plus", "eps")])
+    buf = struct.pack("@13P", *[f[n] for n in ("q", "k", "v", "qo", "ko", "vo", "q_w", "k_w", "pos", "turns", "start",
+                                               "lens", "table")]) + qi._ROPE_HEAD.pack(f["plus"], f["eps"])
     buf += qi._ROPE_TAIL.pack(*[x for n in ("qs", "ks", "vs", "qos", "kos", "vos") for x in f[n]], f["ts"], f["ind"],
                               f["d"], f["wf"], f["B"], f["T"], f["Hq"], f["Hkv"], f["axes"], *f["pairs"], f["halves"],
                               f["pages"], f["rows"], f["width"])
@@ -61,8 +62,8 @@ def _attn(qi, **kw):
              Hkv=2, pages=5, rows=32, width=4, most=128)
     assert set(kw) <= set(f)
     f.update(kw)
-    buf = qi._PAGED_HEAD.pack(*[f[n] for n in ("q", "k", "v", "o", "table", "kv_len", "q_len", "ws", "status", "causal",
-                                               "scale")])
+    buf = struct.pack("@9P", *[f[n] for n in ("q", "k", "v", "o", "table", "kv_len", "q_len", "ws", "status")])
+    buf += qi._PAGED_HEAD.pack(f["causal"], f["scale"])
     buf += qi._PAGED_TAIL.pack(f["ws_bytes"], *[x for n in ("qs", "ks", "vs", "os") for x in f[n]],
                                *[f[n] for n in ("ts", "d", "B", "T", "Hq", "Hkv", "pages", "rows", "width", "most")])
     st = qi.lib().qi_paged_attention(buf, None)
@@ -129,3 +130,26 @@ def test_rope_handles(qi):
                 dict(theta=0.0), dict(theta=-2.0)):
         with pytest.raises(ValueError):
             qi.rope(device="cpu", **bad)
+
+
+def test_descriptions_tell_layouts_apart(qi):
+    """Equal bytes only for tensors of one type, device, shape and strides; addresses beside them."""
+    import torch
+    t = torch.zeros(4, 6, 8)
+    same = qi._describe(t)[0]
+    assert qi._describe(torch.ones(4, 6, 8))[0] == same
+    others = [t.half(), t.int(), t[:3], t.transpose(0, 1), t[:, ::2], t.view(4, 48), t.view(2, 2, 6, 8), t[0], None,
+              torch.zeros(4, 6, 8, device="meta")]
+    keys = [qi._describe(x)[0] for x in others]
+    assert len({same, *keys}) == len(others) + 1
+    assert qi._describe(t, None)[0] != qi._describe(None, t)[0]
+    assert struct.unpack("@3Q", qi._describe(t, None, t[1])[1]) == (t.data_ptr(), 0, t[1].data_ptr())
+    for bad in (3, "x", [t]):
+        with pytest.raises(TypeError):
+            qi._describe(bad)
+    with pytest.raises(ValueError):
+        qi._describe(torch.eye(3).to_sparse())
+    with pytest.raises(ValueError):
+        qi._describe(*[t] * 25)
+    with pytest.raises(ValueError):
+        qi._describe(torch.zeros([1] * 9))
