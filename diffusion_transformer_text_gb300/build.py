@@ -23,7 +23,8 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libqidit.so")
 TENSORS = os.path.join(BUILD, "qi_tensors.so")  # the binding's reader of tensor arguments (csrc/tensors.cpp)
 SOURCES = ["qidit.cu", "gemm.cu", "attention.cu", "kernels_small.cu", "gemm_noalloc.cu", "prefix_attention.cu",
-           "prefix_attention_few.cu", "batch_ops.cu", "rope_ops.cu"]
+           "prefix_attention_few.cu", "paged_attention.cu",
+           "batch_ops.cu", "rope_ops.cu"]
 HEADERS = ["ptx.cuh", "internal.h", "prefix_attention.cuh", "values.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xptxas", "-v",

@@ -81,7 +81,7 @@ static_assert(kRegsLow <= 128 && kRegsHigh >= 128 && kRegsEpi <= 128 && kRegsLow
 // tile up by 700 cycles.
 constexpr int kMessages = 4;
 struct __align__(16) Message {
-  int n, pn, p0, o0;  // p0: with pages, which have no prefix, the sequence's query rows
+  int n, pn, p0, o0;
   int t0, b0, len, rows;
   int h, u;
   long long slot;
@@ -118,16 +118,13 @@ __device__ __forceinline__ uint32_t bar_count(int i) {
   if ((i >= kPFull && i < kPFull + 4) || i == kOEmpty || i == kLFree) return 4;
   return 1;
 }
-constexpr int kSmemBase = (kQBufs + kKStages + kVStages) * kTile + 1024 + kNumBars * 8 + 16 + 2 * 2 * kRows * 4 + 16 +
-                          kMessages * static_cast<int>(sizeof(Message));
-using FlowFull = Flow<2048>;
-template <typename P>
-constexpr int kSmem = kSmemBase + (kFlow<P> ? static_cast<int>(sizeof(FlowFull)) : 0);
-static_assert(kSmem<FlowParams> <= 227 * 1024 && kThreads >= kFlowThreads, "shared memory over the per-block limit");
+constexpr int kSmem = (kQBufs + kKStages + kVStages) * kTile + 1024 + kNumBars * 8 + 16 + 2 * 2 * kRows * 4 + 16 +
+                      kMessages * static_cast<int>(sizeof(Message));
+static_assert(kSmem <= 227 * 1024, "shared memory over the per-block limit");
 
-template <bool BF16, bool JOIN, typename P>
+template <bool BF16, bool JOIN>
 __global__ void __launch_bounds__(kThreads, 1)
-    prefix_attn_tc(const __grid_constant__ Maps tm, const __grid_constant__ P p, float scale_log2) {
+    prefix_attn_tc(const __grid_constant__ Maps tm, const __grid_constant__ Params p, float scale_log2) {
   constexpr uint32_t kIdescQK = BF16 ? idesc_bf16_f32(128, kKeys) : idesc_f16_f32(128, kKeys);
   constexpr uint32_t kIdescPV = BF16 ? idesc_bf16_f32_bmn(128, 128) : idesc_f16_f32_bmn(128, 128);
   extern __shared__ uint8_t smem_raw[];
@@ -144,7 +141,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  FlowFull* pieces = reinterpret_cast<FlowFull*>(messages + kMessages);
+  const int total = p.pl.units;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kNumBars; ++i) mbar_init(&bars[i], bar_count(i));
@@ -171,9 +168,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tmem_slot;
   grid_dep_wait();
   grid_dep_launch_dependents();
-  if constexpr (kFlow<P>) {
-    flow_pieces(p, *pieces);
-  }
 
   if (warp < 4) {
     regs_release<kRegsLow>();
@@ -183,30 +177,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       // only stops its waits and loads, so the warp meets at every cleared tile.
       uint32_t t = 0;
       bool ok = true;
-      for (Walk<P, FlowFull> w(p, pieces); w.more(p); w.step(p)) {
-        const Unit un = w.unit(p);
-        if constexpr (kPaged<P>) {
-          // by pages, a lane a box: a tile's pages are looked up while the one before it waits for its stage
-          ok = __shfl_sync(0xffffffffu, static_cast<int>(ok), 0);
-          int next = page_of(p, un, un.o0 * kKeys, lane);
-          for (int j = 0; ok && j < un.n; ++j) {
-            const uint32_t tt = t + j, st = tt % kVStages;
-            const int key0 = (un.o0 + j) * kKeys, id = next;
-            if (j + 1 < un.n) next = page_of(p, un, key0 + kKeys, lane);
-            ok = __all_sync(0xffffffffu, !*abort_flag && mbar_wait(&bars[kVEmpty + st], ((tt / kVStages) & 1u) ^ 1u));
-            if (!ok) {
-              if (lane == 0) {
-                if (!*abort_flag) report_error(p.err, kErrTimeoutProducer);
-                *abort_flag = 1;
-              }
-              t = tt;  // tiles issued, for the drain below
-              break;
-            }
-            if (lane == 0) mbar_arrive_expect_tx(&bars[kVFull + st], kTile);
-            __syncwarp();
-            load_pages(p, &tm.v, sV + st * kTile, &bars[kVFull + st], un.h, key0, id, lane);
-          }
-        } else if (lane == 0 && ok) {
+      for (int u = blockIdx.x; u < total; u += gridDim.x) {
+        const Unit un = unit_of(p, u);
+        if (lane == 0 && ok) {
           for (int j = 0; j < un.n; ++j) {
             const uint32_t tt = t + j, st = tt % kVStages;
             if (*abort_flag || !mbar_wait(&bars[kVEmpty + st], ((tt / kVStages) & 1u) ^ 1u)) {
@@ -262,8 +235,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t t = 0;
       uint32_t ku = 0, cleared = 0;
       bool ok = true;
-      for (Walk<P, FlowFull> w(p, pieces); ok && w.more(p); w.step(p)) {
-        const Unit un = w.unit(p);
+      for (int u = blockIdx.x; ok && u < total; u += gridDim.x) {
+        const Unit un = unit_of(p, u);
         if (un.n == 0) continue;
         ok = __all_sync(0xffffffffu, !*abort_flag);
         if (!ok) break;
@@ -307,51 +280,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
     } else if (warp == 0) {
-      // ---------------- TMA producer of the K tiles and of each unit's Q rows (lane 0; with pages the
-      // whole warp, a lane a box)
-      if (kPaged<P> || lane == 0) {
+      // ---------------- TMA producer of the K tiles and of each unit's Q rows (lane 0)
+      if (lane == 0) {
       uint32_t t = 0;
       uint32_t nq = 0, nm = 0;
       bool ok = true;
-      for (Walk<P, FlowFull> w(p, pieces); ok && w.more(p); w.step(p)) {
-        const Unit un = w.unit(p);
-        const int u = w.u;
-if constexpr (kPaged<P>) {
-          const uint32_t mb = nm % kMessages, qb = nq % kQBufs;
-          ok = __all_sync(0xffffffffu, !*abort_flag && mbar_wait(&bars[kUEmpty + mb], ((nm / kMessages) & 1u) ^ 1u));
-          if (ok && lane == 0) {
-            messages[mb] = {un.n, 0, un.tq, un.o0, un.t0, un.b0, un.len, un.rows, un.h, u, un.slot};
-            mbar_arrive(&bars[kUFull + mb]);
-          }
-          ++nm;
-          if (ok && un.n > 0) {
-            ok = __all_sync(0xffffffffu, !*abort_flag && mbar_wait(&bars[kQEmpty + qb], ((nq / kQBufs) & 1u) ^ 1u));
-            if (ok) {
-              if (lane == 0) {
-                mbar_arrive_expect_tx(&bars[kQFull + qb], static_cast<uint32_t>(un.rows) * 256u);
-                tma_load_5d(sQ + qb * kTile, &tm.qo, &bars[kQFull + qb], 0, 0, un.h, un.t0, un.b0);
-                tma_load_5d(sQ + qb * kTile + kBox, &tm.qo, &bars[kQFull + qb], 64, 0, un.h, un.t0, un.b0);
-              }
-              ++nq;
-            }
-            int next = page_of(p, un, un.o0 * kKeys, lane);
-            for (int j = 0; ok && j < un.n; ++j) {
-              const uint32_t st = t % kKStages;
-              const int key0 = (un.o0 + j) * kKeys, id = next;
-              if (j + 1 < un.n) next = page_of(p, un, key0 + kKeys, lane);
-              ok = __all_sync(0xffffffffu, !*abort_flag && mbar_wait(&bars[kKEmpty + st], ((t / kKStages) & 1u) ^ 1u));
-              if (!ok) break;
-              if (lane == 0) mbar_arrive_expect_tx(&bars[kKFull + st], kTile);
-              __syncwarp();
-              load_pages(p, &tm.k, sK + st * kTile, &bars[kKFull + st], un.h, key0, id, lane);
-              ++t;
-            }
-          }
-          if (!ok && lane == 0) {
-            if (!*abort_flag) report_error(p.err, kErrTimeoutProducer);
-            *abort_flag = 1;
-          }
-        } else {
+      for (int u = blockIdx.x; ok && u < total; u += gridDim.x) {
+        const Unit un = unit_of(p, u);
         const uint32_t mb = nm % kMessages;
         if (*abort_flag || !mbar_wait(&bars[kUEmpty + mb], ((nm / kMessages) & 1u) ^ 1u)) {
           if (!*abort_flag) report_error(p.err, kErrTimeoutProducer);
@@ -389,19 +324,10 @@ if constexpr (kPaged<P>) {
           tma_load_4d(sK + st * kTile, m, &bars[kKFull + st], 0, un.h, row, bs);
           tma_load_4d(sK + st * kTile + kBox, m, &bars[kKFull + st], 64, un.h, row, bs);
         }
-        }
       }
-      if constexpr (kFlow<P>) {  // no more units
-        const uint32_t mb = nm % kMessages;
-        ok = __all_sync(0xffffffffu, ok && !*abort_flag && mbar_wait(&bars[kUEmpty + mb], ((nm / kMessages) & 1u) ^ 1u));
-        if (ok && lane == 0) {
-          messages[mb].n = -1;
-          mbar_arrive(&bars[kUFull + mb]);
-        }
-      }
-      for (uint32_t i = t > kKStages ? t - kKStages : 0; lane == 0 && i < t; ++i)
+      for (uint32_t i = t > kKStages ? t - kKStages : 0; i < t; ++i)
         if (!mbar_wait(&bars[kKFull + i % kKStages], (i / kKStages) & 1u)) report_error(p.err, kErrTimeoutDrain);
-      for (uint32_t i = nq > kQBufs ? nq - kQBufs : 0; lane == 0 && i < nq; ++i)
+      for (uint32_t i = nq > kQBufs ? nq - kQBufs : 0; i < nq; ++i)
         if (!mbar_wait(&bars[kQFull + i % kQBufs], (i / kQBufs) & 1u)) report_error(p.err, kErrTimeoutDrain);
       }
       __syncwarp();
@@ -412,8 +338,8 @@ if constexpr (kPaged<P>) {
       uint32_t t = 0;
       uint32_t ku = 0;
       bool ok = true;
-      for (Walk<P, FlowFull> w(p, pieces); ok && w.more(p); w.step(p)) {
-        const Unit un = w.unit(p);
+      for (int u = blockIdx.x; ok && u < total; u += gridDim.x) {
+        const Unit un = unit_of(p, u);
         if (un.n == 0) continue;
         const uint32_t qb = ku % kQBufs;
         ok = __all_sync(0xffffffffu, !*abort_flag && mbar_wait(&bars[kQFull + qb], (ku / kQBufs) & 1u));
@@ -466,16 +392,15 @@ if constexpr (kPaged<P>) {
     uint32_t t = 0;
     uint32_t ku = 0, km = 0;
     bool ok = true;
-    for (int u = blockIdx.x; kFlow<P> || u < p.pl.units; u += gridDim.x, ++km) {
+    for (int u = blockIdx.x; u < total; u += gridDim.x, ++km) {
       const uint32_t mb = km % kMessages;
       ok = __all_sync(0xffffffffu, mbar_wait(&bars[kUFull + mb], (km / kMessages) & 1u));
       if (!ok) break;
       const Message un = messages[mb];
-      if (kFlow<P> && un.n < 0) break;
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars[kUEmpty + mb]);
       if (un.n == 0) continue;
-      const int lim_own = own_lim(p, un.len, un.t0 + tok, kPaged<P> ? un.p0 : p.T);
+      const int lim_own = own_lim(p, un.len, un.t0 + tok, p.T);
       // A warp whose 32 rows lie past the block's has nothing to compute: it only keeps the
       // barriers' counts (its lanes of S, P and O hold whatever they held). It still waits
       // for every S, so it is never a phase ahead of the other warps on a P buffer.
@@ -484,9 +409,9 @@ if constexpr (kPaged<P>) {
       float l = 0.f;
       // keys of this half of the tile that the row sees, counted down by tile (few live values:
       // the loop runs at its register limit, and the tile numbers kept instead cost 1.5 %)
-      int left = kPaged<P> ? 0 : p.P - un.p0 * kKeys - h * 64;
+      int left = p.P - un.p0 * kKeys - h * 64;
       const int left_own = lim_own - un.o0 * kKeys - h * 64;
-      const int n = un.n, pn = kPaged<P> ? 0 : un.pn;
+      const int n = un.n, pn = un.pn;
       for (int j = 0; j < n; ++j) {
         const uint32_t tt = t + j;
         const uint32_t b = tt & 1u;
@@ -621,28 +546,26 @@ if constexpr (kPaged<P>) {
     const int g = rit - tok * p.pl.G;
     bool ok = true;
     uint32_t ku = 0, km = 0;
-    for (int u = blockIdx.x; ok && (kFlow<P> || u < p.pl.units); u += gridDim.x, ++km) {
+    for (int u = blockIdx.x; ok && u < total; u += gridDim.x, ++km) {
       const uint32_t mb = km % kMessages;
       ok = __all_sync(0xffffffffu, mbar_wait(&bars[kUFull + mb], (km / kMessages) & 1u));
       if (!ok) break;
       const Message un = messages[mb];
-      if (kFlow<P> && un.n < 0) break;
-      const bool part = kFlow<P> ? un.slot >= 0 : p.pl.split;  // (unless JOIN) the rows are not all the keys'
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars[kUEmpty + mb]);
       // where the row goes: token and sequence (a prefix block runs over sequences)
       int b = un.b0, tk = un.t0 + tok;
-      if (!kPaged<P> && u < p.pl.units_p) {
+      if (u < p.pl.units_p) {
         const int q = quot(p.d_T, tok);
         b += q;
         tk = tok - q * p.T;
       }
-      const bool mine = rit < un.rows && tk < (kPaged<P> ? un.p0 : p.T) && b < p.B;
+      const bool mine = rit < un.rows && tk < p.T && b < p.B;
       uint16_t* orow = p.o + b * p.ob + tk * p.orow + static_cast<long long>(un.h * p.pl.G + g) * p.oh;
       if (un.n == 0) {
         if (JOIN) *reinterpret_cast<float2*>(smem + kJoinMl + rit * 8) = make_float2(-INFINITY, 0.f);
         // no key at all: a joint unit that is its row's only one writes zeros
-        if (!JOIN && !part && mine) {
+        if (!JOIN && !p.pl.split && mine) {
 #pragma unroll
           for (int i = 0; i < 16; ++i) reinterpret_cast<uint4*>(orow)[i] = make_uint4(0u, 0u, 0u, 0u);
         }
@@ -660,9 +583,9 @@ if constexpr (kPaged<P>) {
       const float a0 = mm == -INFINITY ? 1.f : fast_exp2(m0 - mm);
       const float a1 = mm == -INFINITY ? 1.f : fast_exp2(m1 - mm);
       const float den = l0 * a0 + l1 * a1;
-      const float inv = JOIN || part ? 1.f : (den == 0.f ? 0.f : 1.f / den);
+      const float inv = JOIN || p.pl.split ? 1.f : (den == 0.f ? 0.f : 1.f / den);
       const float w0 = a0 * inv, w1 = a1 * inv;
-      if (!JOIN && part && mine) p.ml[un.slot + rit] = make_float2(mm, den);
+      if (!JOIN && p.pl.split && mine) p.ml[un.slot + rit] = make_float2(mm, den);
       ok = __all_sync(0xffffffffu, mbar_wait(&bars[kOFull], ku & 1u));
       if (!ok) break;
       if (quarter * 32 >= un.rows) {  // none of the warp's rows are the block's
@@ -707,7 +630,7 @@ if constexpr (kPaged<P>) {
             float4* d = reinterpret_cast<float4*>(smem + (rit * kJoinPitch + c * 16) * 4);
 #pragma unroll
             for (int i = 0; i < 4; ++i) d[i] = make_float4(ov[4 * i], ov[4 * i + 1], ov[4 * i + 2], ov[4 * i + 3]);
-          } else if (part) {
+          } else if (p.pl.split) {
             float* d = p.part + (un.slot + rit) * kHeadDim + c * 16;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -839,96 +762,6 @@ __global__ void __launch_bounds__(kMergeWarps * 32) merge_partials(const __grid_
       make_uint2(pack16<BF16>(acc.x * inv, acc.y * inv), pack16<BF16>(acc.z * inv, acc.w * inv));
 }
 
-// Joins the parts of a block that was cut (see Flow): block x has the one that piece x took over and ended.
-// A warp has ROWS rows, their loads in flight together, and W warps a row where parts are many: warp w takes
-// parts w, w + W, .., and the W sums are added in order.
-template <bool BF16, int ROWS, int W>
-__global__ void __launch_bounds__(kMergeWarps * 32) merge_flow(const __grid_constant__ FlowParams p) {
-  __shared__ float4 sacc[W > 1 ? kMergeWarps : 1][32];
-  __shared__ float sden[kMergeWarps];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, w = warp % W, last = static_cast<int>(blockIdx.x);
-  const int r0 = (static_cast<int>(blockIdx.y) * (kMergeWarps / W) + warp / W) * ROWS;
-  grid_dep_wait();
-  grid_dep_launch_dependents();
-  const int4 end = p.rec[2 * last];
-  if (end.x < 0 || !end.z) return;  // (the whole block)
-  const int first = end.w, parts = last - first + 1;
-  // part k: what piece `first` left, then what piece first + k took over (none, if it is empty)
-  const auto slot = [&](int k) {
-    return (2ll * (first + k) + (k == 0 ? 1 : 0)) * p.pl.rows_o;
-  };
-  const auto used = [&](int k) {
-    if (k == 0) return true;
-    const int4 x = p.rec[2 * (first + k)];
-    return x.x == end.x && x.y == end.y;
-  };
-  const int b = quot(p.d_nqb, end.x), t0 = (end.x - b * p.pl.nqb) * p.pl.tb, tq = query_rows(p, b);
-  float m[ROWS], den[ROWS];
-  float4 acc[ROWS];
-#pragma unroll
-  for (int i = 0; i < ROWS; ++i) {
-    m[i] = -INFINITY;
-    den[i] = 0.f;
-    acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-  }
-  for (int k = lane; k < parts; k += 32) {
-    const bool u = used(k);
-#pragma unroll
-    for (int i = 0; i < ROWS; ++i)
-      if (r0 + i < p.pl.rows_o) {
-        const float x = p.ml[slot(k) + r0 + i].x;  // (what an empty piece's holds is not used)
-        m[i] = u ? fmaxf(m[i], x) : m[i];
-      }
-  }
-#pragma unroll
-  for (int i = 0; i < ROWS; ++i)
-#pragma unroll
-    for (int d = 16; d; d >>= 1) m[i] = fmaxf(m[i], __shfl_xor_sync(0xffffffffu, m[i], d));
-#pragma unroll 2
-  for (int k = w; k < parts; k += W) {
-    if (!used(k)) continue;
-#pragma unroll
-    for (int i = 0; i < ROWS; ++i) {
-      if (r0 + i >= p.pl.rows_o) break;
-      const long long s = slot(k) + r0 + i;
-      const float2 ml = p.ml[s];
-      const float4 v = reinterpret_cast<const float4*>(p.part + s * kHeadDim)[lane];
-      // (a part in which the row sees no key; m = -inf with another sum is a row of NaN scores, which stays one)
-      const bool none = ml.x == -INFINITY && ml.y == 0.f;
-      const float a = m[i] == -INFINITY ? 1.f : fast_exp2(ml.x - m[i]);
-      den[i] += none ? 0.f : ml.y * a;
-      acc[i].x += none ? 0.f : v.x * a;
-      acc[i].y += none ? 0.f : v.y * a;
-      acc[i].z += none ? 0.f : v.z * a;
-      acc[i].w += none ? 0.f : v.w * a;
-    }
-  }
-  if (W > 1) {  // (ROWS is 1)
-    sacc[warp][lane] = acc[0];
-    if (lane == 0) sden[warp] = den[0];
-    __syncthreads();
-    if (w != 0) return;
-#pragma unroll
-    for (int i = 1; i < W; ++i) {
-      const float4 v = sacc[warp + i][lane];
-      den[0] += sden[warp + i];
-      acc[0].x += v.x;
-      acc[0].y += v.y;
-      acc[0].z += v.z;
-      acc[0].w += v.w;
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < ROWS; ++i) {
-    const int r = r0 + i, tok = quot(p.d_G, r), t = t0 + tok;
-    if (r >= p.pl.rows_o || t >= tq) break;
-    const float inv = den[i] == 0.f ? 0.f : 1.f / den[i];
-    uint16_t* orow = p.o + b * p.ob + t * p.orow + static_cast<long long>(end.y * p.pl.G + r - tok * p.pl.G) * p.oh;
-    reinterpret_cast<uint2*>(orow)[lane] = make_uint2(pack16<BF16>(acc[i].x * inv, acc[i].y * inv),
-                                                      pack16<BF16>(acc[i].z * inv, acc[i].w * inv));
-  }
-}
-
 // ---------------------------------------------------------------- host
 
 qi_status op_fail(qi_status st, const char* fmt, ...) {
@@ -980,10 +813,6 @@ constexpr float kFlowStart = 5.f;           // cutting them, and a second launch
 constexpr float kPiece = 256.f;             // tiles of a piece where blocks share keys
 constexpr float kEvenFrom = 48.f;           // tiles a CTA from which unequal chunks are worth cutting
 constexpr int kFewTiles = 4;                // so few in a unit, and their number does not matter
-struct Sizes {
-  int B, T, Hq, Hkv, P, S, causal;
-  bool from8, paged, ragged;  // ragged: of a cache in pages, whose chunks have lengths of their own
-};
 Plan make_plan(const Sizes& z, int sms) {
   Plan a{};
   a.G = z.Hq / z.Hkv;
@@ -1007,7 +836,7 @@ Plan make_plan(const Sizes& z, int sms) {
     }
   };
   const float convert = z.from8 && z.P > 0 ? kConvertStart + kConvert * static_cast<float>(z.P) * z.Hkv * kHeadDim / (1 << 20) : 0.f;
-const bool even =
+  const bool even =
       z.paged && (z.T <= kRows / a.G ||
                   (z.ragged && z.B > 1 && static_cast<float>(ceil_div(z.T, kRows / a.G)) * z.B * z.Hkv * (a.ot + kFullCost) > kEvenFrom * sms));
   // joint units, every number of chunks that keeps the grid within a few waves
@@ -1158,10 +987,6 @@ size_t partial_rows(const Plan& pl) {
                      static_cast<size_t>(pl.units - pl.units_p) * pl.rows_o) * pl.per
                   : 0;
 }
-// workspace: the prefix in 16 bits (8-bit prefix only), partial O rows, their (max, sum), pieces' records
-struct WsLayout {
-  size_t pk, pv, part, ml, rec, total;
-};
 WsLayout ws_layout(const Plan& pl, int P, int Hkv, bool from8) {
   WsLayout w{};
   const size_t pre = from8 && !pl.few ? align256(static_cast<size_t>(P) * Hkv * kHeadDim * 2) : 0;
@@ -1175,12 +1000,6 @@ WsLayout ws_layout(const Plan& pl, int P, int Hkv, bool from8) {
   return w;
 }
 
-// A stride of a dimension of size 1 is never followed: any legal value will do.
-bool fix_stride(long long* s, int size) {
-  if (size == 1) *s = 8;
-  return *s > 0 && *s % 8 == 0 && *s < (1ll << 38);
-}
-
 bool map_kv(CUtensorMap* m, const Tensor4& t, int heads, int rows, int batch) {
   const unsigned long long dims[4] = {kHeadDim, static_cast<unsigned long long>(heads),
                                       static_cast<unsigned long long>(rows), static_cast<unsigned long long>(batch)};
@@ -1188,16 +1007,6 @@ bool map_kv(CUtensorMap* m, const Tensor4& t, int heads, int rows, int batch) {
                                      static_cast<unsigned long long>(t.row) * 2,
                                      static_cast<unsigned long long>(t.batch) * 2};
   const unsigned box[4] = {64, 1, kKeys, 1};
-  return encode_map_nd(m, t.data, false, 4, dims, str, box);
-}
-
-bool map_pages(CUtensorMap* m, const Tensor4& t, int heads, int page_rows, int pages) {
-  const unsigned long long dims[4] = {kHeadDim, static_cast<unsigned long long>(heads),
-                                      static_cast<unsigned long long>(page_rows), static_cast<unsigned long long>(pages)};
-  const unsigned long long str[3] = {static_cast<unsigned long long>(t.head) * 2,
-                                     static_cast<unsigned long long>(t.row) * 2,
-                                     static_cast<unsigned long long>(t.batch) * 2};
-  const unsigned box[4] = {64, 1, static_cast<unsigned>(page_rows < kKeys ? page_rows : kKeys), 1};
   return encode_map_nd(m, t.data, false, 4, dims, str, box);
 }
 
@@ -1236,23 +1045,7 @@ qi_status check_sizes(const qi_prefix_attn* a) {
 }
 
 template <bool BF16, typename P>
-cudaError_t launch_join(const Maps& tm, const P& p, float scale_log2, cudaStream_t stream) {
-  static std::atomic<unsigned long long> attr_done{0};
-  const cudaError_t e = ensure_smem_limit(prefix_attn_tc<BF16, true, P>, kSmem<P>, attr_done);
-  if (e != cudaSuccess) return e;
-  return launch_clusters(prefix_attn_tc<BF16, true, P>, p.pl.nch, dim3(p.pl.units), dim3(kThreads), kSmem<P>, stream, tm,
-                         p, scale_log2);
-}
-template <bool BF16, typename P>
-cudaError_t launch_walk(const Maps& tm, const P& p, float scale_log2, int grid, cudaStream_t stream) {
-  static std::atomic<unsigned long long> attr_done{0};
-  const cudaError_t e = ensure_smem_limit(prefix_attn_tc<BF16, false, P>, kSmem<P>, attr_done);
-  if (e != cudaSuccess) return e;
-  return launch_dependent(prefix_attn_tc<BF16, false, P>, dim3(grid), dim3(kThreads), kSmem<P>, stream, tm, p, scale_log2);
-}
-
-template <bool BF16, typename P>
-cudaError_t launch_merge(const P& p, cudaStream_t stream) {
+cudaError_t launch_merge_as(const P& p, cudaStream_t stream) {
   // Warps per row: as many as its parts keep busy, unless the rows alone fill the GPU (1024
   // rows of 16 parts, with the attention before it: 31.6 us at one warp a row, 29.4 at 4 or 8)
   const long long rows = static_cast<long long>(p.B) * p.T * p.Hq;
@@ -1269,35 +1062,22 @@ cudaError_t launch_merge(const P& p, cudaStream_t stream) {
 template <bool BF16>
 cudaError_t launch(const Maps& tm, const Maps8* t8, const Params& p, float scale_log2, int sms, cudaStream_t stream) {
   cudaError_t e;
-  if (p.pl.few)
+  if (p.pl.few) {
     e = launch_few(tm, t8, p, BF16, scale_log2, sms, stream);
-  else if (p.pl.join)
-    e = launch_join<BF16>(tm, p, scale_log2, stream);
-  else
-    e = launch_walk<BF16>(tm, p, scale_log2, p.pl.units < sms ? p.pl.units : sms, stream);
-  return e != cudaSuccess || !p.pl.split ? e : launch_merge<BF16>(p, stream);
-}
-
-template <bool BF16>
-cudaError_t launch_paged(const Maps& tm, const FlowParams& f, float scale_log2, int sms, cudaStream_t stream) {
-  const Plan& pl = f.pl;
-  const PagedParams& p = f;
-  if (pl.join)
-    return pl.few ? launch_few(tm, p, BF16, scale_log2, stream) : launch_join<BF16>(tm, p, scale_log2, stream);
-  if (!pl.flow) {
-    const cudaError_t e = launch_walk<BF16>(tm, p, scale_log2, pl.units < sms ? pl.units : sms, stream);
-    return e != cudaSuccess || !pl.split ? e : launch_merge<BF16>(p, stream);
+  } else {
+    static std::atomic<unsigned long long> attr_done{0}, attr_done_join{0};
+    if (p.pl.join) {
+      e = ensure_smem_limit(prefix_attn_tc<BF16, true>, kSmem, attr_done_join);
+      if (e != cudaSuccess) return e;
+      return launch_clusters(prefix_attn_tc<BF16, true>, p.pl.nch, dim3(p.pl.units), dim3(kThreads), kSmem, stream, tm, p,
+                             scale_log2);
+    }
+    e = ensure_smem_limit(prefix_attn_tc<BF16, false>, kSmem, attr_done);
+    if (e != cudaSuccess) return e;
+    const int grid = p.pl.units < sms ? p.pl.units : sms;
+    e = launch_dependent(prefix_attn_tc<BF16, false>, dim3(grid), dim3(kThreads), kSmem, stream, tm, p, scale_log2);
   }
-  const cudaError_t e = pl.few ? launch_few(tm, f, BF16, scale_log2, stream)
-                               : launch_walk<BF16>(tm, f, scale_log2, pl.units, stream);
-  const int pieces = pl.units * pl.flow;
-  if (e != cudaSuccess || pieces == 1) return e;
-  // few rows may have many parts, many rows have two or three
-  constexpr int kRowsEach = 4, kWarpsEach = 4;
-  const auto kernel = pl.few ? merge_flow<BF16, 1, kWarpsEach> : merge_flow<BF16, kRowsEach, 1>;
-  const int each = pl.few ? kMergeWarps / kWarpsEach : kMergeWarps * kRowsEach;
-  return launch_dependent(kernel, dim3(pieces, static_cast<unsigned>(ceil_div(pl.rows_o, each))), dim3(kMergeWarps * 32), 0,
-                          stream, f);
+  return e != cudaSuccess || !p.pl.split ? e : launch_merge_as<BF16>(p, stream);
 }
 
 // What does not come from where the keys are
@@ -1355,6 +1135,17 @@ cudaError_t expired_word(int** word) {
 }
 
 }  // namespace
+
+Plan pa::plan_of(const Sizes& z, int sms) { return plan_for(z, sms); }
+WsLayout pa::workspace_of(const Plan& pl) { return ws_layout(pl, 0, 0, false); }
+void pa::set_params(Params* p, const Plan& pl, const Sizes& z, const Tensor4& o) { fill_params(p, pl, z, o); }
+bool pa::map_queries(CUtensorMap* m, const Tensor4& q, const Plan& pl, const Sizes& z) {
+  return map_q(m, q, pl.G, z.Hkv, z.T, z.B, pl.tb, 1, g_stall_prefix_attention.exchange(false));
+}
+cudaError_t pa::status_word(int** word) { return expired_word(word); }
+cudaError_t pa::launch_merge(const PagedParams& p, bool bf16, cudaStream_t s) {
+  return bf16 ? launch_merge_as<true>(p, s) : launch_merge_as<false>(p, s);
+}
 
 int device_sms() {
   static std::atomic<int> cached[64];
@@ -1494,104 +1285,4 @@ extern "C" qi_status qi_prefix_attention_check(qi_stream_t stream) {
   if (code != 0)
     return op_fail(QI_ERR_DEVICE_TIMEOUT, "qi_prefix_attention: a kernel's bounded wait expired (device code %d)", code);
   return QI_OK;
-}
-
-namespace qi {
-namespace {
-
-// a call's sizes, checked but for what the plan makes of them
-qi_status check_paged(const qi_paged_attn* a) {
-  constexpr const char* kName = "qi_paged_attention";
-  if (!a) return op_fail(QI_ERR_INVALID_ARG, "%s: NULL argument", kName);
-  if (a->dtype != QI_DT_F16 && a->dtype != QI_DT_BF16) return op_fail(QI_ERR_INVALID_ARG, "%s: dtype %d", kName, a->dtype);
-  constexpr int kMost = 1 << 24;
-  const int n = a->page_rows;
-  if (a->B < 1 || a->B > 65535 || a->T < 1 || a->T > kMost || a->Hkv < 1 || a->Hkv > 65535 || a->Hq < a->Hkv ||
-      a->Hq % a->Hkv != 0 || a->Hq / a->Hkv > kRows || static_cast<long long>(a->B) * a->T * a->Hq >= (1ll << 31))
-    return op_fail(QI_ERR_SHAPE, "%s: B %d T %d Hq %d Hkv %d", kName, a->B, a->T, a->Hq, a->Hkv);
-  if (n < 16 || n > 65536 || (n & (n - 1)) != 0 || a->pages < 1 || a->table_width < 1 || a->max_len < 1 ||
-      a->max_len > kMost || a->max_len > static_cast<long long>(a->table_width) * n)
-    return op_fail(QI_ERR_SHAPE, "%s: pages %d of %d rows, table of %d, max_len %d", kName, a->pages, n, a->table_width,
-                   a->max_len);
-  return QI_OK;
-}
-Sizes paged_sizes(const qi_paged_attn* a) {
-  return {a->B, a->T, a->Hq, a->Hkv, 0, a->max_len, a->causal != 0, false, true, a->q_len != nullptr};
-}
-
-}  // namespace
-}  // namespace qi
-
-extern "C" size_t qi_paged_attention_workspace(const qi_paged_attn* a) {
-  using namespace qi;
-  if (check_paged(a) != QI_OK) return 0;
-  const int sms = device_sms();
-  if (sms <= 0) return 0;
-  return ws_layout(plan_for(paged_sizes(a), sms), 0, a->Hkv, false).total;
-}
-
-extern "C" qi_status qi_paged_attention(const qi_paged_attn* a, qi_stream_t stream) {
-  using namespace qi;
-  constexpr const char* kName = "qi_paged_attention";
-  const qi_status st = check_paged(a);
-  if (st != QI_OK) return st;
-  if (!a->q || !a->k || !a->v || !a->o || !a->table || !a->kv_len)
-    return op_fail(QI_ERR_INVALID_ARG, "%s: NULL q, k, v, o, table or kv_len", kName);
-  if (!(a->scale > 0.f) || !(a->scale < 3e38f))
-    return op_fail(QI_ERR_INVALID_ARG, "%s: scale must be positive and finite", kName);
-  const auto tensor = [](const void* data, const qi_strides& s) { return Tensor4{data, s.batch, s.row, s.head}; };
-  Tensor4 q = tensor(a->q, a->q_stride), o = tensor(a->o, a->o_stride);
-  Tensor4 k = tensor(a->k, a->k_stride), v = tensor(a->v, a->v_stride);
-  const auto good = [](Tensor4* t, int batch, int rows, int heads) {
-    return (reinterpret_cast<uintptr_t>(t->data) & 15) == 0 && fix_stride(&t->batch, batch) &&
-           fix_stride(&t->row, rows) && fix_stride(&t->head, heads);
-  };
-  if (!good(&q, a->B, a->T, a->Hq) || !good(&o, a->B, a->T, a->Hq) || !good(&k, a->pages, a->page_rows, a->Hkv) ||
-      !good(&v, a->pages, a->page_rows, a->Hkv))
-    return op_fail(QI_ERR_INVALID_ARG, "%s: tensors need 16-byte alignment and strides that are positive multiples of 8",
-                   kName);
-  if ((reinterpret_cast<uintptr_t>(a->table) | reinterpret_cast<uintptr_t>(a->kv_len) |
-       reinterpret_cast<uintptr_t>(a->q_len) | reinterpret_cast<uintptr_t>(a->status)) & 3)
-    return op_fail(QI_ERR_INVALID_ARG, "%s: table, kv_len, q_len and status need 4-byte alignment", kName);
-  if (a->B > 1 && (a->table_stride < a->table_width || a->table_stride >= (1ll << 38)))
-    return op_fail(QI_ERR_INVALID_ARG, "%s: table rows %lld apart", kName, a->table_stride);
-  const int sms = device_sms();
-  if (sms <= 0) return op_fail(QI_ERR_CUDA, "%s: no CUDA device", kName);
-  const Sizes z = paged_sizes(a);
-  const Plan pl = plan_for(z, sms);
-  if (pl.units <= 0) return op_fail(QI_ERR_SHAPE, "%s: too many rows and heads", kName);
-  const WsLayout w = ws_layout(pl, 0, a->Hkv, false);
-  if (w.total > 0 && (!a->ws || a->ws_bytes < w.total || (reinterpret_cast<uintptr_t>(a->ws) & 255)))
-    return op_fail(QI_ERR_INVALID_ARG, "%s: needs a 256-byte aligned workspace of %zu bytes", kName, w.total);
-  Maps tm;
-  if (!map_q(&tm.qo, q, pl.G, a->Hkv, a->T, a->B, pl.tb, 1, g_stall_prefix_attention.exchange(false)) ||
-      !map_pages(&tm.k, k, a->Hkv, a->page_rows, a->pages) || !map_pages(&tm.v, v, a->Hkv, a->page_rows, a->pages))
-    return op_fail(QI_ERR_INVALID_ARG, "%s: tensor map encoding failed (strides?)", kName);
-  tm.qp = tm.qo;  // no prefix: never loaded from
-  tm.pk = tm.k;
-  tm.pv = tm.v;
-  FlowParams p{};
-  fill_params(&p, pl, z, o);
-  p.own_len = a->kv_len;
-  p.q_len = a->q_len;
-  p.table = a->table;
-  p.table_stride = a->B > 1 ? a->table_stride : 0;
-  p.pages = a->pages;
-  while ((1 << p.page_log) < a->page_rows) ++p.page_log;
-  uint8_t* ws = static_cast<uint8_t*>(a->ws);
-  p.part = reinterpret_cast<float*>(ws + w.part);
-  p.ml = reinterpret_cast<float2*>(ws + w.ml);
-  p.err = a->status;
-  if (!p.err) {
-    const cudaError_t e = expired_word(&p.err);
-    if (e != cudaSuccess) return op_fail(QI_ERR_CUDA, "%s: %s", kName, cudaGetErrorString(e));
-  }
-  const float scale_log2 = a->scale * 1.4426950408889634f;
-  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  p.rec = reinterpret_cast<int4*>(ws + w.rec);
-  p.per_slot = ceil_div(a->B * pl.nqb, pl.few ? kFlowSlotsFew : FlowFull::kSlots);
-  p.d_slot = make_div(p.per_slot);
-  const cudaError_t e = a->dtype == QI_DT_BF16 ? launch_paged<true>(tm, p, scale_log2, sms, s)
-                                               : launch_paged<false>(tm, p, scale_log2, sms, s);
-  return e == cudaSuccess ? QI_OK : op_fail(QI_ERR_CUDA, "%s: %s", kName, cudaGetErrorString(e));
 }

@@ -460,6 +460,32 @@ cudaError_t launch_few(const Maps& tm, const Maps8* t8, const Params& p, bool bf
 cudaError_t launch_few(const Maps& tm, const PagedParams& p, bool bf16, float scale_log2, cudaStream_t s);  // pl.join
 cudaError_t launch_few(const Maps& tm, const FlowParams& p, bool bf16, float scale_log2, cudaStream_t s);
 
+// ------------------------------------------------------------------ what the host sides share (prefix_attention.cu)
+
+struct Sizes {
+  int B, T, Hq, Hkv, P, S, causal;
+  bool from8, paged, ragged;  // ragged: of a cache in pages, whose chunks have lengths of their own
+};
+
+// workspace: the prefix in 16 bits (8-bit prefix only), partial O rows, their (max, sum), pieces' records
+struct WsLayout {
+  size_t pk, pv, part, ml, rec, total;
+};
+
+Plan plan_of(const Sizes& z, int sms);
+WsLayout workspace_of(const Plan& pl);  // (without a prefix)
+// what does not come from where the keys are
+void set_params(Params* p, const Plan& pl, const Sizes& z, const Tensor4& o);
+bool map_queries(CUtensorMap* m, const Tensor4& q, const Plan& pl, const Sizes& z);
+// what launches without a status word report into, on the current device
+cudaError_t status_word(int** word);
+cudaError_t launch_merge(const PagedParams& p, bool bf16, cudaStream_t s);  // pl.split
+// A stride of a dimension of size 1 is never followed: any legal value will do.
+inline bool fix_stride(long long* s, int size) {
+  if (size == 1) *s = 8;
+  return *s > 0 && *s % 8 == 0 && *s < (1ll << 38);
+}
+
 // ------------------------------------------------------------------ parts joined by a cluster
 //
 // With pl.join the chunks of a row block are the CTAs of one cluster, one unit each, and their
