@@ -811,6 +811,7 @@ constexpr long long kL2Half = 64ll << 20;
 constexpr int kFullCost = 2, kFewCost = 2;  // of a unit, in tiles, where pieces are cut
 constexpr float kFlowStart = 5.f;           // cutting them, and a second launch
 constexpr float kPiece = 256.f;             // tiles of a piece where blocks share keys
+constexpr float kApart = 1.1f;              // pieces against units that meet in the L2
 constexpr float kEvenFrom = 48.f;           // tiles a CTA from which unequal chunks are worth cutting
 constexpr int kFewTiles = 4;                // so few in a unit, and their number does not matter
 Plan make_plan(const Sizes& z, int sms) {
@@ -839,6 +840,10 @@ Plan make_plan(const Sizes& z, int sms) {
   const bool even =
       z.paged && (z.T <= kRows / a.G ||
                   (z.ragged && z.B > 1 && static_cast<float>(ceil_div(z.T, kRows / a.G)) * z.B * z.Hkv * (a.ot + kFullCost) > kEvenFrom * sms));
+  // what a causal chunk's row blocks see of the longest sequence, on average
+  const float seen = z.paged && z.causal && z.T < z.S ? 1.f - 0.5f * static_cast<float>(z.T) / static_cast<float>(z.S)
+                     : z.paged && z.causal            ? 0.5f
+                                                      : 1.f;
   // joint units, every number of chunks that keeps the grid within a few waves
   const auto joint = [&](Plan c, Rate r, bool always_split, float more) {
     const int n = c.pt + c.ot;
@@ -853,7 +858,7 @@ Plan make_plan(const Sizes& z, int sms) {
       c.split = always_split || nch > 1;
       const float waves = static_cast<float>((blocks * nch + sms - 1) / sms);
       const float parts = c.split ? kMergeTiles + static_cast<float>(blocks * nch) * c.rows_o * c.per / kPartRows : 0.f;
-      const float cost = kStart + waves * (c.ct * each + r.of(c.rows_o)) + parts + more;
+      const float cost = kStart + waves * (c.ct * seen * each + r.of(c.rows_o)) + parts + more;
       if (cost < best_cost && blocks * nch <= INT_MAX / 2) {
         best_cost = cost;
         c.units = static_cast<int>(blocks * nch);
@@ -919,10 +924,10 @@ Plan make_plan(const Sizes& z, int sms) {
   // key on meet in the L2, and pieces do not (3 x 2461 causal rows, 16 key heads: 139 us, in pieces 168).
   const auto flow = [&](Plan c, Rate r) {
     const long long blocks = static_cast<long long>(z.B) * c.nqb * z.Hkv;
-    if (!even || blocks > INT_MAX) return;
+    if (!z.paged || blocks > INT_MAX) return;
     c.nch = c.ct = 1;
     c.cost = c.few ? kFewCost : kFullCost;
-    const float each = static_cast<float>(blocks) * (c.ot * r.tile + r.of(c.rows_o)) / sms;
+    const float each = static_cast<float>(blocks) * (c.ot * seen * r.tile + r.of(c.rows_o)) / sms * (even ? 1.f : kApart);
     const float cost = kStart + kFlowStart + each + kMergeTiles;
     if (cost < best_cost) {
       best_cost = cost;

@@ -219,57 +219,64 @@ __device__ __forceinline__ long long flow_upto(const FlowParams& p, const F& f, 
   for (int x = slot * p.per_slot; x < e; ++x) s += flow_cost(p, x);
   return s;
 }
-// where on a line of `all` piece v of n begins
-__device__ __forceinline__ long long flow_at(long long all, int v, int n) {
-  return all / n * v + all % n * v / n;
+// where on a line of `all` piece v of n begins (N: int where all fits, whose divisions are short)
+template <typename N>
+__device__ __forceinline__ N flow_at(N all, int v, int n) {
+  return all / n * v + static_cast<N>(static_cast<long long>(all % n) * v / n);
+}
+template <>
+__device__ __forceinline__ int flow_at(int all, int v, int n) {
+  return all / n * v + all % n * v / n;  // (n is below 2^15)
 }
 
-template <typename F>
-__device__ __forceinline__ FlowCut flow_cut(const FlowParams& p, const F& f, int v, int n, int* first) {
+template <typename N, typename F>
+__device__ __forceinline__ FlowCut flow_cut(const FlowParams& p, const F& f, N all, int v, int n, int* first) {
   const int nqb = p.pl.nqb, cost = p.pl.cost;
-  const long long all = flow_upto(p, f, p.B * nqb) * p.Hkv, pos = flow_at(all, v, n);
+  const N pos = flow_at<N>(all, v, n);
   if (pos >= all) return {p.B, 0, 0, 0};
+  const auto upto = [&](int e) { return static_cast<N>(flow_upto(p, f, e)); };
   int lo = 0, hi = p.B;  // the sequence: the last one that begins at or before pos
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (flow_upto(p, f, mid * nqb) * p.Hkv <= pos)
+    if (upto(mid * nqb) * p.Hkv <= pos)
       lo = mid;
     else
       hi = mid;
   }
   FlowCut x{lo, 0, 0, 0};
   const int e0 = x.b * nqb;
-  const long long base = flow_upto(p, f, e0), head = flow_upto(p, f, e0 + nqb) - base;
-  long long rest = pos - base * p.Hkv;
+  const N base = upto(e0), head = upto(e0 + nqb) - base;
+  N rest = pos - base * p.Hkv;
   x.h = static_cast<int>(rest / head);
   rest -= x.h * head;
   lo = 0, hi = nqb;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (flow_upto(p, f, e0 + mid) - base <= rest)
+    if (upto(e0 + mid) - base <= rest)
       lo = mid;
     else
       hi = mid;
   }
   x.qb = lo;
-  rest -= flow_upto(p, f, e0 + lo) - base;
-  const int tiles = flow_cost(p, e0 + lo) - cost;
+  rest -= upto(e0 + lo) - base;
   x.j = static_cast<int>(rest) - cost;
   if (x.j < kLeast) {
     x.j = 0;
-  } else if (tiles - x.j < kLeast) {
+    return x;
+  }
+  if (flow_cost(p, e0 + lo) - cost - x.j < kLeast) {
     x.j = 0;
     if (++x.qb == nqb) {
       x.qb = 0;
       if (++x.h == p.Hkv) x.h = 0, ++x.b;
     }
-  }
-  if (x.j > 0 && first) {
+  } else if (first) {
     // the first cut that stays within the block, and the piece before it
-    const long long least = pos - rest + cost + kLeast;
-    int w = static_cast<int>(static_cast<double>(least) * n / static_cast<double>(all));
-    while (flow_at(all, w, n) < least) ++w;
-    while (w > 0 && flow_at(all, w - 1, n) >= least) --w;
+    const N least = pos - rest + cost + kLeast, each = all / n;  // (a piece is each or each + 1)
+    int w = each > 0 ? v - static_cast<int>((pos - least) / each) - 1 : 0;
+    if (w < 0) w = 0;
+    while (flow_at<N>(all, w, n) < least) ++w;
+    while (w > 0 && flow_at<N>(all, w - 1, n) >= least) --w;
     *first = w - 1;
   }
   return x;
@@ -305,8 +312,11 @@ __device__ __forceinline__ void flow_pieces(const FlowParams& p, F& f) {
   __syncthreads();
   const int n = p.pl.flow * static_cast<int>(gridDim.x);
   if ((tid & 3) == 0 && tid < 8 * p.pl.flow) {
-    const int k = tid >> 2, v = (k >> 1) * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x);
-    f.cut[k] = flow_cut(p, f, v + (k & 1), n, (k & 1) ? nullptr : &f.first[k >> 1]);
+    const int k = tid >> 2, v = (k >> 1) * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x) + (k & 1);
+    int* first = (k & 1) ? nullptr : &f.first[k >> 1];
+    const long long all = flow_upto(p, f, pairs) * p.Hkv;
+    f.cut[k] = all <= 0x7fffffff ? flow_cut<int>(p, f, static_cast<int>(all), v, n, first)
+                                 : flow_cut<long long>(p, f, all, v, n, first);
   }
   __syncthreads();
   if (tid < p.pl.flow) {
