@@ -1,7 +1,7 @@
 """Python binding of libqidit.so, the GB300 Qwen-Image-2.1 DiT step library.
 
-Argument marshalling only: every step of the DiT pass runs in the library's
-CUDA kernels. Tensors are torch tensors (device memory and streams come from
+Argument marshalling only (a part of it compiled, csrc/tensors.cpp): every step of the DiT pass runs in
+the library's CUDA kernels. Tensors are torch tensors (device memory and streams come from
 PyTorch); the calls mirror include/qidit.h one to one. There is no fallback:
 if the library is missing or fails to load, `lib()` raises.
 """
@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import operator
 import os
 import struct
 from typing import NamedTuple
@@ -80,26 +81,17 @@ class SchedParams(ctypes.Structure):
 
 
 _lib = None
-_describe = None  # qi_tensors.describe, once lib() has run
 
 
 def lib() -> ctypes.CDLL:
     """Load libqidit.so (built in-tree by build()); raises if it is absent."""
-    global _lib, _describe
+    global _lib
     if _lib is not None:
         return _lib
     path = os.environ.get("QIDIT_LIB", LIB)
     if not os.path.exists(path):
         raise RuntimeError(f"{path} is missing: run diffusion_transformer_text_gb300.build() first")
     L = ctypes.CDLL(path)
-    if not os.path.exists(TENSORS):
-        raise RuntimeError(f"{TENSORS} is missing: run diffusion_transformer_text_gb300.build() first")
-    import importlib.util
-    import torch  # noqa: F401  (what the module is linked to)
-    spec = importlib.util.spec_from_file_location("qi_tensors", TENSORS)
-    tensors = importlib.util.module_from_spec(spec)
-    spec.loader.exec_module(tensors)
-    _describe = tensors.describe
     P, I, F, U, S = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_uint, ctypes.c_size_t
     sig = {
         "qi_dit_create": [ctypes.POINTER(DitConfig), I, ctypes.POINTER(P)],
@@ -686,6 +678,21 @@ def rope(axes=(16, 56, 56), theta: float = 10000.0, freqs=None, halves: bool = F
     return Rope(turns, tuple(d // 2 for d in axes), bool(halves))
 
 
+def _describe(*tensors):
+    """describe of csrc/tensors.cpp, which takes this function's place; the first call loads it and libqidit.so."""
+    global _describe
+    import importlib.util
+    import torch  # noqa: F401  (what the module is linked to)
+    lib()
+    if not os.path.exists(TENSORS):
+        raise RuntimeError(f"{TENSORS} is missing: run diffusion_transformer_text_gb300.build() first")
+    spec = importlib.util.spec_from_file_location("qi_tensors", TENSORS)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    _describe = module.describe
+    return _describe(*tensors)
+
+
 def _strided(t, dtype, shape, dev, name):
     """Strides of [.., row, head, 128] of a tensor of this type, shape and device."""
     if t.dtype != dtype or t.device != dev or tuple(t.shape) != shape:
@@ -786,8 +793,6 @@ def qk_norm_rope(q, k, v=None, rope: Rope | None = None, pos=None, q_w=None, k_w
     hold anything and are not written (and are zero in outputs that are made here). stream: default the current one of q's
     device. Returns (q_out, k_out, v_out), None for what was not given or went to the cache. No gradients."""
     import torch
-    if _lib is None:
-        lib()
     outs = (None, None, None) if out is None else out
     qo, ko, vo = outs
     if cache is None:
@@ -862,10 +867,10 @@ def paged_attention(q, cache: PagedKV, table, kv_len, q_len=None, causal: bool =
     that sees nothing is zero. status, stream and strides as for prefix_attention, whose check
     (prefix_attention_check) tells of expired waits. Returns o [B, T, Hq, 128]. No gradients."""
     import torch
-    if _lib is None:
-        lib()
     ck, cv = cache
     layout, addresses = _describe(q, ck, cv, out, table, kv_len, q_len, None, status)
+    if max_len is not None:
+        max_len = operator.index(max_len)
     key = (layout, max_len, bool(causal))
     plan = None if stream is not None else _paged_layouts.get(key)
     if plan is None or plan[0] != torch._C._cuda_getDevice():

@@ -23,8 +23,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libqidit.so")
 TENSORS = os.path.join(BUILD, "qi_tensors.so")  # the binding's reader of tensor arguments (csrc/tensors.cpp)
 SOURCES = ["qidit.cu", "gemm.cu", "attention.cu", "kernels_small.cu", "gemm_noalloc.cu", "prefix_attention.cu",
-           "prefix_attention_few.cu", "paged_attention.cu",
-           "batch_ops.cu", "rope_ops.cu"]
+           "prefix_attention_few.cu", "paged_attention.cu", "batch_ops.cu", "rope_ops.cu"]
 HEADERS = ["ptx.cuh", "internal.h", "prefix_attention.cuh", "values.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xptxas", "-v",
@@ -38,22 +37,25 @@ def nvcc() -> str:
     raise RuntimeError("nvcc not found: the CUDA 13 toolkit is required to build libqidit.so")
 
 
-def _torch_dir() -> str:
+def _torch_dir() -> str | None:
     import importlib.util
     spec = importlib.util.find_spec("torch")
-    if spec is None or not spec.submodule_search_locations:
-        raise RuntimeError("PyTorch not found: the binding is compiled against its headers")
-    return list(spec.submodule_search_locations)[0]
+    return list(spec.submodule_search_locations)[0] if spec is not None and spec.submodule_search_locations else None
 
 
 def _torch_version() -> str:
+    if _torch_dir() is None:
+        return ""
     with open(os.path.join(_torch_dir(), "version.py")) as f:
         return f.read()
 
 
 def _build_tensors() -> None:
-    """qi_tensors.so, a CPython module over PyTorch's headers (host code only)."""
+    """qi_tensors.so, a CPython module over PyTorch's headers (host code only); without PyTorch there is none, and
+    the library alone is built."""
     t, py = _torch_dir(), sysconfig.get_paths()["include"]
+    if t is None:
+        return
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
     tmp = TENSORS + ".tmp"
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-I" + py, "-I" + os.path.join(t, "include"),
@@ -62,7 +64,7 @@ def _build_tensors() -> None:
            "-lc10", "-Wl,-rpath," + os.path.join(t, "lib")]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"g++ failed on tensors.cpp:\n{r.stdout}\n{r.stderr}")
+        raise RuntimeError(f"{cmd[0]} failed on tensors.cpp:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, TENSORS)
 
 
@@ -84,7 +86,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     stamp = os.path.join(BUILD, "libqidit.stamp")
     fp = _fingerprint()
-    if not force and os.path.exists(LIB) and os.path.exists(TENSORS) and os.path.exists(stamp):
+    if not force and os.path.exists(LIB) and os.path.exists(stamp) and (os.path.exists(TENSORS) or _torch_dir() is None):
         with open(stamp) as f:
             if f.read().strip() == fp:
                 return LIB

@@ -44,7 +44,6 @@ struct __align__(16) Message {
   int n, tq, o0, rows;  // n < 0: no more units
   int t0, b0, len, h;
   long long slot;
-  long long pad;
 };
 
 enum : int {
@@ -141,7 +140,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = __all_sync(0xffffffffu, !*abort_flag && mbar_wait(&bars[kUEmpty + mb], ((nm / kMessages) & 1u) ^ 1u));
         if (!ok) break;
         if (lane == 0) {
-          messages[mb] = {un.n, un.tq, un.o0, un.rows, un.t0, un.b0, un.len, un.h, un.slot, 0};
+          messages[mb] = {un.n, un.tq, un.o0, un.rows, un.t0, un.b0, un.len, un.h, un.slot};
           mbar_arrive(&bars[kUFull + mb]);
         }
         ++nm;
@@ -606,7 +605,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) merge_flow(const __grid_cons
   const int r0 = (static_cast<int>(blockIdx.y) * (kMergeWarps / W) + warp / W) * ROWS;
   grid_dep_wait();
   grid_dep_launch_dependents();
-  const int4 end = p.rec[2 * last];
+  const int4 end = p.rec[last];
   if (end.x < 0 || !end.z) return;  // (the whole block)
   const int first = end.w, parts = last - first + 1;
   // part k: what piece `first` left, then what piece first + k took over (none, if it is empty)
@@ -615,7 +614,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) merge_flow(const __grid_cons
   };
   const auto used = [&](int k) {
     if (k == 0) return true;
-    const int4 x = p.rec[2 * (first + k)];
+    const int4 x = p.rec[first + k];
     return x.x == end.x && x.y == end.y;
   };
   const int b = quot(p.d_nqb, end.x), t0 = (end.x - b * p.pl.nqb) * p.pl.tb, tq = query_rows(p, b);

@@ -837,9 +837,10 @@ Plan make_plan(const Sizes& z, int sms) {
     }
   };
   const float convert = z.from8 && z.P > 0 ? kConvertStart + kConvert * static_cast<float>(z.P) * z.Hkv * kHeadDim / (1 << 20) : 0.f;
-  const bool even =
-      z.paged && (z.T <= kRows / a.G ||
-                  (z.ragged && z.B > 1 && static_cast<float>(ceil_div(z.T, kRows / a.G)) * z.B * z.Hkv * (a.ot + kFullCost) > kEvenFrom * sms));
+  // single tokens, or chunks of unlike lengths with enough tiles to cut
+  const bool even = z.paged && (z.T <= kRows / a.G ||
+                                (z.ragged && z.B > 1 &&
+                                 static_cast<float>(ceil_div(z.T, kRows / a.G)) * z.B * z.Hkv * (a.ot + kFullCost) > kEvenFrom * sms));
   // what a causal chunk's row blocks see of the longest sequence, on average
   const float seen = z.paged && z.causal && z.T < z.S ? 1.f - 0.5f * static_cast<float>(z.T) / static_cast<float>(z.S)
                      : z.paged && z.causal            ? 0.5f
@@ -1001,7 +1002,7 @@ WsLayout ws_layout(const Plan& pl, int P, int Hkv, bool from8) {
   w.part = 2 * pre;
   w.ml = w.part + align256(rows * kHeadDim * 4);
   w.rec = w.ml + align256(rows * 8);
-  w.total = w.rec + (pl.flow ? align256(static_cast<size_t>(pl.units) * pl.flow * 2 * sizeof(int4)) : 0);
+  w.total = w.rec + (pl.flow ? align256(static_cast<size_t>(pl.units) * pl.flow * sizeof(int4)) : 0);
   return w;
 }
 

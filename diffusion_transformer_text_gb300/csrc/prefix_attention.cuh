@@ -69,7 +69,7 @@ struct PagedParams : Params {
 struct FlowParams : PagedParams {
   int per_slot;  // (sequence, row block) pairs to a sum
   Div d_slot;    // ... as a divisor
-  int4* rec;     // what each piece begins and ends with, two a piece (see Flow)
+  int4* rec;     // the block that each piece takes over (see Flow)
 };
 template <typename P>
 constexpr bool kPaged = false;
@@ -197,8 +197,7 @@ struct Flow {
   int first[kMostRounds];        // the piece in which the block that a piece begins in began
 };
 // partial rows of piece v: of the block that it takes over, 2 v; of the one that it leaves, 2 v + 1.
-// rec[2 v] = (pair, head, whether that block ends here, piece that it began in), pair -1: none;
-// rec[2 v + 1] = (pair, head, -, -) of the one left
+// rec[v] = (pair, head, whether that block ends here, piece that it began in) of the first, pair -1: none
 
 // tiles of a pair, and whether it has rows at all
 __device__ __forceinline__ int flow_tiles(const FlowParams& p, int e, bool& live) {
@@ -323,9 +322,8 @@ __device__ __forceinline__ void flow_pieces(const FlowParams& p, F& f) {
     const int v = tid * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x);
     const FlowCut a = f.cut[2 * tid], z = f.cut[2 * tid + 1];
     const bool one = a.b == z.b && a.h == z.h && a.qb == z.qb;  // the piece ends in the block that it begins in
-    const bool takes = a.j > 0 && !(one && a.j == z.j), leaves = z.j > 0 && !(one && a.j > 0);
-    p.rec[2 * v] = make_int4(takes ? a.b * p.pl.nqb + a.qb : -1, a.h, one ? 0 : 1, takes ? f.first[tid] : 0);
-    p.rec[2 * v + 1] = make_int4(leaves ? z.b * p.pl.nqb + z.qb : -1, z.h, 0, 0);
+    const bool takes = a.j > 0 && !(one && a.j == z.j);
+    p.rec[v] = make_int4(takes ? a.b * p.pl.nqb + a.qb : -1, a.h, one ? 0 : 1, takes ? f.first[tid] : 0);
   }
 }
 

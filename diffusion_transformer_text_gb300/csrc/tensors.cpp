@@ -50,6 +50,9 @@ PyObject* describe(PyObject*, PyObject* const* args, Py_ssize_t n) {
   } catch (const std::exception& e) {
     PyErr_SetString(PyExc_ValueError, e.what());
     return nullptr;
+  } catch (...) {
+    PyErr_SetString(PyExc_RuntimeError, "tensor arguments could not be read");
+    return nullptr;
   }
   return Py_BuildValue("(y#y#)", reinterpret_cast<const char*>(layout), used * static_cast<Py_ssize_t>(sizeof(int64_t)),
                        reinterpret_cast<const char*>(address), n * static_cast<Py_ssize_t>(sizeof(int64_t)));

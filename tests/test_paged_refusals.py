@@ -153,3 +153,27 @@ def test_descriptions_tell_layouts_apart(qi):
         qi._describe(*[t] * 25)
     with pytest.raises(ValueError):
         qi._describe(torch.zeros([1] * 9))
+
+
+def test_longest_length_is_a_number(qi):
+    """The plan is kept by max_len's value: what has none that holds, or could change, is no key."""
+    import torch
+    q, cache = torch.zeros(1, 1, 2, 128, dtype=torch.float16), qi.paged_kv(4, 16, 2, torch.float16, device="cpu")
+    table, n = torch.zeros(1, 4, dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
+    for bad in (32.0, "32", [32]):
+        with pytest.raises(TypeError):
+            qi.paged_attention(q, cache, table, n, max_len=bad)
+
+
+def test_library_without_torch(qi, monkeypatch, tmp_path):
+    """The library is built and loaded without PyTorch; only what takes tensors wants the compiled reader."""
+    import importlib
+    import subprocess
+    import sys
+    code = "import sys, diffusion_transformer_text_gb300 as q; q.lib(); assert 'torch' not in sys.modules"
+    subprocess.run([sys.executable, "-c", code], check=True, cwd=importlib.import_module("oracle").__path__[0] + "/..")
+    b = importlib.import_module("diffusion_transformer_text_gb300.build")
+    monkeypatch.setattr(b, "_torch_dir", lambda: None)
+    monkeypatch.setattr(b, "TENSORS", str(tmp_path / "absent.so"))
+    b._build_tensors()
+    assert b._torch_version() == "" and not (tmp_path / "absent.so").exists()
