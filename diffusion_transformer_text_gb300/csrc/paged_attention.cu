@@ -266,6 +266,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
     } else {
       // ---------------- O += P V, a half of the keys at a time: a unit's first tile overwrites O
+      if constexpr (kFlow<P>) flow_record(p, *pieces);  // (long before the first P)
       const uint64_t vdesc0 = sw128_mnmajor_desc(smem_u32(sV), kBox, 1024);
       uint32_t t = 0, ku = 0, cleared = 0;
       bool ok = true;
@@ -838,6 +839,7 @@ extern "C" qi_status qi_paged_attention(const qi_paged_attn* a, qi_stream_t stre
   p.rec = reinterpret_cast<int4*>(ws + w.rec);
   p.per_slot = ceil_div(a->B * pl.nqb, pl.few ? kFlowSlotsFew : FlowFull::kSlots);
   p.d_slot = make_div(p.per_slot);
+  p.d_pieces = make_div(pl.flow ? pl.units * pl.flow : 1);
   const cudaError_t e = a->dtype == QI_DT_BF16 ? launch<true>(tm, p, scale_log2, sms, s)
                                                : launch<false>(tm, p, scale_log2, sms, s);
   return e == cudaSuccess ? QI_OK : op_fail(QI_ERR_CUDA, "%s: %s", kName, cudaGetErrorString(e));

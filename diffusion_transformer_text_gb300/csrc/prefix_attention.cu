@@ -808,7 +808,7 @@ constexpr float kConvert = 0.5f, kConvertStart = 2.5f;
 constexpr float kStart = 3.f;      // of a kernel whose CTAs walk the units
 constexpr float kJoinTiles = 2.6f, kJoinRow = 1.f / 32;  // start of a CTA in a cluster and its join; each row
 constexpr long long kL2Half = 64ll << 20;
-constexpr int kFullCost = 2, kFewCost = 2;  // of a unit, in tiles, where pieces are cut
+constexpr int kFullCost = 4, kFewCost = 8;  // of a unit, in 1/kLine of a tile, where pieces are cut
 constexpr float kFlowStart = 5.f;           // cutting them, and a second launch
 constexpr float kPiece = 256.f;             // tiles of a piece where blocks share keys
 constexpr float kApart = 1.1f;              // pieces against units that meet in the L2
@@ -840,7 +840,7 @@ Plan make_plan(const Sizes& z, int sms) {
   // single tokens, or chunks of unlike lengths with enough tiles to cut
   const bool even = z.paged && (z.T <= kRows / a.G ||
                                 (z.ragged && z.B > 1 &&
-                                 static_cast<float>(ceil_div(z.T, kRows / a.G)) * z.B * z.Hkv * (a.ot + kFullCost) > kEvenFrom * sms));
+                                 static_cast<float>(ceil_div(z.T, kRows / a.G)) * z.B * z.Hkv * (a.ot + 2) > kEvenFrom * sms));
   // what a causal chunk's row blocks see of the longest sequence, on average
   const float seen = z.paged && z.causal && z.T < z.S ? 1.f - 0.5f * static_cast<float>(z.T) / static_cast<float>(z.S)
                      : z.paged && z.causal            ? 0.5f

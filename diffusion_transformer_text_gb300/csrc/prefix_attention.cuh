@@ -41,7 +41,7 @@ struct Plan {
   int join;       // joint units whose chunks are a cluster of CTAs and join their parts themselves
   int per;        // partials per unit
   int flow;       // a cache in pages: even pieces of all tiles, cut on the device (FlowParams); each CTA's
-  int cost;       // ... of a unit, in tiles, beside its own
+  int cost;       // ... of a unit beside its tiles, in 1/kLine of one
 };
 
 struct Params {
@@ -69,6 +69,7 @@ struct PagedParams : Params {
 struct FlowParams : PagedParams {
   int per_slot;  // (sequence, row block) pairs to a sum
   Div d_slot;    // ... as a divisor
+  Div d_pieces;  // pl.flow x the grid
   int4* rec;     // the block that each piece takes over (see Flow)
 };
 template <typename P>
@@ -179,6 +180,7 @@ __device__ __forceinline__ Unit unit_of(const P& p, int u) {
 // heads, took each CTA twice the time a tile (3 x 2461 causal rows, 16 key heads: 205 us, units cut on the
 // host 139).
 constexpr int kLeast = 2;
+constexpr int kLineLog = 2, kLine = 1 << kLineLog;  // of the line to a tile
 constexpr int kFlowThreads = 384;  // that add up: the smaller kernel's
 constexpr int kMostRounds = 8;
 
@@ -194,21 +196,21 @@ struct Flow {
   long long sum[SLOTS + 1];  // of one head's costs of all pairs before a slot's first, and of all
   long long warp_sum[kFlowThreads / 32];
   FlowCut cut[2 * kMostRounds];  // begin and end of the CTA's pieces
-  int first[kMostRounds];        // the piece in which the block that a piece begins in began
+  long long from[kMostRounds];   // where the block that a piece begins in lies on the line
 };
 // partial rows of piece v: of the block that it takes over, 2 v; of the one that it leaves, 2 v + 1.
 // rec[v] = (pair, head, whether that block ends here, piece that it began in) of the first, pair -1: none
 
 // tiles of a pair, and whether it has rows at all
 __device__ __forceinline__ int flow_tiles(const FlowParams& p, int e, bool& live) {
-  const int b = quot(p.d_nqb, e), t0 = (e - b * p.pl.nqb) * p.pl.tb, tq = query_rows(p, b);
+  const int b = quot(p.d_nqb, e), t0 = (e - b * p.pl.nqb) * p.pl.tb, len = own_len_of(p, b), tq = query_rows(p, b);
   live = t0 < tq;
-  return live ? own_tiles(p, own_len_of(p, b), t0, p.pl.tb, tq) : 0;
+  return own_tiles(p, len, t0, p.pl.tb, tq);
 }
 __device__ __forceinline__ int flow_cost(const FlowParams& p, int e) {
   bool live;
   const int n = flow_tiles(p, e, live);
-  return live ? n + p.pl.cost : 0;
+  return live ? n * kLine + p.pl.cost : 0;
 }
 // costs of the pairs before pair e
 template <typename F>
@@ -218,67 +220,72 @@ __device__ __forceinline__ long long flow_upto(const FlowParams& p, const F& f, 
   for (int x = slot * p.per_slot; x < e; ++x) s += flow_cost(p, x);
   return s;
 }
-// where on a line of `all` piece v of n begins (N: int where all fits, whose divisions are short)
+// where on a line of `all` piece v begins: at floor(all v / pieces) (N: int where all fits)
 template <typename N>
-__device__ __forceinline__ N flow_at(N all, int v, int n) {
-  return all / n * v + static_cast<N>(static_cast<long long>(all % n) * v / n);
+__device__ __forceinline__ N flow_at(const FlowParams& p, N all, int v) {
+  const int n = static_cast<int>(p.d_pieces.d);
+  return all / n * v + all % n * v / n;
 }
 template <>
-__device__ __forceinline__ int flow_at(int all, int v, int n) {
-  return all / n * v + all % n * v / n;  // (n is below 2^15)
+__device__ __forceinline__ int flow_at(const FlowParams& p, int all, int v) {
+  const int n = static_cast<int>(p.d_pieces.d), each = quot(p.d_pieces, all);
+  return each * v + quot(p.d_pieces, (all - each * n) * v);  // (n is below 2^15)
 }
 
+// Where piece v begins, by a warp: its lanes try 32 sequences, then 32 row blocks, at a time (one after the
+// other, a lane's 9 steps for 6 sequences of 49 blocks came to 3 us, a launch's longest step). from: where the
+// block that it begins in lies on the line.
 template <typename N, typename F>
-__device__ __forceinline__ FlowCut flow_cut(const FlowParams& p, const F& f, N all, int v, int n, int* first) {
-  const int nqb = p.pl.nqb, cost = p.pl.cost;
-  const N pos = flow_at<N>(all, v, n);
+__device__ __forceinline__ FlowCut flow_cut(const FlowParams& p, const F& f, N all, int v, N& from) {
+  const int nqb = p.pl.nqb, cost = p.pl.cost, lane = threadIdx.x & 31;
+  const N pos = flow_at<N>(p, all, v);
+  from = pos;
   if (pos >= all) return {p.B, 0, 0, 0};
   const auto upto = [&](int e) { return static_cast<N>(flow_upto(p, f, e)); };
-  int lo = 0, hi = p.B;  // the sequence: the last one that begins at or before pos
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (upto(mid * nqb) * p.Hkv <= pos)
-      lo = mid;
-    else
-      hi = mid;
-  }
-  FlowCut x{lo, 0, 0, 0};
+  // the last of n pairs, `step` apart from e0 on, with upto() mul <= most (the first one is)
+  const auto find = [&](int e0, int n, int step, int mul, N most) {
+    int lo = 0;
+    while (n > 1) {
+      const int each = (n + 31) >> 5, i = lane * each;
+      const unsigned under = __ballot_sync(0xffffffffu, i < n && upto(e0 + (lo + i) * step) * mul <= most);
+      const int k = (31 - __clz(under)) * each;
+      lo += k;
+      n = min(each, n - k);
+    }
+    return lo;
+  };
+  FlowCut x{find(0, p.B, nqb, p.Hkv, pos), 0, 0, 0};
   const int e0 = x.b * nqb;
   const N base = upto(e0), head = upto(e0 + nqb) - base;
   N rest = pos - base * p.Hkv;
   x.h = static_cast<int>(rest / head);
   rest -= x.h * head;
-  lo = 0, hi = nqb;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (upto(e0 + mid) - base <= rest)
-      lo = mid;
-    else
-      hi = mid;
-  }
-  x.qb = lo;
-  rest -= upto(e0 + lo) - base;
-  x.j = static_cast<int>(rest) - cost;
+  x.qb = find(e0, nqb, 1, 1, base + rest);
+  const N begin = upto(e0 + x.qb), length = upto(e0 + x.qb + 1) - begin - cost;
+  rest -= begin - base;
+  from = pos - rest;
+  x.j = (static_cast<int>(rest) - cost) >> kLineLog;
   if (x.j < kLeast) {
     x.j = 0;
-    return x;
-  }
-  if (flow_cost(p, e0 + lo) - cost - x.j < kLeast) {
+  } else if (static_cast<int>(length >> kLineLog) - x.j < kLeast) {
     x.j = 0;
     if (++x.qb == nqb) {
       x.qb = 0;
       if (++x.h == p.Hkv) x.h = 0, ++x.b;
     }
-  } else if (first) {
-    // the first cut that stays within the block, and the piece before it
-    const N least = pos - rest + cost + kLeast, each = all / n;  // (a piece is each or each + 1)
-    int w = each > 0 ? v - static_cast<int>((pos - least) / each) - 1 : 0;
-    if (w < 0) w = 0;
-    while (flow_at<N>(all, w, n) < least) ++w;
-    while (w > 0 && flow_at<N>(all, w - 1, n) >= least) --w;
-    *first = w - 1;
   }
   return x;
+}
+// The piece in which a block began that lies at `from` and that a later one has the end of: the one before
+// the first whose beginning is kLeast tiles into it.
+template <typename N>
+__device__ __forceinline__ int flow_first(const FlowParams& p, N all, N from) {
+  const N least = from + p.pl.cost + kLeast * kLine;
+  // (floor(all w / n) >= least: an estimate, and steps from it)
+  int w = static_cast<int>(__fdividef(static_cast<float>(least) * static_cast<float>(p.d_pieces.d), static_cast<float>(all)));
+  while (flow_at<N>(p, all, w) < least) ++w;
+  while (w > 0 && flow_at<N>(p, all, w - 1) >= least) --w;
+  return w - 1;
 }
 
 // The CTA's pieces; all of its threads, of which the first kFlowThreads add up
@@ -309,22 +316,42 @@ __device__ __forceinline__ void flow_pieces(const FlowParams& p, F& f) {
     if (tid == kFlowThreads - 1) f.sum[slots] = at + mine;
   }
   __syncthreads();
-  const int n = p.pl.flow * static_cast<int>(gridDim.x);
-  if ((tid & 3) == 0 && tid < 8 * p.pl.flow) {
-    const int k = tid >> 2, v = (k >> 1) * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x) + (k & 1);
-    int* first = (k & 1) ? nullptr : &f.first[k >> 1];
-    const long long all = flow_upto(p, f, pairs) * p.Hkv;
-    f.cut[k] = all <= 0x7fffffff ? flow_cut<int>(p, f, static_cast<int>(all), v, n, first)
-                                 : flow_cut<long long>(p, f, all, v, n, first);
+  const long long all = f.sum[slots] * p.Hkv;
+  for (int k = warp; k < 2 * p.pl.flow; k += static_cast<int>(blockDim.x) >> 5) {
+    const int v = (k >> 1) * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x) + (k & 1);
+    FlowCut x;
+    long long from;
+    if (all <= 0x7fffffff) {
+      int at;
+      x = flow_cut<int>(p, f, static_cast<int>(all), v, at);
+      from = at;
+    } else {
+      x = flow_cut<long long>(p, f, all, v, from);
+    }
+    if (lane == 0) {
+      f.cut[k] = x;
+      if (!(k & 1)) f.from[k >> 1] = from;
+    }
   }
   __syncthreads();
-  if (tid < p.pl.flow) {
-    const int v = tid * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x);
-    const FlowCut a = f.cut[2 * tid], z = f.cut[2 * tid + 1];
+}
+// What merge_flow is told of the CTA's pieces; a warp, which has the time
+template <typename F>
+__device__ __forceinline__ void flow_record(const FlowParams& p, const F& f) {
+  const int r = threadIdx.x & 31;
+  if (r < p.pl.flow) {
+    const int pairs = p.B * p.pl.nqb, slots = quot(p.d_slot, pairs + p.per_slot - 1);
+    const long long all = f.sum[slots] * p.Hkv;
+    const FlowCut a = f.cut[2 * r], z = f.cut[2 * r + 1];
     const bool one = a.b == z.b && a.h == z.h && a.qb == z.qb;  // the piece ends in the block that it begins in
-    const bool takes = a.j > 0 && !(one && a.j == z.j);
-    p.rec[v] = make_int4(takes ? a.b * p.pl.nqb + a.qb : -1, a.h, one ? 0 : 1, takes ? f.first[tid] : 0);
+    int4 rec = make_int4(-1, 0, 0, 0);
+    if (a.j > 0 && !(one && a.j == z.j))
+      rec = make_int4(a.b * p.pl.nqb + a.qb, a.h, one ? 0 : 1,
+                      all <= 0x7fffffff ? flow_first<int>(p, static_cast<int>(all), static_cast<int>(f.from[r]))
+                                        : flow_first<long long>(p, all, f.from[r]));
+    p.rec[r * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x)] = rec;
   }
+  __syncwarp();
 }
 
 // The units of a CTA: unit blockIdx, blockIdx + grid, .., or those of its pieces

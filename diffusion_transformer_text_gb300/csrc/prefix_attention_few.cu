@@ -247,9 +247,7 @@ __global__ void __launch_bounds__(Cfg<Q8>::kThreads, 1)
   const uint32_t tmem = *tmem_slot;
   grid_dep_wait();
   grid_dep_launch_dependents();
-  if constexpr (kFlow<P>) {
-    flow_pieces(p, *pieces);
-  }
+  if constexpr (kFlow<P>) flow_pieces(p, *pieces);
 
   if (warp == 0 || warp == 2) {
     // ---------------- producers: K tiles and Q (warp 0), V tiles (warp 2). Lane 0 works; warp 2
@@ -411,6 +409,7 @@ __global__ void __launch_bounds__(Cfg<Q8>::kThreads, 1)
       __syncwarp();
     }
   } else if (warp == 3) {
+    if constexpr (kFlow<P>) flow_record(p, *pieces);  // (long before the first P)
     // ---------------- O^T issuer: the first tile of each warpgroup in a unit overwrites its O^T
     // (which it has read: its P comes after)
     {
