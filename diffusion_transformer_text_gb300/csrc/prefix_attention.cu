@@ -810,7 +810,8 @@ constexpr float kJoinTiles = 2.6f, kJoinRow = 1.f / 32;  // start of a CTA in a 
 constexpr long long kL2Half = 64ll << 20;
 constexpr int kFullCost = 4, kFewCost = 8;  // of a unit, in 1/kLine of a tile, where pieces are cut
 constexpr float kFlowStart = 5.f;           // cutting them, and a second launch
-constexpr float kPiece = 256.f;             // tiles of a piece where blocks share keys
+constexpr float kSpan = 80 << 20;           // bytes of keys and values that row blocks share in a round of pieces
+constexpr float kPiece = 24.f;              // tiles of a piece at least
 constexpr float kApart = 1.1f;              // pieces against units that meet in the L2
 constexpr float kEvenFrom = 48.f;           // tiles a CTA from which unequal chunks are worth cutting
 constexpr int kFewTiles = 4;                // so few in a unit, and their number does not matter
@@ -920,9 +921,14 @@ Plan make_plan(const Sizes& z, int sms) {
     }
   };
   // Even pieces of a cache in pages, where the sequences' shares of the work are known on the device alone
-  // (single tokens, chunks of lengths of their own), in rounds of about kPiece tiles where row blocks share keys.
-  // Chunks of one length keep units of equal length: CTAs that walk neighbouring row blocks from the same
-  // key on meet in the L2, and pieces do not (3 x 2461 causal rows, 16 key heads: 139 us, in pieces 168).
+  // (single tokens, chunks of lengths of their own), or where units would leave a ragged wave. Row blocks that
+  // share keys follow one another on the line, so the CTAs go over it in rounds of about kSpan bytes of keys, which
+  // stay in the L2 meanwhile: 12 x 141 rows over up to 20000 keys (450 MB) in one round 300 us, in rounds of
+  // 32, 64, 80, 128 MB 264, 264, 264, 254; all 20000 long 722, then 514, 515, 517, 594; 2048 rows over 32768 keys 768,
+  // then 753, 753, 752, 807; 3 x 3461 rows (146 MB) 138, then 150, 144, 137, 139: more rounds are more parts to join.
+  // Where the plan has units enough for even waves, chunks of one length keep them: CTAs that walk neighbouring row
+  // blocks from the same key on meet in the L2, and pieces do not (3 x 2461 causal rows, 16 key heads: 139 us, in
+  // pieces 168).
   const auto flow = [&](Plan c, Rate r) {
     const long long blocks = static_cast<long long>(z.B) * c.nqb * z.Hkv;
     if (!z.paged || blocks > INT_MAX) return;
@@ -933,7 +939,8 @@ Plan make_plan(const Sizes& z, int sms) {
     if (cost < best_cost) {
       best_cost = cost;
       c.units = blocks * c.ot < sms ? static_cast<int>(blocks * c.ot) : sms;
-      c.flow = c.nqb > 1 ? static_cast<int>(each / kPiece + 0.5f) : 1;
+      const float span = static_cast<float>(z.B) * c.ot * z.Hkv * (2 * kTile) / kSpan + 0.5f;
+      c.flow = static_cast<int>(c.nqb == 1 ? 1.f : span < each / kPiece ? span : each / kPiece);
       c.flow = c.flow < 1 ? 1 : c.flow > kMostRounds ? kMostRounds : c.flow;
       best = c;
     }

@@ -176,9 +176,7 @@ __device__ __forceinline__ Unit unit_of(const P& p, int u) {
 // it writes, and at either end a part of one, which it leaves as partials for merge_flow. A cut closer than
 // kLeast tiles to an end of its block moves there. Every CTA works its cuts out for itself, from sums over the
 // sequences. More rounds than one keep the CTAs, at any one time, on a stretch of the line whose keys stay
-// in the L2 while the row blocks that share them pass by: one round over 60 MB of keys, row blocks before
-// heads, took each CTA twice the time a tile (3 x 2461 causal rows, 16 key heads: 205 us, units cut on the
-// host 139).
+// in the L2 while the row blocks that share them pass by (figures: make_plan).
 constexpr int kLeast = 2;
 constexpr int kLineLog = 2, kLine = 1 << kLineLog;  // of the line to a tile
 constexpr int kFlowThreads = 384;  // that add up: the smaller kernel's
