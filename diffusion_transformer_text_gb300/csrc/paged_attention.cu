@@ -51,8 +51,7 @@ enum : int {
   kKEmpty = kKFull + kKStages,
   kVFull = kKEmpty + kKStages,
   kVEmpty = kVFull + kVStages,
-  kVClean = kVEmpty + kVStages,  // rows past a sequence's last in the unit's last V tile cleared; one per stage
-  kQFull = kVClean + kVStages,
+  kQFull = kVEmpty + kVStages,
   kQEmpty = kQFull + kQBufs,
   kSFull = kQEmpty + kQBufs,
   kSFree = kSFull + 1,   // scores in registers (8 softmax warps)
@@ -182,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
     } else if (warp == 2) {
-      // ---------------- V tiles; the rows past a sequence's last are set to zero (0 x NaN is NaN)
+      // ---------------- V tiles
       uint32_t t = 0;
       bool ok = true;
       for (Walk<P, FlowFull> w(p, pieces); ok && w.more(p); w.step(p)) {
@@ -199,22 +198,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           load_pages(p, &tm.v, sV + st * kTile, &bars[kVFull + st], un.h, key0, id, lane);
           ++t;
-        }
-        if (ok && un.clear) {
-          const uint32_t last = t - 1, st = last % kVStages;
-          ok = __all_sync(0xffffffffu, mbar_wait(&bars[kVFull + st], (last / kVStages) & 1u));
-          if (!ok) break;
-          // rows r0 .. 127 of both 64-dim boxes (a row's 128 bytes stay within the row under the swizzle)
-          const int r0 = un.len - (un.o0 + un.n - 1) * kKeys;
-          const int n16 = (kKeys - r0) * 8;
-          uint8_t* base = sV + st * kTile + r0 * 128;
-          for (int i = lane; i < n16; i += 32) {
-            *reinterpret_cast<uint4*>(base + i * 16) = make_uint4(0u, 0u, 0u, 0u);
-            *reinterpret_cast<uint4*>(base + kBox + i * 16) = make_uint4(0u, 0u, 0u, 0u);
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bars[kVClean + st]);
         }
       }
       if (lane == 0) {
@@ -268,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---------------- O += P V, a half of the keys at a time: a unit's first tile overwrites O
       if constexpr (kFlow<P>) flow_record(p, *pieces);  // (long before the first P)
       const uint64_t vdesc0 = sw128_mnmajor_desc(smem_u32(sV), kBox, 1024);
-      uint32_t t = 0, ku = 0, cleared = 0;
+      uint32_t t = 0, ku = 0;
       bool ok = true;
       for (Walk<P, FlowFull> w(p, pieces); ok && w.more(p); w.step(p)) {
         const Unit un = w.unit(p);
@@ -277,9 +260,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int j = 0; ok && j < un.n; ++j, ++t) {
           const uint32_t st = t % kVStages, b = t & 1u;
           ok = mbar_wait(&bars[kVFull + st], (t / kVStages) & 1u);
+          // rows past the sequence's last, whatever they hold (0 x NaN is NaN)
           if (un.clear && j + 1 == un.n) {
-            ok = ok && mbar_wait(&bars[kVClean + st], (cleared >> st) & 1u);
-            cleared ^= 1u << st;  // the stage's phase
+            ok = __all_sync(0xffffffffu, ok);
+            if (ok) clear_rows(sV + st * kTile, un.len - (un.o0 + j) * kKeys, lane);
           }
           const uint64_t vd = vdesc0 + ((st * kTile) >> 4);
           for (int h = 0; h < 2; ++h) {

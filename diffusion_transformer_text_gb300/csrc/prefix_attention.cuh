@@ -450,6 +450,20 @@ __device__ __forceinline__ void load_pages(const PagedParams& p, const CUtensorM
                 key0 & ((1 << p.page_log) - 1), id);
 }
 
+// Zeros for the rows of a V tile from r0 on, by a warp, in time for a product that it issues (a row's 128
+// bytes stay within the row under the swizzle). The issuing warp does it, which would wait for P now: by the
+// loading one, which then had to wait for its own load, the next unit's V came late
+// (128 single tokens over up to 900 rows, 32 heads, 197 us; here 181; padded chunks of 777 rows, 98 and 95).
+__device__ __forceinline__ void clear_rows(uint8_t* tile, int r0, int lane) {
+  uint8_t* base = tile + r0 * 128;
+  for (int i = lane; i < (kKeys - r0) * 8; i += 32) {
+    *reinterpret_cast<uint4*>(base + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+    *reinterpret_cast<uint4*>(base + kBox + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
+}
+
 // One lane of a converged warp, always the same
 __device__ __forceinline__ bool elect_one() {
   uint32_t one;

@@ -62,8 +62,7 @@ enum : int {
   kEmpty = kFull + 6,            // [K, V][3] ... read by its product
   kCFull = kEmpty + 6,           // [K, V][2] codes in place
   kCEmpty = kCFull + 4,          // [K, V][2] ... turned into 16 bits (4 warps)
-  kVClean = kCEmpty + 4,         // [3] rows past own_len of a unit's last V tile cleared
-  kQFull = kVClean + 3,
+  kQFull = kCEmpty + 4,
   kQEmpty = kQFull + kQBufs,
   kSFull = kQEmpty + kQBufs,
   kSFree = kSFull + kSBufs,      // S^T in registers (4 warps)
@@ -250,8 +249,8 @@ __global__ void __launch_bounds__(Cfg<Q8>::kThreads, 1)
   if constexpr (kFlow<P>) flow_pieces(p, *pieces);
 
   if (warp == 0 || warp == 2) {
-    // ---------------- producers: K tiles and Q (warp 0), V tiles (warp 2). Lane 0 works; warp 2
-    // clears V rows past own_len as a whole, so every lane walks the units.
+    // ---------------- producers: K tiles and Q (warp 0), V tiles (warp 2); keys in pages by the whole warp, a lane
+    // a box, else by lane 0
     const int kv = warp == 0 ? 0 : 1;
     uint32_t t = 0, tc = 0, nq = 0;  // tiles; of which requested as codes; Q blocks
     uint64_t* full = &bars[kFull + 3 * kv];
@@ -344,25 +343,6 @@ __global__ void __launch_bounds__(Cfg<Q8>::kThreads, 1)
         if (!ok) give_up(kErrTimeoutProducer);
       }
       t += un.n;
-      if (kv == 1 && un.clear) {
-        const uint32_t last = t - 1, st = last % kSt;
-        if (lane == 0 && ok && !mbar_wait(&full[st], (last / kSt) & 1u)) {
-          give_up(kErrTimeoutProducer);
-          ok = false;
-        }
-        if (__shfl_sync(0xffffffffu, static_cast<int>(ok), 0)) {
-          const int r0 = un.len - (un.o0 + un.on - 1) * kKeys;
-          const int n16 = (kKeys - r0) * 8;
-          uint8_t* base = tiles + st * kTile + r0 * 128;
-          for (int i = lane; i < n16; i += 32) {
-            *reinterpret_cast<uint4*>(base + i * 16) = make_uint4(0u, 0u, 0u, 0u);
-            *reinterpret_cast<uint4*>(base + kBox + i * 16) = make_uint4(0u, 0u, 0u, 0u);
-          }
-          fence_proxy_async_smem();
-        }
-        __syncwarp();
-        if (lane == 0 && ok) mbar_arrive(&bars[kVClean + st]);
-      }
     }
   } else if (warp == 1) {
     // ---------------- S^T issuer. The issuing warps walk as a whole, so that the descriptors are
@@ -415,16 +395,17 @@ __global__ void __launch_bounds__(Cfg<Q8>::kThreads, 1)
     {
       const uint64_t vdesc0 = sw128_mnmajor_desc(smem_u32(sT + kSt * kTile), kBox, 1024);
       const uint64_t pdesc0 = sw128_kmajor_desc(smem_u32(sP));
-      uint32_t t = 0, cleared = 0;
+      uint32_t t = 0;
       bool ok = true;
       for (Walk<P, F> w(p, pieces); ok && w.more(p); w.step(p)) {
         const Unit un = w.unit(p);
         for (int j = 0; j < un.n; ++j, ++t) {
           const uint32_t st = t % kSt, sb = t % kSBufs;
           ok = mbar_wait(&bars[kFull + 3 + st], (t / kSt) & 1u);
+          // rows past the sequence's last, whatever they hold (0 x NaN is NaN)
           if (un.clear && j + 1 == un.n) {
-            ok = ok && mbar_wait(&bars[kVClean + st], (cleared >> st) & 1u);
-            cleared ^= 1u << st;  // the stage's phase
+            ok = __all_sync(0xffffffffu, ok);
+            if (ok) clear_rows(sT + (kSt + st) * kTile, un.len - (un.o0 + un.on - 1) * kKeys, lane);
           }
           ok = __all_sync(0xffffffffu, ok && mbar_wait(&bars[kPFull + sb], (t / kSBufs) & 1u));
           if (!ok) break;
