@@ -38,7 +38,7 @@ constexpr int kThreads = 512;
 constexpr uint32_t kRegsLow = 96, kRegsHigh = 160, kRegsEpi = 96;
 static_assert(kRegsLow + 2 * kRegsHigh + kRegsEpi == 4 * 128, "register split must equal the launch allotment");
 
-// A unit's numbers for the softmax and epilogue warps, worked out once, by the K producer, which is ahead of them
+// A unit's numbers for the other warps, worked out once, by the K producer, which is ahead of them
 constexpr int kMessages = 4;
 struct __align__(16) Message {
   int n, tq, o0, rows;  // n < 0: no more units
@@ -62,13 +62,13 @@ enum : int {
   kLFull = kOEmpty + 1,       // the unit's row sums and maxima in shared memory (8 softmax warps)
   kLFree = kLFull + 1,        // ... read by the epilogue (4 warps)
   kUFull = kLFree + 1,        // [message]
-  kUEmpty = kUFull + kMessages,  // [message] (12 warps)
+  kUEmpty = kUFull + kMessages,  // [message] (15 warps)
   kDrainQK = kUEmpty + kMessages,
   kDrainPV = kDrainQK + 1,
   kNumBars = kDrainPV + 1
 };
 __device__ __forceinline__ uint32_t bar_count(int i) {
-  if (i >= kUEmpty && i < kUEmpty + kMessages) return 12;
+  if (i >= kUEmpty && i < kUEmpty + kMessages) return 15;
   if (i == kSFree || i == kLFull) return 8;
   if ((i >= kPFull && i < kPFull + 4) || i == kOEmpty || i == kLFree) return 4;
   return 1;
@@ -127,6 +127,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   grid_dep_launch_dependents();
   if constexpr (kFlow<P>) flow_pieces(p, *pieces);
 
+  // the next unit's numbers
+  uint32_t km = 0;
+  const auto receive = [&](Message& un) {
+    const uint32_t mb = km % kMessages;
+    if (!__all_sync(0xffffffffu, mbar_wait(&bars[kUFull + mb], (km / kMessages) & 1u))) return false;
+    un = messages[mb];
+    ++km;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars[kUEmpty + mb]);
+    return true;
+  };
+
   if (warp < 4) {
     regs_release<kRegsLow>();
     if (warp == 0) {
@@ -184,8 +196,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---------------- V tiles
       uint32_t t = 0;
       bool ok = true;
-      for (Walk<P, FlowFull> w(p, pieces); ok && w.more(p); w.step(p)) {
-        const Unit un = w.unit(p);
+      for (;;) {
+        Message un;
+        ok = ok && receive(un);
+        if (!ok || un.n < 0) break;
         if (un.n == 0) continue;
         int next = page_of(p, un, un.o0 * kKeys, lane);
         for (int j = 0; j < un.n; ++j) {
@@ -212,8 +226,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t kdesc0 = sw128_kmajor_desc(smem_u32(sK));
       uint32_t t = 0, ku = 0;
       bool ok = true;
-      for (Walk<P, FlowFull> w(p, pieces); ok && w.more(p); w.step(p)) {
-        const Unit un = w.unit(p);
+      for (;;) {
+        Message un;
+        ok = receive(un);
+        if (!ok || un.n < 0) break;
         if (un.n == 0) continue;
         const uint32_t qb = ku % kQBufs;
         ok = __all_sync(0xffffffffu, !*abort_flag && mbar_wait(&bars[kQFull + qb], (ku / kQBufs) & 1u));
@@ -253,15 +269,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t vdesc0 = sw128_mnmajor_desc(smem_u32(sV), kBox, 1024);
       uint32_t t = 0, ku = 0;
       bool ok = true;
-      for (Walk<P, FlowFull> w(p, pieces); ok && w.more(p); w.step(p)) {
-        const Unit un = w.unit(p);
+      for (;;) {
+        Message un;
+        ok = receive(un);
+        if (!ok || un.n < 0) break;
         if (un.n == 0) continue;
+        const bool clear = un.len < (un.o0 + un.n) * kKeys;
         ok = __all_sync(0xffffffffu, !*abort_flag && (ku == 0 || mbar_wait(&bars[kOEmpty], (ku - 1) & 1u)));
         for (int j = 0; ok && j < un.n; ++j, ++t) {
           const uint32_t st = t % kVStages, b = t & 1u;
           ok = mbar_wait(&bars[kVFull + st], (t / kVStages) & 1u);
           // rows past the sequence's last, whatever they hold (0 x NaN is NaN)
-          if (un.clear && j + 1 == un.n) {
+          if (clear && j + 1 == un.n) {
             ok = __all_sync(0xffffffffu, ok);
             if (ok) clear_rows(sV + st * kTile, un.len - (un.o0 + j) * kKeys, lane);
           }
@@ -306,16 +325,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tO = tmem + lane_off + kColO + 128u * h;
     const uint64_t sc2 = f2_pack(scale_log2, scale_log2);
     uint32_t t = 0;
-    uint32_t ku = 0, km = 0;
+    uint32_t ku = 0;
     bool ok = true;
-    for (;; ++km) {
-      const uint32_t mb = km % kMessages;
-      ok = __all_sync(0xffffffffu, mbar_wait(&bars[kUFull + mb], (km / kMessages) & 1u));
-      if (!ok) break;
-      const Message un = messages[mb];
-      if (un.n < 0) break;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars[kUEmpty + mb]);
+    for (;;) {
+      Message un;
+      ok = receive(un);
+      if (!ok || un.n < 0) break;
       if (un.n == 0) continue;
       const int lim_own = own_lim(p, un.len, un.t0 + tok, un.tq);
       // A warp whose 32 rows lie past the block's has nothing to compute: it only keeps the
@@ -459,15 +474,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tok = quot(p.d_G, rit);
     const int g = rit - tok * p.pl.G;
     bool ok = true;
-    uint32_t ku = 0, km = 0;
-    for (;; ++km) {
-      const uint32_t mb = km % kMessages;
-      ok = __all_sync(0xffffffffu, mbar_wait(&bars[kUFull + mb], (km / kMessages) & 1u));
-      if (!ok) break;
-      const Message un = messages[mb];
-      if (un.n < 0) break;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars[kUEmpty + mb]);
+    uint32_t ku = 0;
+    for (;;) {
+      Message un;
+      ok = receive(un);
+      if (!ok || un.n < 0) break;
       const bool part = kFlow<P> ? un.slot >= 0 : p.pl.split;  // (unless JOIN) not all of the rows' keys
       const bool mine = rit < un.rows && un.t0 + tok < un.tq;
       uint16_t* orow = p.o + un.b0 * p.ob + (un.t0 + tok) * p.orow + static_cast<long long>(un.h * p.pl.G + g) * p.oh;

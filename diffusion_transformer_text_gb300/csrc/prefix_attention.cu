@@ -838,10 +838,13 @@ Plan make_plan(const Sizes& z, int sms) {
     }
   };
   const float convert = z.from8 && z.P > 0 ? kConvertStart + kConvert * static_cast<float>(z.P) * z.Hkv * kHeadDim / (1 << 20) : 0.f;
+  // pieces can be cut: the line in an int (beyond it, seconds of work, units will do)
+  const auto fits = [&](int nqb) { return static_cast<float>(z.B) * nqb * z.Hkv * ((a.ot + 4) * kLine) < 2e9f; };
   // single tokens, or chunks of unlike lengths with enough tiles to cut
-  const bool even = z.paged && (z.T <= kRows / a.G ||
-                                (z.ragged && z.B > 1 &&
-                                 static_cast<float>(ceil_div(z.T, kRows / a.G)) * z.B * z.Hkv * (a.ot + 2) > kEvenFrom * sms));
+  const int nqb_full = z.paged ? ceil_div(z.T, kRows / a.G) : 0;
+  const bool even = z.paged && fits(nqb_full) &&
+                    (nqb_full == 1 ||
+                     (z.ragged && z.B > 1 && static_cast<float>(nqb_full) * z.B * z.Hkv * (a.ot + 2) > kEvenFrom * sms));
   // what a causal chunk's row blocks see of the longest sequence, on average
   const float seen = z.paged && z.causal && z.T < z.S ? 1.f - 0.5f * static_cast<float>(z.T) / static_cast<float>(z.S)
                      : z.paged && z.causal            ? 0.5f
@@ -931,7 +934,7 @@ Plan make_plan(const Sizes& z, int sms) {
   // pieces 168).
   const auto flow = [&](Plan c, Rate r) {
     const long long blocks = static_cast<long long>(z.B) * c.nqb * z.Hkv;
-    if (!z.paged || blocks > INT_MAX) return;
+    if (!z.paged || !fits(c.nqb)) return;
     c.nch = c.ct = 1;
     c.cost = c.few ? kFewCost : kFullCost;
     const float each = static_cast<float>(blocks) * (c.ot * seen * r.tile + r.of(c.rows_o)) / sms * (even ? 1.f : kApart);

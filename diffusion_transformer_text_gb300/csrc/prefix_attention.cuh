@@ -191,10 +191,10 @@ __device__ __forceinline__ bool before(const FlowCut& x, const FlowCut& y) {
 template <int SLOTS>
 struct Flow {
   static constexpr int kSlots = SLOTS;
-  long long sum[SLOTS + 1];  // of one head's costs of all pairs before a slot's first, and of all
-  long long warp_sum[kFlowThreads / 32];
+  int sum[SLOTS + 1];  // of one head's costs of all pairs before a slot's first, and of all (the plan sees to the range)
+  int warp_sum[kFlowThreads / 32];
   FlowCut cut[2 * kMostRounds];  // begin and end of the CTA's pieces
-  long long from[kMostRounds];   // where the block that a piece begins in lies on the line
+  int from[kMostRounds];         // where the block that a piece begins in lies on the line
 };
 // partial rows of piece v: of the block that it takes over, 2 v; of the one that it leaves, 2 v + 1.
 // rec[v] = (pair, head, whether that block ends here, piece that it began in) of the first, pair -1: none
@@ -212,19 +212,13 @@ __device__ __forceinline__ int flow_cost(const FlowParams& p, int e) {
 }
 // costs of the pairs before pair e
 template <typename F>
-__device__ __forceinline__ long long flow_upto(const FlowParams& p, const F& f, int e) {
+__device__ __forceinline__ int flow_upto(const FlowParams& p, const F& f, int e) {
   const int slot = quot(p.d_slot, e);
-  long long s = f.sum[slot];
+  int s = f.sum[slot];
   for (int x = slot * p.per_slot; x < e; ++x) s += flow_cost(p, x);
   return s;
 }
-// where on a line of `all` piece v begins: at floor(all v / pieces) (N: int where all fits)
-template <typename N>
-__device__ __forceinline__ N flow_at(const FlowParams& p, N all, int v) {
-  const int n = static_cast<int>(p.d_pieces.d);
-  return all / n * v + all % n * v / n;
-}
-template <>
+// where on a line of `all` piece v begins: at floor(all v / pieces)
 __device__ __forceinline__ int flow_at(const FlowParams& p, int all, int v) {
   const int n = static_cast<int>(p.d_pieces.d), each = quot(p.d_pieces, all);
   return each * v + quot(p.d_pieces, (all - each * n) * v);  // (n is below 2^15)
@@ -233,19 +227,18 @@ __device__ __forceinline__ int flow_at(const FlowParams& p, int all, int v) {
 // Where piece v begins, by a warp: its lanes try 32 sequences, then 32 row blocks, at a time (one after the
 // other, a lane's 9 steps for 6 sequences of 49 blocks came to 3 us, a launch's longest step). from: where the
 // block that it begins in lies on the line.
-template <typename N, typename F>
-__device__ __forceinline__ FlowCut flow_cut(const FlowParams& p, const F& f, N all, int v, N& from) {
+template <typename F>
+__device__ __forceinline__ FlowCut flow_cut(const FlowParams& p, const F& f, int all, int v, int& from) {
   const int nqb = p.pl.nqb, cost = p.pl.cost, lane = threadIdx.x & 31;
-  const N pos = flow_at<N>(p, all, v);
+  const int pos = flow_at(p, all, v);
   from = pos;
   if (pos >= all) return {p.B, 0, 0, 0};
-  const auto upto = [&](int e) { return static_cast<N>(flow_upto(p, f, e)); };
   // the last of n pairs, `step` apart from e0 on, with upto() mul <= most (the first one is)
-  const auto find = [&](int e0, int n, int step, int mul, N most) {
+  const auto find = [&](int e0, int n, int step, int mul, int most) {
     int lo = 0;
     while (n > 1) {
       const int each = (n + 31) >> 5, i = lane * each;
-      const unsigned under = __ballot_sync(0xffffffffu, i < n && upto(e0 + (lo + i) * step) * mul <= most);
+      const unsigned under = __ballot_sync(0xffffffffu, i < n && flow_upto(p, f, e0 + (lo + i) * step) * mul <= most);
       const int k = (31 - __clz(under)) * each;
       lo += k;
       n = min(each, n - k);
@@ -254,18 +247,18 @@ __device__ __forceinline__ FlowCut flow_cut(const FlowParams& p, const F& f, N a
   };
   FlowCut x{find(0, p.B, nqb, p.Hkv, pos), 0, 0, 0};
   const int e0 = x.b * nqb;
-  const N base = upto(e0), head = upto(e0 + nqb) - base;
-  N rest = pos - base * p.Hkv;
-  x.h = static_cast<int>(rest / head);
+  const int base = flow_upto(p, f, e0), head = flow_upto(p, f, e0 + nqb) - base;
+  int rest = pos - base * p.Hkv;
+  x.h = rest / head;
   rest -= x.h * head;
   x.qb = find(e0, nqb, 1, 1, base + rest);
-  const N begin = upto(e0 + x.qb), length = upto(e0 + x.qb + 1) - begin - cost;
+  const int begin = flow_upto(p, f, e0 + x.qb), length = flow_upto(p, f, e0 + x.qb + 1) - begin - cost;
   rest -= begin - base;
   from = pos - rest;
-  x.j = (static_cast<int>(rest) - cost) >> kLineLog;
+  x.j = (rest - cost) >> kLineLog;
   if (x.j < kLeast) {
     x.j = 0;
-  } else if (static_cast<int>(length >> kLineLog) - x.j < kLeast) {
+  } else if ((length >> kLineLog) - x.j < kLeast) {
     x.j = 0;
     if (++x.qb == nqb) {
       x.qb = 0;
@@ -276,13 +269,12 @@ __device__ __forceinline__ FlowCut flow_cut(const FlowParams& p, const F& f, N a
 }
 // The piece in which a block began that lies at `from` and that a later one has the end of: the one before
 // the first whose beginning is kLeast tiles into it.
-template <typename N>
-__device__ __forceinline__ int flow_first(const FlowParams& p, N all, N from) {
-  const N least = from + p.pl.cost + kLeast * kLine;
+__device__ __forceinline__ int flow_first(const FlowParams& p, int all, int from) {
+  const int least = from + p.pl.cost + kLeast * kLine;
   // (floor(all w / n) >= least: an estimate, and steps from it)
   int w = static_cast<int>(__fdividef(static_cast<float>(least) * static_cast<float>(p.d_pieces.d), static_cast<float>(all)));
-  while (flow_at<N>(p, all, w) < least) ++w;
-  while (w > 0 && flow_at<N>(p, all, w - 1) >= least) --w;
+  while (flow_at(p, all, w) < least) ++w;
+  while (w > 0 && flow_at(p, all, w - 1) >= least) --w;
   return w - 1;
 }
 
@@ -292,7 +284,7 @@ __device__ __forceinline__ void flow_pieces(const FlowParams& p, F& f) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int pairs = p.B * p.pl.nqb, slots = quot(p.d_slot, pairs + p.per_slot - 1);
   const int each = (slots + kFlowThreads - 1) / kFlowThreads, s0 = tid * each;
-  long long mine = 0, upto = 0;
+  int mine = 0, upto = 0;
   if (tid < kFlowThreads) {
     for (int s = s0; s < s0 + each && s < slots; ++s) {
       f.sum[s] = mine;
@@ -301,31 +293,23 @@ __device__ __forceinline__ void flow_pieces(const FlowParams& p, F& f) {
     upto = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-      const long long x = __shfl_up_sync(0xffffffffu, upto, d);
+      const int x = __shfl_up_sync(0xffffffffu, upto, d);
       if (lane >= d) upto += x;
     }
     if (lane == 31) f.warp_sum[warp] = upto;
   }
   __syncthreads();
   if (tid < kFlowThreads) {
-    long long at = upto - mine;
+    int at = upto - mine;
     for (int w = 0; w < warp; ++w) at += f.warp_sum[w];
     for (int s = s0; s < s0 + each && s < slots; ++s) f.sum[s] += at;
     if (tid == kFlowThreads - 1) f.sum[slots] = at + mine;
   }
   __syncthreads();
-  const long long all = f.sum[slots] * p.Hkv;
+  const int all = f.sum[slots] * p.Hkv;
   for (int k = warp; k < 2 * p.pl.flow; k += static_cast<int>(blockDim.x) >> 5) {
-    const int v = (k >> 1) * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x) + (k & 1);
-    FlowCut x;
-    long long from;
-    if (all <= 0x7fffffff) {
-      int at;
-      x = flow_cut<int>(p, f, static_cast<int>(all), v, at);
-      from = at;
-    } else {
-      x = flow_cut<long long>(p, f, all, v, from);
-    }
+    int from;
+    const FlowCut x = flow_cut(p, f, all, (k >> 1) * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x) + (k & 1), from);
     if (lane == 0) {
       f.cut[k] = x;
       if (!(k & 1)) f.from[k >> 1] = from;
@@ -339,14 +323,11 @@ __device__ __forceinline__ void flow_record(const FlowParams& p, const F& f) {
   const int r = threadIdx.x & 31;
   if (r < p.pl.flow) {
     const int pairs = p.B * p.pl.nqb, slots = quot(p.d_slot, pairs + p.per_slot - 1);
-    const long long all = f.sum[slots] * p.Hkv;
     const FlowCut a = f.cut[2 * r], z = f.cut[2 * r + 1];
     const bool one = a.b == z.b && a.h == z.h && a.qb == z.qb;  // the piece ends in the block that it begins in
     int4 rec = make_int4(-1, 0, 0, 0);
     if (a.j > 0 && !(one && a.j == z.j))
-      rec = make_int4(a.b * p.pl.nqb + a.qb, a.h, one ? 0 : 1,
-                      all <= 0x7fffffff ? flow_first<int>(p, static_cast<int>(all), static_cast<int>(f.from[r]))
-                                        : flow_first<long long>(p, all, f.from[r]));
+      rec = make_int4(a.b * p.pl.nqb + a.qb, a.h, one ? 0 : 1, flow_first(p, f.sum[slots] * p.Hkv, f.from[r]));
     p.rec[r * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x)] = rec;
   }
   __syncwarp();
@@ -436,7 +417,8 @@ __device__ __forceinline__ void tma_load_5d(void* dst, const CUtensorMap* map, u
 // page_log pages (or part of one), each two boxes of 64 dims, a lane a box. Pages behind the sequence and
 // numbers that are none become `pages`, past the map's end, and read as zeros.
 __device__ __forceinline__ int page_boxes(const PagedParams& p) { return p.page_log < 7 ? 256 >> p.page_log : 2; }
-__device__ __forceinline__ int page_of(const PagedParams& p, const Unit& un, int key0, int lane) {
+template <typename U>
+__device__ __forceinline__ int page_of(const PagedParams& p, const U& un, int key0, int lane) {
   const int key = key0 + ((lane >> 1) << p.page_log);
   if (lane >= page_boxes(p) || key >= un.len) return p.pages;
   const int id = p.table[un.b0 * p.table_stride + (key >> p.page_log)];
