@@ -7,9 +7,19 @@
 //
 // The inside of a unit is that of prefix_attention.cu: one CTA per SM, S and the two key halves' O in tensor
 // memory, P written back there as the A operand of P V, two softmax warpgroups of one key half each, an
-// epilogue warpgroup. What differs: K and V come page by page (every page of a tile its own boxes, a lane a box,
-// so warps 0 and 2 load as a whole; page numbers are looked up a tile ahead), there is no prefix, and the softmax and
-// epilogue warps follow the loading one's messages, so that only it and the issuing warps walk the units.
+// epilogue warpgroup. What differs: K and V come page by page (every page of a tile its own boxes; page numbers are
+// looked up a tile ahead), there is no prefix, and only the warp that loads K walks the units: the others follow its
+// messages.
+//
+// What bounds it: from one S of a tile to the next 1640 cycles for 1024 of products (the tensor pipe is busy 59 to 64 %
+// of the time: 4 x 4096 image rows over up to 4590 keys, 32 heads, 805-830 us, 1.4 PFLOP/s; 1024 rows behind 16384, 195
+// us): issue, product, softmax, each after the other, of which the exponentials are 950 cycles of the 32 softmax
+// lanes' 64 keys. Between units, with few tiles in each, instruction fetch: the kernel is longer than the SM's
+// instruction cache, and whatever a unit's beginning or end runs comes from the L2 (6 x 777 rows over up to 3001 keys: a
+// tenth of the warps' time is spent without an instruction). So the code is kept short: units walked by one warp
+// and not by four (6 x 777 rows 94.5 -> 88 us, 16 x 300 66 -> 61), the epilogue in a loop that is not unrolled
+// (16 x 300 rows 61 -> 56); a walk begun a unit ahead, to have its first pages and Q early, cost more than it
+// gave (6 x 777 rows 94.5 -> 99).
 //
 // Units: whole row blocks in the order that prefix_attention.cu's plan gives (chunks of one length), even
 // pieces of all tiles cut on the device (FlowParams: single tokens with many heads, chunks of unlike
@@ -173,7 +183,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
           if (lane == 0) mbar_arrive_expect_tx(&bars[kKFull + st], kTile);
           __syncwarp();
-          load_pages(p, &tm.k, sK + st * kTile, &bars[kKFull + st], un.h, key0, id, lane);
+          if (p.page_log == 4)
+            load_8_pages(&tm.k, sK + st * kTile, &bars[kKFull + st], un.h, id);
+          else
+            load_pages(p, &tm.k, sK + st * kTile, &bars[kKFull + st], un.h, key0, id, lane);
           ++t;
         }
       }
@@ -210,7 +223,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
           if (lane == 0) mbar_arrive_expect_tx(&bars[kVFull + st], kTile);
           __syncwarp();
-          load_pages(p, &tm.v, sV + st * kTile, &bars[kVFull + st], un.h, key0, id, lane);
+          if (p.page_log == 4)
+            load_8_pages(&tm.v, sV + st * kTile, &bars[kVFull + st], un.h, id);
+          else
+            load_pages(p, &tm.v, sV + st * kTile, &bars[kVFull + st], un.h, key0, id, lane);
           ++t;
         }
       }
@@ -517,26 +533,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       // (JOIN: the unit is the CTA's only one and its products are done: the rings are free)
       if (JOIN) *reinterpret_cast<float2*>(smem + kJoinMl + rit * 8) = make_float2(mm, den);
-      // 16 columns of both at a time, the next ones loading while these are stored
+      // 16 columns of both at a time (not unrolled: see above)
       const uint32_t tO = tmem + lane_off + kColO;
       const uint64_t w00 = f2_pack(w0, w0), w11 = f2_pack(w1, w1);
-      uint32_t oa[2][16], ob[2][16];
-      tmem_ld16(tO, oa[0]);
-      tmem_ld16(tO + 128, ob[0]);
-#pragma unroll
+      uint32_t x[16], y[16];
+#pragma unroll 1
       for (int c = 0; c < 8; ++c) {
+        tmem_ld16(tO + c * 16, x);
+        tmem_ld16(tO + 128 + c * 16, y);
         tmem_ld_wait();
-        if (c < 7) {
-          tmem_ld16(tO + (c + 1) * 16, oa[(c + 1) & 1]);
-          tmem_ld16(tO + 128 + (c + 1) * 16, ob[(c + 1) & 1]);
-        } else {
+        if (c == 7) {
           // both are in registers: the next unit's first products may overwrite them
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&bars[kOEmpty]);
         }
-        const uint32_t* x = oa[c & 1];
-        const uint32_t* y = ob[c & 1];
         if (mine) {
           float ov[16];
 #pragma unroll

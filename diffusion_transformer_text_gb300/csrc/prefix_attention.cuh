@@ -413,6 +413,13 @@ __device__ __forceinline__ void tma_load_5d(void* dst, const CUtensorMap* map, u
       : "memory");
 }
 
+// One lane of a converged warp, always the same
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(one));
+  return one != 0;
+}
+
 // The page that lane `lane` fetches for the tile of keys key0 .. key0 + 127 of a sequence: a tile is 128 >>
 // page_log pages (or part of one), each two boxes of 64 dims, a lane a box. Pages behind the sequence and
 // numbers that are none become `pages`, past the map's end, and read as zeros.
@@ -432,6 +439,24 @@ __device__ __forceinline__ void load_pages(const PagedParams& p, const CUtensorM
                 key0 & ((1 << p.page_log) - 1), id);
 }
 
+// ... of a tile of eight pages, by a lane that the pages are told to: by lanes, the boxes went out one in 130
+// cycles, two warps' 32 a tile slower than its products (1024 rows behind 16384 in pages of 16, 234 us, this way
+// 200; 6 x 777 rows 101 and 92; 16 x 300 rows over up to 1000, short units, 56 and 60). With fewer boxes a tile, or few
+// rows, where HBM is the bound, the lanes are no slower and the code is shorter.
+__device__ __forceinline__ void load_8_pages(const CUtensorMap* map, uint8_t* tile, uint64_t* bar, int h, int id) {
+  int page[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) page[i] = __shfl_sync(0xffffffffu, id, 2 * i);
+  if (elect_one()) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      tma_load_4d(tile + i * 2048, map, bar, 0, h, 0, page[i]);
+      tma_load_4d(tile + i * 2048 + kBox, map, bar, 64, h, 0, page[i]);
+    }
+  }
+  __syncwarp();
+}
+
 // Zeros for the rows of a V tile from r0 on, by a warp, in time for a product that it issues (a row's 128
 // bytes stay within the row under the swizzle). The issuing warp does it, which would wait for P now: by the
 // loading one, which then had to wait for its own load, the next unit's V came late
@@ -444,13 +469,6 @@ __device__ __forceinline__ void clear_rows(uint8_t* tile, int r0, int lane) {
   }
   fence_proxy_async_smem();
   __syncwarp();
-}
-
-// One lane of a converged warp, always the same
-__device__ __forceinline__ bool elect_one() {
-  uint32_t one;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(one));
-  return one != 0;
 }
 
 // 32 bytes, 32-byte aligned
