@@ -808,11 +808,14 @@ constexpr float kConvert = 0.5f, kConvertStart = 2.5f;
 constexpr float kStart = 3.f;      // of a kernel whose CTAs walk the units
 constexpr float kJoinTiles = 2.6f, kJoinRow = 1.f / 32;  // start of a CTA in a cluster and its join; each row
 constexpr long long kL2Half = 64ll << 20;
-constexpr int kFullCost = 4, kFewCost = 8;  // of a unit, in 1/kLine of a tile, where pieces are cut
+// Of a unit, in 1/kLine of a tile, where pieces are cut: 2, 3, 4, 6 for full blocks: 6 x 777 rows 100, 94, 91, 90 us,
+// 4 x 2048 180, 176, 171, 173; 4, 8, 12 for few rows: 128 single tokens over up to 900 rows, 32 heads, 214, 198, 191
+// (6, 8, 10 since: 179, 180, 182), 200 x 4 rows 124, 122, 122
+constexpr int kFullCost = 4, kFewCost = 8;
 constexpr float kFlowStart = 5.f;           // cutting them, and a second launch
 constexpr float kSpan = 80 << 20;           // bytes of keys and values that row blocks share in a round of pieces
 constexpr float kPiece = 24.f;              // tiles of a piece at least
-constexpr float kApart = 1.1f;              // pieces against units that meet in the L2
+constexpr float kApart = 1.1f;             // pieces against units that meet in the L2
 constexpr float kEvenFrom = 48.f;           // tiles a CTA from which unequal chunks are worth cutting
 constexpr int kFewTiles = 4;                // so few in a unit, and their number does not matter
 Plan make_plan(const Sizes& z, int sms) {
@@ -929,9 +932,10 @@ Plan make_plan(const Sizes& z, int sms) {
   // stay in the L2 meanwhile: 12 x 141 rows over up to 20000 keys (450 MB) in one round 300 us, in rounds of
   // 32, 64, 80, 128 MB 264, 264, 264, 254; all 20000 long 722, then 514, 515, 517, 594; 2048 rows over 32768 keys 768,
   // then 753, 753, 752, 807; 3 x 3461 rows (146 MB) 138, then 150, 144, 137, 139: more rounds are more parts to join.
-  // Where the plan has units enough for even waves, chunks of one length keep them: CTAs that walk neighbouring row
-  // blocks from the same key on meet in the L2, and pieces do not (3 x 2461 causal rows, 16 key heads: 139 us, in
-  // pieces 168).
+  // Where the plan has units enough for even waves, chunks of one length keep them (kApart): CTAs that walk
+  // neighbouring row blocks from the same key on meet in the L2, and pieces do not (3 x 2461 causal rows, 32 / 16
+  // heads: 132 us, in pieces 140; 4 x 4096 image rows 810 and 882). Else pieces: 1024 rows behind 16384, 32 / 8
+  // heads, 198 us, in units 209.
   const auto flow = [&](Plan c, Rate r) {
     const long long blocks = static_cast<long long>(z.B) * c.nqb * z.Hkv;
     if (!z.paged || !fits(c.nqb)) return;

@@ -20,8 +20,14 @@
 // cluster_join adds the parts through distributed shared memory, in a fixed order. A row
 // whose maximum grows by more than 2^8 rescales O^T (each warp its quarter of the dims).
 //
-// Roles: warp 0 loads K and Q, warp 2 V (and clears V rows past own_len), warp 1 issues
-// S^T, warp 3 O^T; warps 4-7 and 8-11 softmax; with Q8 warps 12-15 turn K codes and warps
+// Keys in pages (PagedParams, FlowParams): the loads are page_of's and load_pages', no prefix. Few rows of a cache
+// in pages come as even pieces (FlowParams: 64 single tokens over up to 4096 rows, 32 / 8 heads, bf16, 103 us, 85 % of
+// the copy rate, where units cut for the longest took 149; one over 131071 88 us, 90 %; the rest is the cut, 4 us, and
+// merge_flow, 5) or, where one wave of clusters has room, as a cluster's chunks (JOIN: 7 x 5 rows over up to 1861 11.3
+// us). With pieces the two softmax warpgroups' parts meet in shared memory, P's place, before they leave the CTA.
+//
+// Roles: warp 0 loads K and Q, warp 2 V, warp 1 issues S^T, warp 3 O^T (and clears V rows past
+// own_len); warps 4-7 and 8-11 softmax; with Q8 warps 12-15 turn K codes and warps
 // 16-19 V codes into 16 bits. Warps that meet at a named barrier never leave their loops
 // early: a wait that expires only makes them skip the work.
 //

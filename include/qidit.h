@@ -366,7 +366,7 @@ qi_status qi_gemm_bf16(qi_dit* dit, const uint16_t* A, const uint16_t* B, float*
  *   The pass's result is then undefined; qi_dit_check (or the next call that
  *   synchronises) returns QI_ERR_DEVICE_TIMEOUT and clears the word, and later
  *   calls run normally.
- * kind 3: the next qi_prefix_attention launch (process-wide, dit may be NULL) waits for bytes of Q
+ * kind 3: the next qi_prefix_attention or qi_paged_attention launch (process-wide, dit may be NULL) waits for bytes of Q
  *   that never come; its waits run out and report into its status word, or to
  *   qi_prefix_attention_check.
  * kind 0: cancel pending injections (of `dit`, if given).
@@ -644,7 +644,7 @@ qi_status qi_add_rmsnorm_mxfp8(const qi_add_rmsnorm* args, qi_stream_t stream);
  * q, k, v: [B, T, Hq or Hkv or Hkv, 128] of in_dtype (dtype, or QI_DT_F32); any of them may be
  * NULL and is passed over. Outputs of dtype (QI_DT_F16 or QI_DT_BF16), 16-byte aligned, strides
  * positive multiples of 16 bytes: q_out [B, T, Hq, 128], which may be q itself; k_out and v_out
- * likewise, or, with a table, the pages [pages, page_rows, Hkv, 128] (page stride in `batch`): row t
+ * likewise (in place: of one type, q's strides), or, with a table, the pages [pages, page_rows, Hkv, 128] (page stride in `batch`): row t
  * goes to cache row start[b] + t. Rows that the table of table_width pages a sequence (rows table_stride
  * apart) does not reach, and page numbers outside 0 .. pages - 1, are passed over: K and V of such a
  * row are not written, its Q is. No two rows may go to one place. Rows at or past lens[b] may hold
@@ -689,7 +689,8 @@ qi_status qi_qk_norm_rope(const qi_qk_rope* args, qi_stream_t stream);
  * of zeros. Rows of a page behind the sequence's last may hold anything, rows before it must be
  * finite. A page may serve several sequences. q, o [B, T, Hq, 128] as for qi_prefix_attention, whose
  * types, roundings and rules for ws and status hold here (NULL status: the same word, told by
- * qi_prefix_attention_check). Results do not depend on what the other sequences hold, and repeat bit for bit.
+ * qi_prefix_attention_check). Results repeat bit for bit and do not depend on what the other sequences hold; how long
+ * the others are moves roundings (where a sequence's keys are cut into parts depends on all lengths).
  * Errors: INVALID_ARG (NULL, dtype, alignment, strides, scale not positive, workspace), SHAPE (B, T,
  * Hkv < 1, Hq % Hkv != 0, Hq / Hkv > 128, B or Hkv > 65535, T or max_len > 2^24, B T Hq >= 2^31,
  * page_rows, pages, table_width, max_len), CUDA. */
@@ -710,7 +711,8 @@ typedef struct qi_paged_attn {
   long long table_stride;
   int dtype, B, T, Hq, Hkv, pages, page_rows, table_width, max_len;
 } qi_paged_attn;
-size_t qi_paged_attention_workspace(const qi_paged_attn* args); /* by the sizes, by whether q_len is NULL; 0 also for bad sizes */
+/* by the sizes, causal and whether q_len is NULL, on the current device; 0 also for bad sizes */
+size_t qi_paged_attention_workspace(const qi_paged_attn* args);
 qi_status qi_paged_attention(const qi_paged_attn* args, qi_stream_t stream);
 
 /* Message for the calling thread's last failed call ("" if none). */

@@ -375,3 +375,30 @@ def test_captured_step(qi):
         g.replay()
         assert torch.equal(o, want[i])
     assert all(torch.equal(a, b) for a, b in zip(cache, final))
+
+
+@pytest.mark.parametrize("G", [4, 17])
+def test_bound_far_above_the_lengths(qi, G):
+    """So many sequences, and so long ones by max_len, that their tiles are not told in 32 bits; all on one page."""
+    import torch
+    B, page, width = 4200, 65536, 256
+    q = _rand(1, B, 1, G, 128)
+    k, v = _rand(2, 1, page, 1, 128), _rand(3, 1, page, 1, 128)
+    n = np.random.default_rng(4).integers(0, 300, B)
+    n[7], n[8] = 0, 1
+    table = torch.full((B, width), -1, dtype=torch.int32, device="cuda")
+    table[:, 0] = 0
+    o = qi.paged_attention(q, qi.PagedKV(k, v), table, _int(n.tolist()), max_len=width * page)
+    s = torch.einsum("bhd,kd->bhk", q[:, 0].double(), k[0, :300, 0].double()) / math.sqrt(128)
+    seen = torch.arange(300, device="cuda")[None, None] < _int(n.tolist())[:, None, None]
+    w = torch.where(seen, torch.exp(s - s.amax(-1, keepdim=True)), 0.0)
+    w = w / w.sum(-1, keepdim=True).clamp(min=1e-300)
+    want, size = w @ v[0, :300, 0].double(), w @ v[0, :300, 0].double().abs()
+    # P and the output rounded to fp16, each by half a step of what it is part of; scores, sums and parts in fp32
+    mag = torch.einsum("bhd,kd->bhk", q[:, 0].double().abs(), k[0, :300, 0].double().abs()).amax(-1, keepdim=True) / math.sqrt(128)
+    ds = mag * (128 * 2.0 ** -23 + 3 * 2.0 ** -24) + 2.0 ** -22
+    tol = (U["fp16"] * (size + want.abs()) * (1 + 2.0 ** -8) + (2 * ds + 2 * 300 * 2.0 ** -23 + 8 * 2.0 ** -22) * size
+           + 300 * 2.0 ** -25 * v[0, :300, 0].double().abs().max() + 2.0 ** -25)
+    err = (o[:, 0].double() - want).abs()
+    assert (o[7] == 0).all()
+    assert (err <= tol).all(), f"{(err / tol).max().item():.2f} of the bound"
