@@ -402,3 +402,39 @@ def test_bound_far_above_the_lengths(qi, G):
     err = (o[:, 0].double() - want).abs()
     assert (o[7] == 0).all()
     assert (err <= tol).all(), f"{(err / tol).max().item():.2f} of the bound"
+
+
+@pytest.mark.parametrize("B,T,Hkv,causal", [(4, 260, 4, True), (8, 100, 8, True), (8, 100, 8, False)])
+def test_pieces_in_several_rounds(qi, B, T, Hkv, causal):
+    """More keys than the L2 holds, shared by several row blocks: the rows of some tokens against 64 bits."""
+    import torch
+    G, S, page = 4, 30000, 64
+    kw = _case(qi, B, T, G * Hkv, Hkv, S, page, ragged=True, seed=5, dtype=torch.bfloat16)
+    rng = np.random.default_rng(6)
+    n, r = rng.integers(S // 3, S + 1, B), rng.integers(1, T + 1, B)
+    n[1], r[2], r[0] = 5, 0, T
+    kw["kv_len"].copy_(_int(n.tolist())), kw["q_len"].copy_(_int(r.tolist()))
+    o = qi.paged_attention(causal=causal, **kw)
+    again = qi.paged_attention(causal=causal, **kw)
+    assert torch.equal(o, again)
+    for b in range(B):
+        assert (o[b, r[b]:] == 0).all()
+        if r[b] == 0:
+            continue
+        rows = sorted({0, r[b] - 1, *(int(x) for x in rng.integers(0, r[b], 4))})
+        pages = kw["table"][b, :-(-n[b] // page)].long()
+        for h in range(Hkv):
+            k, v = (kw["cache"][i][pages, :, h].flatten(0, 1)[:n[b]].double() for i in (0, 1))
+            q = kw["q"][b, rows, h * G:(h + 1) * G].double()
+            s = q @ k.T / math.sqrt(128)
+            lim = torch.tensor([n[b] - r[b] + t + 1 if causal else n[b] for t in rows], device="cuda")
+            s.masked_fill_(torch.arange(n[b], device="cuda") >= lim[:, None, None], -math.inf)
+            w = torch.nan_to_num(torch.softmax(s, -1))  # (a row without a key)
+            want, size = w @ v, w @ v.abs()
+            # P and the output rounded to bf16, each by half a step of what it is part of; scores, sums, parts in fp32
+            mag = (q.abs() @ k.abs().T).amax(-1, keepdim=True) / math.sqrt(128)
+            ds = mag * (128 * 2.0 ** -23 + 3 * 2.0 ** -24) + 2.0 ** -22
+            tol = (U["bf16"] * (size + want.abs()) * (1 + 2.0 ** -8) + (2 * ds + 2 * n[b] * 2.0 ** -23 + 8 * 2.0 ** -22) * size
+                   + 2.0 ** -25)
+            err = (o[b, rows, h * G:(h + 1) * G].double() - want).abs()
+            assert (err <= tol).all(), f"{b} {h}: {(err / tol).max().item():.2f} of the bound"
