@@ -16,7 +16,7 @@ from typing import NamedTuple
 
 import numpy as np
 
-from .build import LIB, TENSORS, build  # noqa: F401  (build() compiles the library)
+from .build import LIB, TENSORS, build, tensors_failure  # noqa: F401  (build() compiles the library)
 
 HIDDEN = 4096
 HEADS = 32
@@ -685,7 +685,8 @@ def _describe(*tensors):
     import torch  # noqa: F401  (what the module is linked to)
     lib()
     if not os.path.exists(TENSORS):
-        raise RuntimeError(f"{TENSORS} is missing: run diffusion_transformer_text_gb300.build() first")
+        raise RuntimeError(f"{TENSORS} is missing: run diffusion_transformer_text_gb300.build() first. "
+                           + tensors_failure())
     spec = importlib.util.spec_from_file_location("qi_tensors", TENSORS)
     module = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(module)

@@ -10,10 +10,12 @@ from __future__ import annotations
 
 import hashlib
 import os
+import shlex
 import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -44,52 +46,99 @@ def _torch_dir() -> str | None:
 
 
 def _torch_version() -> str:
+    return "" if _torch_dir() is None else _read(os.path.join(_torch_dir(), "version.py"))
+
+
+def _tensors_command() -> list:
+    """How qi_tensors.so is compiled (host code over Python's and PyTorch's headers), but for its output."""
+    t, py = _torch_dir(), sysconfig.get_paths()["include"]
+    return [*shlex.split(os.environ.get("CXX", "g++")), "-O2", "-std=c++17", "-shared", "-fPIC", "-I" + py, "-I" + os.path.join(t, "include"),
+            "-I" + os.path.join(t, "include", "torch", "csrc", "api", "include"), os.path.join(CSRC, "tensors.cpp"),
+            "-L" + os.path.join(t, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-Wl,-rpath," + os.path.join(t, "lib")]
+
+
+def _remove(path: str) -> None:
+    if os.path.exists(path):
+        os.remove(path)
+
+
+def _build_tensors(force: bool = False) -> str:
+    """qi_tensors.so, a CPython module; without PyTorch there is none. Returns why it could not be made, or "". Only
+    the calls that read their tensors by it need it, so what went wrong is kept (tensors_failure) for the first of them."""
     if _torch_dir() is None:
         return ""
-    with open(os.path.join(_torch_dir(), "version.py")) as f:
-        return f.read()
-
-
-def _build_tensors() -> None:
-    """qi_tensors.so, a CPython module over PyTorch's headers (host code only); without PyTorch there is none, and
-    the library alone is built."""
-    t, py = _torch_dir(), sysconfig.get_paths()["include"]
-    if t is None:
-        return
-    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
-    tmp = TENSORS + ".tmp"
-    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-I" + py, "-I" + os.path.join(t, "include"),
-           "-I" + os.path.join(t, "include", "torch", "csrc", "api", "include"), "-I" + os.path.join(cuda, "include"),
-           os.path.join(CSRC, "tensors.cpp"), "-o", tmp, "-L" + os.path.join(t, "lib"), "-ltorch_python", "-ltorch_cpu",
-           "-lc10", "-Wl,-rpath," + os.path.join(t, "lib")]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"{cmd[0]} failed on tensors.cpp:\n{r.stdout}\n{r.stderr}")
+    stamp, log, cmd = TENSORS + ".stamp", TENSORS + ".log", _tensors_command()
+    h = hashlib.sha256()
+    with open(os.path.join(CSRC, "tensors.cpp"), "rb") as f:
+        h.update(f.read())
+    h.update("\0".join([*cmd, os.uname().machine, sys.version, _torch_version()]).encode())
+    if not force and os.path.exists(TENSORS) and _read(stamp) == h.hexdigest():
+        return ""
+    tmp, why = TENSORS + ".tmp", ""
+    _remove(tmp)
+    try:
+        r = subprocess.run([*cmd, "-o", tmp], capture_output=True, text=True)
+        if r.returncode != 0 or not os.path.exists(tmp):
+            why = f"{cmd[0]} failed on tensors.cpp (status {r.returncode}):\n{r.stdout}\n{r.stderr}"
+    except OSError as e:
+        why = f"{cmd[0]} could not be run: {e}"
+    _remove(stamp)
+    if why:  # (an older module may be of another PyTorch)
+        _remove(TENSORS)
+        with open(log, "w") as f:
+            f.write(why)
+        return why
     os.replace(tmp, TENSORS)
+    _remove(log)
+    with open(stamp, "w") as f:
+        f.write(h.hexdigest())
+    return ""
+
+
+def tensors_failure() -> str:
+    """Why the last build made no qi_tensors.so, "" if it did."""
+    return _read(TENSORS + ".log")
+
+
+def _read(path: str) -> str:
+    """A text file's contents, "" if there is none."""
+    if not os.path.exists(path):
+        return ""
+    with open(path) as f:
+        return f.read().strip()
 
 
 def _fingerprint() -> str:
     h = hashlib.sha256()
-    for name in SOURCES + HEADERS + ["tensors.cpp"]:
+    for name in SOURCES + HEADERS:
         with open(os.path.join(CSRC, name), "rb") as f:
             h.update(name.encode() + f.read())
     with open(os.path.join(ROOT, "include", "qidit.h"), "rb") as f:
         h.update(f.read())
     h.update(" ".join(ARCH + FLAGS).encode())
     h.update(os.uname().machine.encode())
-    h.update(sys.version.encode() + _torch_version().encode())
     return h.hexdigest()
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile (if sources changed) and return the path of libqidit.so."""
+    """Compile (if sources changed) and return the path of libqidit.so. The binding's qi_tensors.so is compiled
+    beside it; if that fails the library is there all the same, and a warning says why."""
     os.makedirs(BUILD, exist_ok=True)
+    with ThreadPoolExecutor(1) as ex:
+        tensors = ex.submit(_build_tensors, force)
+        _build_library(force, verbose)
+        why = tensors.result()
+    if why:
+        warnings.warn(f"qi_tensors.so was not built, so qk_norm_rope and paged_attention will raise: {why}", RuntimeWarning,
+                      stacklevel=2)
+    return LIB
+
+
+def _build_library(force: bool, verbose: bool) -> None:
     stamp = os.path.join(BUILD, "libqidit.stamp")
     fp = _fingerprint()
-    if not force and os.path.exists(LIB) and os.path.exists(stamp) and (os.path.exists(TENSORS) or _torch_dir() is None):
-        with open(stamp) as f:
-            if f.read().strip() == fp:
-                return LIB
+    if not force and os.path.exists(LIB) and _read(stamp) == fp:
+        return
     cc = nvcc()
 
     def compile_one(src):
@@ -100,10 +149,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
             raise RuntimeError(f"nvcc failed on {src}:\n{r.stdout}\n{r.stderr}")
         return obj, r.stderr
 
-    with ThreadPoolExecutor(len(SOURCES) + 1) as ex:
-        tensors = ex.submit(_build_tensors)
+    with ThreadPoolExecutor(len(SOURCES)) as ex:
         results = list(ex.map(compile_one, SOURCES))
-        tensors.result()
     if verbose:
         for _, log in results:
             sys.stderr.write(log)
@@ -118,7 +165,6 @@ def build(force: bool = False, verbose: bool = False) -> str:
     with open(os.path.join(BUILD, "ptxas.log"), "w") as f:
         for o, log in results:
             f.write(f"== {os.path.basename(o)}\n{log}\n")
-    return LIB
 
 
 if __name__ == "__main__":
