@@ -632,7 +632,7 @@ _paged_layouts: dict = {}
 
 
 class PagedKV(NamedTuple):
-    """K/V in pages: k, v [pages, rows, H, 128] (rows a power of two from 16 up; heads may lie outside rows).
+    """K/V in pages: k, v [pages, rows, H, 128] (rows a power of two, 16 to 65536; heads may lie outside rows).
     `paged_kv` makes an empty one. Which pages are whose says a table, int32 [B, width] on the device: row i
     of sequence b is row i % rows of page table[b, i // rows]."""
     k: "object"
@@ -647,11 +647,11 @@ class Rope(NamedTuple):
 
 
 def paged_kv(pages: int, rows: int, heads: int, dtype=None, device="cuda") -> PagedKV:
-    """A cache of `pages` pages of zeros, `rows` rows each (a power of two from 16 up); dtype: float16 or
+    """A cache of `pages` pages of zeros, `rows` rows each (a power of two, 16 to 65536); dtype: float16 or
     bfloat16 (default)."""
     import torch
-    if rows < 16 or rows & (rows - 1):
-        raise ValueError(f"rows: want a power of two from 16 up, got {rows}")
+    if not 16 <= rows <= 65536 or rows & (rows - 1):
+        raise ValueError(f"rows: want a power of two from 16 to 65536, got {rows}")
     return PagedKV(*(torch.zeros(pages, rows, heads, HEAD_DIM, dtype=torch.bfloat16 if dtype is None else dtype, device=device)
                      for _ in range(2)))
 
