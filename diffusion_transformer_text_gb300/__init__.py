@@ -847,7 +847,9 @@ def _check_paged(key, q, cache, table, kv_len, q_len, max_len, causal, out, stat
     _want(kv_len, torch.int32, (B,), dev, "kv_len")
     _want(q_len, torch.int32, (B,), dev, "q_len")
     _want(status, torch.int32, (1,), dev, "status")
-    longest = min(width * rows, 1 << 24) if max_len is None else max_len
+    longest = width * rows if max_len is None else max_len
+    if max_len is None and longest > 1 << 24:
+        raise ValueError(f"table: reaches row {longest}, lengths go to 2^24: give max_len, the longest kv_len")
     tail = (*qs, *ks, *vs, *os_, stride, dt, B, T, Hq, Hkv, pages, rows, width, longest)
     # (the workspace depends on the sizes and on whether there is a q_len)
     need = _lib.qi_paged_attention_workspace(
@@ -863,9 +865,9 @@ def paged_attention(q, cache: PagedKV, table, kv_len, q_len=None, causal: bool =
     q [B, T, Hq, 128]; cache of the same type, float16 or bfloat16; table int32 [B, width]; kv_len int32 [B], rows
     of each sequence in the cache, the new tokens' among them; q_len int32 [B], its query rows (None: T; the
     others stay as they are in `out` and are zero without it), all on the device. causal: query row t sees rows up
-    to kv_len - q_len + t, else all kv_len. max_len: an upper bound of kv_len known on the host (default: the table's
-    reach), by which the work is cut. scale: default 1 / sqrt(128). A page number that is none reads as zeros; a row
-    that sees nothing is zero. status, stream and strides as for prefix_attention, whose check
+    to kv_len - q_len + t, else all kv_len. max_len: an upper bound of kv_len known on the host, 2^24 at most (default:
+    the table's reach, if that is no more), by which the work is cut. scale: default 1 / sqrt(128). A page number that
+    is none reads as zeros; a row that sees nothing is zero. status, stream and strides as for prefix_attention, whose check
     (prefix_attention_check) tells of expired waits. Returns o [B, T, Hq, 128]. No gradients."""
     import torch
     ck, cv = cache
