@@ -866,9 +866,11 @@ def paged_attention(q, cache: PagedKV, table, kv_len, q_len=None, causal: bool =
     of each sequence in the cache, the new tokens' among them; q_len int32 [B], its query rows (None: T; the
     others stay as they are in `out` and are zero without it), all on the device. causal: query row t sees rows up
     to kv_len - q_len + t, else all kv_len. max_len: an upper bound of kv_len known on the host, 2^24 at most (default:
-    the table's reach, if that is no more), by which the work is cut. scale: default 1 / sqrt(128). A page number that
-    is none reads as zeros; a row that sees nothing is zero. status, stream and strides as for prefix_attention, whose check
-    (prefix_attention_check) tells of expired waits. Returns o [B, T, Hq, 128]. No gradients."""
+    the table's reach, if that is no more), by which the work is cut: chunks take up to three times as long under a
+    bound far above the lengths, and one that changes with every call costs 10 us of host time in each (rounded up to
+    128, next to none). scale: default 1 / sqrt(128). A page number that is none reads as zeros; a row that sees
+    nothing is zero. status, stream and strides as for prefix_attention, whose check (prefix_attention_check) tells of
+    expired waits. Returns o [B, T, Hq, 128]. No gradients."""
     import torch
     ck, cv = cache
     layout, addresses = _describe(q, ck, cv, out, table, kv_len, q_len, None, status)

@@ -15,11 +15,11 @@
 // of the time: 4 x 4096 image rows over up to 4590 keys, 32 heads, 805-830 us, 1.4 PFLOP/s; 1024 rows behind 16384, 195
 // us): issue, product, softmax, each after the other, of which the exponentials are 950 cycles of the 32 softmax
 // lanes' 64 keys. Between units, with few tiles in each, instruction fetch: the kernel is longer than the SM's
-// instruction cache, and whatever a unit's beginning or end runs comes from the L2 (6 x 777 rows over up to 3001 keys: a
-// tenth of the warps' time is spent without an instruction). So the code is kept short: units walked by one warp
-// and not by four (6 x 777 rows 94.5 -> 88 us, 16 x 300 66 -> 61), the epilogue in a loop that is not unrolled
-// (16 x 300 rows 61 -> 56); a walk begun a unit ahead, to have its first pages and Q early, cost more than it
-// gave (6 x 777 rows 94.5 -> 99).
+// instruction cache, and whatever a unit's beginning or end runs comes from the L2 (6 x 777 rows over up to 3001
+// keys: 0.45 million misses, 11 % of the warps' time is spent without an instruction). So the code is kept short: units
+// walked by one warp and not by four (6 x 777 rows 94.5 -> 88 us, 16 x 300 66 -> 61), the epilogue in a loop that is not
+// unrolled (16 x 300 rows 61 -> 56, and 60 since load_8_pages); a walk begun a unit ahead, to have its first pages and Q
+// early, cost more than it gave (6 x 777 rows 94.5 -> 99).
 //
 // Units: whole row blocks in the order that prefix_attention.cu's plan gives (chunks of one length), even
 // pieces of all tiles cut on the device (FlowParams: single tokens with many heads, chunks of unlike

@@ -812,12 +812,17 @@ constexpr long long kL2Half = 64ll << 20;
 // 4 x 2048 180, 176, 171, 173; 4, 8, 12 for few rows: 128 single tokens over up to 900 rows, 32 heads, 214, 198, 191
 // (6, 8, 10 since: 179, 180, 182), 200 x 4 rows 124, 122, 122
 constexpr int kFullCost = 4, kFewCost = 8;
-constexpr float kFlowStart = 5.f;           // cutting them, and a second launch
+// The next four against other values: geometric mean over 8 random calls whose plan the value changes. Larger ones
+// would do better for three of them.
+constexpr float kFlowStart = 5.f;           // cutting them, and a second launch. 0: 29 % longer. 10: 39 % shorter, by few row blocks
+                                            // whose pieces leave many parts (1 x 77 rows over 9008 keys 46 -> 14.5 us)
 constexpr float kSpan = 80 << 20;           // bytes of keys and values that row blocks share in a round of pieces
-constexpr float kPiece = 24.f;              // tiles of a piece at least
+constexpr float kPiece = 24.f;              // tiles of a piece at least. 12: 12 % longer, 48: 1 % longer
 constexpr float kApart = 1.1f;             // pieces against units that meet in the L2
-constexpr float kEvenFrom = 48.f;           // tiles a CTA from which unequal chunks are worth cutting
-constexpr int kFewTiles = 4;                // so few in a unit, and their number does not matter
+constexpr float kEvenFrom = 48.f;           // tiles a CTA from which unequal chunks are worth cutting. 12: 28 % longer, 192: 8 %
+                                            // shorter (3 x 452 rows over up to 29394 keys 31 % longer, 3 x 85 over 58545 25 % shorter)
+constexpr int kFewTiles = 4;                // so few in a unit, and their number does not matter. 1: 18 % longer, 8: 13 % shorter
+                                            // (92 x 191 rows over up to 774 keys, 32 heads, 26 % longer)
 Plan make_plan(const Sizes& z, int sms) {
   Plan a{};
   a.G = z.Hq / z.Hkv;
@@ -843,7 +848,8 @@ Plan make_plan(const Sizes& z, int sms) {
   const float convert = z.from8 && z.P > 0 ? kConvertStart + kConvert * static_cast<float>(z.P) * z.Hkv * kHeadDim / (1 << 20) : 0.f;
   // pieces can be cut: the line in an int (beyond it, seconds of work, units will do)
   const auto fits = [&](int nqb) { return static_cast<float>(z.B) * nqb * z.Hkv * ((a.ot + 4) * kLine) < 2e9f; };
-  // single tokens, or chunks of unlike lengths with enough tiles to cut
+  // single tokens, or chunks of lengths of their own (q_len) with enough tiles to cut; without q_len the lengths in the
+  // cache may differ all the same, and units cut by the longest then leave CTAs idle
   const int nqb_full = z.paged ? ceil_div(z.T, kRows / a.G) : 0;
   const bool even = z.paged && fits(nqb_full) &&
                     (nqb_full == 1 ||
@@ -874,7 +880,8 @@ Plan make_plan(const Sizes& z, int sms) {
       }
     }
   };
-  // joint units whose chunks join in a cluster: one unit per CTA; clusters of more than two leave
+  // joint units whose chunks join in a cluster: one unit per CTA, counted by the whole bound (by what causal chunks see
+  // 21 of 5483 random calls would change, 8 of which took 16 % less time, 0.49 to 1.14); clusters of more than two leave
   // some SMs of a processing cluster over (of 152: 138 to 144 CTAs in clusters of 3 to 6, 105 of 7)
   const auto joined = [&](Plan c, Rate r, int least, float more) {
     const int n = c.pt + c.ot;

@@ -681,7 +681,8 @@ qi_status qi_qk_norm_rope(const qi_qk_rope* args, qi_stream_t stream);
  * clamped to 0 .. kv_len[b]. A row that sees no key is zero. kv_len (device int32 [B]) is clamped to
  * 0 .. max_len, q_len (device int32 [B], NULL: all T) to 0 .. T, both read when the kernels run; rows
  * of q at or past q_len[b] may hold anything, those of o stay as they are. max_len, at most
- * table_width * page_rows, is what the work is cut by: the nearer to the longest kv_len, the better.
+ * table_width * page_rows, is what the work is cut by: the nearer to the longest kv_len, the better (single chunks
+ * take up to three times as long under a bound far above the lengths).
  *
  * k, v: the pages [pages, page_rows, Hkv, 128] (page stride in `batch`; heads may lie outside
  * rows); table: device int32 [B, table_width], rows table_stride apart, of which the first
